@@ -83,6 +83,8 @@ _SIGS = {
                                          c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                          c_void_p, c_float, c_int32, c_int32, c_void_p, c_void_p,
                                          c_size_t, c_void_p]),
+    "dsa_rmsnorm": (c_int32, [c_int32, c_int32, c_void_p, c_int64, c_void_p, c_void_p, c_float,
+                              c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
     "dsa_decode_mli": (c_int32, [ctypes.POINTER(DecodeDesc), c_void_p, c_void_p, c_void_p,
                                  c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                  c_float, c_int32, c_int32, c_void_p, c_void_p, c_size_t,
@@ -297,6 +299,64 @@ def dsa_decode_fused_fp8kv(desc, q_fp8, q_scale, w, k_fp8, k_scale, q, kv8, out,
         _ptr(topk_in, torch.int32, "topk_in"), _ptr(topk_out, torch.int32, "topk_out"),
         float(sm_scale), int(num_splits), int(max_seqlen), _ptr(out, torch.float32, "out"),
         _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream)), "dsa_decode_fused_fp8kv")
+
+
+def _arg(t, dtype, shape, dev, name):
+    """Pointer of a contiguous tensor of that dtype and shape on CUDA device ``dev`` (None: NULL).  One
+    combined test for the usual case: a small launch is bound by what the host does before it."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch tensor")
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: expected a tensor on the current device cuda:{dev}, got {t.device}")
+    raise ValueError(f"{name}: expected a contiguous tensor")
+
+
+def _rows_arg(t, dtype, dev, name):
+    """(pointer, row stride) of a 2-D tensor with contiguous columns; its rows may be strided."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.dim() != 2:
+        raise TypeError(f"{name}: expected a 2-D {dtype} tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: expected a tensor on the current device cuda:{dev}, got {t.device}")
+    rows, cols = t.shape
+    ld, step = t.stride()
+    if cols > 1 and step != 1:
+        raise ValueError(f"{name}: expected contiguous columns")
+    return t.data_ptr(), (ld if rows > 1 else cols)
+
+
+def _stream_on(stream, dev) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return _stream(stream)
+
+
+def dsa_rmsnorm(x, weight, eps, residual=None, residual_out=None, y=None, y8=None, y_scale=None,
+                group=128, stream=None):
+    """Residual addition and root-mean-square norm of ``x`` [rows, dim] (rows may be strided, e.g. a
+    slice of a wider projection), into ``y`` (bf16) and / or ``y8`` + ``y_scale`` (E4M3 codes as uint8,
+    fp32 scales [rows, ceil(dim / 128)], or [rows, 1] for ``group=0``); see include/dsa.h."""
+    fn, dev, bf16 = lib().dsa_rmsnorm, torch.cuda.current_device(), torch.bfloat16
+    xp, ld = _rows_arg(x, bf16, dev, "x")
+    shape = x.shape
+    rows, dim = shape
+    _check(fn(rows, dim, xp, ld, _arg(residual, bf16, shape, dev, "residual"),
+              _arg(weight, bf16, (dim,), dev, "weight"), eps, group,
+              _arg(residual_out, bf16, shape, dev, "residual_out"), _arg(y, bf16, shape, dev, "y"),
+              _arg(y8, torch.uint8, shape, dev, "y8"),
+              _arg(y_scale, torch.float32, (rows, -(-dim // 128) if group else 1), dev, "y_scale"),
+              _stream_on(stream, dev)), "dsa_rmsnorm")
 
 
 def dsa_decode_mli(desc, q_fp8, q_scale, w, k_fp8, k_scale, q, kv, topk_prev, topk_next, out, ws,

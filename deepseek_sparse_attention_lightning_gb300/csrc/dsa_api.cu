@@ -289,6 +289,29 @@ dsa_status dsa_latent_to_fp8(const uint16_t* kv, int64_t rows, uint8_t* kv8, voi
   return cuda_status(dsa::launch_latent_fp8(kv, rows, kv8, static_cast<cudaStream_t>(stream)));
 }
 
+dsa_status dsa_rmsnorm(int32_t rows, int32_t dim, const uint16_t* x, int64_t ld_x,
+                       const uint16_t* residual, const uint16_t* weight, float eps, int32_t group,
+                       uint16_t* residual_out, uint16_t* y, uint8_t* y8, float* y_scale,
+                       void* stream) {
+  if (rows < 0 || dim < 1 || ld_x < dim || !(eps >= 0.f) || !std::isfinite(eps))
+    return DSA_ERR_INVALID_ARG;
+  if (dim % 8 != 0 || dim > DSA_MAX_NORM_DIM || (group != 0 && group != 128))
+    return DSA_ERR_UNSUPPORTED;
+  if (rows == 0) return DSA_OK;
+  if ((residual == nullptr) != (residual_out == nullptr) || (y8 == nullptr) != (y_scale == nullptr) ||
+      (!y && !y8))
+    return DSA_ERR_INVALID_ARG;
+  if (!x || !weight || ld_x % 8 != 0 || !aligned(x, 16) || !aligned(weight, 16) ||
+      !aligned(residual, 16) || !aligned(residual_out, 16) || !aligned(y, 16) || !aligned(y8, 8) ||
+      !aligned(y_scale, 4))
+    return DSA_ERR_INVALID_ARG;
+  dsa::RmsNormLaunch a{};
+  a.x = x; a.residual = residual; a.weight = weight; a.residual_out = residual_out; a.y = y;
+  a.y8 = y8; a.y_scale = y_scale; a.rows = rows; a.ld_x = ld_x; a.dim = dim; a.group = group;
+  a.eps = eps;
+  return cuda_status(dsa::launch_rmsnorm(a, static_cast<cudaStream_t>(stream)));
+}
+
 dsa_status dsa_merge(int32_t num_rows, int32_t num_splits, const float* mid_o, const float* mid_lse,
                      float* out, float* out_lse, void* stream) {
   if (num_rows < 0 || num_splits < 1) return DSA_ERR_INVALID_ARG;

@@ -84,6 +84,20 @@ struct MlaLaunch {
                         //    completes only after that kernel
 };
 
+struct RmsNormLaunch {
+  const uint16_t* x;             // [rows] rows of dim bf16, ld_x apart
+  const uint16_t* residual;      // [rows][dim] bf16 or nullptr
+  const uint16_t* weight;        // [dim] bf16
+  uint16_t* residual_out;        // [rows][dim] bf16 or nullptr
+  uint16_t* y;                   // [rows][dim] bf16 or nullptr
+  uint8_t* y8;                   // [rows][dim] E4M3 or nullptr
+  float* y_scale;                // [rows][tiles] (with y8)
+  long long rows, ld_x;
+  int dim;
+  int group;                     // 128: a scale for each 128 columns; 0: one a row
+  float eps;
+};
+
 cudaError_t launch_indexer(const IndexerLaunch& a, cudaStream_t s);
 // Bound, in SM cycles, of the indexer's pipeline waits on later launches
 // (<= 0: the default kWaitCycles).
@@ -92,6 +106,7 @@ cudaError_t launch_topk(const TopkLaunch& a, cudaStream_t s);
 cudaError_t launch_sparse_mla(const MlaLaunch& a, cudaStream_t s);
 cudaError_t launch_cache_write(const CacheWriteLaunch& a, cudaStream_t s);
 cudaError_t launch_latent_fp8(const uint16_t* kv, long long rows, uint8_t* kv8, cudaStream_t s);
+cudaError_t launch_rmsnorm(const RmsNormLaunch& a, cudaStream_t s);
 cudaError_t launch_merge(int rows, int splits, const float* mid_o, const float* mid_lse,
                          float* out, float* out_lse, cudaStream_t s, bool pdl = false);
 

@@ -68,6 +68,7 @@ typedef enum dsa_status {
 #define DSA_MAX_TOPK 2048
 #define DSA_MAX_BATCH 1024
 #define DSA_MAX_Q_PER_REQ 4
+#define DSA_MAX_NORM_DIM 32768
 
 /*
  * One decode batch.  Sizes are host integers; seqlens and page_table are
@@ -338,6 +339,39 @@ dsa_status dsa_decode_fused_fp8kv(const dsa_decode_desc* desc,
                                   const int32_t* topk_in, int32_t* topk_out,
                                   float sm_scale, int32_t num_splits, int32_t max_seqlen,
                                   float* out, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * The norm in front of a layer's projections, and of the latent before it is
+ * cached: residual addition, root-mean-square norm, output in bf16 and / or in
+ * FP8 E4M3 with fp32 scales ("Deepseek Details", section "FP8 Training": E4M3,
+ * 1 x 128 tiles; the formulas are the textbook ones).  For each row
+ *   h = x + residual              (h = x without a residual)
+ *   y = h / sqrt(sum(h^2) / dim + eps) * weight
+ *   scale = amax(|y| over a tile) / 448 (a tile of zeros: 1),
+ *   code = E4M3(y / scale), rounded to nearest even and saturated at 448
+ * in fp32; h, y and the codes are each rounded once, where they are stored (y
+ * is normalised from the unrounded h, the codes come from the unrounded y).
+ *   rows, dim     dim a multiple of 8, at most DSA_MAX_NORM_DIM
+ *                 (DSA_ERR_UNSUPPORTED); rows may be 0
+ *   x             [dev] bf16, row r at x + r * ld_x (ld_x >= dim, a multiple of
+ *                 8: the first 512 of a 576-column projection, say)
+ *   residual      [dev] bf16 [rows, dim] or NULL (then residual_out is NULL)
+ *   weight        [dev] bf16 [dim]
+ *   group         128: a scale for every 128 columns (the last tile may be
+ *                 shorter); 0: one scale a row
+ *   residual_out  [dev] bf16 [rows, dim]: h, the next residual; may be the
+ *                 residual itself, or x where ld_x == dim
+ *   y             [dev] bf16 [rows, dim] or NULL; may be x where ld_x == dim
+ *                 (but not a buffer that residual_out uses)
+ *   y8, y_scale   [dev] E4M3 [rows, dim], float [rows, group ? ceil(dim / 128)
+ *                 : 1]; both NULL without an FP8 output (then y is required)
+ * bf16 buffers are 16-byte aligned, y8 8-byte aligned.  Other overlaps of
+ * inputs and outputs are not supported.
+ */
+dsa_status dsa_rmsnorm(int32_t rows, int32_t dim, const uint16_t* x, int64_t ld_x,
+                       const uint16_t* residual, const uint16_t* weight, float eps, int32_t group,
+                       uint16_t* residual_out, uint16_t* y, uint8_t* y8, float* y_scale,
+                       void* stream);
 
 /*
  * One layer of the Multi-layer Indexer schedule ("Multi-layer Indexer:

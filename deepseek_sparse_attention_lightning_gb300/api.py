@@ -83,6 +83,9 @@ _SIGS = {
                                          c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                          c_void_p, c_float, c_int32, c_int32, c_void_p, c_void_p,
                                          c_size_t, c_void_p]),
+    "dsa_mla_decode": (c_int32, [ctypes.POINTER(DecodeDesc), c_void_p, c_void_p, c_float, c_void_p,
+                                 c_void_p, c_void_p, c_size_t, c_void_p]),
+    "dsa_mla_decode_workspace_bytes": (c_size_t, [ctypes.POINTER(DecodeDesc)]),
     "dsa_rmsnorm": (c_int32, [c_int32, c_int32, c_void_p, c_int64, c_void_p, c_void_p, c_float,
                               c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
     "dsa_decode_mli": (c_int32, [ctypes.POINTER(DecodeDesc), c_void_p, c_void_p, c_void_p,
@@ -340,6 +343,22 @@ def _stream_on(stream, dev) -> int:
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(dev)
     return _stream(stream)
+
+
+def dsa_mla_decode_workspace_bytes(desc) -> int:
+    return int(lib().dsa_mla_decode_workspace_bytes(ctypes.byref(desc)))
+
+
+def dsa_mla_decode(desc, q, kv, out, ws, sm_scale, lse=None, stream=None):
+    """Dense latent attention over the paged cache (every visible token): ``out`` bf16 [T, H, 512],
+    ``lse`` float32 [T, H] or None; see include/dsa.h."""
+    fn, dev, bf16 = lib().dsa_mla_decode, torch.cuda.current_device(), torch.bfloat16
+    T, H = desc.batch * desc.q_per_req, desc.num_heads
+    _check(fn(ctypes.byref(desc), _arg(q, bf16, (T, H, 576), dev, "q"),
+              _arg(kv, bf16, (desc.num_pages * PAGE_SIZE, 576), dev, "kv"), sm_scale,
+              _arg(out, bf16, (T, H, 512), dev, "out"), _arg(lse, torch.float32, (T, H), dev, "lse"),
+              _arg(ws, torch.uint8, (ws.numel(),), dev, "ws"), ws.numel(), _stream_on(stream, dev)),
+           "dsa_mla_decode")
 
 
 def dsa_rmsnorm(x, weight, eps, residual=None, residual_out=None, y=None, y8=None, y_scale=None,

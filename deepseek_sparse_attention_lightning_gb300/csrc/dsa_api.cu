@@ -289,6 +289,46 @@ dsa_status dsa_latent_to_fp8(const uint16_t* kv, int64_t rows, uint8_t* kv8, voi
   return cuda_status(dsa::launch_latent_fp8(kv, rows, kv8, static_cast<cudaStream_t>(stream)));
 }
 
+namespace {
+
+// The descriptor of a dense call: topk is not used, and any number of heads up
+// to 128 is taken.
+dsa_status check_dense_desc(const dsa_decode_desc* d) {
+  if (!d) return DSA_ERR_INVALID_ARG;
+  dsa_decode_desc c = *d;
+  c.topk = 1;
+  if (c.num_heads >= 1 && c.num_heads <= 128) c.num_heads = 16;
+  return check_desc(&c);
+}
+
+}  // namespace
+
+size_t dsa_mla_decode_workspace_bytes(const dsa_decode_desc* d) {
+  if (check_dense_desc(d) != DSA_OK) return 0;
+  int tiles, groups;
+  size_t bytes;
+  dsa::mla_decode_plan(d->q_per_req, d->num_heads, &tiles, &groups, &bytes);
+  return bytes;
+}
+
+dsa_status dsa_mla_decode(const dsa_decode_desc* d, const uint16_t* q, const uint16_t* kv,
+                          float sm_scale, uint16_t* out, float* lse, void* ws, size_t ws_bytes,
+                          void* stream) {
+  dsa_status st = check_dense_desc(d);
+  if (st != DSA_OK) return st;
+  if (!q || !kv || !out || !aligned(q, 16) || !aligned(kv, 16) || !aligned(out, 16) ||
+      !aligned(lse, 4))
+    return DSA_ERR_INVALID_ARG;
+  if (!(sm_scale > 0.f) || !std::isfinite(sm_scale)) return DSA_ERR_INVALID_ARG;
+  if (!ws || !aligned(ws, 256) || ws_bytes < dsa_mla_decode_workspace_bytes(d))
+    return DSA_ERR_WORKSPACE;
+  dsa::MlaDecodeLaunch a{};
+  a.q = q; a.kv = kv; a.seqlens = d->seqlens; a.page_table = d->page_table; a.out = out; a.lse = lse;
+  a.batch = d->batch; a.nq = d->q_per_req; a.heads = d->num_heads; a.max_pages = d->max_pages;
+  a.num_pages = d->num_pages; a.sm_scale = sm_scale;
+  return cuda_status(dsa::launch_mla_decode(a, ws, static_cast<cudaStream_t>(stream)));
+}
+
 dsa_status dsa_rmsnorm(int32_t rows, int32_t dim, const uint16_t* x, int64_t ld_x,
                        const uint16_t* residual, const uint16_t* weight, float eps, int32_t group,
                        uint16_t* residual_out, uint16_t* y, uint8_t* y8, float* y_scale,
@@ -724,8 +764,9 @@ dsa_status dsa_decode_step_ring(const dsa_decode_desc* desc, dsa_step_ring* ring
 
 dsa_status dsa_get_device_error(void* stream) {
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return DSA_ERR_CUDA;
-  const int codes[5] = {dsa::fetch_error_indexer(), dsa::fetch_error_topk(), dsa::fetch_error_mla(),
-                        dsa::fetch_error_merge(), dsa::fetch_error_cache()};
+  const int codes[6] = {dsa::fetch_error_indexer(), dsa::fetch_error_topk(), dsa::fetch_error_mla(),
+                        dsa::fetch_error_merge(), dsa::fetch_error_cache(),
+                        dsa::fetch_error_mla_dense()};
   for (int c : codes)
     if (c != 0) return static_cast<dsa_status>(c);
   return DSA_OK;

@@ -98,6 +98,20 @@ struct RmsNormLaunch {
   float eps;
 };
 
+struct MlaDecodeLaunch {
+  const uint16_t* q;             // [T][H][576] bf16
+  const uint16_t* kv;            // [num_pages * 64][576] bf16
+  const int32_t* seqlens;
+  const int32_t* page_table;
+  uint16_t* out;                 // [T][H][512] bf16
+  float* lse;                    // [T][H] or nullptr
+  float* part_o;                 // set by launch_mla_decode: partial outputs and
+  float* part_lse;               //   their log-sum-exps, in the workspace
+  int batch, nq, heads, max_pages, num_pages;
+  int row_tiles, groups, min_pages;   // set by launch_mla_decode
+  float sm_scale;
+};
+
 cudaError_t launch_indexer(const IndexerLaunch& a, cudaStream_t s);
 // Bound, in SM cycles, of the indexer's pipeline waits on later launches
 // (<= 0: the default kWaitCycles).
@@ -107,6 +121,10 @@ cudaError_t launch_sparse_mla(const MlaLaunch& a, cudaStream_t s);
 cudaError_t launch_cache_write(const CacheWriteLaunch& a, cudaStream_t s);
 cudaError_t launch_latent_fp8(const uint16_t* kv, long long rows, uint8_t* kv8, cudaStream_t s);
 cudaError_t launch_rmsnorm(const RmsNormLaunch& a, cudaStream_t s);
+// Dense latent attention: its plan (row tiles of a request, groups of CTA
+// pairs, workspace bytes; no kernel) and its launch.
+void mla_decode_plan(int nq, int heads, int* row_tiles, int* groups, size_t* ws_bytes);
+cudaError_t launch_mla_decode(MlaDecodeLaunch a, void* ws, cudaStream_t s);
 cudaError_t launch_merge(int rows, int splits, const float* mid_o, const float* mid_lse,
                          float* out, float* out_lse, cudaStream_t s, bool pdl = false);
 
@@ -148,6 +166,7 @@ int fetch_error_topk();
 int fetch_error_mla();
 int fetch_error_merge();
 int fetch_error_cache();
+int fetch_error_mla_dense();
 
 // Host helpers (dsa_api.cu).
 // The checks every entry point applies to a decode descriptor: a dsa_status.

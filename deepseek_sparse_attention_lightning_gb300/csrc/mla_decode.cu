@@ -1,0 +1,691 @@
+// mla_decode.cu -- latent attention in its absorbed form over every visible
+// token of the paged latent cache (no selection), for decode and MTP
+// verification ("[SGLang] NSA", section "forward_decode": q_nope absorbed to
+// 512 dims + 64 rope dims against 576-dim latent rows whose first 512 dims are
+// the values; "MTP and sparse attention: NSA and DSA": the dense MLA the
+// sparse layer replaces).
+//
+//   x[row, s] = sm_scale * q[row] . c[s]      (576 dims, s < vis[row])
+//   out[row]  = sum_s softmax(x)[s] * c[s, 0:512],   lse = log sum_s exp(x)
+//
+// A request's n_q * H query rows are cut into row tiles of 128; a tile's keys
+// are the request's pages (64 tokens).  The matrix work of a page and a row
+// tile (128 x 64 x 1088 multiply-adds) against its 73.7 KB is close to the
+// GPU's ridge, so both pipes matter.
+//
+// Two CTAs (a cluster on one pair of SMs) share a row tile: tcgen05 with
+// cta_group::2 and M = 128, 64 rows in each CTA.  The fp32 output of 64 rows x
+// 512 dims takes 256 of a CTA's 512 TMEM columns (64 rows use all 128 lanes:
+// lanes 0-63 hold the first half of an MMA's N columns, lanes 64-127 the
+// second), which leaves room for double-buffered scores; and each CTA keeps
+// only its share of the operands: for Q K^T half of the page's tokens (32 x
+// 576), for P V half of the value dims of all 64.  A CTA that works alone
+// holds half of the output only by computing all of Q K^T twice.
+//
+// Shared memory: q 72 KB (64 rows), two stages of K (36 KB) and of V (32 KB),
+// two P tiles (8 KB).  A page is fetched as three tensor copies in the 128B
+// swizzled layout that the MMAs read.  K of a page is freed by its Q K^T, V by
+// its P V, so the copies run two pages ahead.
+//
+// Work: the pages of all requests form one line that is cut evenly over the
+// CTA pairs (n_q * H > 128: over groups of pairs, one pair for each row tile,
+// which walk the same pages at the same time and share them in L2).  A pair
+// may end one request and begin the next; a request that spans pairs is
+// joined by mla_merge_kernel from fp32 partials and their log-sum-exps.
+//
+// Roles (256 threads a CTA): warp 0 copies q and K, warp 2 copies V, warp 1
+// of the leading CTA issues the MMAs of both, warps 4-7 are softmax and
+// epilogue (thread = row and half of the tile's keys; the two threads of a row
+// agree on its maximum through shared memory).  Q K^T of page j + 1 runs while
+// page j is in the softmax.  The running maximum is raised lazily (only when a
+// page exceeds it by 2^8 does the output get rescaled).  P is rounded to bf16
+// for the matrix pipe (as values and keys are); its sum is kept unrounded in
+// fp32, so the log-sum-exp has fp32 accuracy.
+//
+// Rows of V that no query row sees (behind the request's end in its last page,
+// or a page whose id is out of range) are cleared in shared memory before P V:
+// their probabilities are zero, but stale cache memory may hold NaN.
+#include "dsa_ptx.cuh"
+#include "dsa_internal.h"
+
+DSA_DEFINE_ERROR_WORD(mla_dense)
+
+namespace dsa {
+namespace {
+
+constexpr int kRowsCta = 64;                              // query rows of a CTA
+constexpr int kRowTile = 2 * kRowsCta;
+constexpr int kAtoms = kLatentDim / 64;                   // 9 atoms of 64 dims
+constexpr int kQBytes = kRowsCta * kLatentDim * 2;        // 72 KB
+constexpr int kKBytes = (kPage / 2) * kLatentDim * 2;     // 36 KB
+constexpr int kVBytes = kPage * (kVDim / 2) * 2;          // 32 KB
+constexpr int kPBytes = kRowsCta * kPage * 2;             // 8 KB
+constexpr int kQAtom = kRowsCta * 128, kKAtom = (kPage / 2) * 128, kVAtom = kPage * 128;
+constexpr int kOffQ = 0;
+constexpr int kOffK = kOffQ + kQBytes;
+constexpr int kOffV = kOffK + 2 * kKBytes;
+constexpr int kOffP = kOffV + 2 * kVBytes;
+constexpr int kOffXchg = kOffP + 2 * kPBytes;             // 2 x 128 floats
+constexpr int kOffBar = kOffXchg + 2 * 128 * 4;
+constexpr int kOffInfo = kOffBar + 24 * 8;
+constexpr int kSmemBytes = kOffInfo + 32 + 1024;
+static_assert(kSmemBytes <= 232448, "shared memory");
+constexpr int kColO = 0, kColS = 256, kTmemCols = 512;    // S: 2 x 32 columns
+constexpr int kThreads = 256;
+constexpr int kSoftWarps = 4;
+constexpr float kRaiseLog2 = 8.0f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Tokens of request r: seqlens[r], at least 0 and at most what its row of the
+// page table covers (more is an error the kernel reports).
+__device__ __forceinline__ int request_len(const MlaDecodeLaunch& p, int r) {
+  const int s = __ldg(p.seqlens + r);
+  if (s > p.max_pages * kPage) {
+    raise_error(kErrCheck);
+    return p.max_pages * kPage;
+  }
+  return s < 0 ? 0 : s;
+}
+
+__device__ __forceinline__ int pages_of(int len) { return (len + kPage - 1) / kPage; }
+
+// The line of pages: total number of pages, and the groups it is cut into.
+struct Line {
+  long long total;
+  int groups;
+};
+
+__device__ __forceinline__ long long cut(const Line& ln, int g) { return ln.total * g / ln.groups; }
+
+// (one warp) Total pages of all requests.
+__device__ __forceinline__ Line scan_total(const MlaDecodeLaunch& p, int lane) {
+  long long n = 0;
+  for (int r = lane; r < p.batch; r += 32) n += pages_of(request_len(p, r));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+  Line ln;
+  ln.total = n;
+  const long long most = (n + p.min_pages - 1) / p.min_pages;
+  ln.groups = most < p.groups ? static_cast<int>(most < 1 ? 1 : most) : p.groups;
+  return ln;
+}
+
+// (one warp) The request that holds page `at` of the line (at < total), and
+// the line position of its first page.
+__device__ __forceinline__ void locate(const MlaDecodeLaunch& p, long long at, int lane, int& req,
+                                       long long& first) {
+  long long base = 0;
+  req = 0;
+  first = 0;
+  for (int r0 = 0; r0 < p.batch; r0 += 32) {
+    const int r = r0 + lane;
+    const int n = r < p.batch ? pages_of(request_len(p, r)) : 0;
+    long long incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long u = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += u;
+    }
+    const uint32_t hit = __ballot_sync(0xffffffffu, base + incl > at);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      req = r0 + l;
+      first = base + __shfl_sync(0xffffffffu, incl - n, l);
+      return;
+    }
+    base += __shfl_sync(0xffffffffu, incl, 31);
+  }
+}
+
+// The stretches of requests in a group's part [lo, hi) of the line, in order.
+struct Walk {
+  long long pos, hi;     // next page of the line, end of the part
+  int req;               // request of the stretch
+  int len;               // its tokens
+  int t0, t1, nt;        // the stretch's pages [t0, t1) of the request's nt
+  __device__ __forceinline__ bool next(const MlaDecodeLaunch& p) {
+    if (pos >= hi) return false;
+    if (t1 > 0 || nt == 0) {     // not the first stretch: on to the next request with pages
+      do {
+        ++req;
+        len = request_len(p, req);
+        nt = pages_of(len);
+      } while (nt == 0);
+      t0 = 0;
+    }
+    const long long left = hi - pos;
+    t1 = static_cast<int>(left < nt - t0 ? t0 + left : nt);
+    pos += t1 - t0;
+    return true;
+  }
+};
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    mla_decode_kernel(const __grid_constant__ CUtensorMap tmap_q,
+                      const __grid_constant__ CUtensorMap tmap_k,
+                      const __grid_constant__ CUtensorMap tmap_v, const MlaDecodeLaunch p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int worker = blockIdx.x >> 1;
+  const int group = worker / p.row_tiles, mtile = worker % p.row_tiles;
+  const int rows_req = p.nq * p.heads;
+  const float ninf = __int_as_float(0xff800000);
+
+  const uint32_t bar0 = sbase + kOffBar;
+// In the leading CTA (both CTAs' threads and copies arrive there):
+//   Q_FULL, K_FULL(s): q / K of stage s landed in both CTAs; P_FULL(s): P of
+//   stage s written and V of stage s landed in both; O_FREE: the epilogue has
+//   read the output.
+// In both (the MMAs' completion arrives in both): S_FULL(s), K_EMPTY(s),
+//   V_EMPTY(s) (P V of the stage's page done).  V_FULL(s): this CTA's V copies.
+#define Q_FULL (bar0)
+#define O_FREE (bar0 + 8u)
+#define DRAIN (bar0 + 16u)
+#define K_FULL(s) (bar0 + 24u + 8u * (s))
+#define K_EMPTY(s) (bar0 + 40u + 8u * (s))
+#define V_FULL(s) (bar0 + 56u + 8u * (s))
+#define V_EMPTY(s) (bar0 + 72u + 8u * (s))
+#define S_FULL(s) (bar0 + 88u + 8u * (s))
+#define P_FULL(s) (bar0 + 104u + 8u * (s))
+  long long* info = reinterpret_cast<long long*>(smem + kOffInfo);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffInfo + 28);
+
+  if (warp == 0 && lane == 0) {
+    mbar_init(Q_FULL, 1);
+    mbar_init(O_FREE, 2 * kSoftWarps);
+    mbar_init(DRAIN, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(K_FULL(s), 1);
+      mbar_init(K_EMPTY(s), 1);
+      mbar_init(V_FULL(s), 1);
+      mbar_init(V_EMPTY(s), 1);
+      mbar_init(S_FULL(s), 1);
+      mbar_init(P_FULL(s), 2 * kSoftWarps);
+    }
+    fence_mbar_init();
+    prefetch_tmap(&tmap_q);
+    prefetch_tmap(&tmap_k);
+    prefetch_tmap(&tmap_v);
+  }
+  if (warp == 1) {
+    tmem_alloc_2cta(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish_2cta();
+  }
+  if (warp == 3) {
+    const Line ln = scan_total(p, lane);
+    long long lo = 0, hi = 0, first = 0;
+    int req = 0;
+    if (group < ln.groups && ln.total > 0) {
+      lo = cut(ln, group);
+      hi = cut(ln, group + 1);
+      if (hi > lo) locate(p, lo, lane, req, first);
+    }
+    if (lane == 0) {
+      info[0] = lo;
+      info[1] = hi;
+      info[2] = (first << 11) | req;      // req < 2^11, first < 2^42
+    }
+  }
+  __syncthreads();
+  cluster_sync();     // the other CTA's barriers are initialised
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  Walk wk;
+  wk.pos = info[0];
+  wk.hi = info[1];
+  wk.req = static_cast<int>(info[2] & 2047);
+  wk.len = request_len(p, wk.req);
+  wk.nt = pages_of(wk.len);
+  wk.t0 = static_cast<int>(wk.pos - (info[2] >> 11));
+  wk.t1 = 0;
+
+  if (warp == 0) {
+    // ---------------------------------------------------- q and K copies
+    const uint32_t q_full = mapa_shared(Q_FULL, 0);
+    bool ok = true;
+    int it = 0;
+    for (int seg = 0; ok && wk.next(p); ++seg) {
+      const int* ptab = p.page_table + static_cast<long long>(wk.req) * p.max_pages;
+      int pg = 0;
+      for (int t = wk.t0; ok && t < wk.t1; ++t, ++it) {
+        const int u = (t - wk.t0) & 31;
+        if (u == 0) {
+          pg = t + lane < wk.t1 ? __ldg(ptab + t + lane) : 0;
+          if (pg < 0 || pg >= p.num_pages) {
+            raise_error(kErrCheck);
+            pg = 0;
+          }
+        }
+        const int page = __shfl_sync(0xffffffffu, pg, u);
+        const int st = it & 1;
+        if (it >= 2 && !mbar_wait(K_EMPTY(st), ((it >> 1) - 1) & 1)) ok = false;
+        if (ok && lane == 0) {
+          if (rank == 0) mbar_expect_tx(K_FULL(st), 2 * kKBytes);
+          tma_load_3d_2cta(sbase + kOffK + st * kKBytes, &tmap_k, 0, page * kPage + 32 * static_cast<int>(rank), 0,
+                           mapa_shared(K_FULL(st), 0));
+        }
+        if (t == wk.t0) {
+          // q of the stretch: once Q K^T of the page before is done.
+          if (it >= 1 && ok && !mbar_wait(K_EMPTY((it - 1) & 1), ((it - 1) >> 1) & 1)) ok = false;
+          if (ok && lane == 0) {
+            if (rank == 0) mbar_expect_tx(Q_FULL, 2 * kQBytes);
+            tma_load_3d_2cta(sbase + kOffQ, &tmap_q, 0,
+                             wk.req * rows_req + mtile * kRowTile + kRowsCta * static_cast<int>(rank), 0, q_full);
+          }
+        }
+        ok = __all_sync(0xffffffffu, ok);
+      }
+    }
+    if (!ok && lane == 0) raise_error(kErrTimeout);
+  } else if (warp == 2) {
+    // ---------------------------------------------------------- V copies
+    bool ok = true;
+    int it = 0;
+    while (ok && wk.next(p)) {
+      const int* ptab = p.page_table + static_cast<long long>(wk.req) * p.max_pages;
+      int pg = 0;
+      for (int t = wk.t0; ok && t < wk.t1; ++t, ++it) {
+        const int u = (t - wk.t0) & 31;
+        if (u == 0) {
+          pg = t + lane < wk.t1 ? __ldg(ptab + t + lane) : 0;
+          if (pg < 0 || pg >= p.num_pages) pg = 0;
+        }
+        const int page = __shfl_sync(0xffffffffu, pg, u);
+        const int st = it & 1;
+        if (it >= 2 && !mbar_wait(V_EMPTY(st), ((it >> 1) - 1) & 1)) ok = false;
+        if (ok && lane == 0) {
+          // Output dims of P V's two MMAs: 256 n + 128 rank .. + 127.
+          mbar_expect_tx(V_FULL(st), kVBytes);
+          const uint32_t dst = sbase + kOffV + st * kVBytes;
+          tma_load_3d(dst, &tmap_v, 0, page * kPage, 2 * static_cast<int>(rank), V_FULL(st));
+          tma_load_3d(dst + 2 * kVAtom, &tmap_v, 0, page * kPage, 4 + 2 * static_cast<int>(rank), V_FULL(st));
+        }
+        ok = __all_sync(0xffffffffu, ok);
+      }
+    }
+    if (!ok && lane == 0) raise_error(kErrTimeout);
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMAs
+    if (rank == 0 && lane == 0) {
+      constexpr uint32_t idesc_qk = make_idesc(1, 1, 0, 0, kPage, kRowTile);
+      constexpr uint32_t idesc_pv = make_idesc(1, 1, 0, 1, 256, kRowTile);
+      const uint64_t dq = smem_desc_sw128(sbase + kOffQ, 16, 1024);
+      const uint64_t dk0 = smem_desc_sw128(sbase + kOffK, 16, 1024);
+      const uint64_t dp0 = smem_desc_sw128(sbase + kOffP, 16, 1024);
+      const uint64_t dv0 = smem_desc_sw128(sbase + kOffV, kVAtom, 1024);
+      bool ok = true;
+      int it = 0, npv = 0;
+      // P V of page npv (its stretch's first: the output starts at zero, once
+      // the epilogue has read the stretch before).
+      int pv_seg = 0, pv_left = 0;
+      Walk pvw = wk;
+      auto issue_pv = [&]() -> bool {
+        uint32_t fresh = 0;
+        if (pv_left == 0) {
+          pvw.next(p);
+          pv_left = pvw.t1 - pvw.t0;
+          fresh = 1;
+          if (pv_seg > 0 && !mbar_wait(O_FREE, (pv_seg - 1) & 1)) return false;
+          ++pv_seg;
+        }
+        const int st = npv & 1;
+        if (!mbar_wait(P_FULL(st), (npv >> 1) & 1)) return false;
+        tc_fence_after();
+        const uint64_t dp = dp0 + static_cast<uint64_t>((st * kPBytes) >> 4);
+        const uint64_t dv = dv0 + static_cast<uint64_t>((st * kVBytes) >> 4);
+#pragma unroll
+        for (int j = 0; j < kPage / 16; ++j)
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+            mma_f16_ss_2cta(tmem + kColO + 128 * n, dp + static_cast<uint64_t>((32 * j) >> 4),
+                            dv + static_cast<uint64_t>((n * 2 * kVAtom + j * 2048) >> 4), idesc_pv,
+                            (j > 0 || !fresh) ? 1u : 0u);
+        tc_commit_2cta(V_EMPTY(st), 3);
+        --pv_left;
+        ++npv;
+        return true;
+      };
+      for (int seg = 0; ok && wk.next(p); ++seg) {
+        if (!mbar_wait(Q_FULL, seg & 1)) {
+          ok = false;
+          break;
+        }
+        for (int t = wk.t0; t < wk.t1; ++t, ++it) {
+          const int st = it & 1;
+          // (Scores of page it - 2 were read: P V of it - 2 was issued, after
+          // its P_FULL.)
+          if (!mbar_wait(K_FULL(st), (it >> 1) & 1)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t dk = dk0 + static_cast<uint64_t>((st * kKBytes) >> 4);
+#pragma unroll
+          for (int j = 0; j < kLatentDim / 16; ++j)
+            mma_f16_ss_2cta(tmem + kColS + 32 * st,
+                            dq + static_cast<uint64_t>(((j >> 2) * kQAtom + (j & 3) * 32) >> 4),
+                            dk + static_cast<uint64_t>(((j >> 2) * kKAtom + (j & 3) * 32) >> 4), idesc_qk,
+                            j > 0 ? 1u : 0u);
+          tc_commit_2cta(K_EMPTY(st), 3);
+          tc_commit_2cta(S_FULL(st), 3);
+          if (it > 0 && !(ok = issue_pv())) break;
+        }
+      }
+      if (ok && it > 0) ok = issue_pv();
+      if (!ok) raise_error(kErrTimeout);
+      tc_commit_2cta(DRAIN, 1);      // every MMA is done before TMEM is freed
+      mbar_wait(DRAIN, 0);
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ---------------------------------------------- softmax and epilogue
+    const int tid = threadIdx.x - 128;             // = TMEM lane
+    const int w4 = warp & 3;
+    const int row = tid & 63, half = tid >> 6;
+    const uint32_t lanebase = static_cast<uint32_t>(w4 * 32) << 16;
+    const int rrow = mtile * kRowTile + kRowsCta * static_cast<int>(rank) + row;   // row of the request
+    const bool live = rrow < rows_req;
+    const int qi = live ? rrow / p.heads : 0;
+    float* xchg = reinterpret_cast<float*>(smem + kOffXchg);
+    const uint32_t p_full0 = mapa_shared(P_FULL(0), 0), o_free = mapa_shared(O_FREE, 0);
+    const float sc = p.sm_scale * kLog2e;
+    bool ok = true;
+    int it = 0;
+    while (wk.next(p)) {
+      const int* ptab = p.page_table + static_cast<long long>(wk.req) * p.max_pages;
+      const int vis = live ? wk.len - (p.nq - 1 - qi) : 0;
+      float mrun = ninf, lrun = 0.f;      // maximum and sum (this thread's keys) in the exp2 domain
+      uint32_t good = 0;                  // validity of the next 32 page ids
+      for (int t = wk.t0; t < wk.t1; ++t, ++it) {
+        const int st = it & 1, u = (t - wk.t0) & 31;
+        if (u == 0) {
+          const int pg = t + lane < wk.t1 ? __ldg(ptab + t + lane) : 0;
+          good = __ballot_sync(0xffffffffu, pg >= 0 && pg < p.num_pages);
+        }
+        const bool page_ok = (good >> u) & 1u;
+        if (ok && !mbar_wait(S_FULL(st), (it >> 1) & 1)) ok = false;
+        tc_fence_after();
+        uint32_t sr[32];
+        tmem_ld32(tmem + lanebase + kColS + 32 * st, sr);
+        const int seen = page_ok ? vis - t * kPage - 32 * half : 0;   // visible keys among this thread's 32
+        float tmax = ninf;
+        if (seen >= 32) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) tmax = fmaxf(tmax, __uint_as_float(sr[j]));
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            if (j >= seen) sr[j] = __float_as_uint(ninf);
+            tmax = fmaxf(tmax, __uint_as_float(sr[j]));
+          }
+        }
+        // The row's maximum over both halves (the two threads of a row are in
+        // warps w and w + 2).
+        xchg[st * 128 + tid] = tmax;
+        named_bar_sync(1 + (w4 & 1), 64);
+        tmax = fmaxf(tmax, xchg[st * 128 + (tid ^ 64)]) * sc;
+        const bool raise = tmax > mrun + kRaiseLog2;
+        const bool rescale = raise && mrun > ninf;
+        if (__any_sync(0xffffffffu, rescale)) {
+          // P V of the page before has to be in the output first.
+          if (ok && !mbar_wait(V_EMPTY(st ^ 1), ((it - 1) >> 1) & 1)) ok = false;
+          tc_fence_after();
+          const float f = rescale ? ex2(mrun - tmax) : 1.f;
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            uint32_t o[32];
+            tmem_ld32(tmem + lanebase + kColO + 32 * c, o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st32(tmem + lanebase + kColO + 32 * c, o);
+          }
+          lrun *= f;
+        }
+        if (raise) mrun = tmax;
+        const float mref = mrun > ninf ? mrun : 0.f;
+        uint32_t pk[16];
+        float ls = 0.f;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const float p0 = ex2(fmaf(__uint_as_float(sr[2 * j]), sc, -mref));
+          const float p1 = ex2(fmaf(__uint_as_float(sr[2 * j + 1]), sc, -mref));
+          ls += p0 + p1;
+          pk[j] = pack_bf16x2(p0, p1);
+        }
+        lrun += ls;
+        // P of page it - 2 has been read.
+        if (it >= 2 && ok && !mbar_wait(V_EMPTY(st), ((it >> 1) - 1) & 1)) ok = false;
+        uint8_t* prow = smem + kOffP + st * kPBytes + row * 128;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          *reinterpret_cast<uint4*>(prow + (((half * 4 + c) ^ (row & 7)) << 4)) =
+              make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+        if (ok && !mbar_wait(V_FULL(st), (it >> 1) & 1)) ok = false;
+        // Rows of V behind every query's view are cleared.
+        const int vlive = page_ok ? wk.len - t * kPage : 0;
+        if (vlive < kPage) {
+          uint8_t* v = smem + kOffV + st * kVBytes;
+          for (int e = tid; e < kVBytes / 16; e += 128)
+            if (((e >> 3) & (kPage - 1)) >= vlive)
+              reinterpret_cast<uint4*>(v)[e] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(p_full0 + 8u * st);
+      }
+      // ---------------------------------------------------------- epilogue
+      const int last = it - 1;
+      if (ok && !mbar_wait(V_EMPTY(last & 1), (last >> 1) & 1)) ok = false;
+      tc_fence_after();
+      // Row sum over both halves (the parity that page `last` did not use).
+      xchg[(it & 1) * 128 + tid] = lrun;
+      named_bar_sync(1 + (w4 & 1), 64);
+      const float l = lrun + xchg[(it & 1) * 128 + (tid ^ 64)];
+      named_bar_sync(1 + (w4 & 1), 64);
+      const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+      const float lse = l > 0.f || l != l ? (mrun + log2f(l)) * kLn2 : ninf;
+      const bool whole = wk.t0 == 0 && wk.t1 == wk.nt;
+      const long long grow = static_cast<long long>(wk.req) * rows_req + rrow;
+      const long long slot = (static_cast<long long>(worker) * 2 + (wk.t0 > 0 ? 0 : 1)) * kRowTile +
+                             kRowsCta * static_cast<int>(rank) + row;
+#pragma unroll 1
+      for (int c = 0; c < 8; ++c) {
+        uint32_t o[32];
+        tmem_ld32(tmem + lanebase + kColO + 32 * c, o);
+        const int dim = 256 * (c >> 2) + 128 * half + 32 * (c & 3);
+        if (!live) continue;
+        if (whole) {
+          uint4* dst = reinterpret_cast<uint4*>(p.out + grow * kVDim + dim);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            dst[e] = make_uint4(
+                pack_bf16x2(__uint_as_float(o[8 * e]) * inv, __uint_as_float(o[8 * e + 1]) * inv),
+                pack_bf16x2(__uint_as_float(o[8 * e + 2]) * inv, __uint_as_float(o[8 * e + 3]) * inv),
+                pack_bf16x2(__uint_as_float(o[8 * e + 4]) * inv, __uint_as_float(o[8 * e + 5]) * inv),
+                pack_bf16x2(__uint_as_float(o[8 * e + 6]) * inv, __uint_as_float(o[8 * e + 7]) * inv));
+        } else {
+          float4* dst = reinterpret_cast<float4*>(p.part_o + slot * kVDim + dim);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            dst[e] = make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
+                                 __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
+        }
+      }
+      if (live && half == 0) {
+        if (!whole) p.part_lse[slot] = lse;
+        else if (p.lse) p.lse[grow] = lse;
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(o_free);
+    }
+    if (!ok && lane == 0) raise_error(kErrTimeout);
+  } else if (mtile == 0) {
+    // Warp 3: requests without tokens (no page of the line is theirs).
+    for (int r = group * 2 + static_cast<int>(rank); r < p.batch; r += 2 * p.groups) {
+      if (request_len(p, r) > 0) continue;
+      const long long row0 = static_cast<long long>(r) * rows_req;
+      uint4* dst = reinterpret_cast<uint4*>(p.out + row0 * kVDim);
+      for (long long e = lane; e < static_cast<long long>(rows_req) * (kVDim / 8); e += 32)
+        dst[e] = make_uint4(0u, 0u, 0u, 0u);
+      if (p.lse)
+        for (int e = lane; e < rows_req; e += 32) p.lse[row0 + e] = ninf;
+    }
+  }
+  __syncthreads();
+  grid_dep_launch();
+  cluster_sync();     // no arrival is under way to a CTA that has ended
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_2cta(tmem, kTmemCols);
+  }
+#undef Q_FULL
+#undef O_FREE
+#undef DRAIN
+#undef K_FULL
+#undef K_EMPTY
+#undef V_FULL
+#undef V_EMPTY
+#undef S_FULL
+#undef P_FULL
+}
+
+// Joins the partials of a request that spans groups.  Block (i, c): cut i + 1
+// of the line, rows kMergeRows * c .. of the request it falls into; the block
+// works if that cut is the first one inside the request.  The request's first
+// part is slot 1 of its group (a stretch from the request's start), the others
+// slot 0 of theirs.
+constexpr int kMergeRows = 2;
+constexpr int kMergeThreads = kMergeRows * (kVDim / 4);
+
+__global__ void __launch_bounds__(kMergeThreads) mla_merge_kernel(const MlaDecodeLaunch p) {
+  __shared__ int s_req, s_last;
+  const int i = blockIdx.x + 1;
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    const Line ln = scan_total(p, lane);
+    int req = -1, last = 0;
+    if (i < ln.groups && ln.total > 0) {
+      const long long at = cut(ln, i);
+      long long first;
+      int r;
+      locate(p, at, lane, r, first);
+      if (at > first && cut(ln, i - 1) <= first) {
+        const long long end = first + pages_of(request_len(p, r)) - 1;
+        req = r;
+        last = static_cast<int>(((end + 1) * ln.groups - 1) / ln.total);
+      }
+    }
+    if (lane == 0) {
+      s_req = req;
+      s_last = last;
+    }
+  }
+  __syncthreads();
+  grid_dep_wait();
+  if (s_req < 0) return;
+  const int rows_req = p.nq * p.heads;
+  const int rrow = blockIdx.y * kMergeRows + threadIdx.x / (kVDim / 4);
+  if (rrow >= rows_req) return;
+  const int c4 = threadIdx.x % (kVDim / 4);
+  const int m = rrow / kRowTile, lrow = rrow % kRowTile;
+  const int g0 = i - 1, g1 = s_last;
+  const float ninf = __int_as_float(0xff800000);
+  auto slot = [&](int g) {
+    return (static_cast<long long>(g * p.row_tiles + m) * 2 + (g == g0 ? 1 : 0)) * kRowTile + lrow;
+  };
+  float mx = ninf;
+  for (int g = g0; g <= g1; ++g) mx = fmaxf(mx, p.part_lse[slot(g)]);
+  const float mref = mx > ninf ? mx : 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float tot = 0.f;
+  for (int b0 = g0; b0 <= g1; b0 += 4) {
+    float4 v[4];
+    float w[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int g = b0 + u;
+      w[u] = 0.f;
+      v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (g <= g1) {
+        const long long s = slot(g);
+        w[u] = ex2((p.part_lse[s] - mref) * kLog2e);
+        v[u] = reinterpret_cast<const float4*>(p.part_o + s * kVDim)[c4];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      tot += w[u];
+      acc.x = fmaf(w[u], v[u].x, acc.x);
+      acc.y = fmaf(w[u], v[u].y, acc.y);
+      acc.z = fmaf(w[u], v[u].z, acc.z);
+      acc.w = fmaf(w[u], v[u].w, acc.w);
+    }
+  }
+  const bool any = tot > 0.f || tot != tot;
+  const float inv = any ? 1.f / tot : 0.f;
+  const long long grow = static_cast<long long>(s_req) * rows_req + rrow;
+  reinterpret_cast<uint2*>(p.out + grow * kVDim)[c4] =
+      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  if (p.lse && c4 == 0) p.lse[grow] = any ? mx + log2f(tot) * kLn2 : ninf;
+}
+
+constexpr int kMinPages = 1;   // pages a group takes at least
+
+}  // namespace
+
+// Row tiles of a request, groups of CTA pairs (one pair a row tile), and the
+// bytes of the partials: two stretches a pair.
+void mla_decode_plan(int nq, int heads, int* row_tiles, int* groups, size_t* ws_bytes) {
+  const int mt = (nq * heads + kRowTile - 1) / kRowTile;
+  int g = device_sm_count() / 2 / mt;
+  if (g < 1) g = 1;
+  *row_tiles = mt;
+  *groups = g;
+  *ws_bytes = static_cast<size_t>(g) * mt * 2 * kRowTile * (kVDim + 1) * sizeof(float);
+}
+
+cudaError_t launch_mla_decode(MlaDecodeLaunch a, void* ws, cudaStream_t s) {
+  size_t bytes;
+  mla_decode_plan(a.nq, a.heads, &a.row_tiles, &a.groups, &bytes);
+  a.min_pages = kMinPages;
+  a.part_o = static_cast<float*>(ws);
+  a.part_lse = a.part_o + static_cast<size_t>(a.groups) * a.row_tiles * 2 * kRowTile * kVDim;
+  // Rows as 64-dim atoms: one copy brings a box of rows x atoms, each atom's
+  // rows 128 bytes apart (128B swizzle).
+  const uint64_t qrows = static_cast<uint64_t>(a.batch) * a.nq * a.heads;
+  const uint64_t crows = static_cast<uint64_t>(a.num_pages) * kPage;
+  const uint64_t strides[2] = {kLatentDim * 2, 128};
+  const uint64_t qdims[3] = {64, qrows, kAtoms}, cdims[3] = {64, crows, kAtoms};
+  const uint32_t qbox[3] = {64, kRowsCta, kAtoms}, kbox[3] = {64, kPage / 2, kAtoms},
+                 vbox[3] = {64, kPage, 2};
+  CUtensorMap tq, tk, tv;
+  if (!encode_tmap_nd(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, 3, qdims, strides, qbox,
+                      CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_tmap_nd(&tk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.kv, 3, cdims, strides, kbox,
+                      CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_tmap_nd(&tv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.kv, 3, cdims, strides, vbox,
+                      CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(mla_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       kSmemBytes);
+  if (e != cudaSuccess) return e;
+  e = launch_kernel(mla_decode_kernel, dim3(2 * a.groups * a.row_tiles), dim3(kThreads), kSmemBytes, s,
+                    false, 1, tq, tk, tv, a);
+  if (e != cudaSuccess || a.groups == 1) return e;
+  const int chunks = (a.nq * a.heads + kMergeRows - 1) / kMergeRows;
+  return launch_kernel(mla_merge_kernel, dim3(a.groups - 1, chunks), dim3(kMergeThreads), 0, s, true, 1, a);
+}
+
+}  // namespace dsa

@@ -341,6 +341,42 @@ dsa_status dsa_decode_fused_fp8kv(const dsa_decode_desc* desc,
                                   float* out, void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * Dense latent attention in the absorbed form: every query attends every token
+ * it sees, without a selection ("[SGLang] NSA", section "forward_decode": q_nope
+ * absorbed + q_rope against the latent rows; "MTP and sparse attention: NSA and
+ * DSA": the dense MLA that the sparse layer is compared with).  For a model's
+ * dense layers, and for contexts of any length whose scores need no indexer.
+ * For row (t, h), t = r * q_per_req + i, over positions s < vis[t]:
+ *   x_s = sm_scale * q[t,h,:] . kv[row(s),:]                    (576 dims)
+ *   out[t,h,:] = sum_s softmax(x)_s * kv[row(s), 0:512]
+ *   lse[t,h]   = log(sum_s exp(x_s))                             (natural log)
+ * A query that sees nothing (seqlens[r] < q_per_req is allowed here, 0 too)
+ * gets out = 0, lse = -inf.  bf16 products accumulated in fp32 on tcgen05
+ * tensor cores, softmax statistics in fp32, probabilities rounded to bf16 for
+ * the second product, out rounded once from fp32.
+ *   desc     topk is not used; num_heads may be any of 1 .. 128
+ *   q        [dev] bf16 [T, H, 576], 16-B aligned
+ *   kv       [dev] bf16 [num_pages*64, 576] latent cache, 16-B aligned
+ *   out      [dev] bf16 [T, H, 512], 16-B aligned
+ *   lse      [dev] float [T, H] or NULL
+ *   ws       [dev] dsa_mla_decode_workspace_bytes(desc) bytes, 256-B aligned;
+ *            partials of requests that several CTA pairs share.  Its size does
+ *            not depend on the lengths.  Calls that may run at the same time
+ *            need workspaces of their own.
+ * Rows of a request's last page behind its end are not read into the result
+ * (they may hold anything); rows that a later query of the same request sees
+ * have to be finite.  A page id outside [0, num_pages) masks the page's tokens,
+ * a seqlens[r] above max_pages * 64 is cut to it; both raise
+ * DSA_ERR_DEVICE_CHECK.
+ */
+dsa_status dsa_mla_decode(const dsa_decode_desc* desc, const uint16_t* q, const uint16_t* kv,
+                          float sm_scale, uint16_t* out, float* lse, void* ws, size_t ws_bytes,
+                          void* stream);
+
+/* Workspace bytes of dsa_mla_decode (0 for a descriptor it rejects). */
+size_t dsa_mla_decode_workspace_bytes(const dsa_decode_desc* desc);
+
+/*
  * The norm in front of a layer's projections, and of the latent before it is
  * cached: residual addition, root-mean-square norm, output in bf16 and / or in
  * FP8 E4M3 with fp32 scales ("Deepseek Details", section "FP8 Training": E4M3,

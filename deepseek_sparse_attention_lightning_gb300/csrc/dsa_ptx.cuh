@@ -214,6 +214,14 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
                : "memory");
 }
 
+// The same for a writer whose shared-memory writes the tensor cores read (made
+// visible by fence_proxy_async_smem before it): without the cluster-scope
+// release, which waits for every outstanding memory operation of the thread
+// (measured at ~1900 cycles an arrival beside a full copy pipeline).
+__device__ __forceinline__ void mbar_arrive_remote_async(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // Tiled 4-D TMA store: the box at coordinates (x, y, z, w) of the tensor map
 // is written from shared memory (laid out as the map's swizzle says);
 // elements outside the tensor are not written.
@@ -325,12 +333,17 @@ __device__ __forceinline__ void tmem_dealloc_2cta(uint32_t taddr, uint32_t ncols
                : "memory");
 }
 
+// Called by a whole warp in uniform control flow with `issue` non-zero in one
+// lane: the operands then stay in uniform registers.  Issued from a branch that
+// one lane takes, every MMA first moves its operands there, and one thread
+// issues an MMA per ~51 cycles (measured) however small it is; this way N = 64
+// takes 25 cycles and N = 128 its full rate, 32 (M = 128 on the pair).
 __device__ __forceinline__ void mma_f16_ss_2cta(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                                uint32_t accumulate) {
+                                                uint32_t accumulate, uint32_t issue) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(issue)
       : "memory");
 }
 

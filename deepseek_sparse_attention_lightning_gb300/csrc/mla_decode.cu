@@ -82,6 +82,11 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// mbar_wait by a whole warp: the same answer in every lane.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+}
+
 // Tokens of request r: seqlens[r], at least 0 and at most what its row of the
 // page table covers (more is an error the kernel reports).
 __device__ __forceinline__ int request_len(const MlaDecodeLaunch& p, int r) {
@@ -174,7 +179,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const int worker = blockIdx.x >> 1;
   const int group = worker / p.row_tiles, mtile = worker % p.row_tiles;
@@ -239,7 +244,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncthreads();
   cluster_sync();     // the other CTA's barriers are initialised
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   Walk wk;
   wk.pos = info[0];
   wk.hi = info[1];
@@ -316,7 +321,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (!ok && lane == 0) raise_error(kErrTimeout);
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMAs
-    if (rank == 0 && lane == 0) {
+    if (rank == 0) {
+      // The whole warp runs this; one lane issues.
+      const uint32_t el = elect_one() ? 1u : 0u;
       constexpr uint32_t idesc_qk = make_idesc(1, 1, 0, 0, kPage, kRowTile);
       constexpr uint32_t idesc_pv = make_idesc(1, 1, 0, 1, 256, kRowTile);
       const uint64_t dq = smem_desc_sw128(sbase + kOffQ, 16, 1024);
@@ -335,11 +342,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           pvw.next(p);
           pv_left = pvw.t1 - pvw.t0;
           fresh = 1;
-          if (pv_seg > 0 && !mbar_wait(O_FREE, (pv_seg - 1) & 1)) return false;
+          if (pv_seg > 0 && !warp_wait(O_FREE, (pv_seg - 1) & 1)) return false;
           ++pv_seg;
         }
         const int st = npv & 1;
-        if (!mbar_wait(P_FULL(st), (npv >> 1) & 1)) return false;
+        if (!warp_wait(P_FULL(st), (npv >> 1) & 1)) return false;
         tc_fence_after();
         const uint64_t dp = dp0 + static_cast<uint64_t>((st * kPBytes) >> 4);
         const uint64_t dv = dv0 + static_cast<uint64_t>((st * kVBytes) >> 4);
@@ -349,14 +356,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int n = 0; n < 2; ++n)
             mma_f16_ss_2cta(tmem + kColO + 128 * n, dp + static_cast<uint64_t>((32 * j) >> 4),
                             dv + static_cast<uint64_t>((n * 2 * kVAtom + j * 2048) >> 4), idesc_pv,
-                            (j > 0 || !fresh) ? 1u : 0u);
-        tc_commit_2cta(V_EMPTY(st), 3);
+                            (j > 0 || !fresh) ? 1u : 0u, el);
+        if (el) tc_commit_2cta(V_EMPTY(st), 3);
+        __syncwarp();
         --pv_left;
         ++npv;
         return true;
       };
       for (int seg = 0; ok && wk.next(p); ++seg) {
-        if (!mbar_wait(Q_FULL, seg & 1)) {
+        if (!warp_wait(Q_FULL, seg & 1)) {
           ok = false;
           break;
         }
@@ -364,7 +372,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const int st = it & 1;
           // (Scores of page it - 2 were read: P V of it - 2 was issued, after
           // its P_FULL.)
-          if (!mbar_wait(K_FULL(st), (it >> 1) & 1)) {
+          if (!warp_wait(K_FULL(st), (it >> 1) & 1)) {
             ok = false;
             break;
           }
@@ -375,15 +383,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mma_f16_ss_2cta(tmem + kColS + 32 * st,
                             dq + static_cast<uint64_t>(((j >> 2) * kQAtom + (j & 3) * 32) >> 4),
                             dk + static_cast<uint64_t>(((j >> 2) * kKAtom + (j & 3) * 32) >> 4), idesc_qk,
-                            j > 0 ? 1u : 0u);
-          tc_commit_2cta(K_EMPTY(st), 3);
-          tc_commit_2cta(S_FULL(st), 3);
+                            j > 0 ? 1u : 0u, el);
+          if (el) {
+            tc_commit_2cta(K_EMPTY(st), 3);
+            tc_commit_2cta(S_FULL(st), 3);
+          }
+          __syncwarp();
           if (it > 0 && !(ok = issue_pv())) break;
         }
       }
       if (ok && it > 0) ok = issue_pv();
-      if (!ok) raise_error(kErrTimeout);
-      tc_commit_2cta(DRAIN, 1);      // every MMA is done before TMEM is freed
+      if (!ok && el) raise_error(kErrTimeout);
+      if (el) tc_commit_2cta(DRAIN, 1);      // every MMA is done before TMEM is freed
+      __syncwarp();
       mbar_wait(DRAIN, 0);
     }
     __syncwarp();
@@ -482,7 +494,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_remote(p_full0 + 8u * st);
+        if (lane == 0) mbar_arrive_remote_async(p_full0 + 8u * st);
       }
       // ---------------------------------------------------------- epilogue
       const int last = it - 1;
@@ -528,7 +540,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_remote(o_free);
+      if (lane == 0) mbar_arrive_remote_async(o_free);
     }
     if (!ok && lane == 0) raise_error(kErrTimeout);
   } else if (mtile == 0) {

@@ -108,7 +108,7 @@ struct MlaDecodeLaunch {
   float* part_o;                 // set by launch_mla_decode: partial outputs and
   float* part_lse;               //   their log-sum-exps, in the workspace
   int batch, nq, heads, max_pages, num_pages;
-  int row_tiles, groups, min_pages;   // set by launch_mla_decode
+  int row_tiles, groups, min_tiles;   // set by launch_mla_decode
   float sm_scale;
 };
 

@@ -8,39 +8,45 @@
 //   x[row, s] = sm_scale * q[row] . c[s]      (576 dims, s < vis[row])
 //   out[row]  = sum_s softmax(x)[s] * c[s, 0:512],   lse = log sum_s exp(x)
 //
-// A request's n_q * H query rows are cut into row tiles of 128; a tile's keys
-// are the request's pages (64 tokens).  The matrix work of a page and a row
-// tile (128 x 64 x 1088 multiply-adds) against its 73.7 KB is close to the
-// GPU's ridge, so both pipes matter.
+// A request's n_q * H query rows are cut into row tiles of 128, its keys into
+// tiles of two pages (128 tokens).  The matrix work of a key and a row tile
+// (128 x 1088 multiply-adds) against the key's 1152 bytes is close to the GPU's
+// ridge, so both pipes matter.
 //
 // Two CTAs (a cluster on one pair of SMs) share a row tile: tcgen05 with
 // cta_group::2 and M = 128, 64 rows in each CTA.  The fp32 output of 64 rows x
 // 512 dims takes 256 of a CTA's 512 TMEM columns (64 rows use all 128 lanes:
 // lanes 0-63 hold the first half of an MMA's N columns, lanes 64-127 the
 // second), which leaves room for double-buffered scores; and each CTA keeps
-// only its share of the operands: for Q K^T half of the page's tokens (32 x
-// 576), for P V half of the value dims of all 64.  A CTA that works alone
-// holds half of the output only by computing all of Q K^T twice.
+// only its share of the operands: for Q K^T one of the tile's two pages (64 x
+// 576), for P V half of the value dims of both.  A CTA that works alone holds
+// half of the output only by computing all of Q K^T twice.
 //
-// Shared memory: q 72 KB (64 rows), two stages of K (36 KB) and of V (32 KB),
-// two P tiles (8 KB).  A page is fetched as three tensor copies in the 128B
-// swizzled layout that the MMAs read.  K of a page is freed by its Q K^T, V by
-// its P V, so the copies run two pages ahead.
+// N = 128 for Q K^T: with one page a step (N = 64) an MMA reads 3 KB of shared
+// memory for 16 cycles of work and takes 25 (measured); with two it runs at
+// its full rate, 32.
 //
-// Work: the pages of all requests form one line that is cut evenly over the
-// CTA pairs (n_q * H > 128: over groups of pairs, one pair for each row tile,
-// which walk the same pages at the same time and share them in L2).  A pair
-// may end one request and begin the next; a request that spans pairs is
+// Shared memory: q 72 KB (64 rows), K 72 KB in three groups of 3 atoms (64
+// dims each), V 64 KB (two pages), P 16 KB.  All of it is single-buffered:
+// a K group is free once its MMAs of the tile are done and is needed again a
+// P V and two groups' MMAs later, a V page is free after its half of P V, and
+// the copies (one tensor copy a K group, two a V page, in the 128B-swizzled
+// layout that the MMAs read) have that long.
+//
+// Work: the key tiles of all requests form one line that is cut evenly over
+// the CTA pairs (n_q * H > 128: over groups of pairs, one pair for each row
+// tile, which walk the same tiles at the same time and share them in L2).  A
+// pair may end one request and begin the next; a request that spans pairs is
 // joined by mla_merge_kernel from fp32 partials and their log-sum-exps.
 //
 // Roles (256 threads a CTA): warp 0 copies q and K, warp 2 copies V, warp 1
 // of the leading CTA issues the MMAs of both, warps 4-7 are softmax and
-// epilogue (thread = row and half of the tile's keys; the two threads of a row
-// agree on its maximum through shared memory).  Q K^T of page j + 1 runs while
-// page j is in the softmax.  The running maximum is raised lazily (only when a
-// page exceeds it by 2^8 does the output get rescaled).  P is rounded to bf16
-// for the matrix pipe (as values and keys are); its sum is kept unrounded in
-// fp32, so the log-sum-exp has fp32 accuracy.
+// epilogue (thread = row and page of the tile; the two threads of a row agree
+// on its maximum through shared memory).  Q K^T of tile j + 1 runs while tile
+// j is in the softmax.  The running maximum is raised lazily (only when a tile
+// exceeds it by 2^8 does the output get rescaled).  P is rounded to bf16 for
+// the matrix pipe (as values and keys are); its sum is kept unrounded in fp32,
+// so the log-sum-exp has fp32 accuracy.
 //
 // Rows of V that no query row sees (behind the request's end in its last page,
 // or a page whose id is out of range) are cleared in shared memory before P V:
@@ -57,20 +63,23 @@ constexpr int kRowsCta = 64;                              // query rows of a CTA
 constexpr int kRowTile = 2 * kRowsCta;
 constexpr int kAtoms = kLatentDim / 64;                   // 9 atoms of 64 dims
 constexpr int kQBytes = kRowsCta * kLatentDim * 2;        // 72 KB
-constexpr int kKBytes = (kPage / 2) * kLatentDim * 2;     // 36 KB
-constexpr int kVBytes = kPage * (kVDim / 2) * 2;          // 32 KB
-constexpr int kPBytes = kRowsCta * kPage * 2;             // 8 KB
-constexpr int kQAtom = kRowsCta * 128, kKAtom = (kPage / 2) * 128, kVAtom = kPage * 128;
+constexpr int kTileKeys = 2 * kPage;
+constexpr int kAtom = 64 * 128;                           // 64 rows x 64 dims of q, K, V or P: 8 KB
+constexpr int kKGroups = 3, kGroupAtoms = kAtoms / kKGroups;
+constexpr int kKGroupBytes = kGroupAtoms * kAtom;         // 24 KB
+constexpr int kVBytes = 4 * kAtom;                        // one page, this CTA's 256 value dims
+constexpr int kPBytes = 2 * kAtom;
+static_assert(kRowsCta == 64 && kPage == 64, "atoms of 64 rows");
 constexpr int kOffQ = 0;
 constexpr int kOffK = kOffQ + kQBytes;
-constexpr int kOffV = kOffK + 2 * kKBytes;
+constexpr int kOffV = kOffK + kKGroups * kKGroupBytes;
 constexpr int kOffP = kOffV + 2 * kVBytes;
-constexpr int kOffXchg = kOffP + 2 * kPBytes;             // 2 x 128 floats
+constexpr int kOffXchg = kOffP + kPBytes;                 // 2 x 128 floats
 constexpr int kOffBar = kOffXchg + 2 * 128 * 4;
-constexpr int kOffInfo = kOffBar + 24 * 8;
+constexpr int kOffInfo = kOffBar + 16 * 8;
 constexpr int kSmemBytes = kOffInfo + 32 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory");
-constexpr int kColO = 0, kColS = 256, kTmemCols = 512;    // S: 2 x 32 columns
+constexpr int kColO = 0, kColS = 256, kTmemCols = 512;    // S: 2 x 64 columns
 constexpr int kThreads = 256;
 constexpr int kSoftWarps = 4;
 constexpr float kRaiseLog2 = 8.0f;
@@ -98,9 +107,9 @@ __device__ __forceinline__ int request_len(const MlaDecodeLaunch& p, int r) {
   return s < 0 ? 0 : s;
 }
 
-__device__ __forceinline__ int pages_of(int len) { return (len + kPage - 1) / kPage; }
+__device__ __forceinline__ int tiles_of(int len) { return (len + kTileKeys - 1) / kTileKeys; }
 
-// The line of pages: total number of pages, and the groups it is cut into.
+// The line of key tiles: their total number, and the groups it is cut into.
 struct Line {
   long long total;
   int groups;
@@ -108,21 +117,21 @@ struct Line {
 
 __device__ __forceinline__ long long cut(const Line& ln, int g) { return ln.total * g / ln.groups; }
 
-// (one warp) Total pages of all requests.
+// (one warp) Total tiles of all requests.
 __device__ __forceinline__ Line scan_total(const MlaDecodeLaunch& p, int lane) {
   long long n = 0;
-  for (int r = lane; r < p.batch; r += 32) n += pages_of(request_len(p, r));
+  for (int r = lane; r < p.batch; r += 32) n += tiles_of(request_len(p, r));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
   Line ln;
   ln.total = n;
-  const long long most = (n + p.min_pages - 1) / p.min_pages;
+  const long long most = (n + p.min_tiles - 1) / p.min_tiles;
   ln.groups = most < p.groups ? static_cast<int>(most < 1 ? 1 : most) : p.groups;
   return ln;
 }
 
-// (one warp) The request that holds page `at` of the line (at < total), and
-// the line position of its first page.
+// (one warp) The request that holds tile `at` of the line (at < total), and
+// the line position of its first tile.
 __device__ __forceinline__ void locate(const MlaDecodeLaunch& p, long long at, int lane, int& req,
                                        long long& first) {
   long long base = 0;
@@ -130,7 +139,7 @@ __device__ __forceinline__ void locate(const MlaDecodeLaunch& p, long long at, i
   first = 0;
   for (int r0 = 0; r0 < p.batch; r0 += 32) {
     const int r = r0 + lane;
-    const int n = r < p.batch ? pages_of(request_len(p, r)) : 0;
+    const int n = r < p.batch ? tiles_of(request_len(p, r)) : 0;
     long long incl = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -150,17 +159,17 @@ __device__ __forceinline__ void locate(const MlaDecodeLaunch& p, long long at, i
 
 // The stretches of requests in a group's part [lo, hi) of the line, in order.
 struct Walk {
-  long long pos, hi;     // next page of the line, end of the part
+  long long pos, hi;     // next tile of the line, end of the part
   int req;               // request of the stretch
   int len;               // its tokens
-  int t0, t1, nt;        // the stretch's pages [t0, t1) of the request's nt
+  int t0, t1, nt;        // the stretch's tiles [t0, t1) of the request's nt
   __device__ __forceinline__ bool next(const MlaDecodeLaunch& p) {
     if (pos >= hi) return false;
-    if (t1 > 0 || nt == 0) {     // not the first stretch: on to the next request with pages
+    if (t1 > 0 || nt == 0) {     // not the first stretch: on to the next request with tokens
       do {
         ++req;
         len = request_len(p, req);
-        nt = pages_of(len);
+        nt = tiles_of(len);
       } while (nt == 0);
       t0 = 0;
     }
@@ -168,6 +177,19 @@ struct Walk {
     t1 = static_cast<int>(left < nt - t0 ? t0 + left : nt);
     pos += t1 - t0;
     return true;
+  }
+};
+
+// Page ids of a request: table entry i, kNone behind the last page, kBad for an
+// id outside the cache.
+struct PageIds {
+  static constexpr int kNone = -1, kBad = -2;
+  const int32_t* table;
+  int pages, num_pages;
+  __device__ __forceinline__ int get(int i) const {
+    if (i >= pages) return kNone;
+    const int id = __ldg(table + i);
+    return id >= 0 && id < num_pages ? id : kBad;
   }
 };
 
@@ -188,20 +210,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   const uint32_t bar0 = sbase + kOffBar;
 // In the leading CTA (both CTAs' threads and copies arrive there):
-//   Q_FULL, K_FULL(s): q / K of stage s landed in both CTAs; P_FULL(s): P of
-//   stage s written and V of stage s landed in both; O_FREE: the epilogue has
-//   read the output.
-// In both (the MMAs' completion arrives in both): S_FULL(s), K_EMPTY(s),
-//   V_EMPTY(s) (P V of the stage's page done).  V_FULL(s): this CTA's V copies.
+//   Q_FULL, K_FULL(g): q / K group g landed in both CTAs; P_FULL: P written
+//   and V landed in both; O_FREE: the epilogue has read the output.
+// In both (the MMAs' completion arrives in both): S_FULL(b), K_EMPTY(g),
+//   V_EMPTY(h) (P V of page h of the tile done).  V_FULL(h): this CTA's copies.
 #define Q_FULL (bar0)
 #define O_FREE (bar0 + 8u)
 #define DRAIN (bar0 + 16u)
-#define K_FULL(s) (bar0 + 24u + 8u * (s))
-#define K_EMPTY(s) (bar0 + 40u + 8u * (s))
-#define V_FULL(s) (bar0 + 56u + 8u * (s))
-#define V_EMPTY(s) (bar0 + 72u + 8u * (s))
-#define S_FULL(s) (bar0 + 88u + 8u * (s))
-#define P_FULL(s) (bar0 + 104u + 8u * (s))
+#define P_FULL (bar0 + 24u)
+#define K_FULL(g) (bar0 + 32u + 8u * (g))
+#define K_EMPTY(g) (bar0 + 56u + 8u * (g))
+#define V_FULL(h) (bar0 + 80u + 8u * (h))
+#define V_EMPTY(h) (bar0 + 96u + 8u * (h))
+#define S_FULL(b) (bar0 + 112u + 8u * (b))
   long long* info = reinterpret_cast<long long*>(smem + kOffInfo);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffInfo + 28);
 
@@ -209,13 +230,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(Q_FULL, 1);
     mbar_init(O_FREE, 2 * kSoftWarps);
     mbar_init(DRAIN, 1);
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(K_FULL(s), 1);
-      mbar_init(K_EMPTY(s), 1);
-      mbar_init(V_FULL(s), 1);
-      mbar_init(V_EMPTY(s), 1);
-      mbar_init(S_FULL(s), 1);
-      mbar_init(P_FULL(s), 2 * kSoftWarps);
+    mbar_init(P_FULL, 2 * kSoftWarps);
+    for (int g = 0; g < kKGroups; ++g) {
+      mbar_init(K_FULL(g), 1);
+      mbar_init(K_EMPTY(g), 1);
+    }
+    for (int h = 0; h < 2; ++h) {
+      mbar_init(V_FULL(h), 1);
+      mbar_init(V_EMPTY(h), 1);
+      mbar_init(S_FULL(h), 1);
     }
     fence_mbar_init();
     prefetch_tmap(&tmap_q);
@@ -250,39 +273,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   wk.hi = info[1];
   wk.req = static_cast<int>(info[2] & 2047);
   wk.len = request_len(p, wk.req);
-  wk.nt = pages_of(wk.len);
+  wk.nt = tiles_of(wk.len);
   wk.t0 = static_cast<int>(wk.pos - (info[2] >> 11));
   wk.t1 = 0;
 
   if (warp == 0) {
     // ---------------------------------------------------- q and K copies
-    const uint32_t q_full = mapa_shared(Q_FULL, 0);
+    const uint32_t q_full = mapa_shared(Q_FULL, 0), k_full0 = mapa_shared(K_FULL(0), 0);
     bool ok = true;
     int it = 0;
-    for (int seg = 0; ok && wk.next(p); ++seg) {
-      const int* ptab = p.page_table + static_cast<long long>(wk.req) * p.max_pages;
+    while (ok && wk.next(p)) {
+      const PageIds ids{p.page_table + static_cast<long long>(wk.req) * p.max_pages,
+                        (wk.len + kPage - 1) / kPage, p.num_pages};
       int pg = 0;
       for (int t = wk.t0; ok && t < wk.t1; ++t, ++it) {
-        const int u = (t - wk.t0) & 31;
+        const int u = (t - wk.t0) & 15;
         if (u == 0) {
-          pg = t + lane < wk.t1 ? __ldg(ptab + t + lane) : 0;
-          if (pg < 0 || pg >= p.num_pages) {
-            raise_error(kErrCheck);
+          pg = ids.get(2 * t + lane);
+          if (pg < 0) {
+            if (pg == PageIds::kBad) raise_error(kErrCheck);
             pg = 0;
           }
         }
-        const int page = __shfl_sync(0xffffffffu, pg, u);
-        const int st = it & 1;
-        if (it >= 2 && !mbar_wait(K_EMPTY(st), ((it >> 1) - 1) & 1)) ok = false;
-        if (ok && lane == 0) {
-          if (rank == 0) mbar_expect_tx(K_FULL(st), 2 * kKBytes);
-          tma_load_3d_2cta(sbase + kOffK + st * kKBytes, &tmap_k, 0, page * kPage + 32 * static_cast<int>(rank), 0,
-                           mapa_shared(K_FULL(st), 0));
-        }
-        if (t == wk.t0) {
-          // q of the stretch: once Q K^T of the page before is done.
-          if (it >= 1 && ok && !mbar_wait(K_EMPTY((it - 1) & 1), ((it - 1) >> 1) & 1)) ok = false;
+        const int page = __shfl_sync(0xffffffffu, pg, 2 * u + rank);
+#pragma unroll
+        for (int g = 0; g < kKGroups; ++g) {
+          if (it >= 1 && ok && !mbar_wait(K_EMPTY(g), (it - 1) & 1)) ok = false;
           if (ok && lane == 0) {
+            if (rank == 0) mbar_expect_tx(K_FULL(g), 2 * kKGroupBytes);
+            tma_load_3d_2cta(sbase + kOffK + g * kKGroupBytes, &tmap_k, 0, page * kPage, kGroupAtoms * g,
+                             k_full0 + 8u * g);
+          }
+          // q of the stretch (Q K^T of the tile before is done with its last
+          // group).
+          if (g == kKGroups - 1 && t == wk.t0 && ok && lane == 0) {
             if (rank == 0) mbar_expect_tx(Q_FULL, 2 * kQBytes);
             tma_load_3d_2cta(sbase + kOffQ, &tmap_q, 0,
                              wk.req * rows_req + mtile * kRowTile + kRowsCta * static_cast<int>(rank), 0, q_full);
@@ -297,23 +321,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     bool ok = true;
     int it = 0;
     while (ok && wk.next(p)) {
-      const int* ptab = p.page_table + static_cast<long long>(wk.req) * p.max_pages;
+      const PageIds ids{p.page_table + static_cast<long long>(wk.req) * p.max_pages,
+                        (wk.len + kPage - 1) / kPage, p.num_pages};
       int pg = 0;
       for (int t = wk.t0; ok && t < wk.t1; ++t, ++it) {
-        const int u = (t - wk.t0) & 31;
-        if (u == 0) {
-          pg = t + lane < wk.t1 ? __ldg(ptab + t + lane) : 0;
-          if (pg < 0 || pg >= p.num_pages) pg = 0;
-        }
-        const int page = __shfl_sync(0xffffffffu, pg, u);
-        const int st = it & 1;
-        if (it >= 2 && !mbar_wait(V_EMPTY(st), ((it >> 1) - 1) & 1)) ok = false;
-        if (ok && lane == 0) {
-          // Output dims of P V's two MMAs: 256 n + 128 rank .. + 127.
-          mbar_expect_tx(V_FULL(st), kVBytes);
-          const uint32_t dst = sbase + kOffV + st * kVBytes;
-          tma_load_3d(dst, &tmap_v, 0, page * kPage, 2 * static_cast<int>(rank), V_FULL(st));
-          tma_load_3d(dst + 2 * kVAtom, &tmap_v, 0, page * kPage, 4 + 2 * static_cast<int>(rank), V_FULL(st));
+        const int u = (t - wk.t0) & 15;
+        if (u == 0) pg = max(0, ids.get(2 * t + lane));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int page = __shfl_sync(0xffffffffu, pg, 2 * u + h);
+          if (it >= 1 && ok && !mbar_wait(V_EMPTY(h), (it - 1) & 1)) ok = false;
+          if (ok && lane == 0) {
+            // Output dims of P V's two MMAs: 256 n + 128 rank .. + 127.
+            mbar_expect_tx(V_FULL(h), kVBytes);
+            const uint32_t dst = sbase + kOffV + h * kVBytes;
+            tma_load_3d(dst, &tmap_v, 0, page * kPage, 2 * static_cast<int>(rank), V_FULL(h));
+            tma_load_3d(dst + 2 * kAtom, &tmap_v, 0, page * kPage, 4 + 2 * static_cast<int>(rank), V_FULL(h));
+          }
         }
         ok = __all_sync(0xffffffffu, ok);
       }
@@ -324,15 +348,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (rank == 0) {
       // The whole warp runs this; one lane issues.
       const uint32_t el = elect_one() ? 1u : 0u;
-      constexpr uint32_t idesc_qk = make_idesc(1, 1, 0, 0, kPage, kRowTile);
+      constexpr uint32_t idesc_qk = make_idesc(1, 1, 0, 0, kTileKeys, kRowTile);
       constexpr uint32_t idesc_pv = make_idesc(1, 1, 0, 1, 256, kRowTile);
       const uint64_t dq = smem_desc_sw128(sbase + kOffQ, 16, 1024);
-      const uint64_t dk0 = smem_desc_sw128(sbase + kOffK, 16, 1024);
-      const uint64_t dp0 = smem_desc_sw128(sbase + kOffP, 16, 1024);
-      const uint64_t dv0 = smem_desc_sw128(sbase + kOffV, kVAtom, 1024);
+      const uint64_t dk = smem_desc_sw128(sbase + kOffK, 16, 1024);
+      const uint64_t dp = smem_desc_sw128(sbase + kOffP, 16, 1024);
+      const uint64_t dv = smem_desc_sw128(sbase + kOffV, kAtom, 1024);
       bool ok = true;
       int it = 0, npv = 0;
-      // P V of page npv (its stretch's first: the output starts at zero, once
+      // P V of tile npv (its stretch's first: the output starts at zero, once
       // the epilogue has read the stretch before).
       int pv_seg = 0, pv_left = 0;
       Walk pvw = wk;
@@ -345,20 +369,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (pv_seg > 0 && !warp_wait(O_FREE, (pv_seg - 1) & 1)) return false;
           ++pv_seg;
         }
-        const int st = npv & 1;
-        if (!warp_wait(P_FULL(st), (npv >> 1) & 1)) return false;
+        if (!warp_wait(P_FULL, npv & 1)) return false;
         tc_fence_after();
-        const uint64_t dp = dp0 + static_cast<uint64_t>((st * kPBytes) >> 4);
-        const uint64_t dv = dv0 + static_cast<uint64_t>((st * kVBytes) >> 4);
 #pragma unroll
-        for (int j = 0; j < kPage / 16; ++j)
+        for (int h = 0; h < 2; ++h) {
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
-            mma_f16_ss_2cta(tmem + kColO + 128 * n, dp + static_cast<uint64_t>((32 * j) >> 4),
-                            dv + static_cast<uint64_t>((n * 2 * kVAtom + j * 2048) >> 4), idesc_pv,
-                            (j > 0 || !fresh) ? 1u : 0u, el);
-        if (el) tc_commit_2cta(V_EMPTY(st), 3);
-        __syncwarp();
+          for (int j = 0; j < kPage / 16; ++j)
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+              mma_f16_ss_2cta(tmem + kColO + 128 * n, dp + static_cast<uint64_t>((h * kAtom + 32 * j) >> 4),
+                              dv + static_cast<uint64_t>((h * kVBytes + n * 2 * kAtom + j * 2048) >> 4),
+                              idesc_pv, (h > 0 || j > 0 || !fresh) ? 1u : 0u, el);
+          if (el) tc_commit_2cta(V_EMPTY(h), 3);
+          __syncwarp();
+        }
         --pv_left;
         ++npv;
         return true;
@@ -369,25 +393,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           break;
         }
         for (int t = wk.t0; t < wk.t1; ++t, ++it) {
-          const int st = it & 1;
-          // (Scores of page it - 2 were read: P V of it - 2 was issued, after
-          // its P_FULL.)
-          if (!warp_wait(K_FULL(st), (it >> 1) & 1)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint64_t dk = dk0 + static_cast<uint64_t>((st * kKBytes) >> 4);
+          // (Scores of tile it - 2 were read: its P V was issued, after its
+          // P_FULL.)
 #pragma unroll
-          for (int j = 0; j < kLatentDim / 16; ++j)
-            mma_f16_ss_2cta(tmem + kColS + 32 * st,
-                            dq + static_cast<uint64_t>(((j >> 2) * kQAtom + (j & 3) * 32) >> 4),
-                            dk + static_cast<uint64_t>(((j >> 2) * kKAtom + (j & 3) * 32) >> 4), idesc_qk,
-                            j > 0 ? 1u : 0u, el);
-          if (el) {
-            tc_commit_2cta(K_EMPTY(st), 3);
-            tc_commit_2cta(S_FULL(st), 3);
+          for (int g = 0; g < kKGroups; ++g) {
+            if (!(ok = ok && warp_wait(K_FULL(g), it & 1))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int a = kGroupAtoms * g; a < kGroupAtoms * (g + 1); ++a)
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                mma_f16_ss_2cta(tmem + kColS + 64 * (it & 1),
+                                dq + static_cast<uint64_t>((a * kAtom + j * 32) >> 4),
+                                dk + static_cast<uint64_t>((a * kAtom + j * 32) >> 4), idesc_qk,
+                                (a > 0 || j > 0) ? 1u : 0u, el);
+            if (el) tc_commit_2cta(K_EMPTY(g), 3);
+            __syncwarp();
           }
+          if (!ok) break;
+          if (el) tc_commit_2cta(S_FULL(it & 1), 3);
           __syncwarp();
           if (it > 0 && !(ok = issue_pv())) break;
         }
@@ -401,7 +425,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp >= 4) {
     // ---------------------------------------------- softmax and epilogue
-    const int tid = threadIdx.x - 128;             // = TMEM lane
+    const int tid = threadIdx.x - 128;             // = TMEM lane; half: page of the tile, half of O's dims
     const int w4 = warp & 3;
     const int row = tid & 63, half = tid >> 6;
     const uint32_t lanebase = static_cast<uint32_t>(w4 * 32) << 16;
@@ -409,48 +433,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const bool live = rrow < rows_req;
     const int qi = live ? rrow / p.heads : 0;
     float* xchg = reinterpret_cast<float*>(smem + kOffXchg);
-    const uint32_t p_full0 = mapa_shared(P_FULL(0), 0), o_free = mapa_shared(O_FREE, 0);
+    const uint32_t p_full = mapa_shared(P_FULL, 0), o_free = mapa_shared(O_FREE, 0);
     const float sc = p.sm_scale * kLog2e;
     bool ok = true;
     int it = 0;
     while (wk.next(p)) {
-      const int* ptab = p.page_table + static_cast<long long>(wk.req) * p.max_pages;
+      const PageIds ids{p.page_table + static_cast<long long>(wk.req) * p.max_pages,
+                        (wk.len + kPage - 1) / kPage, p.num_pages};
       const int vis = live ? wk.len - (p.nq - 1 - qi) : 0;
       float mrun = ninf, lrun = 0.f;      // maximum and sum (this thread's keys) in the exp2 domain
       uint32_t good = 0;                  // validity of the next 32 page ids
       for (int t = wk.t0; t < wk.t1; ++t, ++it) {
-        const int st = it & 1, u = (t - wk.t0) & 31;
-        if (u == 0) {
-          const int pg = t + lane < wk.t1 ? __ldg(ptab + t + lane) : 0;
-          good = __ballot_sync(0xffffffffu, pg >= 0 && pg < p.num_pages);
-        }
-        const bool page_ok = (good >> u) & 1u;
-        if (ok && !mbar_wait(S_FULL(st), (it >> 1) & 1)) ok = false;
+        const int b = it & 1, u = (t - wk.t0) & 15;
+        if (u == 0) good = __ballot_sync(0xffffffffu, ids.get(2 * t + lane) >= 0);
+        const uint32_t ok2 = good >> (2 * u);          // bit h: page h of the tile can be read
+        if (ok && !mbar_wait(S_FULL(b), (it >> 1) & 1)) ok = false;
         tc_fence_after();
-        uint32_t sr[32];
-        tmem_ld32(tmem + lanebase + kColS + 32 * st, sr);
-        const int seen = page_ok ? vis - t * kPage - 32 * half : 0;   // visible keys among this thread's 32
+        uint32_t sr[64];
+        tmem_ld64(tmem + lanebase + kColS + 64 * b, sr);
+        // Visible keys among this thread's 64.
+        const int seen = ((ok2 >> half) & 1u) ? vis - t * kTileKeys - kPage * half : 0;
         float tmax = ninf;
-        if (seen >= 32) {
+        if (seen >= kPage) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) tmax = fmaxf(tmax, __uint_as_float(sr[j]));
+          for (int j = 0; j < kPage; ++j) tmax = fmaxf(tmax, __uint_as_float(sr[j]));
         } else {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
+          for (int j = 0; j < kPage; ++j) {
             if (j >= seen) sr[j] = __float_as_uint(ninf);
             tmax = fmaxf(tmax, __uint_as_float(sr[j]));
           }
         }
         // The row's maximum over both halves (the two threads of a row are in
         // warps w and w + 2).
-        xchg[st * 128 + tid] = tmax;
+        xchg[b * 128 + tid] = tmax;
         named_bar_sync(1 + (w4 & 1), 64);
-        tmax = fmaxf(tmax, xchg[st * 128 + (tid ^ 64)]) * sc;
+        tmax = fmaxf(tmax, xchg[b * 128 + (tid ^ 64)]) * sc;
         const bool raise = tmax > mrun + kRaiseLog2;
         const bool rescale = raise && mrun > ninf;
         if (__any_sync(0xffffffffu, rescale)) {
-          // P V of the page before has to be in the output first.
-          if (ok && !mbar_wait(V_EMPTY(st ^ 1), ((it - 1) >> 1) & 1)) ok = false;
+          // P V of the tile before has to be in the output first.
+          if (ok && !mbar_wait(V_EMPTY(1), (it - 1) & 1)) ok = false;
           tc_fence_after();
           const float f = rescale ? ex2(mrun - tmax) : 1.f;
 #pragma unroll 1
@@ -465,42 +488,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         if (raise) mrun = tmax;
         const float mref = mrun > ninf ? mrun : 0.f;
-        uint32_t pk[16];
+        uint32_t pk[32];
         float ls = 0.f;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
+        for (int j = 0; j < 32; ++j) {
           const float p0 = ex2(fmaf(__uint_as_float(sr[2 * j]), sc, -mref));
           const float p1 = ex2(fmaf(__uint_as_float(sr[2 * j + 1]), sc, -mref));
           ls += p0 + p1;
           pk[j] = pack_bf16x2(p0, p1);
         }
         lrun += ls;
-        // P of page it - 2 has been read.
-        if (it >= 2 && ok && !mbar_wait(V_EMPTY(st), ((it >> 1) - 1) & 1)) ok = false;
-        uint8_t* prow = smem + kOffP + st * kPBytes + row * 128;
+        // P of the tile before has been read.
+        if (it >= 1 && ok && !mbar_wait(V_EMPTY(1), (it - 1) & 1)) ok = false;
+        uint8_t* prow = smem + kOffP + half * kAtom + row * 128;
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          *reinterpret_cast<uint4*>(prow + (((half * 4 + c) ^ (row & 7)) << 4)) =
+        for (int c = 0; c < 8; ++c)
+          *reinterpret_cast<uint4*>(prow + ((c ^ (row & 7)) << 4)) =
               make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
-        if (ok && !mbar_wait(V_FULL(st), (it >> 1) & 1)) ok = false;
-        // Rows of V behind every query's view are cleared.
-        const int vlive = page_ok ? wk.len - t * kPage : 0;
-        if (vlive < kPage) {
-          uint8_t* v = smem + kOffV + st * kVBytes;
-          for (int e = tid; e < kVBytes / 16; e += 128)
-            if (((e >> 3) & (kPage - 1)) >= vlive)
-              reinterpret_cast<uint4*>(v)[e] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (ok && !mbar_wait(V_FULL(h), it & 1)) ok = false;
+          // Rows of V behind every query's view are cleared.
+          const int vlive = ((ok2 >> h) & 1u) ? wk.len - t * kTileKeys - kPage * h : 0;
+          if (vlive < kPage) {
+            uint4* v = reinterpret_cast<uint4*>(smem + kOffV + h * kVBytes);
+            for (int e = tid; e < kVBytes / 16; e += 128)
+              if (((e >> 3) & (kPage - 1)) >= vlive) v[e] = make_uint4(0u, 0u, 0u, 0u);
+          }
         }
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_remote_async(p_full0 + 8u * st);
+        if (lane == 0) mbar_arrive_remote_async(p_full);
       }
       // ---------------------------------------------------------- epilogue
-      const int last = it - 1;
-      if (ok && !mbar_wait(V_EMPTY(last & 1), (last >> 1) & 1)) ok = false;
+      if (ok && !mbar_wait(V_EMPTY(1), (it - 1) & 1)) ok = false;
       tc_fence_after();
-      // Row sum over both halves (the parity that page `last` did not use).
+      // Row sum over both halves (the buffer that the last tile did not use).
       xchg[(it & 1) * 128 + tid] = lrun;
       named_bar_sync(1 + (w4 & 1), 64);
       const float l = lrun + xchg[(it & 1) * 128 + (tid ^ 64)];
@@ -594,7 +618,7 @@ __global__ void __launch_bounds__(kMergeThreads) mla_merge_kernel(const MlaDecod
       int r;
       locate(p, at, lane, r, first);
       if (at > first && cut(ln, i - 1) <= first) {
-        const long long end = first + pages_of(request_len(p, r)) - 1;
+        const long long end = first + tiles_of(request_len(p, r)) - 1;
         req = r;
         last = static_cast<int>(((end + 1) * ln.groups - 1) / ln.total);
       }
@@ -653,7 +677,7 @@ __global__ void __launch_bounds__(kMergeThreads) mla_merge_kernel(const MlaDecod
   if (p.lse && c4 == 0) p.lse[grow] = any ? mx + log2f(tot) * kLn2 : ninf;
 }
 
-constexpr int kMinPages = 1;   // pages a group takes at least
+constexpr int kMinTiles = 1;   // key tiles a group takes at least
 
 }  // namespace
 
@@ -671,7 +695,7 @@ void mla_decode_plan(int nq, int heads, int* row_tiles, int* groups, size_t* ws_
 cudaError_t launch_mla_decode(MlaDecodeLaunch a, void* ws, cudaStream_t s) {
   size_t bytes;
   mla_decode_plan(a.nq, a.heads, &a.row_tiles, &a.groups, &bytes);
-  a.min_pages = kMinPages;
+  a.min_tiles = kMinTiles;
   a.part_o = static_cast<float*>(ws);
   a.part_lse = a.part_o + static_cast<size_t>(a.groups) * a.row_tiles * 2 * kRowTile * kVDim;
   // Rows as 64-dim atoms: one copy brings a box of rows x atoms, each atom's
@@ -680,7 +704,7 @@ cudaError_t launch_mla_decode(MlaDecodeLaunch a, void* ws, cudaStream_t s) {
   const uint64_t crows = static_cast<uint64_t>(a.num_pages) * kPage;
   const uint64_t strides[2] = {kLatentDim * 2, 128};
   const uint64_t qdims[3] = {64, qrows, kAtoms}, cdims[3] = {64, crows, kAtoms};
-  const uint32_t qbox[3] = {64, kRowsCta, kAtoms}, kbox[3] = {64, kPage / 2, kAtoms},
+  const uint32_t qbox[3] = {64, kRowsCta, kAtoms}, kbox[3] = {64, kPage, kGroupAtoms},
                  vbox[3] = {64, kPage, 2};
   CUtensorMap tq, tk, tv;
   if (!encode_tmap_nd(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, 3, qdims, strides, qbox,

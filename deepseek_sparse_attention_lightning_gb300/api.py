@@ -86,6 +86,9 @@ _SIGS = {
     "dsa_mla_decode": (c_int32, [ctypes.POINTER(DecodeDesc), c_void_p, c_void_p, c_float, c_void_p,
                                  c_void_p, c_void_p, c_size_t, c_void_p]),
     "dsa_mla_decode_workspace_bytes": (c_size_t, [ctypes.POINTER(DecodeDesc)]),
+    "dsa_mla_prefill": (c_int32, [c_int32, c_int32, c_int32, c_int32, c_int32, c_void_p, c_void_p,
+                                  c_void_p, c_void_p, c_void_p, c_int64, c_float, c_int32, c_void_p,
+                                  c_void_p, c_void_p]),
     "dsa_rmsnorm": (c_int32, [c_int32, c_int32, c_void_p, c_int64, c_void_p, c_void_p, c_float,
                               c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
     "dsa_decode_mli": (c_int32, [ctypes.POINTER(DecodeDesc), c_void_p, c_void_p, c_void_p,
@@ -359,6 +362,29 @@ def dsa_mla_decode(desc, q, kv, out, ws, sm_scale, lse=None, stream=None):
               _arg(out, bf16, (T, H, 512), dev, "out"), _arg(lse, torch.float32, (T, H), dev, "lse"),
               _arg(ws, torch.uint8, (ws.numel(),), dev, "ws"), ws.numel(), _stream_on(stream, dev)),
            "dsa_mla_decode")
+
+
+def dsa_mla_prefill(q, kv, k_rope, cu_q, cu_k, out, max_q, sm_scale, causal=True, lse=None,
+                    stream=None):
+    """Attention of packed prompts over expanded keys and values: ``q`` [total_q, H, 192], ``kv``
+    [total_k, H, 256] (key 128, value 128), ``k_rope`` [total_k, 64] (rows may be strided: the last 64
+    columns of latent rows), ``out`` [total_q, H, 128], all bf16; see include/dsa.h."""
+    fn, dev, bf16, i32 = lib().dsa_mla_prefill, torch.cuda.current_device(), torch.bfloat16, torch.int32
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise TypeError("q: expected a 3-D tensor")
+    if not isinstance(cu_q, torch.Tensor) or cu_q.dim() != 1 or cu_q.shape[0] < 2:
+        raise TypeError("cu_q: expected a 1-D tensor of at least two offsets")
+    rp, ld = _rows_arg(k_rope, bf16, dev, "k_rope")
+    Tq, H, _ = q.shape
+    Tk, B1 = k_rope.shape[0], cu_q.shape[0]
+    if k_rope.shape[1] != 64:
+        raise ValueError(f"k_rope: expected 64 columns, got {k_rope.shape[1]}")
+    _check(fn(B1 - 1, H, Tq, Tk, max_q, _arg(cu_q, i32, (B1,), dev, "cu_q"),
+              _arg(cu_k, i32, (B1,), dev, "cu_k"), _arg(q, bf16, (Tq, H, 192), dev, "q"),
+              _arg(kv, bf16, (Tk, H, 256), dev, "kv"), rp, ld, sm_scale, 1 if causal else 0,
+              _arg(out, bf16, (Tq, H, 128), dev, "out"),
+              _arg(lse, torch.float32, (Tq, H), dev, "lse"), _stream_on(stream, dev)),
+           "dsa_mla_prefill")
 
 
 def dsa_rmsnorm(x, weight, eps, residual=None, residual_out=None, y=None, y8=None, y_scale=None,

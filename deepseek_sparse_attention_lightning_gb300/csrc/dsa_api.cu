@@ -329,6 +329,30 @@ dsa_status dsa_mla_decode(const dsa_decode_desc* d, const uint16_t* q, const uin
   return cuda_status(dsa::launch_mla_decode(a, ws, static_cast<cudaStream_t>(stream)));
 }
 
+dsa_status dsa_mla_prefill(int32_t batch, int32_t heads, int32_t total_q, int32_t total_k,
+                           int32_t max_q, const int32_t* cu_q, const int32_t* cu_k,
+                           const uint16_t* q, const uint16_t* kv, const uint16_t* k_rope,
+                           int64_t ld_rope, float sm_scale, int32_t causal, uint16_t* out,
+                           float* lse, void* stream) {
+  if (batch < 1 || heads < 1 || total_q < 0 || total_k < 0 || max_q < 0 || ld_rope < 64)
+    return DSA_ERR_INVALID_ARG;
+  if (!(sm_scale > 0.f) || !std::isfinite(sm_scale)) return DSA_ERR_INVALID_ARG;
+  if (batch > DSA_MAX_PREFILL_BATCH || heads > DSA_MAX_PREFILL_HEADS) return DSA_ERR_UNSUPPORTED;
+  if (!cu_q || !cu_k || !aligned(cu_q, 4) || !aligned(cu_k, 4)) return DSA_ERR_INVALID_ARG;
+  if (total_q == 0 || max_q == 0) return DSA_OK;
+  if (!q || !out || !aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4)) return DSA_ERR_INVALID_ARG;
+  // Without a key the pointers are not read, but the copies' maps need some.
+  if (total_k > 0 && (!kv || !k_rope || !aligned(kv, 16) || !aligned(k_rope, 16)))
+    return DSA_ERR_INVALID_ARG;
+  if (ld_rope % 8 != 0) return DSA_ERR_INVALID_ARG;
+  dsa::MlaPrefillLaunch a{};
+  a.q = q; a.kv = total_k > 0 ? kv : q; a.k_rope = total_k > 0 ? k_rope : q; a.cu_q = cu_q;
+  a.cu_k = cu_k; a.out = out; a.lse = lse; a.ld_rope = ld_rope; a.batch = batch; a.heads = heads;
+  a.total_q = total_q; a.total_k = total_k; a.max_q = max_q < total_q ? max_q : total_q;
+  a.causal = causal != 0; a.sm_scale = sm_scale;
+  return cuda_status(dsa::launch_mla_prefill(a, static_cast<cudaStream_t>(stream)));
+}
+
 dsa_status dsa_rmsnorm(int32_t rows, int32_t dim, const uint16_t* x, int64_t ld_x,
                        const uint16_t* residual, const uint16_t* weight, float eps, int32_t group,
                        uint16_t* residual_out, uint16_t* y, uint8_t* y8, float* y_scale,
@@ -764,9 +788,9 @@ dsa_status dsa_decode_step_ring(const dsa_decode_desc* desc, dsa_step_ring* ring
 
 dsa_status dsa_get_device_error(void* stream) {
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return DSA_ERR_CUDA;
-  const int codes[6] = {dsa::fetch_error_indexer(), dsa::fetch_error_topk(), dsa::fetch_error_mla(),
+  const int codes[7] = {dsa::fetch_error_indexer(), dsa::fetch_error_topk(), dsa::fetch_error_mla(),
                         dsa::fetch_error_merge(), dsa::fetch_error_cache(),
-                        dsa::fetch_error_mla_dense()};
+                        dsa::fetch_error_mla_dense(), dsa::fetch_error_mla_prefill()};
   for (int c : codes)
     if (c != 0) return static_cast<dsa_status>(c);
   return DSA_OK;

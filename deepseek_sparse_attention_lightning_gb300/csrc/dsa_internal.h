@@ -112,6 +112,19 @@ struct MlaDecodeLaunch {
   float sm_scale;
 };
 
+struct MlaPrefillLaunch {
+  const uint16_t* q;             // [total_q][H][192] bf16
+  const uint16_t* kv;            // [total_k][H][256] bf16: key 128, value 128
+  const uint16_t* k_rope;        // [total_k] rows of 64 bf16, ld_rope apart
+  const int32_t* cu_q;           // [batch + 1]
+  const int32_t* cu_k;
+  uint16_t* out;                 // [total_q][H][128] bf16
+  float* lse;                    // [total_q][H] or nullptr
+  long long ld_rope;
+  int batch, heads, total_q, total_k, max_q, causal;
+  float sm_scale;
+};
+
 cudaError_t launch_indexer(const IndexerLaunch& a, cudaStream_t s);
 // Bound, in SM cycles, of the indexer's pipeline waits on later launches
 // (<= 0: the default kWaitCycles).
@@ -125,6 +138,7 @@ cudaError_t launch_rmsnorm(const RmsNormLaunch& a, cudaStream_t s);
 // pairs, workspace bytes; no kernel) and its launch.
 void mla_decode_plan(int nq, int heads, int* row_tiles, int* groups, size_t* ws_bytes);
 cudaError_t launch_mla_decode(MlaDecodeLaunch a, void* ws, cudaStream_t s);
+cudaError_t launch_mla_prefill(const MlaPrefillLaunch& a, cudaStream_t s);
 cudaError_t launch_merge(int rows, int splits, const float* mid_o, const float* mid_lse,
                          float* out, float* out_lse, cudaStream_t s, bool pdl = false);
 
@@ -167,6 +181,7 @@ int fetch_error_mla();
 int fetch_error_merge();
 int fetch_error_cache();
 int fetch_error_mla_dense();
+int fetch_error_mla_prefill();
 
 // Host helpers (dsa_api.cu).
 // The checks every entry point applies to a decode descriptor: a dsa_status.

@@ -69,6 +69,8 @@ typedef enum dsa_status {
 #define DSA_MAX_BATCH 1024
 #define DSA_MAX_Q_PER_REQ 4
 #define DSA_MAX_NORM_DIM 32768
+#define DSA_MAX_PREFILL_BATCH 65535
+#define DSA_MAX_PREFILL_HEADS 1024
 
 /*
  * One decode batch.  Sizes are host integers; seqlens and page_table are
@@ -375,6 +377,42 @@ dsa_status dsa_mla_decode(const dsa_decode_desc* desc, const uint16_t* q, const 
 
 /* Workspace bytes of dsa_mla_decode (0 for a descriptor it rejects). */
 size_t dsa_mla_decode_workspace_bytes(const dsa_decode_desc* desc);
+
+/*
+ * Latent attention in the expanded form, for prompts: each head has its own
+ * 128-dim keys and values (the latent rows times the up-projection) and all
+ * heads share the 64-dim rope key cached beside the latent ("Deepseek Details",
+ * section "DSA": latent 512 + rope 64; the expanded form is the textbook one).
+ * Requests are packed: request b has query rows [cu_q[b], cu_q[b+1]) and key
+ * rows [cu_k[b], cu_k[b+1]); with n queries and m keys, query i is the request's
+ * token m - n + i (earlier tokens: a prompt taken in chunks, or a shared prefix).
+ *   x_j = sm_scale * (q[i,h,0:128] . kv[j,h,0:128] + q[i,h,128:192] . k_rope[j])
+ *   out[i,h,:] = sum_j softmax(x)_j * kv[j,h,128:256],  lse = log(sum_j exp(x_j))
+ * over the keys j <= m - n + i (causal != 0) or all m (causal == 0: keys that
+ * every query sees, e.g. another part of a long prompt, joined by their lse).  A
+ * query without a key gets out = 0, lse = -inf.  Arithmetic as dsa_mla_decode.
+ *   batch, heads    1 .. DSA_MAX_PREFILL_BATCH, 1 .. DSA_MAX_PREFILL_HEADS
+ *   total_q/total_k rows of the packed tensors (cu_q[batch] and cu_k[batch] at
+ *                   most; rows behind the last request are left as they were)
+ *   max_q           the largest number of queries of a request (or more)
+ *   cu_q, cu_k      [dev] int32 [batch + 1], not decreasing
+ *   q       [dev] bf16 [total_q, heads, 192] (nope 128, rope 64), 16-B aligned
+ *   kv      [dev] bf16 [total_k, heads, 256] (key nope 128, value 128), 16-B aligned
+ *   k_rope  [dev] bf16, row j at k_rope + j * ld_rope (64 values; ld_rope a
+ *           multiple of 8: the rope columns of latent rows, k_rope = latent +
+ *           512 with ld_rope = 576), 16-B aligned
+ *   out     [dev] bf16 [total_q, heads, 128], 16-B aligned
+ *   lse     [dev] float [total_q, heads] or NULL
+ * Needs no workspace.  Offsets outside the packed tensors skip their request; a
+ * request with more than max_q queries (rounded up to 256) is not written
+ * whole; both raise DSA_ERR_DEVICE_CHECK.  Keys of a request have to be finite
+ * where any of its queries in the same 256 sees them.
+ */
+dsa_status dsa_mla_prefill(int32_t batch, int32_t heads, int32_t total_q, int32_t total_k,
+                           int32_t max_q, const int32_t* cu_q, const int32_t* cu_k,
+                           const uint16_t* q, const uint16_t* kv, const uint16_t* k_rope,
+                           int64_t ld_rope, float sm_scale, int32_t causal, uint16_t* out,
+                           float* lse, void* stream);
 
 /*
  * The norm in front of a layer's projections, and of the latent before it is

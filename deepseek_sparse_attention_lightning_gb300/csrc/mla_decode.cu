@@ -85,12 +85,6 @@ constexpr int kSoftWarps = 4;
 constexpr float kRaiseLog2 = 8.0f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // mbar_wait by a whole warp: the same answer in every lane.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity));
@@ -456,7 +450,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         float tmax = ninf;
         if (seen >= kPage) {
 #pragma unroll
-          for (int j = 0; j < kPage; ++j) tmax = fmaxf(tmax, __uint_as_float(sr[j]));
+          for (int j = 0; j < kPage; j += 2)
+            tmax = max3(tmax, __uint_as_float(sr[j]), __uint_as_float(sr[j + 1]));
         } else {
 #pragma unroll
           for (int j = 0; j < kPage; ++j) {
@@ -489,15 +484,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (raise) mrun = tmax;
         const float mref = mrun > ninf ? mrun : 0.f;
         uint32_t pk[32];
-        float ls = 0.f;
+        float2 ls = make_float2(0.f, 0.f);
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
-          const float p0 = ex2(fmaf(__uint_as_float(sr[2 * j]), sc, -mref));
-          const float p1 = ex2(fmaf(__uint_as_float(sr[2 * j + 1]), sc, -mref));
-          ls += p0 + p1;
-          pk[j] = pack_bf16x2(p0, p1);
+          const float2 x = fma2(make_float2(__uint_as_float(sr[2 * j]), __uint_as_float(sr[2 * j + 1])),
+                                make_float2(sc, sc), make_float2(-mref, -mref));
+          const float2 e = make_float2(ex2(x.x), ex2(x.y));
+          ls = add2(ls, e);
+          pk[j] = pack_bf16x2(e.x, e.y);
         }
-        lrun += ls;
+        lrun += ls.x + ls.y;
         // P of the tile before has been read.
         if (it >= 1 && ok && !mbar_wait(V_EMPTY(1), (it - 1) & 1)) ok = false;
         uint8_t* prow = smem + kOffP + half * kAtom + row * 128;

@@ -58,16 +58,15 @@ constexpr int kNumBars = 2 * kRing + 9;
 constexpr int kOffSlot = kOffBar + kNumBars * 8;
 constexpr int kSmemBytes = kOffSlot + 16 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory");
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;                  // two softmax warpgroups; copies, MMAs and two idle warps
+// Registers: launched with 168 a thread (384 x 168 = 64512); the softmax holds a
+// row of 128 scores and takes 208, the third warpgroup keeps 88 (256 x 208 +
+// 128 x 88 = 64512).
+constexpr int kSoftRegs = 208, kOtherRegs = 88;
+static_assert(256 * kSoftRegs + 128 * kOtherRegs <= 384 * 168, "registers");
 constexpr int kColS = 0, kColO = 256, kTmemCols = 512;
 constexpr float kRaiseLog2 = 8.0f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity));
@@ -97,13 +96,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (row0 >= qlen) return;
   // Key tiles of the two query tiles.
-  int nt[2];
-#pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const int first = row0 + q * kTile, last = min(first + kTile, qlen) - 1;
-    nt[q] = first < qlen ? (key_limit(last, qlen, klen, p.causal) + kTile - 1) / kTile : 0;
-  }
-  const int ntmax = max(nt[0], nt[1]);
+  auto tiles_from = [&](int first) {
+    if (first >= qlen) return 0;
+    return (key_limit(min(first + kTile, qlen) - 1, qlen, klen, p.causal) + kTile - 1) / kTile;
+  };
+  const int nt0 = tiles_from(row0), nt1 = tiles_from(row0 + kTile), ntmax = max(nt0, nt1);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const float ninf = __int_as_float(0xff800000);
 
@@ -145,6 +142,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
+  if (warp >= 8) {
+  setmaxnreg_dec<kOtherRegs>();
   if (warp == 8) {
     // ------------------------------------------------------------- copies
     if (lane == 0) {
@@ -160,7 +159,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int row = k0 + j * kTile;
           if (g == 2) tma_load_2d(dst, &tmap_rope, 0, row, FULL(s), pol_rope);
           else tma_load_4d(dst, &tmap_kv, 0, row, g < 2 ? g : g - 1, head, FULL(s));
-          if (j == 0 && g < 2 && nt[g] > 0) {
+          if (j == 0 && g < 2 && (g == 0 ? nt0 : nt1) > 0) {
             mbar_expect_tx(Q_FULL(g), kQAtoms * kAtomBytes);
             tma_load_4d(sbase + kOffQ + g * kQAtoms * kAtomBytes, &tmap_q, 0, q0 + row0 + g * kTile, 0,
                         head, Q_FULL(g));
@@ -171,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // No copy is in flight when the CTA ends.
       for (int u = n - 1; u >= 0 && u >= n - kRing; --u) mbar_wait(FULL(u % kRing), (u / kRing) & 1);
       for (int q = 0; q < 2; ++q)
-        if (ntmax > 0 && nt[q] > 0) mbar_wait(Q_FULL(q), 0);
+        if (ntmax > 0 && (q == 0 ? nt0 : nt1) > 0) mbar_wait(Q_FULL(q), 0);
     }
     __syncwarp();
   } else if (warp == 9) {
@@ -216,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                          dv + static_cast<uint64_t>((2048 * k) >> 4),
                          idesc_pv, (j > 0 || k > 0) ? 1u : 0u, el);
       }
-      if (j == nt[q] - 1) {
+      if (j == (q == 0 ? nt0 : nt1) - 1) {
         if (el) tc_commit(O_FULL(q));
         __syncwarp();
       }
@@ -227,24 +226,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     };
     for (int j = 0; ok && j <= ntmax; ++j) {
-      if (j < nt[0]) qk(0, j, true);
+      if (j < nt0) qk(0, j, true);
       if (ok && j >= 1) {
-        if (j - 1 < nt[1]) pv(1, j - 1, j - 1 >= nt[0]);
+        if (j - 1 < nt1) pv(1, j - 1, j - 1 >= nt0);
         release(j - 1, 3, 5);
       }
       if (j == ntmax) break;
-      if (ok && j < nt[1]) qk(1, j, j >= nt[0]);
+      if (ok && j < nt1) qk(1, j, j >= nt0);
       release(j, 0, 3);
-      if (ok && j < nt[0]) pv(0, j, true);
+      if (ok && j < nt0) pv(0, j, true);
     }
     if (!ok && el) raise_error(kErrTimeout);
     if (el) tc_commit(DRAIN);      // every MMA is done before TMEM is freed
     __syncwarp();
     mbar_wait(DRAIN, 0);
+  }
   } else {
     // ---------------------------------------------- softmax and epilogue
+    setmaxnreg_inc<kSoftRegs>();
     const int q = warp >> 2, w4 = warp & 3;
-    const int n = nt[q];
+    const int n = (q == 0 ? nt0 : nt1);
     const int row = row0 + q * kTile + w4 * 32 + lane;     // of the request
     const bool live = row < qlen;
     const uint32_t tS = tmem + (static_cast<uint32_t>(w4 * 32) << 16) + kColS + kTile * q;
@@ -266,7 +267,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (e >= seen) s[e] = __float_as_uint(ninf);
       }
 #pragma unroll
-      for (int e = 0; e < kTile; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(s[e]));
+      for (int e = 0; e < kTile; e += 2)
+        mx[(e >> 1) & 3] = max3(mx[(e >> 1) & 3], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
       const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
       const bool raise = tmax > mrun + kRaiseLog2;
       const bool rescale = raise && mrun > ninf;
@@ -285,24 +287,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (raise) mrun = tmax;
       const float mref = mrun > ninf ? mrun : 0.f;
-      float ls[4] = {0.f, 0.f, 0.f, 0.f};
+      float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         uint32_t pk[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
-          const float p0 = ex2(fmaf(__uint_as_float(s[64 * c + 2 * e]), sc, -mref));
-          const float p1 = ex2(fmaf(__uint_as_float(s[64 * c + 2 * e + 1]), sc, -mref));
-          ls[e & 3] += p0 + p1;
-          pk[e] = pack_bf16x2(p0, p1);
+          const float2 x = fma2(make_float2(__uint_as_float(s[64 * c + 2 * e]),
+                                            __uint_as_float(s[64 * c + 2 * e + 1])),
+                                make_float2(sc, sc), make_float2(-mref, -mref));
+          const float2 w = make_float2(ex2(x.x), ex2(x.y));
+          ls[e & 1] = add2(ls[e & 1], w);
+          pk[e] = pack_bf16x2(w.x, w.y);
         }
         tmem_st32(tS + 32 * c, pk);
       }
-      lrun += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+      lrun += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
       // Rows of V behind the request's end are cleared, by the first query
       // tile that reads them.
       const int vlive = klen - j * kTile;
-      if (vlive < kTile && (q == 0 || j >= nt[0])) {
+      if (vlive < kTile && (q == 0 || j >= nt0)) {
 #pragma unroll 1
         for (int a = 0; a < 2; ++a) {
           const int g = j * kPerTile + 3 + a;

@@ -54,7 +54,8 @@ constexpr int kHeadDim = 128;
 constexpr int kOffQ = 0;
 constexpr int kOffRing = 2 * kQAtoms * kAtomBytes;
 constexpr int kOffBar = kOffRing + kRing * kAtomBytes;
-constexpr int kNumBars = 2 * kRing + 9;
+constexpr int kKGranules = 3;
+constexpr int kNumBars = 17;
 constexpr int kOffSlot = kOffBar + kNumBars * 8;
 constexpr int kSmemBytes = kOffSlot + 16 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory");
@@ -109,20 +110,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sbase = smem_u32(smem);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffSlot);
   const uint32_t bar0 = sbase + kOffBar;
-#define FULL(s) (bar0 + 8u * (s))
-#define EMPTY(s) (bar0 + 8u * (kRing + (s)))
-#define Q_FULL(q) (bar0 + 8u * (2 * kRing + (q)))
-#define S_FULL(q) (bar0 + 8u * (2 * kRing + 2 + (q)))
-#define P_FULL(q) (bar0 + 8u * (2 * kRing + 4 + (q)))
-#define O_FULL(q) (bar0 + 8u * (2 * kRing + 6 + (q)))
-#define DRAIN (bar0 + 8u * (2 * kRing + 8))
+// K / V of key tile j (at most two of each are in the ring): landed, and read.
+#define K_FULL(j) (bar0 + 8u * ((j) & 1))
+#define V_FULL(j) (bar0 + 16u + 8u * ((j) & 1))
+#define K_EMPTY(j) (bar0 + 32u + 8u * ((j) & 1))
+#define V_EMPTY(j) (bar0 + 48u + 8u * ((j) & 1))
+#define PARITY(j) (((j) >> 1) & 1)
+#define Q_FULL(q) (bar0 + 64u + 8u * (q))
+#define S_FULL(q) (bar0 + 80u + 8u * (q))
+#define P_FULL(q) (bar0 + 96u + 8u * (q))
+#define O_FULL(q) (bar0 + 112u + 8u * (q))
+#define DRAIN (bar0 + 128u)
 
   if (warp == 8 && lane == 0) {
-    for (int s = 0; s < kRing; ++s) {
-      mbar_init(FULL(s), 1);
-      mbar_init(EMPTY(s), 1);
-    }
     for (int q = 0; q < 2; ++q) {
+      mbar_init(K_FULL(q), 1);
+      mbar_init(V_FULL(q), 1);
+      mbar_init(K_EMPTY(q), 1);
+      mbar_init(V_EMPTY(q), 1);
       mbar_init(Q_FULL(q), 1);
       mbar_init(S_FULL(q), 1);
       mbar_init(P_FULL(q), kTile);
@@ -152,13 +157,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t pol_rope = policy_evict_last();      // every head reads it
       for (int j = 0; ok && j < ntmax; ++j) {
         for (int g = 0; g < kPerTile; ++g, ++n) {
-          const int s = n % kRing;
-          if (n >= kRing && !(ok = mbar_wait(EMPTY(s), (n / kRing - 1) & 1))) break;
-          mbar_expect_tx(FULL(s), kAtomBytes);
-          const uint32_t dst = sbase + kOffRing + s * kAtomBytes;
+          // The granule's slot held granule n - kRing, of an earlier tile.
+          const int old = n - kRing, oj = old / kPerTile;
+          if (old >= 0 &&
+              !(ok = mbar_wait(old % kPerTile < kKGranules ? K_EMPTY(oj) : V_EMPTY(oj), PARITY(oj))))
+            break;
+          const uint32_t bar = g < kKGranules ? K_FULL(j) : V_FULL(j);
+          if (g == 0) mbar_expect_tx(bar, kKGranules * kAtomBytes);
+          if (g == kKGranules) mbar_expect_tx(bar, (kPerTile - kKGranules) * kAtomBytes);
+          const uint32_t dst = sbase + kOffRing + (n % kRing) * kAtomBytes;
           const int row = k0 + j * kTile;
-          if (g == 2) tma_load_2d(dst, &tmap_rope, 0, row, FULL(s), pol_rope);
-          else tma_load_4d(dst, &tmap_kv, 0, row, g < 2 ? g : g - 1, head, FULL(s));
+          if (g == 2) tma_load_2d(dst, &tmap_rope, 0, row, bar, pol_rope);
+          else tma_load_4d(dst, &tmap_kv, 0, row, g < 2 ? g : g - 1, head, bar);
           if (j == 0 && g < 2 && (g == 0 ? nt0 : nt1) > 0) {
             mbar_expect_tx(Q_FULL(g), kQAtoms * kAtomBytes);
             tma_load_4d(sbase + kOffQ + g * kQAtoms * kAtomBytes, &tmap_q, 0, q0 + row0 + g * kTile, 0,
@@ -168,7 +178,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) raise_error(kErrTimeout);
       // No copy is in flight when the CTA ends.
-      for (int u = n - 1; u >= 0 && u >= n - kRing; --u) mbar_wait(FULL(u % kRing), (u / kRing) & 1);
+      if (ok)
+        for (int j = max(0, ntmax - 2); j < ntmax; ++j) {
+          mbar_wait(K_FULL(j), PARITY(j));
+          mbar_wait(V_FULL(j), PARITY(j));
+        }
       for (int q = 0; q < 2; ++q)
         if (ntmax > 0 && (q == 0 ? nt0 : nt1) > 0) mbar_wait(Q_FULL(q), 0);
     }
@@ -183,15 +197,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     // (V: MN-major, an MMA for each granule's 64 dims: with A in tensor memory
     // N = 64 runs at the full rate, and granules need not lie side by side.)
     bool ok = true;
-    auto qk = [&](int q, int j, bool first) {
-      if (j == 0 && !(ok = ok && warp_wait(Q_FULL(q), 0))) return;
+    // A phase is tested before the last MMAs of the step before go out, so that
+    // the test's latency hides behind them; `want` waits only if it was not
+    // complete then.
+    uint32_t done_bar = 0, done_parity = 0;
+    auto want = [&](uint32_t bar, uint32_t parity) {
+      if (ok && !(done_bar == bar && done_parity == parity)) ok = warp_wait(bar, parity);
+      done_bar = 0;
+    };
+    auto peek = [&](uint32_t bar, uint32_t parity) {
+      if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) {
+        done_bar = bar;
+        done_parity = parity;
+      }
+    };
+    // (A phase that completed stays the barrier's latest until its data has
+    // been used, so a remembered answer does not go stale before that; it is
+    // dropped after a use.)
+    // What the step after the current one waits for: K, V or P.
+    auto qk = [&](int q, int j, uint32_t next_bar, uint32_t next_parity) {
 #pragma unroll
       for (int a = 0; a < kQAtoms; ++a) {
-        const int n = j * kPerTile + a, s = n % kRing;
-        if (first && !(ok = ok && warp_wait(FULL(s), (n / kRing) & 1))) return;
-        tc_fence_after();
-        const uint64_t dk = dr0 + static_cast<uint64_t>((s * kAtomBytes) >> 4);
+        const uint64_t dk = dr0 + static_cast<uint64_t>((((j * kPerTile + a) % kRing) * kAtomBytes) >> 4);
         const uint64_t dq = dq0 + static_cast<uint64_t>(((q * kQAtoms + a) * kAtomBytes) >> 4);
+        if (a == kQAtoms - 1) peek(next_bar, next_parity);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           mma_f16_ss_uni(tmem + kColS + kTile * q, dq + static_cast<uint64_t>((32 * k) >> 4),
@@ -200,41 +229,56 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (el) tc_commit(S_FULL(q));
       __syncwarp();
     };
-    auto pv = [&](int q, int j, bool first) {
-      if (!(ok = ok && warp_wait(P_FULL(q), j & 1))) return;
-      tc_fence_after();
+    auto pv = [&](int q, int j, uint32_t next_bar, uint32_t next_parity) {
 #pragma unroll
       for (int a = 0; a < 2; ++a) {
-        const int n = j * kPerTile + 3 + a, s = n % kRing;
-        if (first && !(ok = ok && warp_wait(FULL(s), (n / kRing) & 1))) return;
-        tc_fence_after();
-        const uint64_t dv = dr0 + static_cast<uint64_t>((s * kAtomBytes) >> 4);
+        const uint64_t dv = dr0 + static_cast<uint64_t>((((j * kPerTile + 3 + a) % kRing) * kAtomBytes) >> 4);
+        if (a == 1) peek(next_bar, next_parity);
 #pragma unroll
         for (int k = 0; k < kTile / 16; ++k)
           mma_f16_ts_uni(tmem + kColO + kHeadDim * q + 64 * a, tmem + kColS + kTile * q + 8 * k,
-                         dv + static_cast<uint64_t>((2048 * k) >> 4),
-                         idesc_pv, (j > 0 || k > 0) ? 1u : 0u, el);
+                         dv + static_cast<uint64_t>((2048 * k) >> 4), idesc_pv, (j > 0 || k > 0) ? 1u : 0u,
+                         el);
       }
       if (j == (q == 0 ? nt0 : nt1) - 1) {
         if (el) tc_commit(O_FULL(q));
         __syncwarp();
       }
     };
-    auto release = [&](int j, int g0, int g1) {
-      if (el)
-        for (int g = g0; g < g1; ++g) tc_commit(EMPTY((j * kPerTile + g) % kRing));
+    auto commit = [&](uint32_t bar) {
+      if (el) tc_commit(bar);
       __syncwarp();
     };
     for (int j = 0; ok && j <= ntmax; ++j) {
-      if (j < nt0) qk(0, j, true);
-      if (ok && j >= 1) {
-        if (j - 1 < nt1) pv(1, j - 1, j - 1 >= nt0);
-        release(j - 1, 3, 5);
+      if (j < nt0) {
+        if (j == 0) ok = warp_wait(Q_FULL(0), 0);
+        want(K_FULL(j), PARITY(j));
+        tc_fence_after();
+        if (ok) qk(0, j, P_FULL(1), (j - 1) & 1);
       }
-      if (j == ntmax) break;
-      if (ok && j < nt1) qk(1, j, j >= nt0);
-      release(j, 0, 3);
-      if (ok && j < nt0) pv(0, j, true);
+      if (ok && j >= 1) {
+        if (j - 1 < nt1) {
+          if (j - 1 >= nt0) ok = ok && warp_wait(V_FULL(j - 1), PARITY(j - 1));
+          want(P_FULL(1), (j - 1) & 1);
+          tc_fence_after();
+          if (ok) pv(1, j - 1, K_FULL(j), PARITY(j));
+        }
+        commit(V_EMPTY(j - 1));
+      }
+      if (!ok || j == ntmax) break;
+      if (j < nt1) {
+        if (j == 0) ok = warp_wait(Q_FULL(1), 0);
+        if (j >= nt0) want(K_FULL(j), PARITY(j));
+        tc_fence_after();
+        if (ok) qk(1, j, P_FULL(0), j & 1);
+      }
+      commit(K_EMPTY(j));
+      if (j < nt0) {
+        want(P_FULL(0), j & 1);
+        ok = ok && warp_wait(V_FULL(j), PARITY(j));
+        tc_fence_after();
+        if (ok) pv(0, j, K_FULL(j + 1), PARITY(j + 1));
+      }
     }
     if (!ok && el) raise_error(kErrTimeout);
     if (el) tc_commit(DRAIN);      // every MMA is done before TMEM is freed
@@ -307,11 +351,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // tile that reads them.
       const int vlive = klen - j * kTile;
       if (vlive < kTile && (q == 0 || j >= nt0)) {
+        if (ok && !mbar_wait(V_FULL(j), PARITY(j))) ok = false;
 #pragma unroll 1
         for (int a = 0; a < 2; ++a) {
-          const int g = j * kPerTile + 3 + a;
-          if (ok && !mbar_wait(FULL(g % kRing), (g / kRing) & 1)) ok = false;
-          uint4* v = reinterpret_cast<uint4*>(smem + kOffRing + (g % kRing) * kAtomBytes);
+          uint4* v = reinterpret_cast<uint4*>(smem + kOffRing + ((j * kPerTile + 3 + a) % kRing) * kAtomBytes);
           for (int e = (threadIdx.x & 127) + vlive * 8; e < kAtomBytes / 16; e += 128)
             v[e] = make_uint4(0u, 0u, 0u, 0u);
         }
@@ -355,8 +398,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
-#undef FULL
-#undef EMPTY
+#undef K_FULL
+#undef V_FULL
+#undef K_EMPTY
+#undef V_EMPTY
+#undef PARITY
 #undef Q_FULL
 #undef S_FULL
 #undef P_FULL

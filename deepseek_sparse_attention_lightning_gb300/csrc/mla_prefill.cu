@@ -27,6 +27,12 @@
 // MMA order: QK0(j), PV1(j-1), QK1(j), PV0(j), QK0(j+1), ...: a tile's softmax
 // has the other tile's P V and Q K^T (1280 cycles of matrix work) to hide in.
 //
+// A grid of one CTA for each 256 queries of a head, late queries (most keys)
+// first within a head; but a CTA that runs goes on with the work of CTAs that
+// have not started (a request for one is under way while the CTA works), so
+// that its copies run into the next item while this one's last tiles and
+// output are under way, and the SMs end close together.
+//
 // Warps 0-3 and 4-7: softmax and epilogue of query tile 0 and 1, a row a
 // thread.  Warp 8: copies.  Warp 9: MMAs, issued from uniform control flow.
 // The running maximum is raised lazily (by 2^8 at least), by the row's own
@@ -55,16 +61,20 @@ constexpr int kOffQ = 0;
 constexpr int kOffRing = 2 * kQAtoms * kAtomBytes;
 constexpr int kOffBar = kOffRing + kRing * kAtomBytes;
 constexpr int kKGranules = 3;
-constexpr int kNumBars = 17;
-constexpr int kOffSlot = kOffBar + kNumBars * 8;
+constexpr int kNumBars = 24;
+constexpr int kOffTaken = kOffBar + kNumBars * 8;     // an answer of 16 bytes
+constexpr int kOffItem = kOffTaken + 16;             // two records
+constexpr int kOffSlot = kOffItem + 2 * 48;
 constexpr int kSmemBytes = kOffSlot + 16 + 1024;
+static_assert(kOffTaken % 16 == 0, "alignment");
 static_assert(kSmemBytes <= 232448, "shared memory");
 constexpr int kThreads = 384;                  // two softmax warpgroups; copies, MMAs and two idle warps
 // Registers: launched with 168 a thread (384 x 168 = 64512); the softmax holds a
 // row of 128 scores and takes 208, the third warpgroup keeps 88 (256 x 208 +
 // 128 x 88 = 64512).
-constexpr int kSoftRegs = 208, kOtherRegs = 88;
+constexpr int kSoftRegs = 216, kOtherRegs = 72;
 static_assert(256 * kSoftRegs + 128 * kOtherRegs <= 384 * 168, "registers");
+constexpr int kItemReaders = 9;                // eight softmax warps and the MMA warp
 constexpr int kColS = 0, kColO = 256, kTmemCols = 512;
 constexpr float kRaiseLog2 = 8.0f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -78,30 +88,47 @@ __device__ __forceinline__ int key_limit(int row, int qlen, int klen, int causal
   return causal ? max(0, klen - qlen + row + 1) : klen;
 }
 
+// The work of one CTA of the grid: 256 queries of a head.
+struct Item {
+  int work;                  // it has queries (a record: 0 ends the CTA's work)
+  int head, row0;            // first query row of the request
+  int q0, k0, qlen, klen;    // the request in the packed tensors
+  int nt0, nt1;              // key tiles of the two query tiles
+  int base;                  // key tiles of the CTA's items before it
+};
+static_assert(sizeof(Item) <= 48, "record");
+
+__device__ __forceinline__ Item item_of(const MlaPrefillLaunch& p, int x, int y, int z) {
+  Item it;
+  it.base = 0;
+  it.head = y;
+  const int blocks = gridDim.x;
+  it.row0 = (blocks - 1 - x) * kCtaRows;      // late queries see the most keys: they start first
+  it.q0 = __ldg(p.cu_q + z);
+  it.k0 = __ldg(p.cu_k + z);
+  it.qlen = __ldg(p.cu_q + z + 1) - it.q0;
+  it.klen = max(0, __ldg(p.cu_k + z + 1) - it.k0);
+  // Offsets outside the packed tensors, or a length above max_q, are reported;
+  // the request's rows are left as they were, or not all of them written.
+  const bool bad = it.q0 < 0 || it.k0 < 0 || it.qlen < 0 || it.qlen > p.total_q - it.q0 ||
+                   it.klen > p.total_k - it.k0;
+  if (bad || it.qlen > blocks * kCtaRows) raise_error(kErrCheck);
+  it.work = !bad && it.row0 < it.qlen ? 1 : 0;
+  auto tiles_from = [&](int first) {
+    if (!it.work || first >= it.qlen) return 0;
+    const int lim = key_limit(min(first + kTile, it.qlen) - 1, it.qlen, it.klen, p.causal);
+    return (min(lim, it.klen) + kTile - 1) / kTile;
+  };
+  it.nt0 = tiles_from(it.row0);
+  it.nt1 = tiles_from(it.row0 + kTile);
+  return it;
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
     mla_prefill_kernel(const __grid_constant__ CUtensorMap tmap_q,
                        const __grid_constant__ CUtensorMap tmap_kv,
                        const __grid_constant__ CUtensorMap tmap_rope, const MlaPrefillLaunch p) {
   extern __shared__ uint8_t smem_raw[];
-  const int head = blockIdx.y, req = blockIdx.z;
-  // Late queries see the most keys: they start first.
-  const int row0 = static_cast<int>(gridDim.x - 1 - blockIdx.x) * kCtaRows;
-  const int q0 = __ldg(p.cu_q + req), k0 = __ldg(p.cu_k + req);
-  const int qlen = __ldg(p.cu_q + req + 1) - q0, klen = max(0, __ldg(p.cu_k + req + 1) - k0);
-  // Offsets outside the packed tensors, or a length above max_q, are reported;
-  // the request's rows are left as they were, or not all of them written.
-  const bool bad = q0 < 0 || k0 < 0 || qlen < 0 || q0 + qlen > p.total_q || k0 + klen > p.total_k;
-  if (bad || qlen > static_cast<int>(gridDim.x) * kCtaRows) {
-    if (threadIdx.x == 0) raise_error(kErrCheck);
-    if (bad) return;
-  }
-  if (row0 >= qlen) return;
-  // Key tiles of the two query tiles.
-  auto tiles_from = [&](int first) {
-    if (first >= qlen) return 0;
-    return (key_limit(min(first + kTile, qlen) - 1, qlen, klen, p.causal) + kTile - 1) / kTile;
-  };
-  const int nt0 = tiles_from(row0), nt1 = tiles_from(row0 + kTile), ntmax = max(nt0, nt1);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const float ninf = __int_as_float(0xff800000);
 
@@ -110,17 +137,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sbase = smem_u32(smem);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffSlot);
   const uint32_t bar0 = sbase + kOffBar;
-// K / V of key tile j (at most two of each are in the ring): landed, and read.
+// K / V of key tile j, counted over the CTA's items (at most two of each are in
+// the ring): landed, and read.
 #define K_FULL(j) (bar0 + 8u * ((j) & 1))
 #define V_FULL(j) (bar0 + 16u + 8u * ((j) & 1))
 #define K_EMPTY(j) (bar0 + 32u + 8u * ((j) & 1))
 #define V_EMPTY(j) (bar0 + 48u + 8u * ((j) & 1))
 #define PARITY(j) (((j) >> 1) & 1)
+// Of query tile q: q landed / read by its last Q K^T, scores, probabilities,
+// output of the item complete.
 #define Q_FULL(q) (bar0 + 64u + 8u * (q))
-#define S_FULL(q) (bar0 + 80u + 8u * (q))
-#define P_FULL(q) (bar0 + 96u + 8u * (q))
+#define Q_EMPTY(q) (bar0 + 80u + 8u * (q))
+#define S_FULL(q) (bar0 + 96u + 8u * (q))
 #define O_FULL(q) (bar0 + 112u + 8u * (q))
-#define DRAIN (bar0 + 128u)
+#define P_FULL(q) (bar0 + 128u + 8u * (q))
+#define DRAIN (bar0 + 144u)
+#define TAKEN (bar0 + 152u)
+// Item k's record written / no longer needed by any role.
+#define ITEM_FULL(k) (bar0 + 160u + 8u * ((k) & 1))
+#define ITEM_EMPTY(k) (bar0 + 176u + 8u * ((k) & 1))
 
   if (warp == 8 && lane == 0) {
     for (int q = 0; q < 2; ++q) {
@@ -129,11 +164,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(K_EMPTY(q), 1);
       mbar_init(V_EMPTY(q), 1);
       mbar_init(Q_FULL(q), 1);
+      mbar_init(Q_EMPTY(q), 1);
+      mbar_init(ITEM_FULL(q), 1);
+      mbar_init(ITEM_EMPTY(q), kItemReaders);
       mbar_init(S_FULL(q), 1);
       mbar_init(P_FULL(q), kTile);
       mbar_init(O_FULL(q), 1);
     }
     mbar_init(DRAIN, 1);
+    mbar_init(TAKEN, 1);
     fence_mbar_init();
     prefetch_tmap(&tmap_q);
     prefetch_tmap(&tmap_kv);
@@ -147,44 +186,79 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
+  const Item* items = reinterpret_cast<const Item*>(smem + kOffItem);      // 48 bytes apart
+  auto record = [&](int k) -> const Item& {
+    return *reinterpret_cast<const Item*>(reinterpret_cast<const uint8_t*>(items) + 48 * (k & 1));
+  };
+
   if (warp >= 8) {
   setmaxnreg_dec<kOtherRegs>();
   if (warp == 8) {
     // ------------------------------------------------------------- copies
     if (lane == 0) {
       bool ok = true;
-      int n = 0;
+      int n = 0;                                          // granules so far
+      int uses0 = 0, uses1 = 0;                           // items that had each query tile
       const uint64_t pol_rope = policy_evict_last();      // every head reads it
-      for (int j = 0; ok && j < ntmax; ++j) {
-        for (int g = 0; g < kPerTile; ++g, ++n) {
-          // The granule's slot held granule n - kRing, of an earlier tile.
-          const int old = n - kRing, oj = old / kPerTile;
-          if (old >= 0 &&
-              !(ok = mbar_wait(old % kPerTile < kKGranules ? K_EMPTY(oj) : V_EMPTY(oj), PARITY(oj))))
-            break;
-          const uint32_t bar = g < kKGranules ? K_FULL(j) : V_FULL(j);
-          if (g == 0) mbar_expect_tx(bar, kKGranules * kAtomBytes);
-          if (g == kKGranules) mbar_expect_tx(bar, (kPerTile - kKGranules) * kAtomBytes);
-          const uint32_t dst = sbase + kOffRing + (n % kRing) * kAtomBytes;
-          const int row = k0 + j * kTile;
-          if (g == 2) tma_load_2d(dst, &tmap_rope, 0, row, bar, pol_rope);
-          else tma_load_4d(dst, &tmap_kv, 0, row, g < 2 ? g : g - 1, head, bar);
-          if (j == 0 && g < 2 && (g == 0 ? nt0 : nt1) > 0) {
-            mbar_expect_tx(Q_FULL(g), kQAtoms * kAtomBytes);
-            tma_load_4d(sbase + kOffQ + g * kQAtoms * kAtomBytes, &tmap_q, 0, q0 + row0 + g * kTile, 0,
-                        head, Q_FULL(g));
+      Item it = item_of(p, blockIdx.x, blockIdx.y, blockIdx.z);
+      int base = 0, k = 0, asked = 0;
+      bool more = true;
+      while (ok) {
+        if (it.work || !more) {
+          // The other roles work from the record (one with work = 0 ends them).
+          if (k >= 2 && !(ok = mbar_wait(ITEM_EMPTY(k), PARITY(k) ^ 1))) break;
+          it.base = base;
+          if (!more) it.work = 0;
+          const_cast<Item&>(record(k)) = it;
+          mbar_arrive(ITEM_FULL(k));
+          ++k;
+          if (!more) break;
+        }
+        const int ntmax = max(it.nt0, it.nt1);
+        for (int j = 0; ok && j < ntmax; ++j) {
+          for (int g = 0; g < kPerTile; ++g, ++n) {
+            // The granule's slot held granule n - kRing, of an earlier tile.
+            const int old = n - kRing, oj = old / kPerTile;
+            if (old >= 0 &&
+                !(ok = mbar_wait(old % kPerTile < kKGranules ? K_EMPTY(oj) : V_EMPTY(oj), PARITY(oj))))
+              break;
+            const uint32_t bar = g < kKGranules ? K_FULL(base + j) : V_FULL(base + j);
+            if (g == 0) mbar_expect_tx(bar, kKGranules * kAtomBytes);
+            if (g == kKGranules) mbar_expect_tx(bar, (kPerTile - kKGranules) * kAtomBytes);
+            const uint32_t dst = sbase + kOffRing + (n % kRing) * kAtomBytes;
+            const int row = it.k0 + j * kTile;
+            if (g == 2) tma_load_2d(dst, &tmap_rope, 0, row, bar, pol_rope);
+            else tma_load_4d(dst, &tmap_kv, 0, row, g < 2 ? g : g - 1, it.head, bar);
+            if (j == 0 && g < 2 && (g == 0 ? it.nt0 : it.nt1) > 0) {
+              const int used = g == 0 ? uses0++ : uses1++;
+              if (used > 0 && !(ok = mbar_wait(Q_EMPTY(g), (used - 1) & 1))) break;
+              mbar_expect_tx(Q_FULL(g), kQAtoms * kAtomBytes);
+              tma_load_4d(sbase + kOffQ + g * kQAtoms * kAtomBytes, &tmap_q, 0,
+                          it.q0 + it.row0 + g * kTile, 0, it.head, Q_FULL(g));
+            }
           }
         }
+        base += ntmax;
+        // The next item, once this one's copies are under way (not earlier:
+        // items go to the CTAs that come free first).
+        if (!ok) break;
+        mbar_expect_tx(TAKEN, 16);
+        take_cta(sbase + kOffTaken, TAKEN);
+        if (!(ok = mbar_wait(TAKEN, asked++ & 1))) break;
+        uint32_t x, y, z;
+        more = taken_cta(sbase + kOffTaken, x, y, z);
+        fence_proxy_async_smem();      // read before the next answer is written there
+        if (more) it = item_of(p, x, y, z);
       }
       if (!ok) raise_error(kErrTimeout);
       // No copy is in flight when the CTA ends.
       if (ok)
-        for (int j = max(0, ntmax - 2); j < ntmax; ++j) {
+        for (int j = max(0, base - 2); j < base; ++j) {
           mbar_wait(K_FULL(j), PARITY(j));
           mbar_wait(V_FULL(j), PARITY(j));
         }
-      for (int q = 0; q < 2; ++q)
-        if (ntmax > 0 && (q == 0 ? nt0 : nt1) > 0) mbar_wait(Q_FULL(q), 0);
+      if (ok && uses0 > 0) mbar_wait(Q_FULL(0), (uses0 - 1) & 1);
+      if (ok && uses1 > 0) mbar_wait(Q_FULL(1), (uses1 - 1) & 1);
     }
     __syncwarp();
   } else if (warp == 9) {
@@ -214,11 +288,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     // (A phase that completed stays the barrier's latest until its data has
     // been used, so a remembered answer does not go stale before that; it is
     // dropped after a use.)
-    // What the step after the current one waits for: K, V or P.
-    auto qk = [&](int q, int j, uint32_t next_bar, uint32_t next_parity) {
+    // Descriptor offset of granule g of tile t, broadcast: the compiler then
+    // knows it to be the same in every lane and keeps it in uniform registers.
+    auto slot_of = [&](int t, int g) -> uint64_t {
+      return static_cast<uint32_t>(
+          __shfl_sync(0xffffffffu, (((t * kPerTile + g) % kRing) * kAtomBytes) >> 4, 0));
+    };
+    // Q K^T and P V of query tile q over key tile t (counted over the items);
+    // next_bar: what the step after it waits for.
+    auto qk = [&](int q, int t, uint32_t next_bar, uint32_t next_parity) {
 #pragma unroll
       for (int a = 0; a < kQAtoms; ++a) {
-        const uint64_t dk = dr0 + static_cast<uint64_t>((((j * kPerTile + a) % kRing) * kAtomBytes) >> 4);
+        const uint64_t dk = dr0 + slot_of(t, a);
         const uint64_t dq = dq0 + static_cast<uint64_t>(((q * kQAtoms + a) * kAtomBytes) >> 4);
         if (a == kQAtoms - 1) peek(next_bar, next_parity);
 #pragma unroll
@@ -229,57 +310,105 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (el) tc_commit(S_FULL(q));
       __syncwarp();
     };
-    auto pv = [&](int q, int j, uint32_t next_bar, uint32_t next_parity) {
+    auto pv = [&](int q, int t, bool first, uint32_t next_bar, uint32_t next_parity) {
 #pragma unroll
       for (int a = 0; a < 2; ++a) {
-        const uint64_t dv = dr0 + static_cast<uint64_t>((((j * kPerTile + 3 + a) % kRing) * kAtomBytes) >> 4);
+        const uint64_t dv = dr0 + slot_of(t, kKGranules + a);
         if (a == 1) peek(next_bar, next_parity);
 #pragma unroll
         for (int k = 0; k < kTile / 16; ++k)
           mma_f16_ts_uni(tmem + kColO + kHeadDim * q + 64 * a, tmem + kColS + kTile * q + 8 * k,
-                         dv + static_cast<uint64_t>((2048 * k) >> 4), idesc_pv, (j > 0 || k > 0) ? 1u : 0u,
+                         dv + static_cast<uint64_t>((2048 * k) >> 4), idesc_pv, (!first || k > 0) ? 1u : 0u,
                          el);
-      }
-      if (j == (q == 0 ? nt0 : nt1) - 1) {
-        if (el) tc_commit(O_FULL(q));
-        __syncwarp();
       }
     };
     auto commit = [&](uint32_t bar) {
       if (el) tc_commit(bar);
       __syncwarp();
     };
-    for (int j = 0; ok && j <= ntmax; ++j) {
-      if (j < nt0) {
-        if (j == 0) ok = warp_wait(Q_FULL(0), 0);
-        want(K_FULL(j), PARITY(j));
+    int base = 0, c0 = 0, c1 = 0;          // key tiles so far: all, and of each query tile
+    int items0 = 0, items1 = 0;            // items that had each query tile
+    // P V of query tile 1 goes out one step late, after Q K^T of query tile 0
+    // over the next key tile (the next item's first, at the end of one).
+    bool held = false, held_pv = false, held_v = false, held_first = false, held_last = false;
+    int held_t = 0, held_c = 0;
+    auto issue_held = [&](uint32_t next_bar, uint32_t next_parity) {
+      if (!held || !ok) return;
+      held = false;
+      if (held_pv) {
+        if (!held_v) ok = warp_wait(V_FULL(held_t), PARITY(held_t));
+        want(P_FULL(1), held_c & 1);
         tc_fence_after();
-        if (ok) qk(0, j, P_FULL(1), (j - 1) & 1);
+        if (!ok) return;
+        pv(1, held_t, held_first, next_bar, next_parity);
+        if (held_last) commit(O_FULL(1));
       }
-      if (ok && j >= 1) {
-        if (j - 1 < nt1) {
-          if (j - 1 >= nt0) ok = ok && warp_wait(V_FULL(j - 1), PARITY(j - 1));
-          want(P_FULL(1), (j - 1) & 1);
+      commit(V_EMPTY(held_t));
+    };
+    for (int item = 0; ok; ++item) {
+      // (What is held back does not wait for a record, or an item without keys,
+      // to come.)
+      if (!__all_sync(0xffffffffu, mbar_test_wait(ITEM_FULL(item), PARITY(item)))) issue_held(DRAIN, 0);
+      if (!(ok = ok && warp_wait(ITEM_FULL(item), PARITY(item)))) break;
+      const int work = __shfl_sync(0xffffffffu, record(item).work, 0);
+      const int nt0 = __shfl_sync(0xffffffffu, record(item).nt0, 0);
+      const int nt1 = __shfl_sync(0xffffffffu, record(item).nt1, 0), ntmax = max(nt0, nt1);
+      if (lane == 0) mbar_arrive(ITEM_EMPTY(item));
+      if (!work) break;
+      if (ntmax == 0) issue_held(DRAIN, 0);
+      for (int j = 0; ok && j < ntmax; ++j) {
+        const int t = base + j;
+        if (j < nt0) {
+          // (A new item's q and first keys may not have landed yet: then the
+          // P V that is held back does not wait for them.)
+          if (j == 0) {
+            if (held && !__all_sync(0xffffffffu, mbar_test_wait(Q_FULL(0), items0 & 1) &&
+                                                     mbar_test_wait(K_FULL(t), PARITY(t))))
+              issue_held(K_FULL(t), PARITY(t));
+            ok = ok && warp_wait(Q_FULL(0), items0 & 1);
+            ++items0;
+          }
+          want(K_FULL(t), PARITY(t));
           tc_fence_after();
-          if (ok) pv(1, j - 1, K_FULL(j), PARITY(j));
+          if (!ok) break;
+          qk(0, t, P_FULL(1), held_c & 1);
+          if (j == nt0 - 1) commit(Q_EMPTY(0));
         }
-        commit(V_EMPTY(j - 1));
+        issue_held(K_FULL(t), PARITY(t));
+        if (!ok) break;
+        if (j < nt1) {
+          if (j == 0) {
+            ok = warp_wait(Q_FULL(1), items1 & 1);
+            ++items1;
+          }
+          if (j >= nt0) want(K_FULL(t), PARITY(t));
+          tc_fence_after();
+          if (!ok) break;
+          qk(1, t, P_FULL(0), c0 & 1);
+          if (j == nt1 - 1) commit(Q_EMPTY(1));
+        }
+        commit(K_EMPTY(t));
+        if (j < nt0) {
+          if (!mbar_test_wait(V_FULL(t), PARITY(t))) ok = warp_wait(V_FULL(t), PARITY(t));
+          want(P_FULL(0), c0 & 1);
+          tc_fence_after();
+          if (!ok) break;
+          pv(0, t, j == 0, K_FULL(t + 1), PARITY(t + 1));
+          if (j == nt0 - 1) commit(O_FULL(0));
+          ++c0;
+        }
+        held = true;
+        held_pv = j < nt1;
+        held_v = j < nt0;
+        held_first = j == 0;
+        held_last = j == nt1 - 1;
+        held_t = t;
+        held_c = c1;
+        if (j < nt1) ++c1;
       }
-      if (!ok || j == ntmax) break;
-      if (j < nt1) {
-        if (j == 0) ok = warp_wait(Q_FULL(1), 0);
-        if (j >= nt0) want(K_FULL(j), PARITY(j));
-        tc_fence_after();
-        if (ok) qk(1, j, P_FULL(0), j & 1);
-      }
-      commit(K_EMPTY(j));
-      if (j < nt0) {
-        want(P_FULL(0), j & 1);
-        ok = ok && warp_wait(V_FULL(j), PARITY(j));
-        tc_fence_after();
-        if (ok) pv(0, j, K_FULL(j + 1), PARITY(j + 1));
-      }
+      base += ntmax;
     }
+    issue_held(DRAIN, 0);
     if (!ok && el) raise_error(kErrTimeout);
     if (el) tc_commit(DRAIN);      // every MMA is done before TMEM is freed
     __syncwarp();
@@ -289,21 +418,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------------------------------------- softmax and epilogue
     setmaxnreg_inc<kSoftRegs>();
     const int q = warp >> 2, w4 = warp & 3;
-    const int n = (q == 0 ? nt0 : nt1);
-    const int row = row0 + q * kTile + w4 * 32 + lane;     // of the request
-    const bool live = row < qlen;
     const uint32_t tS = tmem + (static_cast<uint32_t>(w4 * 32) << 16) + kColS + kTile * q;
     const uint32_t tO = tmem + (static_cast<uint32_t>(w4 * 32) << 16) + kColO + kHeadDim * q;
-    const int lim = live ? min(klen, key_limit(row, qlen, klen, p.causal)) : 0;
     const float sc = p.sm_scale * kLog2e;
-    float mrun = ninf, lrun = 0.f;
     bool ok = true;
-    for (int j = 0; j < n; ++j) {
-      if (ok && !mbar_wait(S_FULL(q), j & 1)) ok = false;
+    int phase = 0;             // parities: bit 0 of the scores, bit 1 of the outputs
+    for (int item = 0; ok; ++item) {
+    if (!(ok = warp_wait(ITEM_FULL(item), PARITY(item)))) break;
+    const int row = q * kTile + w4 * 32 + lane;     // from the item's first
+    int n, lim, vlive;
+    {
+      const Item& it = record(item);
+      if (!it.work) break;
+      n = q == 0 ? it.nt0 : it.nt1;
+      lim = min(it.klen, key_limit(it.row0 + row, it.qlen, it.klen, p.causal));
+      // Keys of the request behind the tile's start, where this query tile is
+      // the first to read the tile's V.
+      vlive = it.klen;
+    }
+    float mrun = ninf, lrun = 0.f;
+    for (int j = 0; j < n; ++j, phase ^= 1, lim -= kTile, vlive -= kTile) {
+      if (ok && !mbar_wait(S_FULL(q), phase & 1)) ok = false;
       tc_fence_after();
       uint32_t s[128];
       tmem_ld128(tS, s);
-      const int seen = lim - j * kTile;
+      const int seen = lim;
       float mx[4] = {ninf, ninf, ninf, ninf};
       if (__any_sync(0xffffffffu, seen < kTile)) {
 #pragma unroll
@@ -331,48 +470,52 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (raise) mrun = tmax;
       const float mref = mrun > ninf ? mrun : 0.f;
-      float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t pk[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const float2 x = fma2(make_float2(__uint_as_float(s[64 * c + 2 * e]),
-                                            __uint_as_float(s[64 * c + 2 * e + 1])),
-                                make_float2(sc, sc), make_float2(-mref, -mref));
-          const float2 w = make_float2(ex2(x.x), ex2(x.y));
-          ls[e & 1] = add2(ls[e & 1], w);
-          pk[e] = pack_bf16x2(w.x, w.y);
-        }
-        tmem_st32(tS + 32 * c, pk);
-      }
-      lrun += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
       // Rows of V behind the request's end are cleared, by the first query
       // tile that reads them.
-      const int vlive = klen - j * kTile;
-      if (vlive < kTile && (q == 0 || j >= nt0)) {
-        if (ok && !mbar_wait(V_FULL(j), PARITY(j))) ok = false;
+      if (vlive < kTile && (q == 0 || j >= record(item).nt0)) {
+        const int t = record(item).base + j;
+        if (ok && !mbar_wait(V_FULL(t), PARITY(t))) ok = false;
 #pragma unroll 1
         for (int a = 0; a < 2; ++a) {
-          uint4* v = reinterpret_cast<uint4*>(smem + kOffRing + ((j * kPerTile + 3 + a) % kRing) * kAtomBytes);
+          uint4* v = reinterpret_cast<uint4*>(smem + kOffRing + ((t * kPerTile + 3 + a) % kRing) * kAtomBytes);
           for (int e = (threadIdx.x & 127) + vlive * 8; e < kAtomBytes / 16; e += 128)
             v[e] = make_uint4(0u, 0u, 0u, 0u);
         }
         fence_proxy_async_smem();
       }
+      // P V over the first 64 keys starts while the others' exponentials run.
+      float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float2 x = fma2(make_float2(__uint_as_float(s[32 * c + 2 * e]),
+                                            __uint_as_float(s[32 * c + 2 * e + 1])),
+                                make_float2(sc, sc), make_float2(-mref, -mref));
+          const float2 w = make_float2(ex2(x.x), ex2(x.y));
+          ls[e & 1] = add2(ls[e & 1], w);
+          pk[e] = pack_bf16x2(w.x, w.y);
+        }
+        tmem_st16_async(tS + 16 * c, pk);
+      }
+      tmem_st_wait();
       tc_fence_before();
       mbar_arrive(P_FULL(q));
+      lrun += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
     }
     if (n > 0) {
-      if (ok && !mbar_wait(O_FULL(q), 0)) ok = false;
+      if (ok && !mbar_wait(O_FULL(q), (phase >> 1) & 1)) ok = false;
       tc_fence_after();
+      phase ^= 2;
     }
-    if (!ok && lane == 0) raise_error(kErrTimeout);
-    const bool any = lrun > 0.f || lrun != lrun;
-    const float inv = any ? 1.f / lrun : 0.f;
-    const long long orow = (static_cast<long long>(q0) + row) * p.heads + head;
-    uint4* dst = reinterpret_cast<uint4*>(p.out + orow * kHeadDim);
-    if (row0 + q * kTile < qlen) {
+    const Item& it = record(item);
+    if (it.row0 + q * kTile < it.qlen) {
+      const bool live = it.row0 + row < it.qlen;
+      const bool any = lrun > 0.f || lrun != lrun;
+      const float inv = any ? 1.f / lrun : 0.f;
+      const long long at = static_cast<long long>(it.q0 + it.row0 + row) * p.heads + it.head;
+      uint4* dst = reinterpret_cast<uint4*>(p.out + at * kHeadDim);
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
         uint32_t o[32];
@@ -389,9 +532,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           dst[4 * c + e] = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
-      if (live && p.lse) p.lse[orow] = any ? (mrun + log2f(lrun)) * kLn2 : ninf;
+      if (live && p.lse) p.lse[at] = any ? (mrun + log2f(lrun)) * kLn2 : ninf;
     }
     tc_fence_before();
+    ok = __all_sync(0xffffffffu, ok);
+    if (lane == 0) mbar_arrive(ITEM_EMPTY(item));
+    }
+    if (!ok && lane == 0) raise_error(kErrTimeout);
   }
   __syncthreads();
   if (warp == 9) {
@@ -407,6 +554,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #undef S_FULL
 #undef P_FULL
 #undef O_FULL
+#undef Q_EMPTY
+#undef TAKEN
+#undef ITEM_FULL
+#undef ITEM_EMPTY
 #undef DRAIN
 }
 

@@ -85,6 +85,8 @@ _SIGS = {
                                          c_size_t, c_void_p]),
     "dsa_mla_decode": (c_int32, [ctypes.POINTER(DecodeDesc), c_void_p, c_void_p, c_float, c_void_p,
                                  c_void_p, c_void_p, c_size_t, c_void_p]),
+    "dsa_mla_decode_fp8kv": (c_int32, [ctypes.POINTER(DecodeDesc), c_void_p, c_void_p, c_float,
+                                       c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
     "dsa_mla_decode_workspace_bytes": (c_size_t, [ctypes.POINTER(DecodeDesc)]),
     "dsa_mla_prefill": (c_int32, [c_int32, c_int32, c_int32, c_int32, c_int32, c_void_p, c_void_p,
                                   c_void_p, c_void_p, c_void_p, c_int64, c_float, c_int32, c_void_p,
@@ -362,6 +364,17 @@ def dsa_mla_decode(desc, q, kv, out, ws, sm_scale, lse=None, stream=None):
               _arg(out, bf16, (T, H, 512), dev, "out"), _arg(lse, torch.float32, (T, H), dev, "lse"),
               _arg(ws, torch.uint8, (ws.numel(),), dev, "ws"), ws.numel(), _stream_on(stream, dev)),
            "dsa_mla_decode")
+
+
+def dsa_mla_decode_fp8kv(desc, q, kv8, out, ws, sm_scale, lse=None, stream=None):
+    """dsa_mla_decode over the FP8 latent cache ``kv8`` (uint8 [num_pages * 64, 656])."""
+    fn, dev, bf16 = lib().dsa_mla_decode_fp8kv, torch.cuda.current_device(), torch.bfloat16
+    T, H = desc.batch * desc.q_per_req, desc.num_heads
+    _check(fn(ctypes.byref(desc), _arg(q, bf16, (T, H, 576), dev, "q"),
+              _arg(kv8, torch.uint8, (desc.num_pages * PAGE_SIZE, 656), dev, "kv8"), sm_scale,
+              _arg(out, bf16, (T, H, 512), dev, "out"), _arg(lse, torch.float32, (T, H), dev, "lse"),
+              _arg(ws, torch.uint8, (ws.numel(),), dev, "ws"), ws.numel(), _stream_on(stream, dev)),
+           "dsa_mla_decode_fp8kv")
 
 
 def dsa_mla_prefill(q, kv, k_rope, cu_q, cu_k, out, max_q, sm_scale, causal=True, lse=None,

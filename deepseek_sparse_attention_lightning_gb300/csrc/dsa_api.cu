@@ -311,22 +311,39 @@ size_t dsa_mla_decode_workspace_bytes(const dsa_decode_desc* d) {
   return bytes;
 }
 
-dsa_status dsa_mla_decode(const dsa_decode_desc* d, const uint16_t* q, const uint16_t* kv,
-                          float sm_scale, uint16_t* out, float* lse, void* ws, size_t ws_bytes,
-                          void* stream) {
+namespace {
+
+// Dense attention over the bf16 cache kv, or over the FP8 cache kv8.
+dsa_status mla_dense(const dsa_decode_desc* d, const uint16_t* q, const uint16_t* kv,
+                     const uint8_t* kv8, float sm_scale, uint16_t* out, float* lse, void* ws,
+                     size_t ws_bytes, void* stream) {
   dsa_status st = check_dense_desc(d);
   if (st != DSA_OK) return st;
-  if (!q || !kv || !out || !aligned(q, 16) || !aligned(kv, 16) || !aligned(out, 16) ||
-      !aligned(lse, 4))
+  if (!q || (!kv && !kv8) || !out || !aligned(q, 16) || !aligned(kv, 16) || !aligned(kv8, 16) ||
+      !aligned(out, 16) || !aligned(lse, 4))
     return DSA_ERR_INVALID_ARG;
   if (!(sm_scale > 0.f) || !std::isfinite(sm_scale)) return DSA_ERR_INVALID_ARG;
   if (!ws || !aligned(ws, 256) || ws_bytes < dsa_mla_decode_workspace_bytes(d))
     return DSA_ERR_WORKSPACE;
   dsa::MlaDecodeLaunch a{};
-  a.q = q; a.kv = kv; a.seqlens = d->seqlens; a.page_table = d->page_table; a.out = out; a.lse = lse;
-  a.batch = d->batch; a.nq = d->q_per_req; a.heads = d->num_heads; a.max_pages = d->max_pages;
-  a.num_pages = d->num_pages; a.sm_scale = sm_scale;
+  a.q = q; a.kv = kv; a.kv8 = kv8; a.seqlens = d->seqlens; a.page_table = d->page_table; a.out = out;
+  a.lse = lse; a.batch = d->batch; a.nq = d->q_per_req; a.heads = d->num_heads;
+  a.max_pages = d->max_pages; a.num_pages = d->num_pages; a.sm_scale = sm_scale;
   return cuda_status(dsa::launch_mla_decode(a, ws, static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+dsa_status dsa_mla_decode(const dsa_decode_desc* d, const uint16_t* q, const uint16_t* kv,
+                          float sm_scale, uint16_t* out, float* lse, void* ws, size_t ws_bytes,
+                          void* stream) {
+  return mla_dense(d, q, kv, nullptr, sm_scale, out, lse, ws, ws_bytes, stream);
+}
+
+dsa_status dsa_mla_decode_fp8kv(const dsa_decode_desc* d, const uint16_t* q, const uint8_t* kv8,
+                                float sm_scale, uint16_t* out, float* lse, void* ws,
+                                size_t ws_bytes, void* stream) {
+  return mla_dense(d, q, nullptr, kv8, sm_scale, out, lse, ws, ws_bytes, stream);
 }
 
 dsa_status dsa_mla_prefill(int32_t batch, int32_t heads, int32_t total_q, int32_t total_k,

@@ -101,6 +101,7 @@ struct RmsNormLaunch {
 struct MlaDecodeLaunch {
   const uint16_t* q;             // [T][H][576] bf16
   const uint16_t* kv;            // [num_pages * 64][576] bf16
+  const uint8_t* kv8;            // non-null: the latent cache in FP8 rows of 656 bytes (kv unused)
   const int32_t* seqlens;
   const int32_t* page_table;
   uint16_t* out;                 // [T][H][512] bf16

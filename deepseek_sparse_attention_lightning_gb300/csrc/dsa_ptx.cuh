@@ -586,13 +586,22 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
-// Two fp32 operations in one instruction: (x, y) * m + a, and sums.
+// Two fp32 operations in one instruction: x * m + a, products and sums.
 __device__ __forceinline__ float2 fma2(float2 x, float2 m, float2 a) {
   float2 d;
   asm("{\n .reg .b64 p, q, r;\n mov.b64 p, {%2, %3};\n mov.b64 q, {%4, %5};\n mov.b64 r, {%6, %7};\n"
       " fma.rn.f32x2 p, p, q, r;\n mov.b64 {%0, %1}, p;\n}\n"
       : "=f"(d.x), "=f"(d.y)
       : "f"(x.x), "f"(x.y), "f"(m.x), "f"(m.y), "f"(a.x), "f"(a.y));
+  return d;
+}
+
+__device__ __forceinline__ float2 mul2(float2 x, float2 y) {
+  float2 d;
+  asm("{\n .reg .b64 p, q;\n mov.b64 p, {%2, %3};\n mov.b64 q, {%4, %5};\n"
+      " mul.rn.f32x2 p, p, q;\n mov.b64 {%0, %1}, p;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
   return d;
 }
 

@@ -48,9 +48,20 @@
 // the matrix pipe (as values and keys are); its sum is kept unrounded in fp32,
 // so the log-sum-exp has fp32 accuracy.
 //
+// FP8 latent rows (kFp8; 656 bytes: 512 E4M3 codes, the four 128-dim tiles'
+// scales, 64 rope dims in bf16): two more warpgroups take the place of the
+// copies.  One fetches its page's rows for K, the other both pages' half rows
+// for V, each a tile ahead in registers (a warp's eight-lane quarters hold
+// rows whose swizzled 16-byte pieces fall on distinct banks), multiply the
+// codes by their scale, round once to bf16 and write the layout that the MMAs
+// read.  The matrix work is the same; a page is 41 KB instead of 72.
+//
 // Rows of V that no query row sees (behind the request's end in its last page,
 // or a page whose id is out of range) are cleared in shared memory before P V:
 // their probabilities are zero, but stale cache memory may hold NaN.
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
 #include "dsa_ptx.cuh"
 #include "dsa_internal.h"
 
@@ -80,8 +91,13 @@ constexpr int kOffInfo = kOffBar + 16 * 8;
 constexpr int kSmemBytes = kOffInfo + 32 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory");
 constexpr int kColO = 0, kColS = 256, kTmemCols = 512;    // S: 2 x 64 columns
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kThreadsFp8 = 512;
 constexpr int kSoftWarps = 4;
+constexpr int kF8RowBytes = 656, kF8ScaleOff = 512, kF8RopeOff = 528;
+// FP8: registers a thread by warpgroup (launched with 128 each): copies and
+// MMAs, softmax, K, V.
+constexpr int kRegsMma = 80, kRegsSoft = 184, kRegsK = 128, kRegsV = 120;
+static_assert(kRegsMma + kRegsSoft + kRegsK + kRegsV <= 4 * 128, "registers");
 constexpr float kRaiseLog2 = 8.0f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -187,7 +203,52 @@ struct PageIds {
   }
 };
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+// 16 E4M3 codes times their scale, as bf16.
+__device__ __forceinline__ void dequant16(const uint4 raw, float scale, uint4& lo, uint4& hi) {
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  uint32_t o[8];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const __half2_raw h01 =
+        __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[q] & 0xFFFFu), __NV_E4M3);
+    const __half2_raw h23 =
+        __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[q] >> 16), __NV_E4M3);
+    const float2 f01 = mul2(__half22float2(__half2(h01)), make_float2(scale, scale));
+    const float2 f23 = mul2(__half22float2(__half2(h23)), make_float2(scale, scale));
+    o[2 * q] = pack_bf16x2(f01.x, f01.y);
+    o[2 * q + 1] = pack_bf16x2(f23.x, f23.y);
+  }
+  lo = make_uint4(o[0], o[1], o[2], o[3]);
+  hi = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+// Pages of a stretch's tiles, 16 tiles (32 ids) at a time and one batch ahead,
+// an id a lane.
+struct PageBatch {
+  PageIds ids;
+  int t0, now, next;     // first tile of the stretch; ids of this and the next 16 tiles
+  __device__ __forceinline__ PageBatch(const MlaDecodeLaunch& p, const Walk& wk, int lane)
+      : ids{p.page_table + static_cast<long long>(wk.req) * p.max_pages, (wk.len + kPage - 1) / kPage,
+            p.num_pages},
+        t0(wk.t0), now(0) {
+    next = ids.get(2 * t0 + lane);
+  }
+  // Before tile t's pages are asked for, t going up by one.
+  __device__ __forceinline__ bool advance(int t, int lane) {
+    if (((t - t0) & 15) != 0) return false;
+    now = next;
+    next = ids.get(2 * (t + 16) + lane);
+    return true;
+  }
+  // Page h of tile t or (ahead) of the tile after it.
+  __device__ __forceinline__ int page(int t, int h, bool ahead = false) const {
+    const int u = ((t - t0) & 15) + (ahead ? 1 : 0);
+    return __shfl_sync(0xffffffffu, u < 16 ? now : next, 2 * (u & 15) + h);
+  }
+};
+
+template <bool kFp8>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 : kThreads, 1)
     mla_decode_kernel(const __grid_constant__ CUtensorMap tmap_q,
                       const __grid_constant__ CUtensorMap tmap_k,
                       const __grid_constant__ CUtensorMap tmap_v, const MlaDecodeLaunch p) {
@@ -226,11 +287,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(DRAIN, 1);
     mbar_init(P_FULL, 2 * kSoftWarps);
     for (int g = 0; g < kKGroups; ++g) {
-      mbar_init(K_FULL(g), 1);
+      mbar_init(K_FULL(g), kFp8 ? 8 : 1);      // FP8: four warps of each CTA
       mbar_init(K_EMPTY(g), 1);
     }
     for (int h = 0; h < 2; ++h) {
-      mbar_init(V_FULL(h), 1);
+      mbar_init(V_FULL(h), kFp8 ? 4 : 1);
       mbar_init(V_EMPTY(h), 1);
       mbar_init(S_FULL(h), 1);
     }
@@ -271,29 +332,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   wk.t0 = static_cast<int>(wk.pos - (info[2] >> 11));
   wk.t1 = 0;
 
+  if (warp < 4) {
+  if constexpr (kFp8) setmaxnreg_dec<kRegsMma>();
   if (warp == 0) {
-    // ---------------------------------------------------- q and K copies
+    // -------------------------------------------- q and (bf16 rows) K copies
     const uint32_t q_full = mapa_shared(Q_FULL, 0), k_full0 = mapa_shared(K_FULL(0), 0);
     bool ok = true;
     int it = 0;
     while (ok && wk.next(p)) {
-      const PageIds ids{p.page_table + static_cast<long long>(wk.req) * p.max_pages,
-                        (wk.len + kPage - 1) / kPage, p.num_pages};
-      int pg = 0;
+      PageBatch pages(p, wk, lane);
       for (int t = wk.t0; ok && t < wk.t1; ++t, ++it) {
-        const int u = (t - wk.t0) & 15;
-        if (u == 0) {
-          pg = ids.get(2 * t + lane);
-          if (pg < 0) {
-            if (pg == PageIds::kBad) raise_error(kErrCheck);
-            pg = 0;
-          }
-        }
-        const int page = __shfl_sync(0xffffffffu, pg, 2 * u + rank);
+        if (pages.advance(t, lane) && pages.now == PageIds::kBad) raise_error(kErrCheck);
+        const int page = max(0, pages.page(t, rank));
 #pragma unroll
         for (int g = 0; g < kKGroups; ++g) {
           if (it >= 1 && ok && !mbar_wait(K_EMPTY(g), (it - 1) & 1)) ok = false;
-          if (ok && lane == 0) {
+          if (!kFp8 && ok && lane == 0) {
             if (rank == 0) mbar_expect_tx(K_FULL(g), 2 * kKGroupBytes);
             tma_load_3d_2cta(sbase + kOffK + g * kKGroupBytes, &tmap_k, 0, page * kPage, kGroupAtoms * g,
                              k_full0 + 8u * g);
@@ -310,20 +364,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
     if (!ok && lane == 0) raise_error(kErrTimeout);
-  } else if (warp == 2) {
+  } else if (!kFp8 && warp == 2) {
     // ---------------------------------------------------------- V copies
     bool ok = true;
     int it = 0;
     while (ok && wk.next(p)) {
-      const PageIds ids{p.page_table + static_cast<long long>(wk.req) * p.max_pages,
-                        (wk.len + kPage - 1) / kPage, p.num_pages};
-      int pg = 0;
+      PageBatch pages(p, wk, lane);
       for (int t = wk.t0; ok && t < wk.t1; ++t, ++it) {
-        const int u = (t - wk.t0) & 15;
-        if (u == 0) pg = max(0, ids.get(2 * t + lane));
+        pages.advance(t, lane);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int page = __shfl_sync(0xffffffffu, pg, 2 * u + h);
+          const int page = max(0, pages.page(t, h));
           if (it >= 1 && ok && !mbar_wait(V_EMPTY(h), (it - 1) & 1)) ok = false;
           if (ok && lane == 0) {
             // Output dims of P V's two MMAs: 256 n + 128 rank .. + 127.
@@ -417,8 +468,131 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_wait(DRAIN, 0);
     }
     __syncwarp();
-  } else if (warp >= 4) {
+  } else if (warp == 3 && mtile == 0) {
+    // Requests without tokens (no page of the line is theirs).
+    for (int r = group * 2 + static_cast<int>(rank); r < p.batch; r += 2 * p.groups) {
+      if (request_len(p, r) > 0) continue;
+      const long long row0 = static_cast<long long>(r) * rows_req;
+      uint4* dst = reinterpret_cast<uint4*>(p.out + row0 * kVDim);
+      for (long long e = lane; e < static_cast<long long>(rows_req) * (kVDim / 8); e += 32)
+        dst[e] = make_uint4(0u, 0u, 0u, 0u);
+      if (p.lse)
+        for (int e = lane; e < rows_req; e += 32) p.lse[row0 + e] = ninf;
+    }
+  }
+  } else if (kFp8 && warp >= 8) {
+    // ------------------------------------------- FP8 rows to bf16 operands
+    // Two threads a row (a: its even or odd 16-code chunks), one page's 64 rows
+    // at a time.  Eight consecutive lanes hold rows r, r + 1, r + 4, r + 5.
+    const int a = lane & 1;
+    const int row = ((warp & 3) << 4) | ((lane >> 1) & 1) | ((lane >> 1) & 4 ? 2 : 0) |
+                    (lane & 4) | ((lane >> 1) & 8);
+    const int swz = row & 7;
+    bool ok = true;
+    int it = 0;
+    auto row_of = [&](int page) {
+      return p.kv8 + (static_cast<long long>(max(0, page)) * kPage + row) * kF8RowBytes;
+    };
+    // Chunk c of the row (16 bf16 values: two 16-byte pieces) at `base`, atoms
+    // kAtom apart.
+    auto store = [&](uint8_t* base, int c, const uint4& lo, const uint4& hi) {
+      uint8_t* at = base + (c >> 2) * kAtom + row * 128;
+      const int piece = 2 * (c & 3);
+      *reinterpret_cast<uint4*>(at + ((piece ^ swz) << 4)) = lo;
+      *reinterpret_cast<uint4*>(at + (((piece + 1) ^ swz) << 4)) = hi;
+    };
+    if (warp < 12) {
+      setmaxnreg_dec<kRegsK>();
+      const uint32_t k_full0 = mapa_shared(K_FULL(0), 0);
+      while (ok && wk.next(p)) {
+        PageBatch pages(p, wk, lane);
+        uint4 raw[16], rope[4];
+        float4 sc;
+        auto fetch = [&](const uint8_t* src) {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) raw[k] = __ldg(reinterpret_cast<const uint4*>(src) + 2 * k + a);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            rope[k] = __ldg(reinterpret_cast<const uint4*>(src + kF8RopeOff) + 2 * k + a);
+          sc = __ldg(reinterpret_cast<const float4*>(src + kF8ScaleOff));
+        };
+        for (int t = wk.t0; ok && t < wk.t1; ++t, ++it) {
+          pages.advance(t, lane);
+          if (t == wk.t0) fetch(row_of(pages.page(t, rank)));
+          const uint8_t* nsrc = row_of(pages.page(t, rank, true));      // (behind the stretch: page 0)
+          const float4 nsc = __ldg(reinterpret_cast<const float4*>(nsrc + kF8ScaleOff));
+          const float scale[4] = {sc.x, sc.y, sc.z, sc.w};
+#pragma unroll
+          for (int g = 0; g < kKGroups; ++g) {
+            if (it >= 1 && ok && !mbar_wait(K_EMPTY(g), (it - 1) & 1)) ok = false;
+            uint8_t* dst = smem + kOffK;
+#pragma unroll
+            for (int k = 6 * g; k < (g < 2 ? 6 * g + 6 : 16); ++k) {
+              uint4 lo, hi;
+              dequant16(raw[k], scale[k >> 2], lo, hi);
+              raw[k] = __ldg(reinterpret_cast<const uint4*>(nsrc) + 2 * k + a);
+              store(dst, 2 * k + a, lo, hi);
+            }
+            if (g == kKGroups - 1) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                *reinterpret_cast<uint4*>(dst + 8 * kAtom + row * 128 + (((2 * k + a) ^ swz) << 4)) = rope[k];
+                rope[k] = __ldg(reinterpret_cast<const uint4*>(nsrc + kF8RopeOff) + 2 * k + a);
+              }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote_async(k_full0 + 8u * g);
+          }
+          sc = nsc;
+          ok = __all_sync(0xffffffffu, ok);
+        }
+      }
+    } else {
+      setmaxnreg_dec<kRegsV>();
+      // Output dims of P V's two MMAs: 256 n + 128 rank .. + 127, code tiles
+      // rank and 2 + rank.
+      const int off0 = 128 * static_cast<int>(rank), off1 = 256 + off0;
+      while (ok && wk.next(p)) {
+        PageBatch pages(p, wk, lane);
+        uint4 raw[16];
+        float sc[4];
+        auto fetch_page = [&](int h, const uint8_t* src) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            raw[8 * h + k] = __ldg(reinterpret_cast<const uint4*>(src + (k < 4 ? off0 : off1)) + 2 * (k & 3) + a);
+          sc[2 * h] = __ldg(reinterpret_cast<const float*>(src + kF8ScaleOff) + rank);
+          sc[2 * h + 1] = __ldg(reinterpret_cast<const float*>(src + kF8ScaleOff) + 2 + rank);
+        };
+        for (int t = wk.t0; ok && t < wk.t1; ++t, ++it) {
+          pages.advance(t, lane);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int page = pages.page(t, h), npage = pages.page(t, h, true);
+            if (t == wk.t0) fetch_page(h, row_of(page));
+            // (Rows that no query sees are zero, whatever the cache holds.)
+            const bool live = page >= 0 && t * kTileKeys + kPage * h + row < wk.len;
+            if (it >= 1 && ok && !mbar_wait(V_EMPTY(h), (it - 1) & 1)) ok = false;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              uint4 lo, hi;
+              dequant16(raw[8 * h + k], sc[2 * h + (k >> 2)], lo, hi);
+              if (!live) lo = hi = make_uint4(0u, 0u, 0u, 0u);
+              store(smem + kOffV + h * kVBytes, 2 * k + a, lo, hi);
+            }
+            fetch_page(h, row_of(npage));
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(V_FULL(h));
+          }
+          ok = __all_sync(0xffffffffu, ok);
+        }
+      }
+    }
+    if (!ok && lane == 0) raise_error(kErrTimeout);
+  } else {
     // ---------------------------------------------- softmax and epilogue
+    if constexpr (kFp8) setmaxnreg_inc<kRegsSoft>();
     const int tid = threadIdx.x - 128;             // = TMEM lane; half: page of the tile, half of O's dims
     const int w4 = warp & 3;
     const int row = tid & 63, half = tid >> 6;
@@ -432,14 +606,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     bool ok = true;
     int it = 0;
     while (wk.next(p)) {
-      const PageIds ids{p.page_table + static_cast<long long>(wk.req) * p.max_pages,
-                        (wk.len + kPage - 1) / kPage, p.num_pages};
+      PageBatch pages(p, wk, lane);
       const int vis = live ? wk.len - (p.nq - 1 - qi) : 0;
       float mrun = ninf, lrun = 0.f;      // maximum and sum (this thread's keys) in the exp2 domain
       uint32_t good = 0;                  // validity of the next 32 page ids
       for (int t = wk.t0; t < wk.t1; ++t, ++it) {
         const int b = it & 1, u = (t - wk.t0) & 15;
-        if (u == 0) good = __ballot_sync(0xffffffffu, ids.get(2 * t + lane) >= 0);
+        if (pages.advance(t, lane)) good = __ballot_sync(0xffffffffu, pages.now >= 0);
         const uint32_t ok2 = good >> (2 * u);          // bit h: page h of the tile can be read
         if (ok && !mbar_wait(S_FULL(b), (it >> 1) & 1)) ok = false;
         tc_fence_after();
@@ -506,7 +679,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (ok && !mbar_wait(V_FULL(h), it & 1)) ok = false;
           // Rows of V behind every query's view are cleared.
           const int vlive = ((ok2 >> h) & 1u) ? wk.len - t * kTileKeys - kPage * h : 0;
-          if (vlive < kPage) {
+          if (!kFp8 && vlive < kPage) {
             uint4* v = reinterpret_cast<uint4*>(smem + kOffV + h * kVBytes);
             for (int e = tid; e < kVBytes / 16; e += 128)
               if (((e >> 3) & (kPage - 1)) >= vlive) v[e] = make_uint4(0u, 0u, 0u, 0u);
@@ -563,17 +736,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive_remote_async(o_free);
     }
     if (!ok && lane == 0) raise_error(kErrTimeout);
-  } else if (mtile == 0) {
-    // Warp 3: requests without tokens (no page of the line is theirs).
-    for (int r = group * 2 + static_cast<int>(rank); r < p.batch; r += 2 * p.groups) {
-      if (request_len(p, r) > 0) continue;
-      const long long row0 = static_cast<long long>(r) * rows_req;
-      uint4* dst = reinterpret_cast<uint4*>(p.out + row0 * kVDim);
-      for (long long e = lane; e < static_cast<long long>(rows_req) * (kVDim / 8); e += 32)
-        dst[e] = make_uint4(0u, 0u, 0u, 0u);
-      if (p.lse)
-        for (int e = lane; e < rows_req; e += 32) p.lse[row0 + e] = ninf;
-    }
   }
   __syncthreads();
   grid_dep_launch();
@@ -702,18 +864,21 @@ cudaError_t launch_mla_decode(MlaDecodeLaunch a, void* ws, cudaStream_t s) {
   const uint64_t qdims[3] = {64, qrows, kAtoms}, cdims[3] = {64, crows, kAtoms};
   const uint32_t qbox[3] = {64, kRowsCta, kAtoms}, kbox[3] = {64, kPage, kGroupAtoms},
                  vbox[3] = {64, kPage, 2};
+  const bool fp8 = a.kv8 != nullptr;
   CUtensorMap tq, tk, tv;
   if (!encode_tmap_nd(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, 3, qdims, strides, qbox,
-                      CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode_tmap_nd(&tk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.kv, 3, cdims, strides, kbox,
-                      CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode_tmap_nd(&tv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.kv, 3, cdims, strides, vbox,
                       CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(mla_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       kSmemBytes);
+  tk = tv = tq;      // FP8 rows are not copied by maps
+  if (!fp8 && (!encode_tmap_nd(&tk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.kv, 3, cdims, strides, kbox,
+                               CU_TENSOR_MAP_SWIZZLE_128B) ||
+               !encode_tmap_nd(&tv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.kv, 3, cdims, strides, vbox,
+                               CU_TENSOR_MAP_SWIZZLE_128B)))
+    return cudaErrorInvalidValue;
+  auto kern = fp8 ? mla_decode_kernel<true> : mla_decode_kernel<false>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
-  e = launch_kernel(mla_decode_kernel, dim3(2 * a.groups * a.row_tiles), dim3(kThreads), kSmemBytes, s,
+  e = launch_kernel(kern, dim3(2 * a.groups * a.row_tiles), dim3(fp8 ? kThreadsFp8 : kThreads), kSmemBytes, s,
                     false, 1, tq, tk, tv, a);
   if (e != cudaSuccess || a.groups == 1) return e;
   const int chunks = (a.nq * a.heads + kMergeRows - 1) / kMergeRows;

@@ -375,7 +375,17 @@ dsa_status dsa_mla_decode(const dsa_decode_desc* desc, const uint16_t* q, const 
                           float sm_scale, uint16_t* out, float* lse, void* ws, size_t ws_bytes,
                           void* stream);
 
-/* Workspace bytes of dsa_mla_decode (0 for a descriptor it rejects). */
+/*
+ * dsa_mla_decode over the FP8 latent cache kv8 [num_pages * 64, 656] (rows of
+ * dsa_latent_to_fp8; 16-byte aligned): each value is its code times its scale,
+ * rounded once to bf16 for the tensor cores.  Other arguments, outputs,
+ * workspace and errors as there.
+ */
+dsa_status dsa_mla_decode_fp8kv(const dsa_decode_desc* desc, const uint16_t* q, const uint8_t* kv8,
+                                float sm_scale, uint16_t* out, float* lse, void* ws,
+                                size_t ws_bytes, void* stream);
+
+/* Workspace bytes of dsa_mla_decode and dsa_mla_decode_fp8kv (0 for a descriptor it rejects). */
 size_t dsa_mla_decode_workspace_bytes(const dsa_decode_desc* desc);
 
 /*

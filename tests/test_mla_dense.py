@@ -139,3 +139,45 @@ def test_matches_formula(L, lens, nq, H):
     _check(c, out, lse)
     again, _ = _run(c, lse=False)
     assert torch.equal(out, again)
+
+
+def _fp8(c):
+    """The case with its cache in FP8 rows; unused rows stay NaN codes with NaN scales."""
+    kv8 = torch.full((c["kv"].shape[0], 656), 0xFF, dtype=torch.uint8, device="cuda")
+    used = ~torch.isnan(c["kv"][:, 0])
+    rows = torch.empty((int(used.sum()), 656), dtype=torch.uint8, device="cuda")
+    api.dsa_latent_to_fp8(c["kv"][used].contiguous(), rows)
+    kv8[used] = rows
+    table, seq = c["keep"][1].cpu(), c["lens"]
+    keys = []
+    for r, n in enumerate(seq):
+        pos = torch.arange(n)
+        x = kv8[(table[r, pos // 64].long() * 64 + pos % 64).cuda()]
+        sc = x[:, 512:528].contiguous().view(torch.float32).double().repeat_interleave(128, dim=1)
+        codes = x[:, :512].contiguous().view(torch.float8_e4m3fn).double()
+        keys.append(torch.cat([codes * sc, x[:, 528:].contiguous().view(torch.bfloat16).double()], dim=1))
+    return {**c, "keys": keys}, kv8
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens,nq,H", CASES)
+def test_fp8_rows_match_formula(L, lens, nq, H):
+    c, kv8 = _fp8(_case(lens, nq, H, seed=len(lens) * 100 + nq * 10 + H))
+    out, lse = _run(c, call=api.dsa_mla_decode_fp8kv, kv=kv8)
+    assert api.dsa_get_device_error() == 0
+    _check(c, out, lse, rel_key=2.0 ** -8)
+    again, _ = _run(c, lse=False, call=api.dsa_mla_decode_fp8kv, kv=kv8)
+    assert torch.equal(out, again)
+
+
+@pytest.mark.gpu
+def test_large_scores_raise_the_maximum(L):
+    """Keys that grow along the request: the running maximum rises by far more than 2^8 several times."""
+    c = _case([1500], 1, 128, seed=3)
+    ramp = (1.0 + torch.arange(1500, device="cuda") / 100.0)[:, None]
+    c["keys"][0].copy_((c["keys"][0].float() * ramp).to(torch.bfloat16))
+    table = c["keep"][1].cpu()
+    pos = torch.arange(1500)
+    c["kv"][(table[0, pos // 64].long() * 64 + pos % 64).cuda()] = c["keys"][0]
+    out, lse = _run(c)
+    _check(c, out, lse)

@@ -50,11 +50,13 @@
 //
 // FP8 latent rows (kFp8; 656 bytes: 512 E4M3 codes, the four 128-dim tiles'
 // scales, 64 rope dims in bf16): two more warpgroups take the place of the
-// copies.  One fetches its page's rows for K, the other both pages' half rows
-// for V, each a tile ahead in registers (a warp's eight-lane quarters hold
-// rows whose swizzled 16-byte pieces fall on distinct banks), multiply the
-// codes by their scale, round once to bf16 and write the layout that the MMAs
-// read.  The matrix work is the same; a page is 41 KB instead of 72.
+// copies (but for the rope dims).  One fetches its page's codes for K, the other
+// both pages' half rows for V, each a tile ahead in registers, multiply them by
+// their scale, round once to bf16 and write the layout that the MMAs read.  A
+// warp reads 256 consecutive bytes of two rows at a time: the load path serves
+// a line of 128 bytes a cycle, and with 32 bytes of 16 rows a load it, not the
+// arithmetic, took 5 us a tile (decode_varlen 419 us).  The matrix work is the
+// same as for bf16 rows; K's three groups are dims 0-255, 256-511 and rope.
 //
 // Rows of V that no query row sees (behind the request's end in its last page,
 // or a page whose id is out of range) are cleared in shared memory before P V:
@@ -78,6 +80,11 @@ constexpr int kTileKeys = 2 * kPage;
 constexpr int kAtom = 64 * 128;                           // 64 rows x 64 dims of q, K, V or P: 8 KB
 constexpr int kKGroups = 3, kGroupAtoms = kAtoms / kKGroups;
 constexpr int kKGroupBytes = kGroupAtoms * kAtom;         // 24 KB
+// First atom of K's group g.
+template <bool kFp8>
+__host__ __device__ constexpr int group_atom(int g) {
+  return kFp8 ? (g < 2 ? 4 * g : 8 + (g - 2)) : kGroupAtoms * g;
+}
 constexpr int kVBytes = 4 * kAtom;                        // one page, this CTA's 256 value dims
 constexpr int kPBytes = 2 * kAtom;
 static_assert(kRowsCta == 64 && kPage == 64, "atoms of 64 rows");
@@ -287,7 +294,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
     mbar_init(DRAIN, 1);
     mbar_init(P_FULL, 2 * kSoftWarps);
     for (int g = 0; g < kKGroups; ++g) {
-      mbar_init(K_FULL(g), kFp8 ? 8 : 1);      // FP8: four warps of each CTA
+      mbar_init(K_FULL(g), kFp8 && g < 2 ? 8 : 1);      // FP8 codes: four warps of each CTA
       mbar_init(K_EMPTY(g), 1);
     }
     for (int h = 0; h < 2; ++h) {
@@ -351,6 +358,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
             if (rank == 0) mbar_expect_tx(K_FULL(g), 2 * kKGroupBytes);
             tma_load_3d_2cta(sbase + kOffK + g * kKGroupBytes, &tmap_k, 0, page * kPage, kGroupAtoms * g,
                              k_full0 + 8u * g);
+          }
+          if (kFp8 && g == kKGroups - 1 && ok && lane == 0) {
+            if (rank == 0) mbar_expect_tx(K_FULL(g), 2 * kAtom);
+            tma_load_3d_2cta(sbase + kOffK + 8 * kAtom, &tmap_k, kF8RopeOff, page * kPage, 0, k_full0 + 8u * g);
           }
           // q of the stretch (Q K^T of the tile before is done with its last
           // group).
@@ -445,7 +456,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
             if (!(ok = ok && warp_wait(K_FULL(g), it & 1))) break;
             tc_fence_after();
 #pragma unroll
-            for (int a = kGroupAtoms * g; a < kGroupAtoms * (g + 1); ++a)
+            for (int a = group_atom<kFp8>(g); a < group_atom<kFp8>(g + 1); ++a)
 #pragma unroll
               for (int j = 0; j < 4; ++j)
                 mma_f16_ss_2cta(tmem + kColS + 64 * (it & 1),
@@ -482,105 +493,126 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
   }
   } else if (kFp8 && warp >= 8) {
     // ------------------------------------------- FP8 rows to bf16 operands
-    // Two threads a row (a: its even or odd 16-code chunks), one page's 64 rows
-    // at a time.  Eight consecutive lanes hold rows r, r + 1, r + 4, r + 5.
-    const int a = lane & 1;
-    const int row = ((warp & 3) << 4) | ((lane >> 1) & 1) | ((lane >> 1) & 4 ? 2 : 0) |
-                    (lane & 4) | ((lane >> 1) & 8);
-    const int swz = row & 7;
+    // A warp has 16 rows of a page and takes two at a time: lane = row r2 of the
+    // two, and 16-code chunk c of 256 bytes of it.  Eight neighbouring lanes
+    // hold an atom's four chunks of both rows: whose swizzled pieces fall on
+    // distinct banks.
+    const int r2 = (lane >> 2) & 1, c = (lane & 3) | ((lane >> 3) << 2), row0 = (warp & 3) * 16;
     bool ok = true;
     int it = 0;
-    auto row_of = [&](int page) {
-      return p.kv8 + (static_cast<long long>(max(0, page)) * kPage + row) * kF8RowBytes;
+    auto rows_of = [&](int page) {
+      return p.kv8 + (static_cast<long long>(max(0, page)) * kPage + row0 + r2) * kF8RowBytes;
     };
-    // Chunk c of the row (16 bf16 values: two 16-byte pieces) at `base`, atoms
-    // kAtom apart.
-    auto store = [&](uint8_t* base, int c, const uint4& lo, const uint4& hi) {
-      uint8_t* at = base + (c >> 2) * kAtom + row * 128;
-      const int piece = 2 * (c & 3);
-      *reinterpret_cast<uint4*>(at + ((piece ^ swz) << 4)) = lo;
-      *reinterpret_cast<uint4*>(at + (((piece + 1) ^ swz) << 4)) = hi;
+    // The chunk's 16 bf16 values: pair k's row at `base` (atoms kAtom apart).
+    const int row_off = (c >> 2) * kAtom + (row0 + r2) * 128;
+    auto store = [&](uint8_t* base, int k, const uint4& lo, const uint4& hi) {
+      uint8_t* at = base + row_off + 256 * k;
+      const int piece = (2 * (c & 3)) ^ ((2 * k + r2) & 7);
+      *reinterpret_cast<uint4*>(at + (piece << 4)) = lo;
+      *reinterpret_cast<uint4*>(at + ((piece ^ 1) << 4)) = hi;
     };
     if (warp < 12) {
       setmaxnreg_dec<kRegsK>();
       const uint32_t k_full0 = mapa_shared(K_FULL(0), 0);
       while (ok && wk.next(p)) {
         PageBatch pages(p, wk, lane);
-        uint4 raw[16], rope[4];
-        float4 sc;
-        auto fetch = [&](const uint8_t* src) {
-#pragma unroll
-          for (int k = 0; k < 16; ++k) raw[k] = __ldg(reinterpret_cast<const uint4*>(src) + 2 * k + a);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            rope[k] = __ldg(reinterpret_cast<const uint4*>(src + kF8RopeOff) + 2 * k + a);
-          sc = __ldg(reinterpret_cast<const float4*>(src + kF8ScaleOff));
+        uint4 raw[16];       // 8 row pairs of dims 0-255, then of 256-511
+        float sc[2];         // scales of row pairs 0-3 / 4-7: lane = row r2, pair, tile
+        const int sc_row = (lane >> 3) * 2, sc_tile = lane & 3;
+        auto code_at = [&](const uint8_t* rows, int k) {
+          return __ldg(reinterpret_cast<const uint4*>(rows + 2 * (k & 7) * kF8RowBytes + 256 * (k >> 3)) + c);
+        };
+        auto scale_at = [&](const uint8_t* rows, int half) {
+          return __ldg(reinterpret_cast<const float*>(rows + (8 * half + sc_row) * kF8RowBytes + kF8ScaleOff) +
+                       sc_tile);
         };
         for (int t = wk.t0; ok && t < wk.t1; ++t, ++it) {
           pages.advance(t, lane);
-          if (t == wk.t0) fetch(row_of(pages.page(t, rank)));
-          const uint8_t* nsrc = row_of(pages.page(t, rank, true));      // (behind the stretch: page 0)
-          const float4 nsc = __ldg(reinterpret_cast<const float4*>(nsrc + kF8ScaleOff));
-          const float scale[4] = {sc.x, sc.y, sc.z, sc.w};
+          if (t == wk.t0) {
+            const uint8_t* rows = rows_of(pages.page(t, rank));
 #pragma unroll
-          for (int g = 0; g < kKGroups; ++g) {
+            for (int k = 0; k < 16; ++k) raw[k] = code_at(rows, k);
+            sc[0] = scale_at(rows, 0);
+            sc[1] = scale_at(rows, 1);
+          }
+          // The next tile's page (behind the stretch: page 0) is fetched as this
+          // one is used up.
+          const uint8_t* ahead = rows_of(pages.page(t, rank, true));
+          const float nsc0 = scale_at(ahead, 0), nsc1 = scale_at(ahead, 1);
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            float scale[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              scale[k] = __shfl_sync(0xffffffffu, sc[k >> 2], (k & 3) * 8 + r2 * 4 + 2 * g + (c >> 3));
             if (it >= 1 && ok && !mbar_wait(K_EMPTY(g), (it - 1) & 1)) ok = false;
-            uint8_t* dst = smem + kOffK;
 #pragma unroll
-            for (int k = 6 * g; k < (g < 2 ? 6 * g + 6 : 16); ++k) {
+            for (int k = 0; k < 8; ++k) {
               uint4 lo, hi;
-              dequant16(raw[k], scale[k >> 2], lo, hi);
-              raw[k] = __ldg(reinterpret_cast<const uint4*>(nsrc) + 2 * k + a);
-              store(dst, 2 * k + a, lo, hi);
-            }
-            if (g == kKGroups - 1) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                *reinterpret_cast<uint4*>(dst + 8 * kAtom + row * 128 + (((2 * k + a) ^ swz) << 4)) = rope[k];
-                rope[k] = __ldg(reinterpret_cast<const uint4*>(nsrc + kF8RopeOff) + 2 * k + a);
-              }
+              dequant16(raw[8 * g + k], scale[k], lo, hi);
+              raw[8 * g + k] = code_at(ahead, 8 * g + k);
+              store(smem + kOffK + 4 * g * kAtom, k, lo, hi);
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive_remote_async(k_full0 + 8u * g);
           }
-          sc = nsc;
+          sc[0] = nsc0;
+          sc[1] = nsc1;
           ok = __all_sync(0xffffffffu, ok);
         }
       }
     } else {
       setmaxnreg_dec<kRegsV>();
       // Output dims of P V's two MMAs: 256 n + 128 rank .. + 127, code tiles
-      // rank and 2 + rank.
-      const int off0 = 128 * static_cast<int>(rank), off1 = 256 + off0;
+      // rank (chunks c < 8) and 2 + rank.
+      const int off = 128 * static_cast<int>(rank) + (c < 8 ? 0 : 256) + (c & 7) * 16;
       while (ok && wk.next(p)) {
         PageBatch pages(p, wk, lane);
-        uint4 raw[16];
-        float sc[4];
-        auto fetch_page = [&](int h, const uint8_t* src) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            raw[8 * h + k] = __ldg(reinterpret_cast<const uint4*>(src + (k < 4 ? off0 : off1)) + 2 * (k & 3) + a);
-          sc[2 * h] = __ldg(reinterpret_cast<const float*>(src + kF8ScaleOff) + rank);
-          sc[2 * h + 1] = __ldg(reinterpret_cast<const float*>(src + kF8ScaleOff) + 2 + rank);
+        uint4 raw[16];       // 8 row pairs of either page
+        float sc[2];         // scales of a page's 16 rows: lane = row r2, tile, pair
+        const int sc_row = ((lane & 1) | ((lane >> 3) << 1)) * 2, sc_tile = rank + (lane & 2);
+        // Rows that no query sees are zero, whatever the cache holds: they are
+        // not fetched.  (live: rows of this warp's 16, from this lane's first.)
+        auto code_at = [&](const uint8_t* rows, int k, int live) {
+          return 2 * k < live ? __ldg(reinterpret_cast<const uint4*>(rows + 2 * k * kF8RowBytes + off))
+                              : make_uint4(0u, 0u, 0u, 0u);
+        };
+        auto scale_at = [&](const uint8_t* rows, int live) {
+          return sc_row < live ? __ldg(reinterpret_cast<const float*>(rows + sc_row * kF8RowBytes + kF8ScaleOff) +
+                                       sc_tile)
+                               : 0.f;
+        };
+        auto live_of = [&](int t, int h, int page) {
+          return page >= 0 ? wk.len - t * kTileKeys - kPage * h - row0 - r2 : 0;
         };
         for (int t = wk.t0; ok && t < wk.t1; ++t, ++it) {
           pages.advance(t, lane);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const int page = pages.page(t, h), npage = pages.page(t, h, true);
-            if (t == wk.t0) fetch_page(h, row_of(page));
-            // (Rows that no query sees are zero, whatever the cache holds.)
-            const bool live = page >= 0 && t * kTileKeys + kPage * h + row < wk.len;
+            if (t == wk.t0) {
+              const int page = pages.page(t, h), live = live_of(t, h, page);
+              const uint8_t* rows = rows_of(page);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) raw[8 * h + k] = code_at(rows, k, live);
+              sc[h] = scale_at(rows, live);
+            }
+            const int page = pages.page(t, h, true), live = live_of(t + 1, h, page);
+            const uint8_t* ahead = rows_of(page);
+            const float nsc = scale_at(ahead, live);
+            float scale[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              scale[k] = __shfl_sync(0xffffffffu, sc[h], ((k >> 1) << 3) | (r2 << 2) | ((c >> 3) << 1) | (k & 1));
             if (it >= 1 && ok && !mbar_wait(V_EMPTY(h), (it - 1) & 1)) ok = false;
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
               uint4 lo, hi;
-              dequant16(raw[8 * h + k], sc[2 * h + (k >> 2)], lo, hi);
-              if (!live) lo = hi = make_uint4(0u, 0u, 0u, 0u);
-              store(smem + kOffV + h * kVBytes, 2 * k + a, lo, hi);
+              dequant16(raw[8 * h + k], scale[k], lo, hi);
+              raw[8 * h + k] = code_at(ahead, k, live);
+              store(smem + kOffV + h * kVBytes, k, lo, hi);
             }
-            fetch_page(h, row_of(npage));
+            sc[h] = nsc;
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(V_FULL(h));
@@ -869,12 +901,20 @@ cudaError_t launch_mla_decode(MlaDecodeLaunch a, void* ws, cudaStream_t s) {
   if (!encode_tmap_nd(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, 3, qdims, strides, qbox,
                       CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
-  tk = tv = tq;      // FP8 rows are not copied by maps
-  if (!fp8 && (!encode_tmap_nd(&tk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.kv, 3, cdims, strides, kbox,
-                               CU_TENSOR_MAP_SWIZZLE_128B) ||
-               !encode_tmap_nd(&tv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.kv, 3, cdims, strides, vbox,
-                               CU_TENSOR_MAP_SWIZZLE_128B)))
+  if (fp8) {
+    // The rope dims of the rows as bytes, laid out like a bf16 atom.
+    const uint64_t rdims[3] = {kF8RowBytes, crows, 1}, rstr[2] = {kF8RowBytes, crows * kF8RowBytes};
+    const uint32_t rbox[3] = {128, kPage, 1};
+    if (!encode_tmap_nd(&tk, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.kv8, 3, rdims, rstr, rbox,
+                        CU_TENSOR_MAP_SWIZZLE_128B))
+      return cudaErrorInvalidValue;
+    tv = tk;
+  } else if (!encode_tmap_nd(&tk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.kv, 3, cdims, strides, kbox,
+                             CU_TENSOR_MAP_SWIZZLE_128B) ||
+             !encode_tmap_nd(&tv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.kv, 3, cdims, strides, vbox,
+                             CU_TENSOR_MAP_SWIZZLE_128B)) {
     return cudaErrorInvalidValue;
+  }
   auto kern = fp8 ? mla_decode_kernel<true> : mla_decode_kernel<false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;

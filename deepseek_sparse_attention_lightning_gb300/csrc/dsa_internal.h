@@ -107,7 +107,8 @@ struct MlaDecodeLaunch {
   uint16_t* out;                 // [T][H][512] bf16
   float* lse;                    // [T][H] or nullptr
   float* part_o;                 // set by launch_mla_decode: partial outputs and
-  float* part_lse;               //   their log-sum-exps, in the workspace
+  float* part_lse;               //   their log-sum-exps, in the workspace, and for
+  int2* joins;                   //   each group the request joined from it on
   int batch, nq, heads, max_pages, num_pages;
   int row_tiles, groups, min_tiles;   // set by launch_mla_decode
   float sm_scale;

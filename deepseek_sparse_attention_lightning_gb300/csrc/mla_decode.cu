@@ -258,7 +258,9 @@ template <bool kFp8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 : kThreads, 1)
     mla_decode_kernel(const __grid_constant__ CUtensorMap tmap_q,
                       const __grid_constant__ CUtensorMap tmap_k,
-                      const __grid_constant__ CUtensorMap tmap_v, const MlaDecodeLaunch p) {
+                      const __grid_constant__ CUtensorMap tmap_v,
+                      const __grid_constant__ CUtensorMap tmap_out,
+                      const __grid_constant__ CUtensorMap tmap_part, const MlaDecodeLaunch p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -319,6 +321,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
       lo = cut(ln, group);
       hi = cut(ln, group + 1);
       if (hi > lo) locate(p, lo, lane, req, first);
+    }
+    // What the merge has to join: the request that this group's first cut falls
+    // into, if it is the first cut inside that request, and its last group.
+    if (mtile == 0 && rank == 0 && lane == 0) {
+      int2 join = make_int2(-1, 0);
+      if (group > 0 && hi > lo && lo > first && cut(ln, group - 1) <= first) {
+        const long long end = first + tiles_of(request_len(p, req));
+        join = make_int2(req, static_cast<int>((end * ln.groups - 1) / ln.total));
+      }
+      p.joins[group] = join;
     }
     if (lane == 0) {
       info[0] = lo;
@@ -733,30 +745,79 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
       const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
       const float lse = l > 0.f || l != l ? (mrun + log2f(l)) * kLn2 : ninf;
       const bool whole = wk.t0 == 0 && wk.t1 == wk.nt;
+      const bool whole_warp = (rrow | 31) < rows_req;      // (rrow - lane is a multiple of 32)
       const long long grow = static_cast<long long>(wk.req) * rows_req + rrow;
       const long long slot = (static_cast<long long>(worker) * 2 + (wk.t0 > 0 ? 0 : 1)) * kRowTile +
                              kRowsCta * static_cast<int>(rank) + row;
+      if (whole_warp) {
+        // 32 rows at once: staged in this warp's part of the P tile (128B
+        // swizzled, so that eight rows' 16-byte pieces fall on distinct banks)
+        // and written by a tensor store a chunk of 128 bytes a row.  Stored
+        // from registers, every instruction touches 32 lines: 4 us for a
+        // stretch's 64 x 512 floats.
+        uint8_t* stage = smem + kOffP + half * kAtom + (row & 32) * 128;
+        const uint32_t stage_s = smem_u32(stage);
+        const int row_w = static_cast<int>((whole ? grow : slot) - lane);
 #pragma unroll 1
-      for (int c = 0; c < 8; ++c) {
-        uint32_t o[32];
-        tmem_ld32(tmem + lanebase + kColO + 32 * c, o);
-        const int dim = 256 * (c >> 2) + 128 * half + 32 * (c & 3);
-        if (!live) continue;
-        if (whole) {
-          uint4* dst = reinterpret_cast<uint4*>(p.out + grow * kVDim + dim);
+        for (int c = 0; c < 8; ++c) {
+          uint32_t o[32];
+          tmem_ld32(tmem + lanebase + kColO + 32 * c, o);
+          const bool start = !whole || (c & 1) == 0, end = !whole || (c & 1) == 1;
+          if (start) {
+            if (lane == 0) bulk_wait_read_all();
+            __syncwarp();
+          }
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            dst[e] = make_uint4(
-                pack_bf16x2(__uint_as_float(o[8 * e]) * inv, __uint_as_float(o[8 * e + 1]) * inv),
-                pack_bf16x2(__uint_as_float(o[8 * e + 2]) * inv, __uint_as_float(o[8 * e + 3]) * inv),
-                pack_bf16x2(__uint_as_float(o[8 * e + 4]) * inv, __uint_as_float(o[8 * e + 5]) * inv),
-                pack_bf16x2(__uint_as_float(o[8 * e + 6]) * inv, __uint_as_float(o[8 * e + 7]) * inv));
-        } else {
-          float4* dst = reinterpret_cast<float4*>(p.part_o + slot * kVDim + dim);
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
+          if (whole) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            dst[e] = make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
-                                 __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
+            for (int e = 0; e < 4; ++e)
+              *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * (c & 1) + e) ^ (lane & 7)) << 4)) =
+                  make_uint4(pack_bf16x2(__uint_as_float(o[8 * e]), __uint_as_float(o[8 * e + 1])),
+                             pack_bf16x2(__uint_as_float(o[8 * e + 2]), __uint_as_float(o[8 * e + 3])),
+                             pack_bf16x2(__uint_as_float(o[8 * e + 4]), __uint_as_float(o[8 * e + 5])),
+                             pack_bf16x2(__uint_as_float(o[8 * e + 6]), __uint_as_float(o[8 * e + 7])));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              *reinterpret_cast<uint4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) =
+                  make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          }
+          if (end) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              const int dim = 256 * (c >> 2) + 128 * half + (whole ? 64 * ((c >> 1) & 1) : 32 * (c & 3));
+              tma_store_2d(whole ? &tmap_out : &tmap_part, stage_s, dim, row_w);
+              bulk_commit();
+            }
+          }
+        }
+        if (lane == 0) bulk_wait_read_all();      // before the next P is written there
+        __syncwarp();
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) {
+          uint32_t o[32];
+          tmem_ld32(tmem + lanebase + kColO + 32 * c, o);
+          const int dim = 256 * (c >> 2) + 128 * half + 32 * (c & 3);
+          if (!live) continue;
+          if (whole) {
+            uint4* dst = reinterpret_cast<uint4*>(p.out + grow * kVDim + dim);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              dst[e] = make_uint4(
+                  pack_bf16x2(__uint_as_float(o[8 * e]) * inv, __uint_as_float(o[8 * e + 1]) * inv),
+                  pack_bf16x2(__uint_as_float(o[8 * e + 2]) * inv, __uint_as_float(o[8 * e + 3]) * inv),
+                  pack_bf16x2(__uint_as_float(o[8 * e + 4]) * inv, __uint_as_float(o[8 * e + 5]) * inv),
+                  pack_bf16x2(__uint_as_float(o[8 * e + 6]) * inv, __uint_as_float(o[8 * e + 7]) * inv));
+          } else {
+            float4* dst = reinterpret_cast<float4*>(p.part_o + slot * kVDim + dim);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              dst[e] = make_float4(__uint_as_float(o[4 * e]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
+                                   __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
+          }
         }
       }
       if (live && half == 0) {
@@ -767,6 +828,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
       __syncwarp();
       if (lane == 0) mbar_arrive_remote_async(o_free);
     }
+    if (lane == 0) bulk_wait_all();      // the stores are done before the CTA ends
     if (!ok && lane == 0) raise_error(kErrTimeout);
   }
   __syncthreads();
@@ -787,87 +849,69 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
 #undef P_FULL
 }
 
-// Joins the partials of a request that spans groups.  Block (i, c): cut i + 1
-// of the line, rows kMergeRows * c .. of the request it falls into; the block
-// works if that cut is the first one inside the request.  The request's first
-// part is slot 1 of its group (a stretch from the request's start), the others
-// slot 0 of theirs.
-constexpr int kMergeRows = 2;
+// Joins the partials of a request that spans groups.  Block (i, c): rows
+// kMergeRows * c .. of the request whose first cut begins group i + 1, if it is
+// one (the attention kernel wrote that down: looking it up again in every block
+// made the merge 21 us of 80).  The request's first part is slot 1 of its group
+// (a stretch from the request's start), the others slot 0 of theirs.
+constexpr int kMergeRows = 1;
 constexpr int kMergeThreads = kMergeRows * (kVDim / 4);
+constexpr int kMergeBatch = 8;      // parts in flight
 
 __global__ void __launch_bounds__(kMergeThreads) mla_merge_kernel(const MlaDecodeLaunch p) {
-  __shared__ int s_req, s_last;
-  const int i = blockIdx.x + 1;
-  if (threadIdx.x < 32) {
-    const int lane = threadIdx.x;
-    const Line ln = scan_total(p, lane);
-    int req = -1, last = 0;
-    if (i < ln.groups && ln.total > 0) {
-      const long long at = cut(ln, i);
-      long long first;
-      int r;
-      locate(p, at, lane, r, first);
-      if (at > first && cut(ln, i - 1) <= first) {
-        const long long end = first + tiles_of(request_len(p, r)) - 1;
-        req = r;
-        last = static_cast<int>(((end + 1) * ln.groups - 1) / ln.total);
-      }
-    }
-    if (lane == 0) {
-      s_req = req;
-      s_last = last;
-    }
-  }
-  __syncthreads();
-  grid_dep_wait();
-  if (s_req < 0) return;
   const int rows_req = p.nq * p.heads;
   const int rrow = blockIdx.y * kMergeRows + threadIdx.x / (kVDim / 4);
-  if (rrow >= rows_req) return;
   const int c4 = threadIdx.x % (kVDim / 4);
   const int m = rrow / kRowTile, lrow = rrow % kRowTile;
-  const int g0 = i - 1, g1 = s_last;
+  const int g0 = blockIdx.x;
   const float ninf = __int_as_float(0xff800000);
-  auto slot = [&](int g) {
-    return (static_cast<long long>(g * p.row_tiles + m) * 2 + (g == g0 ? 1 : 0)) * kRowTile + lrow;
+  grid_dep_wait();
+  const int2 join = p.joins[g0 + 1];
+  if (join.x < 0 || rrow >= rows_req) return;
+  const int n = join.y - g0 + 1;      // parts
+  auto slot = [&](int i) {
+    return (static_cast<long long>((g0 + i) * p.row_tiles + m) * 2 + (i == 0 ? 1 : 0)) * kRowTile + lrow;
   };
-  float mx = ninf;
-  for (int g = g0; g <= g1; ++g) mx = fmaxf(mx, p.part_lse[slot(g)]);
-  const float mref = mx > ninf ? mx : 0.f;
+  float mx = ninf, tot = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float tot = 0.f;
-  for (int b0 = g0; b0 <= g1; b0 += 4) {
-    float4 v[4];
-    float w[4];
+  for (int b0 = 0; b0 < n; b0 += kMergeBatch) {
+    float4 v[kMergeBatch];
+    float e[kMergeBatch];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int g = b0 + u;
-      w[u] = 0.f;
-      v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (g <= g1) {
-        const long long s = slot(g);
-        w[u] = ex2((p.part_lse[s] - mref) * kLog2e);
-        v[u] = reinterpret_cast<const float4*>(p.part_o + s * kVDim)[c4];
-      }
+    for (int u = 0; u < kMergeBatch; ++u) {
+      const bool in = b0 + u < n;
+      const long long s = slot(in ? b0 + u : 0);
+      e[u] = in ? p.part_lse[s] : ninf;
+      v[u] = reinterpret_cast<const float4*>(p.part_o + s * kVDim)[c4];
     }
+    float top = mx;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      tot += w[u];
-      acc.x = fmaf(w[u], v[u].x, acc.x);
-      acc.y = fmaf(w[u], v[u].y, acc.y);
-      acc.z = fmaf(w[u], v[u].z, acc.z);
-      acc.w = fmaf(w[u], v[u].w, acc.w);
+    for (int u = 0; u < kMergeBatch; ++u) top = fmaxf(top, e[u]);
+    const float mref = top > ninf ? top : 0.f;
+    const float f = ex2((mx - mref) * kLog2e);      // (0 for the first batch: its sums are 0)
+    mx = top;
+    tot *= f;
+    acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+#pragma unroll
+    for (int u = 0; u < kMergeBatch; ++u) {
+      const float w = ex2((e[u] - mref) * kLog2e);
+      // (An empty part holds zeros; its weight is 0.)
+      tot += w;
+      acc.x = fmaf(w, v[u].x, acc.x);
+      acc.y = fmaf(w, v[u].y, acc.y);
+      acc.z = fmaf(w, v[u].z, acc.z);
+      acc.w = fmaf(w, v[u].w, acc.w);
     }
   }
   const bool any = tot > 0.f || tot != tot;
   const float inv = any ? 1.f / tot : 0.f;
-  const long long grow = static_cast<long long>(s_req) * rows_req + rrow;
+  const long long grow = static_cast<long long>(join.x) * rows_req + rrow;
   reinterpret_cast<uint2*>(p.out + grow * kVDim)[c4] =
       make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
   if (p.lse && c4 == 0) p.lse[grow] = any ? mx + log2f(tot) * kLn2 : ninf;
 }
 
-constexpr int kMinTiles = 1;   // key tiles a group takes at least
+constexpr int kMinTiles = 2;   // key tiles a group takes at least
 
 }  // namespace
 
@@ -879,7 +923,7 @@ void mla_decode_plan(int nq, int heads, int* row_tiles, int* groups, size_t* ws_
   if (g < 1) g = 1;
   *row_tiles = mt;
   *groups = g;
-  *ws_bytes = static_cast<size_t>(g) * mt * 2 * kRowTile * (kVDim + 1) * sizeof(float);
+  *ws_bytes = static_cast<size_t>(g) * mt * 2 * kRowTile * (kVDim + 1) * sizeof(float) + g * sizeof(int2);
 }
 
 cudaError_t launch_mla_decode(MlaDecodeLaunch a, void* ws, cudaStream_t s) {
@@ -887,7 +931,9 @@ cudaError_t launch_mla_decode(MlaDecodeLaunch a, void* ws, cudaStream_t s) {
   mla_decode_plan(a.nq, a.heads, &a.row_tiles, &a.groups, &bytes);
   a.min_tiles = kMinTiles;
   a.part_o = static_cast<float*>(ws);
-  a.part_lse = a.part_o + static_cast<size_t>(a.groups) * a.row_tiles * 2 * kRowTile * kVDim;
+  const size_t slots = static_cast<size_t>(a.groups) * a.row_tiles * 2 * kRowTile;
+  a.part_lse = a.part_o + slots * kVDim;
+  a.joins = reinterpret_cast<int2*>(a.part_lse + slots);
   // Rows as 64-dim atoms: one copy brings a box of rows x atoms, each atom's
   // rows 128 bytes apart (128B swizzle).
   const uint64_t qrows = static_cast<uint64_t>(a.batch) * a.nq * a.heads;
@@ -915,11 +961,20 @@ cudaError_t launch_mla_decode(MlaDecodeLaunch a, void* ws, cudaStream_t s) {
                              CU_TENSOR_MAP_SWIZZLE_128B)) {
     return cudaErrorInvalidValue;
   }
+  CUtensorMap to, tp;
+  const uint64_t odims[2] = {kVDim, qrows}, ostr[1] = {kVDim * 2};
+  const uint64_t pdims[2] = {kVDim, slots}, pstr[1] = {kVDim * 4};
+  const uint32_t obox[2] = {64, 32}, pbox[2] = {32, 32};
+  if (!encode_tmap_nd(&to, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.out, 2, odims, ostr, obox,
+                      CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_tmap_nd(&tp, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.part_o, 2, pdims, pstr, pbox,
+                      CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
   auto kern = fp8 ? mla_decode_kernel<true> : mla_decode_kernel<false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
   e = launch_kernel(kern, dim3(2 * a.groups * a.row_tiles), dim3(fp8 ? kThreadsFp8 : kThreads), kSmemBytes, s,
-                    false, 1, tq, tk, tv, a);
+                    false, 1, tq, tk, tv, to, tp, a);
   if (e != cudaSuccess || a.groups == 1) return e;
   const int chunks = (a.nq * a.heads + kMergeRows - 1) / kMergeRows;
   return launch_kernel(mla_merge_kernel, dim3(a.groups - 1, chunks), dim3(kMergeThreads), 0, s, true, 1, a);

@@ -98,13 +98,14 @@ constexpr int kOffInfo = kOffBar + 16 * 8;
 constexpr int kSmemBytes = kOffInfo + 32 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory");
 constexpr int kColO = 0, kColS = 256, kTmemCols = 512;    // S: 2 x 64 columns
-constexpr int kThreads = 256, kThreadsFp8 = 512;
+constexpr int kThreads = 256, kThreadsFp8 = 768;
 constexpr int kSoftWarps = 4;
 constexpr int kF8RowBytes = 656, kF8ScaleOff = 512, kF8RopeOff = 528;
-// FP8: registers a thread by warpgroup (launched with 128 each): copies and
-// MMAs, softmax, K, V.
-constexpr int kRegsMma = 80, kRegsSoft = 184, kRegsK = 128, kRegsV = 120;
-static_assert(kRegsMma + kRegsSoft + kRegsK + kRegsV <= 4 * 128, "registers");
+// FP8: eight warps dequantise for K, eight for V.  Registers a thread (launched
+// with 80 each): copies and MMAs, softmax, dequantisation.
+constexpr int kDequantWarps = 8;
+constexpr int kRegsMma = 64, kRegsSoft = 128, kRegsDequant = 72;
+static_assert(kRegsMma + kRegsSoft + 4 * kRegsDequant <= 6 * 80, "registers");
 constexpr float kRaiseLog2 = 8.0f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -296,11 +297,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
     mbar_init(DRAIN, 1);
     mbar_init(P_FULL, 2 * kSoftWarps);
     for (int g = 0; g < kKGroups; ++g) {
-      mbar_init(K_FULL(g), kFp8 && g < 2 ? 8 : 1);      // FP8 codes: four warps of each CTA
+      mbar_init(K_FULL(g), kFp8 && g < 2 ? 2 * kDequantWarps : 1);
       mbar_init(K_EMPTY(g), 1);
     }
     for (int h = 0; h < 2; ++h) {
-      mbar_init(V_FULL(h), kFp8 ? 4 : 1);
+      mbar_init(V_FULL(h), kFp8 ? kDequantWarps : 1);
       mbar_init(V_EMPTY(h), 1);
       mbar_init(S_FULL(h), 1);
     }
@@ -505,11 +506,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
   }
   } else if (kFp8 && warp >= 8) {
     // ------------------------------------------- FP8 rows to bf16 operands
-    // A warp has 16 rows of a page and takes two at a time: lane = row r2 of the
+    // A warp has 8 rows of a page and takes two at a time: lane = row r2 of the
     // two, and 16-code chunk c of 256 bytes of it.  Eight neighbouring lanes
     // hold an atom's four chunks of both rows: whose swizzled pieces fall on
     // distinct banks.
-    const int r2 = (lane >> 2) & 1, c = (lane & 3) | ((lane >> 3) << 2), row0 = (warp & 3) * 16;
+    const int r2 = (lane >> 2) & 1, c = (lane & 3) | ((lane >> 3) << 2), row0 = (warp & 7) * 8;
     bool ok = true;
     int it = 0;
     auto rows_of = [&](int page) {
@@ -523,69 +524,62 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
       *reinterpret_cast<uint4*>(at + (piece << 4)) = lo;
       *reinterpret_cast<uint4*>(at + ((piece ^ 1) << 4)) = hi;
     };
-    if (warp < 12) {
-      setmaxnreg_dec<kRegsK>();
+    setmaxnreg_dec<kRegsDequant>();
+    if (warp < 8 + kDequantWarps) {
       const uint32_t k_full0 = mapa_shared(K_FULL(0), 0);
+      uint4 raw[8];       // 4 row pairs of dims 0-255, then of 256-511
+      float sc = 0.f;     // scales of the 8 rows: lane = pair, row r2, tile
       while (ok && wk.next(p)) {
         PageBatch pages(p, wk, lane);
-        uint4 raw[16];       // 8 row pairs of dims 0-255, then of 256-511
-        float sc[2];         // scales of row pairs 0-3 / 4-7: lane = row r2, pair, tile
-        const int sc_row = (lane >> 3) * 2, sc_tile = lane & 3;
         auto code_at = [&](const uint8_t* rows, int k) {
-          return __ldg(reinterpret_cast<const uint4*>(rows + 2 * (k & 7) * kF8RowBytes + 256 * (k >> 3)) + c);
+          return __ldg(reinterpret_cast<const uint4*>(rows + 2 * (k & 3) * kF8RowBytes + 256 * (k >> 2)) + c);
         };
-        auto scale_at = [&](const uint8_t* rows, int half) {
-          return __ldg(reinterpret_cast<const float*>(rows + (8 * half + sc_row) * kF8RowBytes + kF8ScaleOff) +
-                       sc_tile);
+        auto scale_at = [&](const uint8_t* rows) {
+          return __ldg(reinterpret_cast<const float*>(rows + (lane >> 3) * 2 * kF8RowBytes + kF8ScaleOff) +
+                       (lane & 3));
         };
         for (int t = wk.t0; ok && t < wk.t1; ++t, ++it) {
           pages.advance(t, lane);
           if (t == wk.t0) {
             const uint8_t* rows = rows_of(pages.page(t, rank));
 #pragma unroll
-            for (int k = 0; k < 16; ++k) raw[k] = code_at(rows, k);
-            sc[0] = scale_at(rows, 0);
-            sc[1] = scale_at(rows, 1);
+            for (int k = 0; k < 8; ++k) raw[k] = code_at(rows, k);
+            sc = scale_at(rows);
           }
           // The next tile's page (behind the stretch: page 0) is fetched as this
           // one is used up.
           const uint8_t* ahead = rows_of(pages.page(t, rank, true));
-          const float nsc0 = scale_at(ahead, 0), nsc1 = scale_at(ahead, 1);
+          const float nsc = scale_at(ahead);
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
-            float scale[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              scale[k] = __shfl_sync(0xffffffffu, sc[k >> 2], (k & 3) * 8 + r2 * 4 + 2 * g + (c >> 3));
             if (it >= 1 && ok && !mbar_wait(K_EMPTY(g), (it - 1) & 1)) ok = false;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
+            for (int k = 0; k < 4; ++k) {
+              const float scale = __shfl_sync(0xffffffffu, sc, k * 8 + r2 * 4 + 2 * g + (c >> 3));
               uint4 lo, hi;
-              dequant16(raw[8 * g + k], scale[k], lo, hi);
-              raw[8 * g + k] = code_at(ahead, 8 * g + k);
+              dequant16(raw[4 * g + k], scale, lo, hi);
+              raw[4 * g + k] = code_at(ahead, 4 * g + k);
               store(smem + kOffK + 4 * g * kAtom, k, lo, hi);
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive_remote_async(k_full0 + 8u * g);
           }
-          sc[0] = nsc0;
-          sc[1] = nsc1;
+          sc = nsc;
           ok = __all_sync(0xffffffffu, ok);
         }
       }
     } else {
-      setmaxnreg_dec<kRegsV>();
       // Output dims of P V's two MMAs: 256 n + 128 rank .. + 127, code tiles
       // rank (chunks c < 8) and 2 + rank.
       const int off = 128 * static_cast<int>(rank) + (c < 8 ? 0 : 256) + (c & 7) * 16;
+      const int sc_row = (lane >> 3) * 2, sc_tile = rank + (lane & 2);
+      uint4 raw[8];       // 4 row pairs of either page
+      float sc[2];        // scales of a page's 8 rows: lane = pair, row r2, tile
       while (ok && wk.next(p)) {
         PageBatch pages(p, wk, lane);
-        uint4 raw[16];       // 8 row pairs of either page
-        float sc[2];         // scales of a page's 16 rows: lane = row r2, tile, pair
-        const int sc_row = ((lane & 1) | ((lane >> 3) << 1)) * 2, sc_tile = rank + (lane & 2);
         // Rows that no query sees are zero, whatever the cache holds: they are
-        // not fetched.  (live: rows of this warp's 16, from this lane's first.)
+        // not fetched.  (live: rows of this warp's 8, from this lane's first.)
         auto code_at = [&](const uint8_t* rows, int k, int live) {
           return 2 * k < live ? __ldg(reinterpret_cast<const uint4*>(rows + 2 * k * kF8RowBytes + off))
                               : make_uint4(0u, 0u, 0u, 0u);
@@ -606,22 +600,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
               const int page = pages.page(t, h), live = live_of(t, h, page);
               const uint8_t* rows = rows_of(page);
 #pragma unroll
-              for (int k = 0; k < 8; ++k) raw[8 * h + k] = code_at(rows, k, live);
+              for (int k = 0; k < 4; ++k) raw[4 * h + k] = code_at(rows, k, live);
               sc[h] = scale_at(rows, live);
             }
             const int page = pages.page(t, h, true), live = live_of(t + 1, h, page);
             const uint8_t* ahead = rows_of(page);
             const float nsc = scale_at(ahead, live);
-            float scale[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              scale[k] = __shfl_sync(0xffffffffu, sc[h], ((k >> 1) << 3) | (r2 << 2) | ((c >> 3) << 1) | (k & 1));
             if (it >= 1 && ok && !mbar_wait(V_EMPTY(h), (it - 1) & 1)) ok = false;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
+            for (int k = 0; k < 4; ++k) {
+              const float scale = __shfl_sync(0xffffffffu, sc[h], (k << 3) | (r2 << 2) | ((c >> 3) << 1));
               uint4 lo, hi;
-              dequant16(raw[8 * h + k], scale[k], lo, hi);
-              raw[8 * h + k] = code_at(ahead, k, live);
+              dequant16(raw[4 * h + k], scale, lo, hi);
+              raw[4 * h + k] = code_at(ahead, k, live);
               store(smem + kOffV + h * kVBytes, k, lo, hi);
             }
             sc[h] = nsc;
@@ -700,24 +691,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
         }
         if (raise) mrun = tmax;
         const float mref = mrun > ninf ? mrun : 0.f;
-        uint32_t pk[32];
-        float2 ls = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const float2 x = fma2(make_float2(__uint_as_float(sr[2 * j]), __uint_as_float(sr[2 * j + 1])),
-                                make_float2(sc, sc), make_float2(-mref, -mref));
-          const float2 e = make_float2(ex2(x.x), ex2(x.y));
-          ls = add2(ls, e);
-          pk[j] = pack_bf16x2(e.x, e.y);
-        }
-        lrun += ls.x + ls.y;
-        // P of the tile before has been read.
+        // P of the tile before has been read: its P V runs before the next Q K^T,
+        // which the exponentials then have to hide in.
         if (it >= 1 && ok && !mbar_wait(V_EMPTY(1), (it - 1) & 1)) ok = false;
         uint8_t* prow = smem + kOffP + half * kAtom + row * 128;
+        float2 ls = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-          *reinterpret_cast<uint4*>(prow + ((c ^ (row & 7)) << 4)) =
-              make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+        for (int c = 0; c < 8; ++c) {
+          uint32_t pk[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 x = fma2(make_float2(__uint_as_float(sr[8 * c + 2 * j]), __uint_as_float(sr[8 * c + 2 * j + 1])),
+                                  make_float2(sc, sc), make_float2(-mref, -mref));
+            const float2 e = make_float2(ex2(x.x), ex2(x.y));
+            ls = add2(ls, e);
+            pk[j] = pack_bf16x2(e.x, e.y);
+          }
+          *reinterpret_cast<uint4*>(prow + ((c ^ (row & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+        }
+        lrun += ls.x + ls.y;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if (ok && !mbar_wait(V_FULL(h), it & 1)) ok = false;

@@ -181,3 +181,154 @@ def test_large_scores_raise_the_maximum(L):
     c["kv"][(table[0, pos // 64].long() * 64 + pos % 64).cuda()] = c["keys"][0]
     out, lse = _run(c)
     _check(c, out, lse)
+
+
+def _both_caches(c):
+    fc, kv8 = _fp8(c)
+    return ((c, api.dsa_mla_decode, c["kv"], 0.0), (fc, api.dsa_mla_decode_fp8kv, kv8, 2.0 ** -8))
+
+
+@pytest.mark.gpu
+def test_bad_page_ids_and_lengths_are_reported(L):
+    """A page id outside the cache masks exactly its page's tokens; a length above the page table is cut
+    to it; each is reported, and the rows of other requests stay right (bit for bit where the lengths, and
+    with them the cuts between CTA pairs, are the same)."""
+    c = _case([300, 200, 500], 1, 32, seed=9)
+    seq, table = c["keep"]
+    for case, call, cache, rel in _both_caches(c):
+        good, _ = _run(case, call=call, kv=cache)
+        assert api.dsa_get_device_error() == 0
+        saved = table.clone()
+        table[0, 1], table[2, 4] = -1, case["desc"].num_pages
+        out, lse = _run(case, call=call, kv=cache)
+        assert api.dsa_get_device_error() == 5
+        assert torch.equal(out[1], good[1])
+        keep0 = torch.cat([case["keys"][0][:64], case["keys"][0][128:]])
+        keep2 = torch.cat([case["keys"][2][:256], case["keys"][2][320:]])
+        _check({**case, "q": case["q"][[0, 2]], "keys": [keep0, keep2], "lens": [236, 436]}, out[[0, 2]], lse[[0, 2]], rel)
+        table.copy_(saved)
+        # the page table covers 9 pages (max_pages of this batch): 576 tokens
+        seq[2] = 10 ** 6
+        two = {**case, "q": case["q"][:2], "keys": case["keys"][:2], "lens": [300, 200]}
+        out, lse = _run(case, call=call, kv=cache)
+        assert api.dsa_get_device_error() == 5
+        _check(two, out[:2], lse[:2], rel)
+        seq[2] = -3
+        out, lse = _run(case, call=call, kv=cache)
+        assert api.dsa_get_device_error() == 0
+        assert (out[2] == 0).all() and (lse[2] == float("-inf")).all()
+        _check(two, out[:2], lse[:2], rel)
+        seq[2] = 500
+        again, _ = _run(case, call=call, kv=cache)
+        assert api.dsa_get_device_error() == 0 and torch.equal(again, good)
+
+
+@pytest.mark.gpu
+def test_streams_and_graphs(L):
+    """Two calls at once on two streams with workspaces of their own; a captured call replayed over new
+    lengths, pages and queries."""
+    c1, c2 = _case([4000, 100, 2500], 2, 64, seed=1), _case([70, 3000], 1, 128, seed=2)
+    for (a, call, ca, _), (b, _, cb, _) in zip(_both_caches(c1), _both_caches(c2)):
+        want_a, want_b = _run(a, call=call, kv=ca)[0], _run(b, call=call, kv=cb)[0]
+        s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+        torch.cuda.synchronize()
+        got = []
+        for _ in range(4):
+            for s, case, cache in ((s1, a, ca), (s2, b, cb)):
+                with torch.cuda.stream(s):
+                    got.append(_run(case, call=call, kv=cache, stream=s)[0])
+        torch.cuda.synchronize()
+        assert all(torch.equal(g, want_a) for g in got[0::2]) and all(torch.equal(g, want_b) for g in got[1::2])
+
+        seq, table = a["keep"]
+        q0, seq0 = a["q"].clone(), seq.clone()
+        a["q"].zero_()
+        seq.fill_(2)
+        out = torch.empty((6, 64, 512), dtype=torch.bfloat16, device="cuda")
+        ws = torch.empty(api.dsa_mla_decode_workspace_bytes(a["desc"]), dtype=torch.uint8, device="cuda")
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call(a["desc"], a["q"], ca, out, ws, SM)
+        a["q"].copy_(q0)
+        seq.copy_(seq0)
+        graph.replay()
+        assert torch.equal(out, want_a)
+    assert api.dsa_get_device_error() == 0
+
+
+@pytest.mark.gpu
+def test_equals_the_sparse_layer_that_selects_everything(L):
+    """With k >= the visible tokens the sparse decode layer attends them all: the same outputs, up to the
+    rounding of both (each within its tolerance of the formula)."""
+    from deepseek_sparse_attention_lightning_gb300 import workloads as W
+    spec = W.small_spec("mtp_32k", batch=3, q_per_req=2, num_heads=128, topk=2048, heavy="none", seed=7)
+    wl = W.make_workload(spec, seqlens=[1900, 64, 700]).to("cuda")
+    sparse = api.run_decode(wl)
+    T, H = spec.num_tokens, spec.num_heads
+    desc = api.workload_desc(wl)
+    out = torch.empty((T, H, 512), dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(api.dsa_mla_decode_workspace_bytes(desc), dtype=torch.uint8, device="cuda")
+    api.dsa_mla_decode(desc, wl.q, wl.kv, out, ws, spec.sm_scale)
+    assert api.dsa_get_device_error() == 0
+    assert ((out.float() - sparse).abs() <= 2e-2 + 2e-2 * sparse.abs()).all()
+
+
+@pytest.mark.gpu
+def test_a_cache_past_two_to_the_31(L):
+    """Rows whose byte and element offsets pass 32 bits, and a batch of 1024 requests."""
+    g = torch.Generator(device="cuda").manual_seed(4)
+    num_pages = 1 << 16                                  # 4.2 M rows, 2.4 G values
+    for fp8 in (False, True):
+        kv = torch.zeros((num_pages * 64, 656 if fp8 else 576), dtype=torch.uint8 if fp8 else torch.bfloat16,
+                         device="cuda")
+        lens = [1 + (37 * i) % 130 for i in range(1024)]
+        table = torch.full((1024, 3), -1, dtype=torch.int32)
+        page, keys = num_pages - 1, []
+        for r, n in enumerate(lens):
+            c = torch.randn(n, 576, generator=g, device="cuda").to(torch.bfloat16)
+            if fp8:
+                rows = torch.empty((n, 656), dtype=torch.uint8, device="cuda")
+                api.dsa_latent_to_fp8(c, rows)
+                sc = rows[:, 512:528].contiguous().view(torch.float32).double().repeat_interleave(128, dim=1)
+                keys.append(torch.cat([rows[:, :512].contiguous().view(torch.float8_e4m3fn).double() * sc,
+                                       c[:, 512:].double()], dim=1))
+            else:
+                rows = c
+                keys.append(c)
+            for j in range(-(-n // 64)):
+                table[r, j] = page
+                part = rows[64 * j:64 * j + 64]
+                kv[page * 64:page * 64 + part.shape[0]] = part
+                page -= 1
+        seq, table = torch.tensor(lens, dtype=torch.int32, device="cuda"), table.cuda()
+        q = torch.randn(1024, 16, 576, generator=g, device="cuda").to(torch.bfloat16)
+        case = dict(desc=api.make_desc(seq, table, 1, 16, 1, num_pages), q=q, kv=kv, keys=keys, lens=lens, nq=1,
+                    H=16, keep=(seq, table))
+        out, lse = _run(case, call=api.dsa_mla_decode_fp8kv if fp8 else api.dsa_mla_decode)
+        assert api.dsa_get_device_error() == 0
+        pick = list(range(0, 1024, 41)) + [1023]
+        _check({**case, "q": q[pick], "keys": [keys[i] for i in pick], "lens": [lens[i] for i in pick]},
+               out[pick], lse[pick], 2.0 ** -8 if fp8 else 0.0)
+
+
+@pytest.mark.gpu
+def test_binding_checks(L):
+    c = _case([100, 50], 1, 16, seed=6)
+    ws = torch.empty(api.dsa_mla_decode_workspace_bytes(c["desc"]), dtype=torch.uint8, device="cuda")
+    out = torch.empty((2, 16, 512), dtype=torch.bfloat16, device="cuda")
+    call = lambda q=c["q"], kv=c["kv"], out=out, ws=ws, **k: api.dsa_mla_decode(c["desc"], q, kv, out, ws, SM, **k)
+    call()
+    with pytest.raises(ValueError, match="q:"):
+        call(q=c["q"][:1])
+    with pytest.raises(ValueError, match="kv:"):
+        call(kv=c["kv"][:64])
+    with pytest.raises(TypeError, match="out:"):
+        call(out=out.float())
+    with pytest.raises(ValueError, match="lse:"):
+        call(lse=torch.empty((2, 8), device="cuda"))
+    with pytest.raises(ValueError, match="CUDA"):
+        call(q=c["q"].cpu())
+    with pytest.raises(api.DSAError, match="WORKSPACE"):
+        call(ws=ws[:-1])
+    with pytest.raises(ValueError, match="kv8:"):
+        api.dsa_mla_decode_fp8kv(c["desc"], c["q"], torch.empty((64, 656), dtype=torch.uint8, device="cuda"), out, ws, SM)

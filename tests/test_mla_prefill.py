@@ -114,3 +114,106 @@ def test_matches_formula(L, qlens, klens, H, causal):
     _check(c, causal, out, lse)
     again, _ = _run(c, causal, lse=False)
     assert torch.equal(out, again)
+
+
+@pytest.mark.gpu
+def test_bad_offsets_are_reported(L):
+    c = _case([100, 300, 50], [100, 300, 50], 4, seed=1)
+    good, _ = _run(c, True)
+    # the second request's keys would end behind the packed tensor: skipped, the others as before
+    saved = c["cu_k"].clone()
+    c["cu_k"][2:] += 1000
+    out, _ = _run(c, True)
+    assert api.dsa_get_device_error() == 5
+    assert torch.equal(out[:100], good[:100]) and (out[100:450] == 77).all()
+    c["cu_k"].copy_(saved)
+    # a request longer than max_q says (rounded up to 256): its first queries are written
+    out, _ = _run({**c, "max_q": 200}, True)
+    assert api.dsa_get_device_error() == 5
+    assert torch.equal(out[:100], good[:100]) and torch.equal(out[400:450], good[400:450])
+    out, _ = _run({**c, "max_q": 5000}, True)
+    assert api.dsa_get_device_error() == 0 and torch.equal(out[:450], good[:450])
+
+
+@pytest.mark.gpu
+def test_streams_and_graphs(L):
+    c1, c2 = _case([700, 20], [900, 20], 8, seed=2), _case([300] * 4, [300] * 4, 16, seed=3)
+    want1, want2 = _run(c1, True)[0], _run(c2, False)[0]
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(4):
+        for s, c, causal in ((s1, c1, True), (s2, c2, False)):
+            with torch.cuda.stream(s):
+                got.append(_run(c, causal, stream=s)[0])
+    torch.cuda.synchronize()
+    eq = lambda a, b, n: torch.equal(a[:n], b[:n])
+    assert all(eq(g, want1, 720) for g in got[0::2]) and all(eq(g, want2, 1200) for g in got[1::2])
+    out = torch.empty_like(want1)
+    q0, cu0 = c1["q"].clone(), c1["cu_q"].clone()
+    c1["q"].zero_()
+    c1["cu_q"].copy_(torch.tensor([0, 1, 2], dtype=torch.int32))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        api.dsa_mla_prefill(c1["q"], c1["kv"], c1["rope"], c1["cu_q"], c1["cu_k"], out, c1["max_q"], SM)
+    c1["q"].copy_(q0)
+    c1["cu_q"].copy_(cu0)
+    graph.replay()
+    assert eq(out, want1, 720) and api.dsa_get_device_error() == 0
+
+
+@pytest.mark.gpu
+def test_large_scores_raise_the_maximum(L):
+    """Keys that grow along the request: the running maximum rises by far more than 2^8 several times."""
+    c = _case([700], [700], 2, seed=5)
+    ramp = (1.0 + torch.arange(700, device="cuda") / 40.0).to(torch.bfloat16)
+    c["kv"][:700, :, :128] *= ramp[:, None, None]
+    out, lse = _run(c, True)
+    _check(c, True, out, lse)
+
+
+@pytest.mark.gpu
+def test_keys_past_two_to_the_31(L):
+    """The second request's keys lie behind 2^31 values of the packed tensor."""
+    H, far = 128, 66000
+    g = torch.Generator(device="cuda").manual_seed(8)
+    kv = torch.zeros((far + 300, H, 256), dtype=torch.bfloat16, device="cuda")
+    rope = torch.zeros((far + 300, 64), dtype=torch.bfloat16, device="cuda")
+    kv[far:] = torch.randn(300, H, 256, generator=g, device="cuda").to(torch.bfloat16)
+    rope[far:] = torch.randn(300, 64, generator=g, device="cuda").to(torch.bfloat16)
+    q = torch.randn(1 + 150, H, 192, generator=g, device="cuda").to(torch.bfloat16)
+    cu = lambda *n: torch.tensor(n, dtype=torch.int32, device="cuda")
+    out = torch.empty((151, H, 128), dtype=torch.bfloat16, device="cuda")
+    api.dsa_mla_prefill(q, kv, rope, cu(0, 1, 151), cu(0, far, far + 300), out, 150, SM)
+    assert api.dsa_get_device_error() == 0
+    assert (out[0] == 0).all()                       # a mean of zero values
+    c = dict(q=q[1:], kv=kv[far:], rope=rope[far:], qlens=[150], klens=[300], H=H)
+    _check(c, True, out[1:], None, heads=[0, 77, 127])
+
+
+@pytest.mark.gpu
+def test_binding_checks(L):
+    c = _case([20], [20], 4, seed=6, tail=0)
+    out = torch.empty((20, 4, 128), dtype=torch.bfloat16, device="cuda")
+    call = lambda q=c["q"], kv=c["kv"], rope=c["rope"], cu_q=c["cu_q"], cu_k=c["cu_k"], out=out, **k: \
+        api.dsa_mla_prefill(q, kv, rope, cu_q, cu_k, out, 20, SM, **k)
+    call()
+    call(rope=c["rope"].contiguous())
+    with pytest.raises(ValueError, match="kv:"):
+        call(kv=c["kv"][:, :2])
+    with pytest.raises(ValueError, match="q:"):
+        call(q=c["q"][..., :128])
+    with pytest.raises(ValueError, match="64 columns"):
+        call(rope=c["rope"][:, :32])
+    with pytest.raises(ValueError, match="contiguous columns"):
+        call(rope=c["rope"].contiguous().t().contiguous().t())
+    with pytest.raises(TypeError, match="cu_k:"):
+        call(cu_k=c["cu_k"].long())
+    with pytest.raises(ValueError, match="cu_k:"):
+        call(cu_k=c["cu_k"][:1])
+    with pytest.raises(TypeError, match="cu_q"):
+        call(cu_q=c["cu_q"][:1])
+    with pytest.raises(ValueError, match="out:"):
+        call(out=out[:10])
+    with pytest.raises(ValueError, match="lse:"):
+        call(lse=torch.empty((20, 5), device="cuda"))

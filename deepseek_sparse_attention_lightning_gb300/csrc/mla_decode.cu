@@ -49,14 +49,14 @@
 // so the log-sum-exp has fp32 accuracy.
 //
 // FP8 latent rows (kFp8; 656 bytes: 512 E4M3 codes, the four 128-dim tiles'
-// scales, 64 rope dims in bf16): two more warpgroups take the place of the
-// copies (but for the rope dims).  One fetches its page's codes for K, the other
-// both pages' half rows for V, each a tile ahead in registers, multiply them by
-// their scale, round once to bf16 and write the layout that the MMAs read.  A
-// warp reads 256 consecutive bytes of two rows at a time: the load path serves
-// a line of 128 bytes a cycle, and with 32 bytes of 16 rows a load it, not the
-// arithmetic, took 5 us a tile (decode_varlen 419 us).  The matrix work is the
-// same as for bf16 rows; K's three groups are dims 0-255, 256-511 and rope.
+// scales, 64 rope dims in bf16): a tile is one page, which halves K, V and P and
+// makes room for three stages of raw codes and scales (25 KB each) that the copy
+// engine runs ahead with.  Eight warps dequantise them for K, eight for V: a
+// code times its scale, rounded once to bf16, written in the layout that the
+// MMAs read.  (Read by the warps themselves, the codes of a two-page tile cost
+// more than all else: the load path took 2 of 4.3 us a tile, and 8 ragged
+// requests 351 us.)  K's three groups are dims 0-255, 256-511 and rope, which
+// is copied as it is.
 //
 // Rows of V that no query row sees (behind the request's end in its last page,
 // or a page whose id is out of range) are cleared in shared memory before P V:
@@ -76,31 +76,41 @@ constexpr int kRowsCta = 64;                              // query rows of a CTA
 constexpr int kRowTile = 2 * kRowsCta;
 constexpr int kAtoms = kLatentDim / 64;                   // 9 atoms of 64 dims
 constexpr int kQBytes = kRowsCta * kLatentDim * 2;        // 72 KB
-constexpr int kTileKeys = 2 * kPage;
-constexpr int kAtom = 64 * 128;                           // 64 rows x 64 dims of q, K, V or P: 8 KB
+constexpr int kAtom = 64 * 128;                           // 64 rows x 64 dims of q, V or P: 8 KB
 constexpr int kKGroups = 3, kGroupAtoms = kAtoms / kKGroups;
-constexpr int kKGroupBytes = kGroupAtoms * kAtom;         // 24 KB
-// First atom of K's group g.
-template <bool kFp8>
-__host__ __device__ constexpr int group_atom(int g) {
-  return kFp8 ? (g < 2 ? 4 * g : 8 + (g - 2)) : kGroupAtoms * g;
-}
 constexpr int kVBytes = 4 * kAtom;                        // one page, this CTA's 256 value dims
-constexpr int kPBytes = 2 * kAtom;
 static_assert(kRowsCta == 64 && kPage == 64, "atoms of 64 rows");
-constexpr int kOffQ = 0;
-constexpr int kOffK = kOffQ + kQBytes;
-constexpr int kOffV = kOffK + kKGroups * kKGroupBytes;
-constexpr int kOffP = kOffV + 2 * kVBytes;
-constexpr int kOffXchg = kOffP + kPBytes;                 // 2 x 128 floats
-constexpr int kOffBar = kOffXchg + 2 * 128 * 4;
-constexpr int kOffInfo = kOffBar + 16 * 8;
-constexpr int kSmemBytes = kOffInfo + 32 + 1024;
-static_assert(kSmemBytes <= 232448, "shared memory");
-constexpr int kColO = 0, kColS = 256, kTmemCols = 512;    // S: 2 x 64 columns
+constexpr int kF8RowBytes = 656, kF8ScaleOff = 512, kF8RopeOff = 528;
+constexpr int kRawStages = 3, kRawTile = 32 * 128;        // FP8: codes of 32 rows x 128 dims
+constexpr int kRawBytes = 6 * kRawTile + kPage * 16;      // own rows, the other rows' own dims, scales
+
+// A key tile and the shared memory it takes: two pages of bf16 rows, one of FP8
+// rows.
+template <bool kFp8>
+struct Tile {
+  static constexpr int kPages = kFp8 ? 1 : 2;
+  static constexpr int kKeys = kPages * kPage;
+  static constexpr int kHalf = kKeys / 2;                 // keys of K in a CTA, and of a softmax thread
+  static constexpr int kKAtom = kHalf * 128;
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffK = kOffQ + kQBytes;
+  static constexpr int kOffV = kOffK + kAtoms * kKAtom;
+  static constexpr int kOffP = kOffV + kPages * kVBytes;
+  static constexpr int kOffRaw = kOffP + kPages * kAtom;
+  static constexpr int kOffXchg = kOffRaw + (kFp8 ? kRawStages * kRawBytes : 0);      // 2 x 128 floats
+  static constexpr int kOffBar = kOffXchg + 2 * 128 * 4;
+  static constexpr int kOffInfo = kOffBar + 24 * 8;
+  static constexpr int kSmemBytes = kOffInfo + 32 + 1024;
+  static constexpr int kStageRow = kFp8 ? 64 : 128;       // bytes of a row that an output store takes
+  // First atom of K's group g.
+  __host__ __device__ static constexpr int group_atom(int g) {
+    return kFp8 ? (g < 2 ? 4 * g : 8 + (g - 2)) : kGroupAtoms * g;
+  }
+};
+static_assert(Tile<false>::kSmemBytes <= 232448 && Tile<true>::kSmemBytes <= 232448, "shared memory");
+constexpr int kColO = 0, kColS = 256, kTmemCols = 512;    // S: two buffers of a tile's keys / 2 columns
 constexpr int kThreads = 256, kThreadsFp8 = 768;
 constexpr int kSoftWarps = 4;
-constexpr int kF8RowBytes = 656, kF8ScaleOff = 512, kF8RopeOff = 528;
 // FP8: eight warps dequantise for K, eight for V.  Registers a thread (launched
 // with 80 each): copies and MMAs, softmax, dequantisation.
 constexpr int kDequantWarps = 8;
@@ -125,7 +135,10 @@ __device__ __forceinline__ int request_len(const MlaDecodeLaunch& p, int r) {
   return s < 0 ? 0 : s;
 }
 
-__device__ __forceinline__ int tiles_of(int len) { return (len + kTileKeys - 1) / kTileKeys; }
+template <int kKeys>
+__device__ __forceinline__ int tiles_of(int len) {
+  return (len + kKeys - 1) / kKeys;
+}
 
 // The line of key tiles: their total number, and the groups it is cut into.
 struct Line {
@@ -136,9 +149,10 @@ struct Line {
 __device__ __forceinline__ long long cut(const Line& ln, int g) { return ln.total * g / ln.groups; }
 
 // (one warp) Total tiles of all requests.
+template <int kKeys>
 __device__ __forceinline__ Line scan_total(const MlaDecodeLaunch& p, int lane) {
   long long n = 0;
-  for (int r = lane; r < p.batch; r += 32) n += tiles_of(request_len(p, r));
+  for (int r = lane; r < p.batch; r += 32) n += tiles_of<kKeys>(request_len(p, r));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
   Line ln;
@@ -150,6 +164,7 @@ __device__ __forceinline__ Line scan_total(const MlaDecodeLaunch& p, int lane) {
 
 // (one warp) The request that holds tile `at` of the line (at < total), and
 // the line position of its first tile.
+template <int kKeys>
 __device__ __forceinline__ void locate(const MlaDecodeLaunch& p, long long at, int lane, int& req,
                                        long long& first) {
   long long base = 0;
@@ -157,7 +172,7 @@ __device__ __forceinline__ void locate(const MlaDecodeLaunch& p, long long at, i
   first = 0;
   for (int r0 = 0; r0 < p.batch; r0 += 32) {
     const int r = r0 + lane;
-    const int n = r < p.batch ? tiles_of(request_len(p, r)) : 0;
+    const int n = r < p.batch ? tiles_of<kKeys>(request_len(p, r)) : 0;
     long long incl = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -176,6 +191,7 @@ __device__ __forceinline__ void locate(const MlaDecodeLaunch& p, long long at, i
 }
 
 // The stretches of requests in a group's part [lo, hi) of the line, in order.
+template <int kKeys>
 struct Walk {
   long long pos, hi;     // next tile of the line, end of the part
   int req;               // request of the stretch
@@ -187,7 +203,7 @@ struct Walk {
       do {
         ++req;
         len = request_len(p, req);
-        nt = tiles_of(len);
+        nt = tiles_of<kKeys>(len);
       } while (nt == 0);
       t0 = 0;
     }
@@ -230,28 +246,30 @@ __device__ __forceinline__ void dequant16(const uint4 raw, float scale, uint4& l
   hi = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
-// Pages of a stretch's tiles, 16 tiles (32 ids) at a time and one batch ahead,
-// an id a lane.
+// Pages of a stretch's tiles, 32 ids at a time (an id a lane) and one batch
+// ahead.
+template <int kPages>
 struct PageBatch {
+  static constexpr int kTiles = 32 / kPages;      // of a batch
   PageIds ids;
-  int t0, now, next;     // first tile of the stretch; ids of this and the next 16 tiles
-  __device__ __forceinline__ PageBatch(const MlaDecodeLaunch& p, const Walk& wk, int lane)
+  int t0, now, next;     // first tile of the stretch; ids of this and the next batch
+  template <int kKeys>
+  __device__ __forceinline__ PageBatch(const MlaDecodeLaunch& p, const Walk<kKeys>& wk, int lane)
       : ids{p.page_table + static_cast<long long>(wk.req) * p.max_pages, (wk.len + kPage - 1) / kPage,
             p.num_pages},
         t0(wk.t0), now(0) {
-    next = ids.get(2 * t0 + lane);
+    next = ids.get(kPages * t0 + lane);
   }
   // Before tile t's pages are asked for, t going up by one.
   __device__ __forceinline__ bool advance(int t, int lane) {
-    if (((t - t0) & 15) != 0) return false;
+    if (((t - t0) & (kTiles - 1)) != 0) return false;
     now = next;
-    next = ids.get(2 * (t + 16) + lane);
+    next = ids.get(kPages * (t + kTiles) + lane);
     return true;
   }
-  // Page h of tile t or (ahead) of the tile after it.
-  __device__ __forceinline__ int page(int t, int h, bool ahead = false) const {
-    const int u = ((t - t0) & 15) + (ahead ? 1 : 0);
-    return __shfl_sync(0xffffffffu, u < 16 ? now : next, 2 * (u & 15) + h);
+  // Page h of tile t.
+  __device__ __forceinline__ int page(int t, int h) const {
+    return __shfl_sync(0xffffffffu, now, kPages * ((t - t0) & (kTiles - 1)) + h);
   }
 };
 
@@ -260,8 +278,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
     mla_decode_kernel(const __grid_constant__ CUtensorMap tmap_q,
                       const __grid_constant__ CUtensorMap tmap_k,
                       const __grid_constant__ CUtensorMap tmap_v,
+                      const __grid_constant__ CUtensorMap tmap_sc,
                       const __grid_constant__ CUtensorMap tmap_out,
                       const __grid_constant__ CUtensorMap tmap_part, const MlaDecodeLaunch p) {
+  using T = Tile<kFp8>;
+  constexpr int kKeys = T::kKeys;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -273,12 +294,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
   const int rows_req = p.nq * p.heads;
   const float ninf = __int_as_float(0xff800000);
 
-  const uint32_t bar0 = sbase + kOffBar;
+  const uint32_t bar0 = sbase + T::kOffBar;
 // In the leading CTA (both CTAs' threads and copies arrive there):
 //   Q_FULL, K_FULL(g): q / K group g landed in both CTAs; P_FULL: P written
 //   and V landed in both; O_FREE: the epilogue has read the output.
 // In both (the MMAs' completion arrives in both): S_FULL(b), K_EMPTY(g),
-//   V_EMPTY(h) (P V of page h of the tile done).  V_FULL(h): this CTA's copies.
+//   V_EMPTY(h) (P V of page h of the tile done).  In this CTA: V_FULL(h), and
+//   (FP8) RAW_FULL(s), RAW_EMPTY(s) of the raw stages.
 #define Q_FULL (bar0)
 #define O_FREE (bar0 + 8u)
 #define DRAIN (bar0 + 16u)
@@ -288,8 +310,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
 #define V_FULL(h) (bar0 + 80u + 8u * (h))
 #define V_EMPTY(h) (bar0 + 96u + 8u * (h))
 #define S_FULL(b) (bar0 + 112u + 8u * (b))
-  long long* info = reinterpret_cast<long long*>(smem + kOffInfo);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffInfo + 28);
+#define RAW_FULL(s) (bar0 + 128u + 8u * (s))
+#define RAW_EMPTY(s) (bar0 + 152u + 8u * (s))
+  long long* info = reinterpret_cast<long long*>(smem + T::kOffInfo);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + T::kOffInfo + 28);
 
   if (warp == 0 && lane == 0) {
     mbar_init(Q_FULL, 1);
@@ -305,6 +329,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
       mbar_init(V_EMPTY(h), 1);
       mbar_init(S_FULL(h), 1);
     }
+    if (kFp8)
+      for (int st = 0; st < kRawStages; ++st) {
+        mbar_init(RAW_FULL(st), 1);
+        mbar_init(RAW_EMPTY(st), 2 * kDequantWarps);
+      }
     fence_mbar_init();
     prefetch_tmap(&tmap_q);
     prefetch_tmap(&tmap_k);
@@ -315,20 +344,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
     tmem_relinquish_2cta();
   }
   if (warp == 3) {
-    const Line ln = scan_total(p, lane);
+    const Line ln = scan_total<kKeys>(p, lane);
     long long lo = 0, hi = 0, first = 0;
     int req = 0;
     if (group < ln.groups && ln.total > 0) {
       lo = cut(ln, group);
       hi = cut(ln, group + 1);
-      if (hi > lo) locate(p, lo, lane, req, first);
+      if (hi > lo) locate<kKeys>(p, lo, lane, req, first);
     }
     // What the merge has to join: the request that this group's first cut falls
     // into, if it is the first cut inside that request, and its last group.
     if (mtile == 0 && rank == 0 && lane == 0) {
       int2 join = make_int2(-1, 0);
       if (group > 0 && hi > lo && lo > first && cut(ln, group - 1) <= first) {
-        const long long end = first + tiles_of(request_len(p, req));
+        const long long end = first + tiles_of<kKeys>(request_len(p, req));
         join = make_int2(req, static_cast<int>((end * ln.groups - 1) / ln.total));
       }
       p.joins[group] = join;
@@ -343,12 +372,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
   cluster_sync();     // the other CTA's barriers are initialised
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-  Walk wk;
+  Walk<kKeys> wk;
   wk.pos = info[0];
   wk.hi = info[1];
   wk.req = static_cast<int>(info[2] & 2047);
   wk.len = request_len(p, wk.req);
-  wk.nt = tiles_of(wk.len);
+  wk.nt = tiles_of<kKeys>(wk.len);
   wk.t0 = static_cast<int>(wk.pos - (info[2] >> 11));
   wk.t1 = 0;
 
@@ -360,27 +389,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
     bool ok = true;
     int it = 0;
     while (ok && wk.next(p)) {
-      PageBatch pages(p, wk, lane);
+      PageBatch<T::kPages> pages(p, wk, lane);
       for (int t = wk.t0; ok && t < wk.t1; ++t, ++it) {
         if (pages.advance(t, lane) && pages.now == PageIds::kBad) raise_error(kErrCheck);
-        const int page = max(0, pages.page(t, rank));
+        // (Two pages a tile: each CTA takes one for K.  One: half of it.)
+        const int page = max(0, pages.page(t, kFp8 ? 0 : rank));
+        const int row = page * kPage + (kFp8 ? T::kHalf * static_cast<int>(rank) : 0);
 #pragma unroll
         for (int g = 0; g < kKGroups; ++g) {
           if (it >= 1 && ok && !mbar_wait(K_EMPTY(g), (it - 1) & 1)) ok = false;
           if (!kFp8 && ok && lane == 0) {
-            if (rank == 0) mbar_expect_tx(K_FULL(g), 2 * kKGroupBytes);
-            tma_load_3d_2cta(sbase + kOffK + g * kKGroupBytes, &tmap_k, 0, page * kPage, kGroupAtoms * g,
+            if (rank == 0) mbar_expect_tx(K_FULL(g), 2 * kGroupAtoms * T::kKAtom);
+            tma_load_3d_2cta(sbase + T::kOffK + g * kGroupAtoms * T::kKAtom, &tmap_k, 0, row, kGroupAtoms * g,
                              k_full0 + 8u * g);
           }
           if (kFp8 && g == kKGroups - 1 && ok && lane == 0) {
-            if (rank == 0) mbar_expect_tx(K_FULL(g), 2 * kAtom);
-            tma_load_3d_2cta(sbase + kOffK + 8 * kAtom, &tmap_k, kF8RopeOff, page * kPage, 0, k_full0 + 8u * g);
+            if (rank == 0) mbar_expect_tx(K_FULL(g), 2 * T::kKAtom);
+            tma_load_3d_2cta(sbase + T::kOffK + 8 * T::kKAtom, &tmap_k, kF8RopeOff, row, 0, k_full0 + 8u * g);
           }
           // q of the stretch (Q K^T of the tile before is done with its last
           // group).
           if (g == kKGroups - 1 && t == wk.t0 && ok && lane == 0) {
             if (rank == 0) mbar_expect_tx(Q_FULL, 2 * kQBytes);
-            tma_load_3d_2cta(sbase + kOffQ, &tmap_q, 0,
+            tma_load_3d_2cta(sbase + T::kOffQ, &tmap_q, 0,
                              wk.req * rows_req + mtile * kRowTile + kRowsCta * static_cast<int>(rank), 0, q_full);
           }
         }
@@ -388,24 +419,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
       }
     }
     if (!ok && lane == 0) raise_error(kErrTimeout);
-  } else if (!kFp8 && warp == 2) {
-    // ---------------------------------------------------------- V copies
+  } else if (warp == 2) {
+    // ----------------------------------------- V copies, or the raw FP8 rows'
     bool ok = true;
     int it = 0;
     while (ok && wk.next(p)) {
-      PageBatch pages(p, wk, lane);
+      PageBatch<T::kPages> pages(p, wk, lane);
       for (int t = wk.t0; ok && t < wk.t1; ++t, ++it) {
         pages.advance(t, lane);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int page = max(0, pages.page(t, h));
-          if (it >= 1 && ok && !mbar_wait(V_EMPTY(h), (it - 1) & 1)) ok = false;
+        if constexpr (kFp8) {
+          const int st = it % kRawStages;
+          const int row = max(0, pages.page(t, 0)) * kPage, mine = 32 * static_cast<int>(rank);
+          if (it >= kRawStages && !mbar_wait(RAW_EMPTY(st), (it / kRawStages - 1) & 1)) ok = false;
           if (ok && lane == 0) {
-            // Output dims of P V's two MMAs: 256 n + 128 rank .. + 127.
-            mbar_expect_tx(V_FULL(h), kVBytes);
-            const uint32_t dst = sbase + kOffV + h * kVBytes;
-            tma_load_3d(dst, &tmap_v, 0, page * kPage, 2 * static_cast<int>(rank), V_FULL(h));
-            tma_load_3d(dst + 2 * kAtom, &tmap_v, 0, page * kPage, 4 + 2 * static_cast<int>(rank), V_FULL(h));
+            // All codes of this CTA's rows (for K and V), its value dims' of the
+            // other rows, every row's scales.
+            mbar_expect_tx(RAW_FULL(st), kRawBytes);
+            const uint32_t dst = sbase + T::kOffRaw + st * kRawBytes;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tma_load_3d(dst + c * kRawTile, &tmap_v, 0, row + mine, c, RAW_FULL(st));
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+              tma_load_3d(dst + (4 + n) * kRawTile, &tmap_v, 0, row + 32 - mine, 2 * n + static_cast<int>(rank),
+                          RAW_FULL(st));
+            tma_load_3d(dst + 6 * kRawTile, &tmap_sc, kF8ScaleOff, row, 0, RAW_FULL(st));
+          }
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int page = max(0, pages.page(t, h));
+            if (it >= 1 && ok && !mbar_wait(V_EMPTY(h), (it - 1) & 1)) ok = false;
+            if (ok && lane == 0) {
+              // Output dims of P V's two MMAs: 256 n + 128 rank .. + 127.
+              mbar_expect_tx(V_FULL(h), kVBytes);
+              const uint32_t dst = sbase + T::kOffV + h * kVBytes;
+              tma_load_3d(dst, &tmap_v, 0, page * kPage, 2 * static_cast<int>(rank), V_FULL(h));
+              tma_load_3d(dst + 2 * kAtom, &tmap_v, 0, page * kPage, 4 + 2 * static_cast<int>(rank), V_FULL(h));
+            }
           }
         }
         ok = __all_sync(0xffffffffu, ok);
@@ -417,18 +467,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
     if (rank == 0) {
       // The whole warp runs this; one lane issues.
       const uint32_t el = elect_one() ? 1u : 0u;
-      constexpr uint32_t idesc_qk = make_idesc(1, 1, 0, 0, kTileKeys, kRowTile);
+      constexpr uint32_t idesc_qk = make_idesc(1, 1, 0, 0, kKeys, kRowTile);
       constexpr uint32_t idesc_pv = make_idesc(1, 1, 0, 1, 256, kRowTile);
-      const uint64_t dq = smem_desc_sw128(sbase + kOffQ, 16, 1024);
-      const uint64_t dk = smem_desc_sw128(sbase + kOffK, 16, 1024);
-      const uint64_t dp = smem_desc_sw128(sbase + kOffP, 16, 1024);
-      const uint64_t dv = smem_desc_sw128(sbase + kOffV, kAtom, 1024);
+      const uint64_t dq = smem_desc_sw128(sbase + T::kOffQ, 16, 1024);
+      const uint64_t dk = smem_desc_sw128(sbase + T::kOffK, 16, 1024);
+      const uint64_t dp = smem_desc_sw128(sbase + T::kOffP, 16, 1024);
+      const uint64_t dv = smem_desc_sw128(sbase + T::kOffV, kAtom, 1024);
       bool ok = true;
       int it = 0, npv = 0;
       // P V of tile npv (its stretch's first: the output starts at zero, once
       // the epilogue has read the stretch before).
       int pv_seg = 0, pv_left = 0;
-      Walk pvw = wk;
+      Walk<kKeys> pvw = wk;
       auto issue_pv = [&]() -> bool {
         uint32_t fresh = 0;
         if (pv_left == 0) {
@@ -441,7 +491,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
         if (!warp_wait(P_FULL, npv & 1)) return false;
         tc_fence_after();
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < T::kPages; ++h) {
 #pragma unroll
           for (int j = 0; j < kPage / 16; ++j)
 #pragma unroll
@@ -469,12 +519,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
             if (!(ok = ok && warp_wait(K_FULL(g), it & 1))) break;
             tc_fence_after();
 #pragma unroll
-            for (int a = group_atom<kFp8>(g); a < group_atom<kFp8>(g + 1); ++a)
+            for (int a = T::group_atom(g); a < T::group_atom(g + 1); ++a)
 #pragma unroll
               for (int j = 0; j < 4; ++j)
-                mma_f16_ss_2cta(tmem + kColS + 64 * (it & 1),
+                mma_f16_ss_2cta(tmem + kColS + T::kHalf * (it & 1),
                                 dq + static_cast<uint64_t>((a * kAtom + j * 32) >> 4),
-                                dk + static_cast<uint64_t>((a * kAtom + j * 32) >> 4), idesc_qk,
+                                dk + static_cast<uint64_t>((a * T::kKAtom + j * 32) >> 4), idesc_qk,
                                 (a > 0 || j > 0) ? 1u : 0u, el);
             if (el) tc_commit_2cta(K_EMPTY(g), 3);
             __syncwarp();
@@ -506,163 +556,131 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
   }
   } else if (kFp8 && warp >= 8) {
     // ------------------------------------------- FP8 rows to bf16 operands
-    // A warp has 8 rows of a page and takes two at a time: lane = row r2 of the
-    // two, and 16-code chunk c of 256 bytes of it.  Eight neighbouring lanes
-    // hold an atom's four chunks of both rows: whose swizzled pieces fall on
-    // distinct banks.
-    const int r2 = (lane >> 2) & 1, c = (lane & 3) | ((lane >> 3) << 2), row0 = (warp & 7) * 8;
+    // A warp takes two rows at a time: lane = row r2 of the two and 16-code
+    // chunk c of two 128-dim tiles of it.  Eight neighbouring lanes hold four
+    // chunks of each row, of different halves of the tile (reads) and with
+    // different swizzles (writes): both fall on distinct banks.
+    const int r2 = (lane >> 2) & 1, c = ((lane & 3) | ((lane >> 3) << 2)) ^ (r2 << 2);
+    const bool for_k = warp < 8 + kDequantWarps;
+    const int w = warp & (kDequantWarps - 1);
+    // K: rows 4 w .. of this CTA's 32, of dims 0-255, then 256-511.  V: rows 8 w
+    // .. of 64, of this CTA's value dims (code tiles rank and 2 + rank).
+    const int row0 = (for_k ? 4 : 8) * w + r2;
+    const bool own = for_k || (w >> 2) == static_cast<int>(rank);
+    const uint32_t k_full0 = mapa_shared(K_FULL(0), 0);
     bool ok = true;
     int it = 0;
-    auto rows_of = [&](int page) {
-      return p.kv8 + (static_cast<long long>(max(0, page)) * kPage + row0 + r2) * kF8RowBytes;
-    };
-    // The chunk's 16 bf16 values: pair k's row at `base` (atoms kAtom apart).
-    const int row_off = (c >> 2) * kAtom + (row0 + r2) * 128;
-    auto store = [&](uint8_t* base, int k, const uint4& lo, const uint4& hi) {
-      uint8_t* at = base + row_off + 256 * k;
-      const int piece = (2 * (c & 3)) ^ ((2 * k + r2) & 7);
-      *reinterpret_cast<uint4*>(at + (piece << 4)) = lo;
-      *reinterpret_cast<uint4*>(at + ((piece ^ 1) << 4)) = hi;
-    };
     setmaxnreg_dec<kRegsDequant>();
-    if (warp < 8 + kDequantWarps) {
-      const uint32_t k_full0 = mapa_shared(K_FULL(0), 0);
-      uint4 raw[8];       // 4 row pairs of dims 0-255, then of 256-511
-      float sc = 0.f;     // scales of the 8 rows: lane = pair, row r2, tile
-      while (ok && wk.next(p)) {
-        PageBatch pages(p, wk, lane);
-        auto code_at = [&](const uint8_t* rows, int k) {
-          return __ldg(reinterpret_cast<const uint4*>(rows + 2 * (k & 3) * kF8RowBytes + 256 * (k >> 2)) + c);
-        };
-        auto scale_at = [&](const uint8_t* rows) {
-          return __ldg(reinterpret_cast<const float*>(rows + (lane >> 3) * 2 * kF8RowBytes + kF8ScaleOff) +
-                       (lane & 3));
-        };
-        for (int t = wk.t0; ok && t < wk.t1; ++t, ++it) {
-          pages.advance(t, lane);
-          if (t == wk.t0) {
-            const uint8_t* rows = rows_of(pages.page(t, rank));
+    while (ok && wk.next(p)) {
+      PageBatch<T::kPages> pages(p, wk, lane);
+      for (int t = wk.t0; ok && t < wk.t1; ++t, ++it) {
+        const int st = it % kRawStages;
+        const uint8_t* stage = smem + T::kOffRaw + st * kRawBytes;
+        const float* scales = reinterpret_cast<const float*>(stage + 6 * kRawTile);
+        pages.advance(t, lane);
+        if (!mbar_wait(RAW_FULL(st), (it / kRawStages) & 1)) ok = false;
+        uint4 raw[4];
+        float scale[4];
+        if (for_k) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) raw[k] = code_at(rows, k);
-            sc = scale_at(rows);
+          for (int u = 0; u < 4; ++u) {
+            const int row = row0 + 2 * (u & 1), tile = 2 * (u >> 1) + (c >> 3);
+            raw[u] = *reinterpret_cast<const uint4*>(stage + tile * kRawTile + row * 128 + (c & 7) * 16);
+            scale[u] = scales[(32 * rank + row) * 4 + tile];
           }
-          // The next tile's page (behind the stretch: page 0) is fetched as this
-          // one is used up.
-          const uint8_t* ahead = rows_of(pages.page(t, rank, true));
-          const float nsc = scale_at(ahead);
+        } else {
+          // Rows that no query sees are zero, whatever the cache holds.
+          const int live = pages.page(t, 0) >= 0 ? wk.len - t * kKeys : 0;
+          const uint8_t* src = stage + (own ? rank + 2 * (c >> 3) : 4 + (c >> 3)) * kRawTile + (c & 7) * 16;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int row = row0 + 2 * u;
+            raw[u] = *reinterpret_cast<const uint4*>(src + (row & 31) * 128);
+            scale[u] = scales[row * 4 + rank + 2 * (c >> 3)];
+            if (row >= live) {
+              raw[u] = make_uint4(0u, 0u, 0u, 0u);
+              scale[u] = 0.f;
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(RAW_EMPTY(st));
+        if (for_k) {
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
             if (it >= 1 && ok && !mbar_wait(K_EMPTY(g), (it - 1) & 1)) ok = false;
+            uint8_t* dst = smem + T::kOffK + (4 * g + (c >> 2)) * T::kKAtom;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float scale = __shfl_sync(0xffffffffu, sc, k * 8 + r2 * 4 + 2 * g + (c >> 3));
+            for (int u = 2 * g; u < 2 * g + 2; ++u) {
+              const int row = row0 + 2 * (u & 1), piece = (2 * (c & 3)) ^ (row & 7);
               uint4 lo, hi;
-              dequant16(raw[4 * g + k], scale, lo, hi);
-              raw[4 * g + k] = code_at(ahead, 4 * g + k);
-              store(smem + kOffK + 4 * g * kAtom, k, lo, hi);
+              dequant16(raw[u], scale[u], lo, hi);
+              *reinterpret_cast<uint4*>(dst + row * 128 + (piece << 4)) = lo;
+              *reinterpret_cast<uint4*>(dst + row * 128 + ((piece ^ 1) << 4)) = hi;
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive_remote_async(k_full0 + 8u * g);
           }
-          sc = nsc;
-          ok = __all_sync(0xffffffffu, ok);
-        }
-      }
-    } else {
-      // Output dims of P V's two MMAs: 256 n + 128 rank .. + 127, code tiles
-      // rank (chunks c < 8) and 2 + rank.
-      const int off = 128 * static_cast<int>(rank) + (c < 8 ? 0 : 256) + (c & 7) * 16;
-      const int sc_row = (lane >> 3) * 2, sc_tile = rank + (lane & 2);
-      uint4 raw[8];       // 4 row pairs of either page
-      float sc[2];        // scales of a page's 8 rows: lane = pair, row r2, tile
-      while (ok && wk.next(p)) {
-        PageBatch pages(p, wk, lane);
-        // Rows that no query sees are zero, whatever the cache holds: they are
-        // not fetched.  (live: rows of this warp's 8, from this lane's first.)
-        auto code_at = [&](const uint8_t* rows, int k, int live) {
-          return 2 * k < live ? __ldg(reinterpret_cast<const uint4*>(rows + 2 * k * kF8RowBytes + off))
-                              : make_uint4(0u, 0u, 0u, 0u);
-        };
-        auto scale_at = [&](const uint8_t* rows, int live) {
-          return sc_row < live ? __ldg(reinterpret_cast<const float*>(rows + sc_row * kF8RowBytes + kF8ScaleOff) +
-                                       sc_tile)
-                               : 0.f;
-        };
-        auto live_of = [&](int t, int h, int page) {
-          return page >= 0 ? wk.len - t * kTileKeys - kPage * h - row0 - r2 : 0;
-        };
-        for (int t = wk.t0; ok && t < wk.t1; ++t, ++it) {
-          pages.advance(t, lane);
+        } else {
+          if (it >= 1 && ok && !mbar_wait(V_EMPTY(0), (it - 1) & 1)) ok = false;
+          uint8_t* dst = smem + T::kOffV + (c >> 2) * kAtom;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (t == wk.t0) {
-              const int page = pages.page(t, h), live = live_of(t, h, page);
-              const uint8_t* rows = rows_of(page);
-#pragma unroll
-              for (int k = 0; k < 4; ++k) raw[4 * h + k] = code_at(rows, k, live);
-              sc[h] = scale_at(rows, live);
-            }
-            const int page = pages.page(t, h, true), live = live_of(t + 1, h, page);
-            const uint8_t* ahead = rows_of(page);
-            const float nsc = scale_at(ahead, live);
-            if (it >= 1 && ok && !mbar_wait(V_EMPTY(h), (it - 1) & 1)) ok = false;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float scale = __shfl_sync(0xffffffffu, sc[h], (k << 3) | (r2 << 2) | ((c >> 3) << 1));
-              uint4 lo, hi;
-              dequant16(raw[4 * h + k], scale, lo, hi);
-              raw[4 * h + k] = code_at(ahead, k, live);
-              store(smem + kOffV + h * kVBytes, k, lo, hi);
-            }
-            sc[h] = nsc;
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(V_FULL(h));
+          for (int u = 0; u < 4; ++u) {
+            const int row = row0 + 2 * u, piece = (2 * (c & 3)) ^ (row & 7);
+            uint4 lo, hi;
+            dequant16(raw[u], scale[u], lo, hi);
+            *reinterpret_cast<uint4*>(dst + row * 128 + (piece << 4)) = lo;
+            *reinterpret_cast<uint4*>(dst + row * 128 + ((piece ^ 1) << 4)) = hi;
           }
-          ok = __all_sync(0xffffffffu, ok);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(V_FULL(0));
         }
+        ok = __all_sync(0xffffffffu, ok);
       }
     }
     if (!ok && lane == 0) raise_error(kErrTimeout);
   } else {
     // ---------------------------------------------- softmax and epilogue
     if constexpr (kFp8) setmaxnreg_inc<kRegsSoft>();
-    const int tid = threadIdx.x - 128;             // = TMEM lane; half: page of the tile, half of O's dims
+    const int tid = threadIdx.x - 128;             // = TMEM lane; half: of the tile's keys, and of O's dims
     const int w4 = warp & 3;
     const int row = tid & 63, half = tid >> 6;
     const uint32_t lanebase = static_cast<uint32_t>(w4 * 32) << 16;
     const int rrow = mtile * kRowTile + kRowsCta * static_cast<int>(rank) + row;   // row of the request
     const bool live = rrow < rows_req;
     const int qi = live ? rrow / p.heads : 0;
-    float* xchg = reinterpret_cast<float*>(smem + kOffXchg);
+    float* xchg = reinterpret_cast<float*>(smem + T::kOffXchg);
     const uint32_t p_full = mapa_shared(P_FULL, 0), o_free = mapa_shared(O_FREE, 0);
     const float sc = p.sm_scale * kLog2e;
     bool ok = true;
     int it = 0;
     while (wk.next(p)) {
-      PageBatch pages(p, wk, lane);
+      PageBatch<T::kPages> pages(p, wk, lane);
       const int vis = live ? wk.len - (p.nq - 1 - qi) : 0;
       float mrun = ninf, lrun = 0.f;      // maximum and sum (this thread's keys) in the exp2 domain
       uint32_t good = 0;                  // validity of the next 32 page ids
       for (int t = wk.t0; t < wk.t1; ++t, ++it) {
-        const int b = it & 1, u = (t - wk.t0) & 15;
+        const int b = it & 1;
         if (pages.advance(t, lane)) good = __ballot_sync(0xffffffffu, pages.now >= 0);
-        const uint32_t ok2 = good >> (2 * u);          // bit h: page h of the tile can be read
+        // Bit h: page h of the tile can be read.
+        const uint32_t ok2 = good >> (T::kPages * ((t - wk.t0) & (32 / T::kPages - 1)));
         if (ok && !mbar_wait(S_FULL(b), (it >> 1) & 1)) ok = false;
         tc_fence_after();
-        uint32_t sr[64];
-        tmem_ld64(tmem + lanebase + kColS + 64 * b, sr);
-        // Visible keys among this thread's 64.
-        const int seen = ((ok2 >> half) & 1u) ? vis - t * kTileKeys - kPage * half : 0;
+        uint32_t sr[T::kHalf];
+        if constexpr (kFp8) tmem_ld32(tmem + lanebase + kColS + T::kHalf * b, sr);
+        else tmem_ld64(tmem + lanebase + kColS + T::kHalf * b, sr);
+        // Visible keys among this thread's.
+        const int seen = ((ok2 >> (kFp8 ? 0 : half)) & 1u) ? vis - t * kKeys - T::kHalf * half : 0;
         float tmax = ninf;
-        if (seen >= kPage) {
+        if (seen >= T::kHalf) {
 #pragma unroll
-          for (int j = 0; j < kPage; j += 2)
+          for (int j = 0; j < T::kHalf; j += 2)
             tmax = max3(tmax, __uint_as_float(sr[j]), __uint_as_float(sr[j + 1]));
         } else {
 #pragma unroll
-          for (int j = 0; j < kPage; ++j) {
+          for (int j = 0; j < T::kHalf; ++j) {
             if (j >= seen) sr[j] = __float_as_uint(ninf);
             tmax = fmaxf(tmax, __uint_as_float(sr[j]));
           }
@@ -676,7 +694,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
         const bool rescale = raise && mrun > ninf;
         if (__any_sync(0xffffffffu, rescale)) {
           // P V of the tile before has to be in the output first.
-          if (ok && !mbar_wait(V_EMPTY(1), (it - 1) & 1)) ok = false;
+          if (ok && !mbar_wait(V_EMPTY(T::kPages - 1), (it - 1) & 1)) ok = false;
           tc_fence_after();
           const float f = rescale ? ex2(mrun - tmax) : 1.f;
 #pragma unroll 1
@@ -693,11 +711,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
         const float mref = mrun > ninf ? mrun : 0.f;
         // P of the tile before has been read: its P V runs before the next Q K^T,
         // which the exponentials then have to hide in.
-        if (it >= 1 && ok && !mbar_wait(V_EMPTY(1), (it - 1) & 1)) ok = false;
-        uint8_t* prow = smem + kOffP + half * kAtom + row * 128;
+        if (it >= 1 && ok && !mbar_wait(V_EMPTY(T::kPages - 1), (it - 1) & 1)) ok = false;
+        uint8_t* prow = smem + T::kOffP + (kFp8 ? 0 : half * kAtom) + row * 128;
+        const int chunk0 = kFp8 ? 4 * half : 0;
         float2 ls = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
+        for (int c = 0; c < T::kHalf / 8; ++c) {
           uint32_t pk[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -707,16 +726,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
             ls = add2(ls, e);
             pk[j] = pack_bf16x2(e.x, e.y);
           }
-          *reinterpret_cast<uint4*>(prow + ((c ^ (row & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+          *reinterpret_cast<uint4*>(prow + (((chunk0 + c) ^ (row & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
         }
         lrun += ls.x + ls.y;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < T::kPages; ++h) {
           if (ok && !mbar_wait(V_FULL(h), it & 1)) ok = false;
           // Rows of V behind every query's view are cleared.
-          const int vlive = ((ok2 >> h) & 1u) ? wk.len - t * kTileKeys - kPage * h : 0;
+          const int vlive = ((ok2 >> h) & 1u) ? wk.len - t * kKeys - kPage * h : 0;
           if (!kFp8 && vlive < kPage) {
-            uint4* v = reinterpret_cast<uint4*>(smem + kOffV + h * kVBytes);
+            uint4* v = reinterpret_cast<uint4*>(smem + T::kOffV + h * kVBytes);
             for (int e = tid; e < kVBytes / 16; e += 128)
               if (((e >> 3) & (kPage - 1)) >= vlive) v[e] = make_uint4(0u, 0u, 0u, 0u);
           }
@@ -727,7 +746,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
         if (lane == 0) mbar_arrive_remote_async(p_full);
       }
       // ---------------------------------------------------------- epilogue
-      if (ok && !mbar_wait(V_EMPTY(1), (it - 1) & 1)) ok = false;
+      if (ok && !mbar_wait(V_EMPTY(T::kPages - 1), (it - 1) & 1)) ok = false;
       tc_fence_after();
       // Row sum over both halves (the buffer that the last tile did not use).
       xchg[(it & 1) * 128 + tid] = lrun;
@@ -742,47 +761,65 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
       const long long slot = (static_cast<long long>(worker) * 2 + (wk.t0 > 0 ? 0 : 1)) * kRowTile +
                              kRowsCta * static_cast<int>(rank) + row;
       if (whole_warp) {
-        // 32 rows at once: staged in this warp's part of the P tile (128B
-        // swizzled, so that eight rows' 16-byte pieces fall on distinct banks)
-        // and written by a tensor store a chunk of 128 bytes a row.  Stored
-        // from registers, every instruction touches 32 lines: 4 us for a
-        // stretch's 64 x 512 floats.
-        uint8_t* stage = smem + kOffP + half * kAtom + (row & 32) * 128;
+        // 32 rows at once: staged in this warp's part of the P tile (swizzled, so
+        // that rows' 16-byte pieces fall on distinct banks) and written by a
+        // tensor store a chunk of kStageRow bytes a row.  Stored from registers,
+        // every instruction touches 32 lines: 4 us for a stretch's 64 x 512
+        // floats.  (FP8: the two warps of a row share 4 KB of P, and write it
+        // again only after the barrier of the next tile's maximum.)
+        uint8_t* stage = smem + T::kOffP + (row & 32) * 128 + half * (kFp8 ? 2048 : kAtom);
         const uint32_t stage_s = smem_u32(stage);
         const int row_w = static_cast<int>((whole ? grow : slot) - lane);
-#pragma unroll 1
-        for (int c = 0; c < 8; ++c) {
-          uint32_t o[32];
-          tmem_ld32(tmem + lanebase + kColO + 32 * c, o);
-          const bool start = !whole || (c & 1) == 0, end = !whole || (c & 1) == 1;
-          if (start) {
+        // Pieces [p0, p0 + n) of the lane's row; the first one of a chunk waits
+        // for the store before, the last one stores.
+        auto put = [&](const uint32_t* v, int p0, int n) {
+          if (p0 == 0) {
             if (lane == 0) bulk_wait_read_all();
             __syncwarp();
           }
 #pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            if (e >= n) break;
+            const int piece = kFp8 ? (p0 + e) ^ ((lane >> 1) & 3) : (p0 + e) ^ (lane & 7);
+            *reinterpret_cast<uint4*>(stage + lane * T::kStageRow + (piece << 4)) =
+                make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+          }
+        };
+        auto flush = [&](int dim) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(whole ? &tmap_out : &tmap_part, stage_s, dim, row_w);
+            bulk_commit();
+          }
+        };
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) {
+          uint32_t o[32];
+          tmem_ld32(tmem + lanebase + kColO + 32 * c, o);
+          const int dim = 256 * (c >> 2) + 128 * half + 32 * (c & 3);
+#pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
           if (whole) {
+            uint32_t h[16];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * (c & 1) + e) ^ (lane & 7)) << 4)) =
-                  make_uint4(pack_bf16x2(__uint_as_float(o[8 * e]), __uint_as_float(o[8 * e + 1])),
-                             pack_bf16x2(__uint_as_float(o[8 * e + 2]), __uint_as_float(o[8 * e + 3])),
-                             pack_bf16x2(__uint_as_float(o[8 * e + 4]), __uint_as_float(o[8 * e + 5])),
-                             pack_bf16x2(__uint_as_float(o[8 * e + 6]), __uint_as_float(o[8 * e + 7])));
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              *reinterpret_cast<uint4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) =
-                  make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-          }
-          if (end) {
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              const int dim = 256 * (c >> 2) + 128 * half + (whole ? 64 * ((c >> 1) & 1) : 32 * (c & 3));
-              tma_store_2d(whole ? &tmap_out : &tmap_part, stage_s, dim, row_w);
-              bulk_commit();
+            for (int e = 0; e < 16; ++e)
+              h[e] = pack_bf16x2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+            if constexpr (kFp8) {
+              put(h, 0, 4);
+              flush(dim);
+            } else {
+              put(h, 4 * (c & 1), 4);
+              if (c & 1) flush(dim - 32);
             }
+          } else if constexpr (kFp8) {
+            put(o, 0, 4);
+            flush(dim);
+            put(o + 16, 0, 4);
+            flush(dim + 16);
+          } else {
+            put(o, 0, 8);
+            flush(dim);
           }
         }
         if (lane == 0) bulk_wait_read_all();      // before the next P is written there
@@ -838,6 +875,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
 #undef V_FULL
 #undef V_EMPTY
 #undef S_FULL
+#undef RAW_FULL
+#undef RAW_EMPTY
 #undef P_FULL
 }
 
@@ -903,7 +942,7 @@ __global__ void __launch_bounds__(kMergeThreads) mla_merge_kernel(const MlaDecod
   if (p.lse && c4 == 0) p.lse[grow] = any ? mx + log2f(tot) * kLn2 : ninf;
 }
 
-constexpr int kMinTiles = 2;   // key tiles a group takes at least
+constexpr int kMinKeys = 256;   // of a group's part of the line, at least
 
 }  // namespace
 
@@ -921,7 +960,6 @@ void mla_decode_plan(int nq, int heads, int* row_tiles, int* groups, size_t* ws_
 cudaError_t launch_mla_decode(MlaDecodeLaunch a, void* ws, cudaStream_t s) {
   size_t bytes;
   mla_decode_plan(a.nq, a.heads, &a.row_tiles, &a.groups, &bytes);
-  a.min_tiles = kMinTiles;
   a.part_o = static_cast<float*>(ws);
   const size_t slots = static_cast<size_t>(a.groups) * a.row_tiles * 2 * kRowTile;
   a.part_lse = a.part_o + slots * kVDim;
@@ -935,38 +973,48 @@ cudaError_t launch_mla_decode(MlaDecodeLaunch a, void* ws, cudaStream_t s) {
   const uint32_t qbox[3] = {64, kRowsCta, kAtoms}, kbox[3] = {64, kPage, kGroupAtoms},
                  vbox[3] = {64, kPage, 2};
   const bool fp8 = a.kv8 != nullptr;
-  CUtensorMap tq, tk, tv;
+  a.min_tiles = kMinKeys / (fp8 ? Tile<true>::kKeys : Tile<false>::kKeys);
+  CUtensorMap tq, tk, tv, ts;
   if (!encode_tmap_nd(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, 3, qdims, strides, qbox,
                       CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   if (fp8) {
-    // The rope dims of the rows as bytes, laid out like a bf16 atom.
+    // The rows as bytes: the rope dims laid out like a bf16 atom, the codes of
+    // 32 rows x 128 dims, and the scales.
     const uint64_t rdims[3] = {kF8RowBytes, crows, 1}, rstr[2] = {kF8RowBytes, crows * kF8RowBytes};
-    const uint32_t rbox[3] = {128, kPage, 1};
+    const uint64_t tdims[3] = {128, crows, 4}, tstr[2] = {kF8RowBytes, 128};
+    const uint32_t rbox[3] = {128, 32, 1}, tbox[3] = {128, 32, 1}, sbox[3] = {16, kPage, 1};
     if (!encode_tmap_nd(&tk, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.kv8, 3, rdims, rstr, rbox,
-                        CU_TENSOR_MAP_SWIZZLE_128B))
+                        CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_tmap_nd(&tv, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.kv8, 3, tdims, tstr, tbox,
+                        CU_TENSOR_MAP_SWIZZLE_NONE) ||
+        !encode_tmap_nd(&ts, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.kv8, 3, rdims, rstr, sbox,
+                        CU_TENSOR_MAP_SWIZZLE_NONE))
       return cudaErrorInvalidValue;
-    tv = tk;
   } else if (!encode_tmap_nd(&tk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.kv, 3, cdims, strides, kbox,
                              CU_TENSOR_MAP_SWIZZLE_128B) ||
              !encode_tmap_nd(&tv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.kv, 3, cdims, strides, vbox,
                              CU_TENSOR_MAP_SWIZZLE_128B)) {
     return cudaErrorInvalidValue;
   }
+  if (!fp8) ts = tq;      // not used
   CUtensorMap to, tp;
   const uint64_t odims[2] = {kVDim, qrows}, ostr[1] = {kVDim * 2};
   const uint64_t pdims[2] = {kVDim, slots}, pstr[1] = {kVDim * 4};
-  const uint32_t obox[2] = {64, 32}, pbox[2] = {32, 32};
+  const uint32_t stage_row = fp8 ? Tile<true>::kStageRow : Tile<false>::kStageRow;
+  const uint32_t obox[2] = {stage_row / 2, 32}, pbox[2] = {stage_row / 4, 32};
+  const CUtensorMapSwizzle swz = fp8 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
   if (!encode_tmap_nd(&to, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.out, 2, odims, ostr, obox,
-                      CU_TENSOR_MAP_SWIZZLE_128B) ||
+                      swz) ||
       !encode_tmap_nd(&tp, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.part_o, 2, pdims, pstr, pbox,
-                      CU_TENSOR_MAP_SWIZZLE_128B))
+                      swz))
     return cudaErrorInvalidValue;
+  const int smem = fp8 ? Tile<true>::kSmemBytes : Tile<false>::kSmemBytes;
   auto kern = fp8 ? mla_decode_kernel<true> : mla_decode_kernel<false>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  e = launch_kernel(kern, dim3(2 * a.groups * a.row_tiles), dim3(fp8 ? kThreadsFp8 : kThreads), kSmemBytes, s,
-                    false, 1, tq, tk, tv, to, tp, a);
+  e = launch_kernel(kern, dim3(2 * a.groups * a.row_tiles), dim3(fp8 ? kThreadsFp8 : kThreads), smem, s,
+                    false, 1, tq, tk, tv, ts, to, tp, a);
   if (e != cudaSuccess || a.groups == 1) return e;
   const int chunks = (a.nq * a.heads + kMergeRows - 1) / kMergeRows;
   return launch_kernel(mla_merge_kernel, dim3(a.groups - 1, chunks), dim3(kMergeThreads), 0, s, true, 1, a);

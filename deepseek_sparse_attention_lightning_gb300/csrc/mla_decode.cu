@@ -114,7 +114,7 @@ constexpr int kSoftWarps = 4;
 // FP8: eight warps dequantise for K, eight for V.  Registers a thread (launched
 // with 80 each): copies and MMAs, softmax, dequantisation.
 constexpr int kDequantWarps = 8;
-constexpr int kRegsMma = 64, kRegsSoft = 128, kRegsDequant = 72;
+constexpr int kRegsMma = 64, kRegsSoft = 96, kRegsDequant = 80;
 static_assert(kRegsMma + kRegsSoft + 4 * kRegsDequant <= 6 * 80, "registers");
 constexpr float kRaiseLog2 = 8.0f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;

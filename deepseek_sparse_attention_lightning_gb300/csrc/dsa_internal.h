@@ -124,6 +124,7 @@ struct MlaPrefillLaunch {
   float* lse;                    // [total_q][H] or nullptr
   long long ld_rope;
   int batch, heads, total_q, total_k, max_q, causal;
+  int out_wide;                  // set by launch_mla_prefill: out is 32-byte aligned
   float sm_scale;
 };
 
@@ -140,7 +141,7 @@ cudaError_t launch_rmsnorm(const RmsNormLaunch& a, cudaStream_t s);
 // pairs, workspace bytes; no kernel) and its launch.
 void mla_decode_plan(int nq, int heads, int* row_tiles, int* groups, size_t* ws_bytes);
 cudaError_t launch_mla_decode(MlaDecodeLaunch a, void* ws, cudaStream_t s);
-cudaError_t launch_mla_prefill(const MlaPrefillLaunch& a, cudaStream_t s);
+cudaError_t launch_mla_prefill(MlaPrefillLaunch a, cudaStream_t s);
 cudaError_t launch_merge(int rows, int splits, const float* mid_o, const float* mid_lse,
                          float* out, float* out_lse, cudaStream_t s, bool pdl = false);
 

@@ -27,8 +27,8 @@
 // MMA order: QK0(j), PV1(j-1), QK1(j), PV0(j), QK0(j+1), ...: a tile's softmax
 // has the other tile's P V and Q K^T (1280 cycles of matrix work) to hide in.
 //
-// A grid of one CTA for each 256 queries of a head, late queries (most keys)
-// first within a head; but a CTA that runs goes on with the work of CTAs that
+// A grid of one CTA for each 256 queries of a head (and at most one more a
+// request), late queries (most keys) first within a request; but a CTA that runs goes on with the work of CTAs that
 // have not started (a request for one is under way while the CTA works), so
 // that its copies run into the next item while this one's last tiles and
 // output are under way, and the SMs end close together.
@@ -98,22 +98,37 @@ struct Item {
 };
 static_assert(sizeof(Item) <= 48, "record");
 
-__device__ __forceinline__ Item item_of(const MlaPrefillLaunch& p, int x, int y, int z) {
+// Request r begins at slot cu_q[r] / 256 + r of the grid's x: that leaves it as
+// many slots as it has blocks of 256 queries, or one more, and the slot of a CTA
+// needs no walk over the requests before it to find its own.
+__device__ __forceinline__ int first_slot(const MlaPrefillLaunch& p, int r) {
+  return max(0, __ldg(p.cu_q + r)) / kCtaRows + r;
+}
+
+__device__ __forceinline__ Item item_of(const MlaPrefillLaunch& p, int x, int y) {
+  int lo = 0, hi = p.batch;      // first_slot(lo) <= x < first_slot(hi), were it asked
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (first_slot(p, mid) <= x) lo = mid;
+    else hi = mid;
+  }
   Item it;
   it.base = 0;
   it.head = y;
-  const int blocks = gridDim.x;
-  it.row0 = (blocks - 1 - x) * kCtaRows;      // late queries see the most keys: they start first
-  it.q0 = __ldg(p.cu_q + z);
-  it.k0 = __ldg(p.cu_k + z);
-  it.qlen = __ldg(p.cu_q + z + 1) - it.q0;
-  it.klen = max(0, __ldg(p.cu_k + z + 1) - it.k0);
+  it.q0 = __ldg(p.cu_q + lo);
+  it.k0 = __ldg(p.cu_k + lo);
+  it.qlen = __ldg(p.cu_q + lo + 1) - it.q0;
+  it.klen = max(0, __ldg(p.cu_k + lo + 1) - it.k0);
+  // Late queries see the most keys: they start first.
+  const int slots = max(0, it.q0 + it.qlen) / kCtaRows - max(0, it.q0) / kCtaRows + 1;
+  it.row0 = (slots - 1 - (x - first_slot(p, lo))) * kCtaRows;
   // Offsets outside the packed tensors, or a length above max_q, are reported;
   // the request's rows are left as they were, or not all of them written.
   const bool bad = it.q0 < 0 || it.k0 < 0 || it.qlen < 0 || it.qlen > p.total_q - it.q0 ||
                    it.klen > p.total_k - it.k0;
-  if (bad || it.qlen > blocks * kCtaRows) raise_error(kErrCheck);
-  it.work = !bad && it.row0 < it.qlen ? 1 : 0;
+  const bool far = it.row0 >= (p.max_q + kCtaRows - 1) / kCtaRows * kCtaRows;
+  it.work = !bad && !far && it.row0 >= 0 && it.row0 < it.qlen ? 1 : 0;
+  if (bad || (far && it.row0 < it.qlen)) raise_error(kErrCheck);
   auto tiles_from = [&](int first) {
     if (!it.work || first >= it.qlen) return 0;
     const int lim = key_limit(min(first + kTile, it.qlen) - 1, it.qlen, it.klen, p.causal);
@@ -200,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int n = 0;                                          // granules so far
       int uses0 = 0, uses1 = 0;                           // items that had each query tile
       const uint64_t pol_rope = policy_evict_last();      // every head reads it
-      Item it = item_of(p, blockIdx.x, blockIdx.y, blockIdx.z);
+      Item it = item_of(p, blockIdx.x, blockIdx.y);
       int base = 0, k = 0, asked = 0;
       bool more = true;
       while (ok) {
@@ -248,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t x, y, z;
         more = taken_cta(sbase + kOffTaken, x, y, z);
         fence_proxy_async_smem();      // read before the next answer is written there
-        if (more) it = item_of(p, x, y, z);
+        if (more) it = item_of(p, x, y);
       }
       if (!ok) raise_error(kErrTimeout);
       // No copy is in flight when the CTA ends.
@@ -521,15 +536,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t o[32];
         if (n > 0) tmem_ld32(tO + 32 * c, o);
         if (!live) continue;
+        uint32_t w[2][8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t w[4];
+        for (int e = 0; e < 16; ++e)
+          w[e >> 3][e & 7] =
+              any ? pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv) : 0u;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            w[i] = any ? pack_bf16x2(__uint_as_float(o[8 * e + 2 * i]) * inv,
-                                     __uint_as_float(o[8 * e + 2 * i + 1]) * inv)
-                       : 0u;
-          dst[4 * c + e] = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int e = 0; e < 2; ++e) {
+          if (p.out_wide) {
+            st_global_32(dst + 4 * c + 2 * e, w[e]);
+          } else {
+            dst[4 * c + 2 * e] = make_uint4(w[e][0], w[e][1], w[e][2], w[e][3]);
+            dst[4 * c + 2 * e + 1] = make_uint4(w[e][4], w[e][5], w[e][6], w[e][7]);
+          }
         }
       }
       if (live && p.lse) p.lse[at] = any ? (mrun + log2f(lrun)) * kLn2 : ninf;
@@ -563,7 +582,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
-cudaError_t launch_mla_prefill(const MlaPrefillLaunch& a, cudaStream_t s) {
+cudaError_t launch_mla_prefill(MlaPrefillLaunch a, cudaStream_t s) {
+  // Outputs of a thread's row are stored 32 bytes (a whole sector) at a time
+  // where they are aligned so.
+  a.out_wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
   const uint64_t H = a.heads, Tq = a.total_q, Tk = a.total_k > 0 ? a.total_k : 1;
   // Rows as 64-dim atoms (a box: 128 rows of one or three atoms of a head).
   const uint64_t qdims[4] = {64, Tq, kQAtoms, H}, qstr[3] = {H * 384, 128, 384};
@@ -580,7 +602,7 @@ cudaError_t launch_mla_prefill(const MlaPrefillLaunch& a, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(mla_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        kSmemBytes);
   if (e != cudaSuccess) return e;
-  const dim3 grid((a.max_q + kCtaRows - 1) / kCtaRows, a.heads, a.batch);
+  const dim3 grid(a.total_q / kCtaRows + a.batch, a.heads);
   return launch_kernel(mla_prefill_kernel, grid, dim3(kThreads), kSmemBytes, s, false, 1, tq, tk, tr, a);
 }
 

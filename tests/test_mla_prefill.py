@@ -217,3 +217,30 @@ def test_binding_checks(L):
         call(out=out[:10])
     with pytest.raises(ValueError, match="lse:"):
         call(lse=torch.empty((20, 5), device="cuda"))
+
+
+@pytest.mark.gpu
+def test_an_output_off_32_bytes(L):
+    """Outputs are stored 32 bytes at a time where they are aligned so; 16 bytes suffice."""
+    c = _case([130, 40], [300, 40], 3, seed=9)
+    want, _ = _run(c, True)
+    n = want.numel()
+    buf = torch.full((n + 16,), 77.0, dtype=torch.bfloat16, device="cuda")
+    for off in (8, 16):
+        out = buf[off:off + n].view(want.shape)
+        assert out.data_ptr() % 32 == (16 if off == 8 else 0)
+        api.dsa_mla_prefill(c["q"], c["kv"], c["rope"], c["cu_q"], c["cu_k"], out, c["max_q"], SM)
+        assert torch.equal(out[:170], want[:170])
+        assert (buf[:off] == 77).all() and (buf[off + n:] == 77).all()
+        buf.fill_(77.0)
+
+
+@pytest.mark.gpu
+def test_many_short_requests_and_a_long_one(L):
+    qlens = [(i * 7) % 5 for i in range(700)]
+    qlens[333] = 1900
+    klens = [n + (i % 3) * 50 for i, n in enumerate(qlens)]
+    c = _case(qlens, klens, 2, seed=10)
+    out, lse = _run(c, True)
+    assert api.dsa_get_device_error() == 0
+    _check(c, True, out, lse, heads=[1])

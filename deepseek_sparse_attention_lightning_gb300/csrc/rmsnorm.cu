@@ -7,9 +7,10 @@
 //   code = E4M3(y / scale), rounded to nearest even and saturated.
 //
 // Everything between the loads and the outputs is fp32: h is rounded only where
-// it is stored as the next residual, y only where it is stored in bf16, and the
-// codes are quantised from the unrounded y (two roundings would move codes
-// that lie near a border).  A tile is 128 columns (the 1 x 128 tiles of
+// it is stored as the next residual, y only where it is stored in bf16.  The
+// codes come from t = h * weight: y = t / rms, so y / scale = t / (amax |t| /
+// 448), without the roundings of the reciprocal root and of y (each moves a
+// few codes that lie near a border).  A tile is 128 columns (the 1 x 128 tiles of
 // "Deepseek Details", section "FP8 Training"; the last may be shorter) or the
 // whole row, the two granularities of the library's other quantisers.
 //
@@ -116,20 +117,25 @@ __global__ void __launch_bounds__(TPR > kNormBlock ? TPR : kNormBlock)
       unpack8(__ldg(wt + c), w);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        h[k][e] = h[k][e] * rstd * w[e];
+        h[k][e] *= w[e];                   // t
         amax = fmaxf(amax, fabsf(h[k][e]));
       }
-      if (yout) yout[c] = pack8(h[k]);
+      if (yout) {
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = h[k][e] * rstd;
+        yout[c] = pack8(y);
+      }
     }
   }
   if (!p.y8) return;
 
   uint2* codes = reinterpret_cast<uint2*>(p.y8 + row * p.dim);
-  float scale = 1.f;
+  float step = 1.f;      // scale / rstd
   if (p.group == 0) {
     amax = row_reduce<TPR, true>(amax, red[1]);
-    scale = amax > 0.f ? amax / 448.f : 1.f;
-    if (tid == 0) p.y_scale[row] = scale;
+    step = amax > 0.f ? amax / 448.f : 1.f;
+    if (tid == 0) p.y_scale[row] = amax > 0.f ? step * rstd : 1.f;
   }
 #pragma unroll
   for (int k = 0; k < V; ++k) {
@@ -142,16 +148,16 @@ __global__ void __launch_bounds__(TPR > kNormBlock ? TPR : kNormBlock)
       for (int e = 0; e < 8; ++e) a = fmaxf(a, fabsf(h[k][e]));
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-      scale = a > 0.f ? a / 448.f : 1.f;
+      step = a > 0.f ? a / 448.f : 1.f;
       if (c < nvec && (c & 15) == 0)
-        p.y_scale[row * ((p.dim + 127) >> 7) + (c >> 4)] = scale;
+        p.y_scale[row * ((p.dim + 127) >> 7) + (c >> 4)] = a > 0.f ? step * rstd : 1.f;
     }
     if (c < nvec) {
       uint32_t o[2] = {0u, 0u};
 #pragma unroll
       for (int e = 0; e < 8; ++e)
         o[e >> 2] |= static_cast<uint32_t>(
-                         __nv_cvt_float_to_fp8(h[k][e] / scale, __NV_SATFINITE, __NV_E4M3))
+                         __nv_cvt_float_to_fp8(h[k][e] / step, __NV_SATFINITE, __NV_E4M3))
                      << (8 * (e & 3));
       codes[c] = make_uint2(o[0], o[1]);
     }

@@ -118,14 +118,14 @@ __device__ __forceinline__ Item item_of(const MlaPrefillLaunch& p, int x, int y)
   it.q0 = __ldg(p.cu_q + lo);
   it.k0 = __ldg(p.cu_k + lo);
   it.qlen = __ldg(p.cu_q + lo + 1) - it.q0;
-  it.klen = max(0, __ldg(p.cu_k + lo + 1) - it.k0);
+  it.klen = __ldg(p.cu_k + lo + 1) - it.k0;
   // Late queries see the most keys: they start first.
   const int slots = max(0, it.q0 + it.qlen) / kCtaRows - max(0, it.q0) / kCtaRows + 1;
   it.row0 = (slots - 1 - (x - first_slot(p, lo))) * kCtaRows;
   // Offsets outside the packed tensors, or a length above max_q, are reported;
   // the request's rows are left as they were, or not all of them written.
-  const bool bad = it.q0 < 0 || it.k0 < 0 || it.qlen < 0 || it.qlen > p.total_q - it.q0 ||
-                   it.klen > p.total_k - it.k0;
+  const bool bad = it.q0 < 0 || it.k0 < 0 || it.qlen < 0 || it.klen < 0 ||
+                   it.qlen > p.total_q - it.q0 || it.klen > p.total_k - it.k0;
   const bool far = it.row0 >= (p.max_q + kCtaRows - 1) / kCtaRows * kCtaRows;
   it.work = !bad && !far && it.row0 >= 0 && it.row0 < it.qlen ? 1 : 0;
   if (bad || (far && it.row0 < it.qlen)) raise_error(kErrCheck);

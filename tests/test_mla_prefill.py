@@ -126,6 +126,12 @@ def test_bad_offsets_are_reported(L):
     out, _ = _run(c, True)
     assert api.dsa_get_device_error() == 5
     assert torch.equal(out[:100], good[:100]) and (out[100:450] == 77).all()
+    # ... or come before the first request's
+    c["cu_k"].copy_(saved)
+    c["cu_k"][2] = 20
+    out, _ = _run(c, True)
+    assert api.dsa_get_device_error() == 5
+    assert torch.equal(out[:100], good[:100]) and (out[100:400] == 77).all()
     c["cu_k"].copy_(saved)
     # a request longer than max_q says (rounded up to 256): its first queries are written
     out, _ = _run({**c, "max_q": 200}, True)

@@ -125,6 +125,7 @@ struct MlaPrefillLaunch {
   long long ld_rope;
   int batch, heads, total_q, total_k, max_q, causal;
   int out_wide;                  // set by launch_mla_prefill: out is 32-byte aligned
+  int parts;                     //   CTAs (a cluster) that share an item's keys
   float sm_scale;
 };
 

@@ -366,10 +366,10 @@ dsa_status dsa_decode_fused_fp8kv(const dsa_decode_desc* desc,
  *            not depend on the lengths.  Calls that may run at the same time
  *            need workspaces of their own.
  * Rows of a request's last page behind its end are not read into the result
- * (they may hold anything); rows that a later query of the same request sees
- * have to be finite.  A page id outside [0, num_pages) masks the page's tokens,
- * a seqlens[r] above max_pages * 64 is cut to it; both raise
- * DSA_ERR_DEVICE_CHECK.
+ * (they may hold anything); values that any query of the request sees have to be
+ * finite (a masked one counts as probability 0 times the value).  A page id
+ * outside [0, num_pages) masks the page's tokens, a seqlens[r] above
+ * max_pages * 64 is cut to it; both raise DSA_ERR_DEVICE_CHECK.
  */
 dsa_status dsa_mla_decode(const dsa_decode_desc* desc, const uint16_t* q, const uint16_t* kv,
                           float sm_scale, uint16_t* out, float* lse, void* ws, size_t ws_bytes,
@@ -415,8 +415,10 @@ size_t dsa_mla_decode_workspace_bytes(const dsa_decode_desc* desc);
  *   lse     [dev] float [total_q, heads] or NULL
  * Needs no workspace.  Offsets outside the packed tensors skip their request; a
  * request with more than max_q queries (rounded up to 256) is not written
- * whole; both raise DSA_ERR_DEVICE_CHECK.  Keys of a request have to be finite
- * where any of its queries in the same 256 sees them.
+ * whole; both raise DSA_ERR_DEVICE_CHECK.  Values that any query of the request
+ * sees have to be finite (a masked one counts as probability 0 times the value).
+ * How the work is split follows from the arguments alone: the same call gives
+ * the same bits.
  */
 dsa_status dsa_mla_prefill(int32_t batch, int32_t heads, int32_t total_q, int32_t total_k,
                            int32_t max_q, const int32_t* cu_q, const int32_t* cu_k,

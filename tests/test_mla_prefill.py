@@ -250,3 +250,60 @@ def test_many_short_requests_and_a_long_one(L):
     out, lse = _run(c, True)
     assert api.dsa_get_device_error() == 0
     _check(c, True, out, lse, heads=[1])
+
+
+# Few items with many keys: the CTAs of a cluster share an item's keys.  More heads leave fewer CTAs for
+# an item (8: six to eight, 16: six, 24: five, 32: four, 40: three, 70: two on 152 SMs); the last ones have a request
+# with fewer key tiles than there are parts, one or none.
+SHARED = [
+    ([130], [4100], 8), ([1], [4001], 16), ([257], [3000], 8), ([3], [5000], 24), ([100], [4100], 32),
+    ([129], [2500], 40), ([64], [2600], 70), ([2, 200, 2], [9000, 300, 1], 3), ([2, 2, 0], [9000, 0, 5], 4),
+    ([300, 5], [6000, 2], 2),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("qlens,klens,H", SHARED)
+def test_shared_keys(L, qlens, klens, H, causal):
+    c = _case(qlens, klens, H, seed=sum(qlens) * 5 + sum(klens) + H)
+    out, lse = _run(c, causal)
+    assert api.dsa_get_device_error() == 0
+    _check(c, causal, out, lse, heads=range(0, H, max(1, H // 8)))
+    again, _ = _run(c, causal, lse=False)
+    assert torch.equal(out, again)
+
+
+@pytest.mark.gpu
+def test_shared_keys_bad_offsets_streams_and_graph(L):
+    c = _case([70, 100], [4000, 3000], 8, seed=3)
+    good, e_good = _run(c, True)
+    saved = c["cu_k"].clone()
+    c["cu_k"][2] += 1000
+    out, _ = _run(c, True)
+    assert api.dsa_get_device_error() == 5
+    assert torch.equal(out[:70], good[:70]) and (out[70:] == 77).all()
+    c["cu_k"].copy_(saved)
+    # two calls at once, and a captured one that finds other lengths when it is replayed
+    d = _case([33], [6000], 8, seed=4)
+    d_good, _ = _run(d, True)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        for s, x in zip(streams, (c, d)):
+            with torch.cuda.stream(s):
+                got.append(_run(x, True)[0])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, good) for a in got[::2]) and all(torch.equal(a, d_good) for a in got[1::2])
+    out, e = torch.full_like(good, 77.0), torch.full_like(e_good, 77.0)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        api.dsa_mla_prefill(c["q"], c["kv"], c["rope"], c["cu_q"], c["cu_k"], out, c["max_q"], SM, lse=e)
+    g.replay()
+    assert torch.equal(out, good) and torch.equal(e, e_good)
+    c["cu_k"].copy_(torch.tensor([0, 5000, 7000], dtype=torch.int32))
+    g.replay()
+    torch.cuda.synchronize()
+    _check({**c, "klens": [5000, 2000]}, True, out, e)
+    assert api.dsa_get_device_error() == 0

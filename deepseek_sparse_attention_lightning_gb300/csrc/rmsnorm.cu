@@ -14,10 +14,18 @@
 // "Deepseek Details", section "FP8 Training"; the last may be shorter) or the
 // whole row, the two granularities of the library's other quantisers.
 //
-// Memory bound: each value is read once, kept in registers across the row's
-// reduction and written once.  TPR threads share a row, each with V vectors of
-// 8 values (16-byte loads, TPR apart, so that a warp's load is 512 consecutive
-// bytes and 16 neighbouring lanes hold one 128-column tile).
+// Each value is read once, kept in registers across the row's reduction and
+// written once.  The threads of a row (as many warps as it takes, with V vectors
+// of 8 values each) load 16 bytes each, so that a warp's load is 512 consecutive
+// bytes and 16 neighbouring lanes hold one 128-column tile.  Rows of few warps
+// share a block: one row of 2048 columns a block of 128 threads took 111 us for
+// 32768 rows, codes alone, against 61; one of 640, 96 against 29.
+//
+// With a residual bound by HBM: 16384 x 8192, both outputs, 177 us (6.8 TB/s of
+// the measured 6.79).  Without one by the arithmetic and the latency of a row's
+// phases: codes alone 113 us (53 %), bf16 as well 123 us (81 %); fewer registers
+// and more rows at a time (V = 2, 3), more vectors a thread (V = 8), the next
+// row's loads under way in blocks that stay: all the same or slower.
 #include <cuda_fp8.h>
 
 #include "dsa_ptx.cuh"
@@ -28,21 +36,28 @@ namespace {
 
 constexpr int kNormBlock = 256;   // threads of a block of several rows
 
-// Sum (or maximum) over the TPR threads of a row; every thread gets it.  `buf`
-// (one float per warp) serves one call of a kernel.
-template <int TPR, bool kMax>
+// Sum (or maximum) over the warps of a row (threadIdx.y of the block); every
+// thread gets it.  `buf`: a float a warp, for one call of a kernel.
+template <bool kMax, bool kWarp>
 __device__ __forceinline__ float row_reduce(float v, float* buf) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     const float u = __shfl_xor_sync(0xffffffffu, v, o);
     v = kMax ? fmaxf(v, u) : v + u;
   }
-  if constexpr (TPR > 32) {
-    constexpr int kW = TPR / 32;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (lane == 0) buf[warp] = v;
-    __syncthreads();
-    v = lane < kW ? buf[lane] : 0.f;
+  const int warps = kWarp ? 1 : blockDim.x >> 5;
+  if (warps > 1) {
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) buf[threadIdx.x >> 5] = v;
+    // (An id that is not a constant reserves all sixteen barriers, and those of
+    // the SM then admit four blocks: 168 us instead of 135 for 32704 x 4104.)
+    switch (threadIdx.y) {
+      case 0: named_bar_sync(1, blockDim.x); break;
+      case 1: named_bar_sync(2, blockDim.x); break;
+      case 2: named_bar_sync(3, blockDim.x); break;
+      default: named_bar_sync(4, blockDim.x); break;
+    }
+    v = lane < warps ? buf[lane] : 0.f;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       const float u = __shfl_xor_sync(0xffffffffu, v, o);
@@ -52,29 +67,25 @@ __device__ __forceinline__ float row_reduce(float v, float* buf) {
   return v;
 }
 
-__device__ __forceinline__ void unpack8(const uint4 v, float (&f)[8]) {
+__device__ __forceinline__ void unpack8(const uint4 v, float2 (&f)[4]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    f[2 * e] = bf16lo_to_f32(w[e]);
-    f[2 * e + 1] = bf16hi_to_f32(w[e]);
-  }
+  for (int e = 0; e < 4; ++e) f[e] = make_float2(bf16lo_to_f32(w[e]), bf16hi_to_f32(w[e]));
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                    pack_bf16x2(f[6], f[7]));
+__device__ __forceinline__ uint4 pack8(const float2 (&f)[4]) {
+  return make_uint4(pack_bf16x2(f[0].x, f[0].y), pack_bf16x2(f[1].x, f[1].y), pack_bf16x2(f[2].x, f[2].y),
+                    pack_bf16x2(f[3].x, f[3].y));
 }
 
-template <int TPR, int V>
-__global__ void __launch_bounds__(TPR > kNormBlock ? TPR : kNormBlock)
-    rmsnorm_kernel(const RmsNormLaunch p) {
+// Block: x = threads of a row, y = rows.
+template <int V, bool kWarp>
+__global__ void __launch_bounds__(kWarp ? kNormBlock : 1024, V == 2 ? 6 : 1) rmsnorm_kernel(const RmsNormLaunch p) {
   __shared__ float red[2][32];
-  const int tid = TPR > 32 ? threadIdx.x : (threadIdx.x & 31);
-  const long long row = TPR > 32 ? static_cast<long long>(blockIdx.x)
-                                 : static_cast<long long>(blockIdx.x) * (kNormBlock / 32) +
-                                       (threadIdx.x >> 5);
-  if (row >= p.rows) return;   // a whole warp (TPR = 32) or never
+  const int tid = threadIdx.x, tpr = kWarp ? 32 : blockDim.x;
+  const long long row = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
+  if (row >= p.rows) return;   // all threads of a row
+  float* buf = red[0] + threadIdx.y * (tpr >> 5);
   const int nvec = p.dim >> 3;
   // Plain loads: an output may be the input it replaces (every thread writes
   // only the vectors it read).
@@ -84,46 +95,47 @@ __global__ void __launch_bounds__(TPR > kNormBlock ? TPR : kNormBlock)
   uint4 xv[V], rv[V];
 #pragma unroll
   for (int k = 0; k < V; ++k) {
-    const int c = tid + k * TPR;
+    const int c = tid + k * tpr;
     xv[k] = c < nvec ? x[c] : make_uint4(0u, 0u, 0u, 0u);
     rv[k] = (res && c < nvec) ? res[c] : make_uint4(0u, 0u, 0u, 0u);
   }
-  float h[V][8];
-  float ss = 0.f;
+  float2 h[V][4];
+  float2 ss2 = make_float2(0.f, 0.f);
 #pragma unroll
   for (int k = 0; k < V; ++k) {
-    float r[8];
+    float2 r[4];
     unpack8(xv[k], h[k]);
     unpack8(rv[k], r);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      h[k][e] += r[e];
-      ss = fmaf(h[k][e], h[k][e], ss);
+    for (int e = 0; e < 4; ++e) {
+      h[k][e] = add2(h[k][e], r[e]);
+      ss2 = fma2(h[k][e], h[k][e], ss2);
     }
   }
-  ss = row_reduce<TPR, false>(ss, red[0]);
+  const float ss = row_reduce<false, kWarp>(ss2.x + ss2.y, buf);
   const float rstd = 1.f / sqrtf(ss / static_cast<float>(p.dim) + p.eps);
 
   const uint4* wt = reinterpret_cast<const uint4*>(p.weight);
   uint4* hout = p.residual_out ? reinterpret_cast<uint4*>(p.residual_out + row * p.dim) : nullptr;
   uint4* yout = p.y ? reinterpret_cast<uint4*>(p.y + row * p.dim) : nullptr;
-  float amax = 0.f;
+  float amax[V];         // of |t| of a vector
 #pragma unroll
   for (int k = 0; k < V; ++k) {
-    const int c = tid + k * TPR;
+    const int c = tid + k * tpr;
+    amax[k] = 0.f;
     if (c < nvec) {
       if (hout) hout[c] = pack8(h[k]);
-      float w[8];
+      float2 w[4];
       unpack8(__ldg(wt + c), w);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        h[k][e] *= w[e];                   // t
-        amax = fmaxf(amax, fabsf(h[k][e]));
+      for (int e = 0; e < 4; ++e) {
+        h[k][e] = mul2(h[k][e], w[e]);                   // t
+        amax[k] = max3(amax[k], fabsf(h[k][e].x), fabsf(h[k][e].y));
       }
       if (yout) {
-        float y[8];
+        float2 y[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = h[k][e] * rstd;
+        for (int e = 0; e < 4; ++e) y[e] = mul2(h[k][e], make_float2(rstd, rstd));
         yout[c] = pack8(y);
       }
     }
@@ -131,57 +143,67 @@ __global__ void __launch_bounds__(TPR > kNormBlock ? TPR : kNormBlock)
   if (!p.y8) return;
 
   uint2* codes = reinterpret_cast<uint2*>(p.y8 + row * p.dim);
-  float step = 1.f;      // scale / rstd
+  float a = 0.f;
   if (p.group == 0) {
-    amax = row_reduce<TPR, true>(amax, red[1]);
-    step = amax > 0.f ? amax / 448.f : 1.f;
-    if (tid == 0) p.y_scale[row] = amax > 0.f ? step * rstd : 1.f;
+#pragma unroll
+    for (int k = 0; k < V; ++k) a = fmaxf(a, amax[k]);
+    a = row_reduce<true, kWarp>(a, buf + 32);
   }
 #pragma unroll
   for (int k = 0; k < V; ++k) {
-    const int c = tid + k * TPR;
+    const int c = tid + k * tpr;
     if (p.group != 0) {
       // 16 lanes hold the vectors of one 128-column tile (past the row's end
       // they hold zeros).
-      float a = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) a = fmaxf(a, fabsf(h[k][e]));
+      a = amax[k];
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-      step = a > 0.f ? a / 448.f : 1.f;
-      if (c < nvec && (c & 15) == 0)
-        p.y_scale[row * ((p.dim + 127) >> 7) + (c >> 4)] = a > 0.f ? step * rstd : 1.f;
     }
-    if (c < nvec) {
-      uint32_t o[2] = {0u, 0u};
+    if (c >= nvec) continue;
+    // (A row whose rms is zero or not finite keeps its NaN in the scale.)
+    if (p.group != 0 ? (c & 15) == 0 : c == 0) {
+      const float scale = a > 0.f || !isfinite(rstd) ? a * rstd / 448.f : 1.f;
+      if (p.group != 0) p.y_scale[row * ((p.dim + 127) >> 7) + (c >> 4)] = scale;
+      else p.y_scale[row] = scale;
+    }
+    // t / (a / 448) as a product: as many roundings, and a division a tile
+    // instead of one a value (16384 x 8192, codes alone: 139 against 112 us).
+    // (The reciprocal of the smallest tiles would overflow.)
+    float top = a;
+    if (top < 0x1p-96f) {
+      top *= 0x1p64f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        o[e >> 2] |= static_cast<uint32_t>(
-                         __nv_cvt_float_to_fp8(h[k][e] / step, __NV_SATFINITE, __NV_E4M3))
-                     << (8 * (e & 3));
-      codes[c] = make_uint2(o[0], o[1]);
+      for (int e = 0; e < 4; ++e) h[k][e] = mul2(h[k][e], make_float2(0x1p64f, 0x1p64f));
     }
+    const float inv = top > 0.f ? 448.f / top : 1.f;
+    uint32_t o[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 q = mul2(h[k][e], make_float2(inv, inv));
+      o[e] = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
+    }
+    codes[c] = make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
   }
 }
 
-template <int TPR, int V>
+template <int V, bool kWarp>
 cudaError_t launch(const RmsNormLaunch& a, cudaStream_t s) {
-  constexpr int threads = TPR > 32 ? TPR : kNormBlock;
-  const long long per = TPR > 32 ? 1 : kNormBlock / 32;
+  const int tpr = ((a.dim >> 3) + 32 * V - 1) / (32 * V) * 32;      // threads of a row
+  const int per = tpr < kNormBlock ? kNormBlock / tpr : 1;
   const long long grid = (a.rows + per - 1) / per;
-  return launch_kernel(rmsnorm_kernel<TPR, V>, dim3(static_cast<unsigned>(grid)), dim3(threads), 0, s,
-                       false, 1, a);
+  return launch_kernel(rmsnorm_kernel<V, kWarp>, dim3(static_cast<unsigned>(grid)), dim3(tpr, per), 0, s, false, 1,
+                       a);
 }
 
 }  // namespace
 
 cudaError_t launch_rmsnorm(const RmsNormLaunch& a, cudaStream_t s) {
   const int nvec = a.dim >> 3;
-  if (nvec <= 64) return launch<32, 2>(a, s);
-  if (nvec <= 512) return launch<128, 4>(a, s);
-  if (nvec <= 1024) return launch<256, 4>(a, s);
-  if (nvec <= 2048) return launch<512, 4>(a, s);
-  return launch<1024, 4>(a, s);
+  // A row a warp: no barrier.  (Two vectors a thread: 40 registers, six blocks an
+  // SM: 32768 x 512 to bf16 in 14.5 us; with 44 registers, five blocks, 16.3.)
+  if (nvec <= 64) return launch<2, true>(a, s);
+  if (nvec <= 128) return launch<4, true>(a, s);
+  return launch<4, false>(a, s);
 }
 
 }  // namespace dsa

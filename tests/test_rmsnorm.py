@@ -166,3 +166,57 @@ def test_binding_checks_shapes(L):
         api.dsa_rmsnorm(x, w, 1e-6)
     empty = torch.empty((0, 256), dtype=torch.bfloat16, device="cuda")
     api.dsa_rmsnorm(empty, w, 1e-6, y=torch.empty_like(empty))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,dim,group,residual", [
+    (50, 1024, 0, False), (9, 1032, 128, False), (50, 1032, 0, True), (21, 1560, 128, False),
+    (7, 2048, 128, True), (7, 2056, 0, False), (301, 3304, 128, False), (3, 4096, 128, False),
+    (11, 6152, 0, True), (5, 12296, 128, False), (2, 32760, 128, False), (1, 64, 0, False),
+])
+def test_rows_that_share_a_block(L, rows, dim, group, residual):
+    """Rows of one to 32 warps, several to a block where they are short, the last block not full."""
+    g = torch.Generator(device="cuda").manual_seed(dim)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)
+    x, w, res = rnd(rows, dim), rnd(dim), rnd(rows, dim) if residual else None
+    guard = torch.full((rows + 8, dim), 77.0, dtype=torch.bfloat16, device="cuda")
+    y8 = torch.full((rows + 8, dim), 55, dtype=torch.uint8, device="cuda")
+    sc = torch.full((rows + 8, -(-dim // 128) if group else 1), 33.0, device="cuda")
+    api.dsa_rmsnorm(x, w, 1e-5, residual=res, residual_out=None if res is None else torch.empty_like(res),
+                    y=guard[:rows], y8=y8[:rows], y_scale=sc[:rows], group=group)
+    assert (guard[rows:] == 77).all() and (y8[rows:] == 55).all() and (sc[rows:] == 33).all()
+    _, ref = _formula(x.cpu(), None if res is None else res.cpu(), w.cpu(), 1e-5)
+    _within(guard[:rows].cpu(), ref, BF16 + 2 * ARITH)
+    _check_fp8(y8[:rows].cpu(), sc[:rows].cpu(), ref, group)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dim", [256, 1032, 4104])
+@pytest.mark.parametrize("group", [0, 128])
+def test_tiny_and_undefined_rows(L, dim, group):
+    g = torch.Generator(device="cuda").manual_seed(dim + group)
+    x = torch.randn(8, dim, generator=g, device="cuda")
+    x[1] *= 1e-33                             # the reciprocal of a tile's largest would overflow
+    x[2, :128] *= 1e-36
+    x[3], x[4, 5], x[6, dim - 1] = 0, float("nan"), float("nan")
+    x = x.to(torch.bfloat16)
+    w = torch.ones(dim, dtype=torch.bfloat16, device="cuda")
+
+    def run(eps):
+        y, y8 = torch.empty_like(x), torch.empty((8, dim), dtype=torch.uint8, device="cuda")
+        sc = torch.empty((8, -(-dim // 128) if group else 1), device="cuda")
+        api.dsa_rmsnorm(x, w, eps, y=y, y8=y8, y_scale=sc, group=group)
+        return y.cpu(), y8.cpu(), sc.cpu()
+
+    y, y8, sc = run(1e-6)
+    _, ref = _formula(x.cpu(), None, w.cpu(), 1e-6)
+    good = torch.tensor([0, 1, 2, 3, 5, 7])
+    # (Below 2^-126, bf16's steps are 2^-126 * 2^-7: a rounding there is off by 2^-134 at most.)
+    _within(y[good], ref[good], BF16 + 2 * ARITH, floor=2.0 ** -134)
+    _check_fp8(y8[good], sc[good], ref[good], group)
+    # a NaN is its whole row's, in both outputs; so is 0 / 0 of a row of zeros without eps
+    wide = lambda s: s.repeat_interleave(128 if group else dim, 1)[:, :dim]
+    undefined = lambda y, y8, sc, r: y[r].isnan().all() and (
+        y8.view(torch.float8_e4m3fn).float() * wide(sc))[r].isnan().all()
+    assert undefined(y, y8, sc, 4) and undefined(y, y8, sc, 6)
+    assert undefined(*run(0.0), 3)

@@ -101,7 +101,7 @@ struct Tile {
   static constexpr int kOffBar = kOffXchg + 2 * 128 * 4;
   static constexpr int kOffInfo = kOffBar + 24 * 8;
   static constexpr int kSmemBytes = kOffInfo + 32 + 1024;
-  static constexpr int kStageRow = kFp8 ? 64 : 128;       // bytes of a row that an output store takes
+  static constexpr int kStages = kPages;                  // of a warp's output staging
   // First atom of K's group g.
   __host__ __device__ static constexpr int group_atom(int g) {
     return kFp8 ? (g < 2 ? 4 * g : 8 + (g - 2)) : kGroupAtoms * g;
@@ -111,6 +111,7 @@ static_assert(Tile<false>::kSmemBytes <= 232448 && Tile<true>::kSmemBytes <= 232
 constexpr int kColO = 0, kColS = 256, kTmemCols = 512;    // S: two buffers of a tile's keys / 2 columns
 constexpr int kThreads = 256, kThreadsFp8 = 768;
 constexpr int kSoftWarps = 4;
+constexpr int kStageRow = 64;                             // bytes of a row that an output store takes
 // FP8: eight warps dequantise for K, eight for V.  Registers a thread (launched
 // with 80 each): copies and MMAs, softmax, dequantisation.
 constexpr int kDequantWarps = 8;
@@ -763,35 +764,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
       if (whole_warp) {
         // 32 rows at once: staged in this warp's part of the P tile (swizzled, so
         // that rows' 16-byte pieces fall on distinct banks) and written by a
-        // tensor store a chunk of kStageRow bytes a row.  Stored from registers,
-        // every instruction touches 32 lines: 4 us for a stretch's 64 x 512
-        // floats.  (FP8: the two warps of a row share 4 KB of P, and write it
-        // again only after the barrier of the next tile's maximum.)
-        uint8_t* stage = smem + T::kOffP + (row & 32) * 128 + half * (kFp8 ? 2048 : kAtom);
-        const uint32_t stage_s = smem_u32(stage);
+        // tensor store, 64 bytes a row at a time.  Stored from registers, every
+        // instruction touches 32 lines: 4 us for a stretch's 64 x 512 floats.
+        // (FP8: the two warps of a row share 4 KB of P, and write it again only
+        // after the barrier of the next tile's maximum.)
+        uint8_t* stage0 = smem + T::kOffP + (row & 32) * 128 + half * (kFp8 ? 2048 : kAtom);
         const int row_w = static_cast<int>((whole ? grow : slot) - lane);
-        // Pieces [p0, p0 + n) of the lane's row; the first one of a chunk waits
-        // for the store before, the last one stores.
-        auto put = [&](const uint32_t* v, int p0, int n) {
-          if (p0 == 0) {
-            if (lane == 0) bulk_wait_read_all();
-            __syncwarp();
-          }
+        int buf = 0;
+        auto put = [&](const uint32_t* v, int dim) {
+          uint8_t* stage = stage0 + buf * 2048;
+          if (lane == 0) bulk_wait_read<T::kStages - 1>();      // this buffer's store before
+          __syncwarp();
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if (e >= n) break;
-            const int piece = kFp8 ? (p0 + e) ^ ((lane >> 1) & 3) : (p0 + e) ^ (lane & 7);
-            *reinterpret_cast<uint4*>(stage + lane * T::kStageRow + (piece << 4)) =
+          for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<uint4*>(stage + lane * kStageRow + ((e ^ ((lane >> 1) & 3)) << 4)) =
                 make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-          }
-        };
-        auto flush = [&](int dim) {
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            tma_store_2d(whole ? &tmap_out : &tmap_part, stage_s, dim, row_w);
+            tma_store_2d(whole ? &tmap_out : &tmap_part, smem_u32(stage), dim, row_w);
             bulk_commit();
           }
+          buf = (buf + 1) % T::kStages;
         };
 #pragma unroll 1
         for (int c = 0; c < 8; ++c) {
@@ -805,24 +799,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
 #pragma unroll
             for (int e = 0; e < 16; ++e)
               h[e] = pack_bf16x2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
-            if constexpr (kFp8) {
-              put(h, 0, 4);
-              flush(dim);
-            } else {
-              put(h, 4 * (c & 1), 4);
-              if (c & 1) flush(dim - 32);
-            }
-          } else if constexpr (kFp8) {
-            put(o, 0, 4);
-            flush(dim);
-            put(o + 16, 0, 4);
-            flush(dim + 16);
+            put(h, dim);
           } else {
-            put(o, 0, 8);
-            flush(dim);
+            put(o, dim);
+            put(o + 16, dim + 16);
           }
         }
-        if (lane == 0) bulk_wait_read_all();      // before the next P is written there
+        if (lane == 0) bulk_wait_read<0>();      // before the next P is written there
         __syncwarp();
       } else {
 #pragma unroll 1
@@ -1016,13 +999,11 @@ cudaError_t launch_mla_decode(MlaDecodeLaunch a, void* ws, cudaStream_t s) {
   CUtensorMap to, tp;
   const uint64_t odims[2] = {kVDim, qrows}, ostr[1] = {kVDim * 2};
   const uint64_t pdims[2] = {kVDim, slots}, pstr[1] = {kVDim * 4};
-  const uint32_t stage_row = fp8 ? Tile<true>::kStageRow : Tile<false>::kStageRow;
-  const uint32_t obox[2] = {stage_row / 2, 32}, pbox[2] = {stage_row / 4, 32};
-  const CUtensorMapSwizzle swz = fp8 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+  const uint32_t obox[2] = {kStageRow / 2, 32}, pbox[2] = {kStageRow / 4, 32};
   if (!encode_tmap_nd(&to, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.out, 2, odims, ostr, obox,
-                      swz) ||
+                      CU_TENSOR_MAP_SWIZZLE_64B) ||
       !encode_tmap_nd(&tp, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.part_o, 2, pdims, pstr, pbox,
-                      swz))
+                      CU_TENSOR_MAP_SWIZZLE_64B))
     return cudaErrorInvalidValue;
   const int smem = fp8 ? Tile<true>::kSmemBytes : Tile<false>::kSmemBytes;
   auto kern = fp8 ? mla_decode_kernel<true> : mla_decode_kernel<false>;

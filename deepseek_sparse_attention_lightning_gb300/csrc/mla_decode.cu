@@ -875,15 +875,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
 // where requests have two or three parts and there are many rows, of two, a warp
 // a row (128 requests of 512 .. 2048 tokens, 128 heads: the call takes 68 us
 // instead of 76; 1 of 4096, 16 heads, where that way is the slower: 20.5 against
-// 16.4).
+// 16.4).  Few rows of many parts: four such groups of threads share a row (kShare;
+// 1 request of 131072, 16 heads, 76 parts: 55 us instead of 61; with 512 rows of
+// 19 parts, 78 against 70).
 constexpr int kMergeThreads = 128;
 
-template <int kParts>
-__global__ void __launch_bounds__(kMergeThreads) mla_merge_kernel(const MlaDecodeLaunch p) {
+template <int kParts, int kShare>
+__global__ void __launch_bounds__(kMergeThreads * kShare) mla_merge_kernel(const MlaDecodeLaunch p) {
   constexpr int kVecs = 8 / kParts;                          // of a row, a thread
   constexpr int kTpr = kVDim / 4 / kVecs, kRows = kMergeThreads / kTpr;
   const int rows_req = p.nq * p.heads;
-  const int rrow = blockIdx.y * kRows + threadIdx.x / kTpr;
+  static_assert(kShare == 1 || kRows == 1, "the groups of a block share a row");
+  const int share = threadIdx.x / kMergeThreads;
+  const int rrow = blockIdx.y * kRows + (kShare > 1 ? 0 : threadIdx.x / kTpr);
   const int c4 = threadIdx.x % kTpr;
   const int m = rrow / kRowTile, lrow = rrow % kRowTile;
   const int g0 = blockIdx.x;
@@ -899,7 +903,7 @@ __global__ void __launch_bounds__(kMergeThreads) mla_merge_kernel(const MlaDecod
   float4 acc[kVecs];
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int b0 = 0; b0 < n; b0 += kParts) {
+  for (int b0 = share * kParts; b0 < n; b0 += kShare * kParts) {
     float4 v[kParts][kVecs];
     float e[kParts];
 #pragma unroll
@@ -930,6 +934,32 @@ __global__ void __launch_bounds__(kMergeThreads) mla_merge_kernel(const MlaDecod
       for (int i = 0; i < kVecs; ++i)
         acc[i] = make_float4(fmaf(w, v[u][i].x, acc[i].x), fmaf(w, v[u][i].y, acc[i].y),
                              fmaf(w, v[u][i].z, acc[i].z), fmaf(w, v[u][i].w, acc[i].w));
+    }
+  }
+  if constexpr (kShare > 1) {
+    __shared__ float4 s_acc[kShare - 1][kMergeThreads];
+    __shared__ float2 s_sum[kShare - 1];
+    if (share > 0) {
+      s_acc[share - 1][c4] = acc[0];
+      if (c4 == 0) s_sum[share - 1] = make_float2(mx, tot);
+    }
+    __syncthreads();
+    if (share > 0) return;
+    float top = mx;
+#pragma unroll
+    for (int u = 0; u < kShare - 1; ++u) top = fmaxf(top, s_sum[u].x);
+    const float mref = top > ninf ? top : 0.f;
+    const float f = ex2((mx - mref) * kLog2e);
+    mx = top;
+    tot *= f;
+    acc[0] = make_float4(acc[0].x * f, acc[0].y * f, acc[0].z * f, acc[0].w * f);
+#pragma unroll
+    for (int u = 0; u < kShare - 1; ++u) {
+      const float w = ex2((s_sum[u].x - mref) * kLog2e);
+      const float4 v = s_acc[u][c4];
+      tot = fmaf(w, s_sum[u].y, tot);
+      acc[0] = make_float4(fmaf(w, v.x, acc[0].x), fmaf(w, v.y, acc[0].y), fmaf(w, v.z, acc[0].z),
+                           fmaf(w, v.w, acc[0].w));
     }
   }
   const bool any = tot > 0.f || tot != tot;
@@ -1015,10 +1045,13 @@ cudaError_t launch_mla_decode(MlaDecodeLaunch a, void* ws, cudaStream_t s) {
                     false, 1, tq, tk, tv, ts, to, tp, a);
   if (e != cudaSuccess || a.groups == 1) return e;
   const int rows = a.nq * a.heads;
-  auto merge = [&](void (*k)(const MlaDecodeLaunch), int per) {
-    return launch_kernel(k, dim3(a.groups - 1, (rows + per - 1) / per), dim3(kMergeThreads), 0, s, true, 1, a);
+  auto merge = [&](void (*k)(const MlaDecodeLaunch), int per, int share) {
+    return launch_kernel(k, dim3(a.groups - 1, (rows + per - 1) / per), dim3(kMergeThreads * share), 0, s, true, 1, a);
   };
-  return 2 * a.batch >= a.groups ? merge(mla_merge_kernel<2>, 4) : merge(mla_merge_kernel<8>, 1);
+  // (The parts of a request, on average: 1 + groups / batch.)
+  if (2 * a.batch >= a.groups) return merge(mla_merge_kernel<2, 1>, 4, 1);
+  if (8 * a.batch <= a.groups && a.batch * rows <= 64) return merge(mla_merge_kernel<8, 4>, 1, 4);
+  return merge(mla_merge_kernel<8, 1>, 1, 1);
 }
 
 }  // namespace dsa

@@ -170,6 +170,27 @@ def test_fp8_rows_match_formula(L, lens, nq, H):
     assert torch.equal(out, again)
 
 
+# Joins of many parts of few rows (FP8: twice the key tiles), of eight parts at a time, and of the
+# few parts that many requests have.
+JOINS = [
+    ([40000], 1, 16), ([39999], 4, 16), ([20000, 30001], 1, 32), ([25000], 2, 128), ([700, 1300, 64] * 14, 1, 128),
+    ([513] * 40, 2, 16), ([2000, 1] * 20, 1, 1), ([300, 1100] * 20, 3, 96),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("lens,nq,H", JOINS)
+def test_joins(L, lens, nq, H, fp8):
+    c = _case(lens, nq, H, seed=len(lens) + nq + H)
+    case, call, cache, rel = _both_caches(c)[fp8]
+    out, lse = _run(case, call=call, kv=cache)
+    assert api.dsa_get_device_error() == 0
+    _check(case, out, lse, rel_key=rel)
+    again, _ = _run(case, lse=False, call=call, kv=cache)
+    assert torch.equal(out, again)
+
+
 @pytest.mark.gpu
 def test_large_scores_raise_the_maximum(L):
     """Keys that grow along the request: the running maximum rises by far more than 2^8 several times."""

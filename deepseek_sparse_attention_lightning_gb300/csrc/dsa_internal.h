@@ -126,6 +126,7 @@ struct MlaPrefillLaunch {
   int batch, heads, total_q, total_k, max_q, causal;
   int out_wide;                  // set by launch_mla_prefill: out is 32-byte aligned
   int parts;                     //   CTAs (a cluster) that share an item's keys
+  int slots, head_group;         //   query blocks of all requests; heads that run together
   float sm_scale;
 };
 

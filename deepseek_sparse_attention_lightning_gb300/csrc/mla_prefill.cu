@@ -15,8 +15,8 @@
 // worth of traffic a key tile.  One CTA = 256 queries of one head, as two query
 // tiles of 128 (M = 128): while one tile's scores are in the softmax, the matrix
 // pipe works on the other's.  Measured: one prompt of 8192 tokens, 128 heads,
-// 1737 us = 1583 TFLOP/s over the visible pairs (83 % of the measured matrix
-// rate, 92 % of the sustained one); 8 ragged prompts of 414 .. 2047, 491 us.
+// 1712 us = 1606 TFLOP/s over the visible pairs (84 % of the measured matrix
+// rate, 94 % of the sustained one); 8 ragged prompts of 414 .. 2047, 489 us.
 //
 // Tensor memory (512 columns): S of the two tiles (128 each, fp32), O of the
 // two (128 each).  P (bf16, 64 columns) overwrites the S it came from and is
@@ -30,10 +30,11 @@
 // has the other tile's P V and Q K^T (1280 cycles of matrix work) to hide in.
 //
 // A grid of one CTA for each 256 queries of a head (and at most one more a
-// request), late queries (most keys) first within a request; but a CTA that runs
-// goes on with the work of CTAs that have not started (a request for one is under
-// way while the CTA works), so that its copies run into the next item while this
-// one's last tiles and output are under way, and the SMs end close together.
+// request), late queries (most keys) first, heads that fit into L2 together; but
+// a CTA that runs goes on with the work of CTAs that have not started (a request
+// for one is under way while the CTA works), so that its copies run into the next
+// item while this one's last tiles and output are under way, and the SMs end
+// close together.
 //
 // Few items with many keys (a short chunk over a long prefix, few heads): the
 // CTAs of a cluster share an item's key tiles, leave their outputs and
@@ -119,7 +120,12 @@ __device__ __forceinline__ int first_slot(const MlaPrefillLaunch& p, int r) {
   return static_cast<int>((static_cast<uint32_t>(max(0, __ldg(p.cu_q + r))) + (kCtaRows - 1u) * r) / kCtaRows);
 }
 
-__device__ __forceinline__ Item item_of(const MlaPrefillLaunch& p, int x, int y) {
+// Item i of the grid: head groups one after another, in a group the slots, a
+// slot's heads next to each other.
+__device__ __forceinline__ Item item_of(const MlaPrefillLaunch& p, int i) {
+  const int group = i / (p.slots * p.head_group), first = group * p.head_group;
+  const int heads = min(p.head_group, p.heads - first), at = i - first * p.slots;
+  const int x = at / heads, y = first + at % heads;
   int lo = 0, hi = p.batch;      // first_slot(lo) <= x < first_slot(hi), were it asked
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -291,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int n = 0;                                          // granules so far
         int uses0 = 0, uses1 = 0;                           // items that had each query tile
         const uint64_t pol_rope = policy_evict_last();      // every head reads it
-        Item it = item_of(p, static_cast<int>(blockIdx.x) / p.parts, blockIdx.y);
+        Item it = item_of(p, static_cast<int>(blockIdx.x) / p.parts);
         if (p.parts > 1) keep_part(it, static_cast<int>(blockIdx.x) % p.parts, p.parts);
         int base = 0, k = 0, asked = 0;
         bool more = true;
@@ -344,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t x, y, z;
           more = taken_cta(sbase + kOffTaken, x, y, z);
           fence_proxy_async_smem();      // read before the next answer is written there
-          if (more) it = item_of(p, x, y);
+          if (more) it = item_of(p, x);
         }
         if (!ok) raise_error(kErrTimeout);
         // No copy is in flight when the CTA ends.  (After a wait that ran out, the
@@ -734,6 +740,21 @@ int clusters_at_once(int parts) {
   return n;
 }
 
+// Heads whose items run together.  Late items are long and early ones short, so
+// the order late to early over all heads ends with short ones and the SMs end
+// close together; but heads that run together share L2, and each item reads a
+// head's keys from its first.  So as many as have 48 MB of keys and values, in
+// groups of equal size.  Measured for one head after another / 16 / 48 / 96 MB /
+// all heads together, us: 4096 tokens, 32 heads, 143 / 143 / 115 / 117 / 117; 4000,
+// 16 heads, 94 / 66 / 66 / 66 / 66; 6000, 32 heads, 268 / 252 / 229 / 232 / 231; 8192,
+// 128 heads, 1712 / 1749 / 1698 / 1659 / 1751; 3000, 128 heads, 270 / 258 / 252 / 258 /
+// 274; 8 of 1037, 128 heads, 397 / 393 / 397 / 432 / 432.
+int heads_at_once(const MlaPrefillLaunch& a) {
+  const double bytes = 48 << 20, head = static_cast<double>(a.total_k) / a.batch * 2 * kHeadDim * 2;
+  const int groups = static_cast<int>(std::ceil(a.heads / std::max(1.0, std::min<double>(a.heads, bytes / (head + 1)))));
+  return (a.heads + groups - 1) / groups;
+}
+
 // CTAs that share an item's keys.  Costs in key tiles (1.75 us), from the mean
 // lengths (the lengths themselves are on the device): the late items' tiles, 4
 // for the start and end of an item of one CTA, 5.5 + 0.3 c with the join of c
@@ -741,9 +762,8 @@ int clusters_at_once(int parts) {
 // 1 / 2 / 4 / 6 / 8 parts, us: 1 query over 16000 keys, 8 heads, 199 / 113 / 64 /
 // 46 / 38; 64 over 16000, 24 heads, 201 / 109 / 64 / 91 / 74 (5: 58); 1000 over
 // 5000, 16 heads, 79 / 51 / 62 / 74 / 106; 1000 over 1000, 25 / 23 / 33 / 46 /
-// 68; 2 x 512 over 16513, 128 heads, 922 / 875 / 1027 / 1144 / 1365; 4000 over
-// 4000, 16 heads, 95 / 103 / 136 / 187 / 271; 77 over 77, 16 heads, 11 / 15 / 15 /
-// 15 / 24.
+// 68; 2 x 512 over 16513, 128 heads, 922 / 875 / 1027 / 1144 / 1365; 77 over 77, 16
+// heads, 11 / 15 / 15 / 15 / 24.
 int choose_parts(const MlaPrefillLaunch& a) {
   const double queries = static_cast<double>(a.total_q) / a.batch;
   const double blocks = std::max(1.0, std::ceil(queries / kCtaRows));      // of a request
@@ -790,7 +810,9 @@ cudaError_t launch_mla_prefill(MlaPrefillLaunch a, cudaStream_t s) {
                                        kSmemBytes);
   if (e != cudaSuccess) return e;
   a.parts = choose_parts(a);
-  const dim3 grid(static_cast<unsigned>((a.total_q + (kCtaRows - 1LL) * a.batch) / kCtaRows) * a.parts, a.heads);
+  a.slots = static_cast<int>((a.total_q + (kCtaRows - 1LL) * a.batch) / kCtaRows);
+  a.head_group = heads_at_once(a);
+  const dim3 grid(static_cast<unsigned>(a.slots) * a.heads * a.parts);
   return launch_kernel(mla_prefill_kernel, grid, dim3(kThreads), kSmemBytes, s, false, a.parts, tq, tk, tr, a);
 }
 

@@ -52,6 +52,7 @@
 // may hold anything.
 #include <algorithm>
 #include <atomic>
+#include <climits>
 #include <cmath>
 
 #include "dsa_ptx.cuh"
@@ -812,7 +813,9 @@ cudaError_t launch_mla_prefill(MlaPrefillLaunch a, cudaStream_t s) {
   a.parts = choose_parts(a);
   a.slots = static_cast<int>((a.total_q + (kCtaRows - 1LL) * a.batch) / kCtaRows);
   a.head_group = heads_at_once(a);
-  const dim3 grid(static_cast<unsigned>(a.slots) * a.heads * a.parts);
+  const long long ctas = static_cast<long long>(a.slots) * a.heads * a.parts;
+  if (ctas > INT_MAX) return cudaErrorInvalidValue;
+  const dim3 grid(static_cast<unsigned>(ctas));
   return launch_kernel(mla_prefill_kernel, grid, dim3(kThreads), kSmemBytes, s, false, a.parts, tq, tk, tr, a);
 }
 

@@ -33,11 +33,12 @@
 // the copies (one tensor copy a K group, two a V page, in the 128B-swizzled
 // layout that the MMAs read) have that long.
 //
-// Work: the key tiles of all requests form one line that is cut evenly over
-// the CTA pairs (n_q * H > 128: over groups of pairs, one pair for each row
-// tile, which walk the same tiles at the same time and share them in L2).  A
-// pair may end one request and begin the next; a request that spans pairs is
-// joined by mla_merge_kernel from fp32 partials and their log-sum-exps.
+// Work: the key tiles of all requests (and what it costs to begin one) form one
+// line that is cut evenly over the CTA pairs (n_q * H > 128: over groups of
+// pairs, one pair for each row tile, which walk the same tiles at the same time
+// and share them in L2).  A pair may end one request and begin the next; a
+// request that spans pairs is joined by mla_merge_kernel from fp32 partials and
+// their log-sum-exps.
 //
 // Roles (256 threads a CTA): warp 0 copies q and K, warp 2 copies V, warp 1
 // of the leading CTA issues the MMAs of both, warps 4-7 are softmax and
@@ -102,6 +103,10 @@ struct Tile {
   static constexpr int kOffInfo = kOffBar + 24 * 8;
   static constexpr int kSmemBytes = kOffInfo + 32 + 1024;
   static constexpr int kStages = kPages;                  // of a warp's output staging
+  // What a request's queries and output cost where it begins, in key tiles (128
+  // requests of 512 .. 2048 bf16 tokens: 67.5 us for 0, 65.0 for 1, 63.9 for 2, 64.4
+  // for 3; 128 of 64 FP8 rows: 33 for 0, 27 for 2).
+  static constexpr int kStretch = 2;
   // First atom of K's group g.
   __host__ __device__ static constexpr int group_atom(int g) {
     return kFp8 ? (g < 2 ? 4 * g : 8 + (g - 2)) : kGroupAtoms * g;
@@ -143,31 +148,41 @@ __device__ __forceinline__ int tiles_of(int len) {
   return (len + kKeys - 1) / kKeys;
 }
 
-// The line of key tiles: their total number, and the groups it is cut into.
+// The line: for each request with tokens kStretch units and one a key tile.  It is
+// cut into groups from unit kStretch on, so that the first request's tiles alone
+// count; a cut among a request's kStretch units falls before its first tile.
 struct Line {
   long long total;
   int groups;
 };
 
-__device__ __forceinline__ long long cut(const Line& ln, int g) { return ln.total * g / ln.groups; }
+template <int kStretch>
+__device__ __forceinline__ long long cut(const Line& ln, int g) {
+  return kStretch + (ln.total - kStretch) * g / ln.groups;
+}
 
-// (one warp) Total tiles of all requests.
-template <int kKeys>
+template <typename T>
+__device__ __forceinline__ int units_of(int len) {
+  return len > 0 ? tiles_of<T::kKeys>(len) + T::kStretch : 0;
+}
+
+// (one warp) The line of all requests.
+template <typename T>
 __device__ __forceinline__ Line scan_total(const MlaDecodeLaunch& p, int lane) {
   long long n = 0;
-  for (int r = lane; r < p.batch; r += 32) n += tiles_of<kKeys>(request_len(p, r));
+  for (int r = lane; r < p.batch; r += 32) n += units_of<T>(request_len(p, r));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
   Line ln;
   ln.total = n;
-  const long long most = (n + p.min_tiles - 1) / p.min_tiles;
+  const long long most = (n - T::kStretch + p.min_tiles - 1) / p.min_tiles;
   ln.groups = most < p.groups ? static_cast<int>(most < 1 ? 1 : most) : p.groups;
   return ln;
 }
 
-// (one warp) The request that holds tile `at` of the line (at < total), and
-// the line position of its first tile.
-template <int kKeys>
+// (one warp) The request that holds unit `at` of the line (at < total), and the
+// line position of its first unit.
+template <typename T>
 __device__ __forceinline__ void locate(const MlaDecodeLaunch& p, long long at, int lane, int& req,
                                        long long& first) {
   long long base = 0;
@@ -175,7 +190,7 @@ __device__ __forceinline__ void locate(const MlaDecodeLaunch& p, long long at, i
   first = 0;
   for (int r0 = 0; r0 < p.batch; r0 += 32) {
     const int r = r0 + lane;
-    const int n = r < p.batch ? tiles_of<kKeys>(request_len(p, r)) : 0;
+    const int n = r < p.batch ? units_of<T>(request_len(p, r)) : 0;
     long long incl = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -194,26 +209,32 @@ __device__ __forceinline__ void locate(const MlaDecodeLaunch& p, long long at, i
 }
 
 // The stretches of requests in a group's part [lo, hi) of the line, in order.
-template <int kKeys>
+template <typename T>
 struct Walk {
-  long long pos, hi;     // next tile of the line, end of the part
+  long long pos, hi;     // next unit of the line, end of the part
   int req;               // request of the stretch
+  int unit;              // unit of it at pos
   int len;               // its tokens
   int t0, t1, nt;        // the stretch's tiles [t0, t1) of the request's nt
   __device__ __forceinline__ bool next(const MlaDecodeLaunch& p) {
-    if (pos >= hi) return false;
-    if (t1 > 0 || nt == 0) {     // not the first stretch: on to the next request with tokens
-      do {
-        ++req;
-        len = request_len(p, req);
-        nt = tiles_of<kKeys>(len);
-      } while (nt == 0);
-      t0 = 0;
+    while (pos < hi) {
+      if (unit == nt + T::kStretch || nt == 0) {     // on to the next request with tokens
+        do {
+          ++req;
+          len = request_len(p, req);
+          nt = tiles_of<T::kKeys>(len);
+        } while (nt == 0);
+        unit = 0;
+      }
+      const long long left = hi - pos;
+      const int end = static_cast<int>(left < nt + T::kStretch - unit ? unit + left : nt + T::kStretch);
+      t0 = max(0, unit - T::kStretch);
+      t1 = max(0, end - T::kStretch);
+      pos += end - unit;
+      unit = end;
+      if (t1 > t0) return true;
     }
-    const long long left = hi - pos;
-    t1 = static_cast<int>(left < nt - t0 ? t0 + left : nt);
-    pos += t1 - t0;
-    return true;
+    return false;
   }
 };
 
@@ -256,8 +277,8 @@ struct PageBatch {
   static constexpr int kTiles = 32 / kPages;      // of a batch
   PageIds ids;
   int t0, now, next;     // first tile of the stretch; ids of this and the next batch
-  template <int kKeys>
-  __device__ __forceinline__ PageBatch(const MlaDecodeLaunch& p, const Walk<kKeys>& wk, int lane)
+  template <typename T>
+  __device__ __forceinline__ PageBatch(const MlaDecodeLaunch& p, const Walk<T>& wk, int lane)
       : ids{p.page_table + static_cast<long long>(wk.req) * p.max_pages, (wk.len + kPage - 1) / kPage,
             p.num_pages},
         t0(wk.t0), now(0) {
@@ -347,21 +368,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
     tmem_relinquish_2cta();
   }
   if (warp == 3) {
-    const Line ln = scan_total<kKeys>(p, lane);
+    const Line ln = scan_total<T>(p, lane);
     long long lo = 0, hi = 0, first = 0;
     int req = 0;
     if (group < ln.groups && ln.total > 0) {
-      lo = cut(ln, group);
-      hi = cut(ln, group + 1);
-      if (hi > lo) locate<kKeys>(p, lo, lane, req, first);
+      lo = cut<T::kStretch>(ln, group);
+      hi = cut<T::kStretch>(ln, group + 1);
+      if (hi > lo) locate<T>(p, lo, lane, req, first);
     }
     // What the merge has to join: the request that this group's first cut falls
     // into, if it is the first cut inside that request, and its last group.
     if (mtile == 0 && rank == 0 && lane == 0) {
       int2 join = make_int2(-1, 0);
-      if (group > 0 && hi > lo && lo > first && cut(ln, group - 1) <= first) {
-        const long long end = first + tiles_of<kKeys>(request_len(p, req));
-        join = make_int2(req, static_cast<int>((end * ln.groups - 1) / ln.total));
+      const long long tile0 = first + T::kStretch;
+      if (group > 0 && hi > lo && lo > tile0 && cut<T::kStretch>(ln, group - 1) <= tile0) {
+        const long long tiles = tile0 + tiles_of<kKeys>(request_len(p, req)) - T::kStretch;      // up to its end
+        join = make_int2(req, static_cast<int>((tiles * ln.groups - 1) / (ln.total - T::kStretch)));
       }
       p.joins[group] = join;
     }
@@ -375,14 +397,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
   cluster_sync();     // the other CTA's barriers are initialised
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-  Walk<kKeys> wk;
+  Walk<T> wk;
   wk.pos = info[0];
   wk.hi = info[1];
   wk.req = static_cast<int>(info[2] & 2047);
   wk.len = request_len(p, wk.req);
   wk.nt = tiles_of<kKeys>(wk.len);
-  wk.t0 = static_cast<int>(wk.pos - (info[2] >> 11));
-  wk.t1 = 0;
+  wk.unit = static_cast<int>(wk.pos - (info[2] >> 11));
+  wk.t0 = wk.t1 = 0;
 
   if (warp < 4) {
   if constexpr (kFp8) setmaxnreg_dec<kRegsMma>();
@@ -481,7 +503,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8 ? kThreadsFp8 :
       // P V of tile npv (its stretch's first: the output starts at zero, once
       // the epilogue has read the stretch before).
       int pv_seg = 0, pv_left = 0;
-      Walk<kKeys> pvw = wk;
+      Walk<T> pvw = wk;
       auto issue_pv = [&]() -> bool {
         uint32_t fresh = 0;
         if (pv_left == 0) {

@@ -94,8 +94,15 @@ constexpr int kColS = 0, kColO = 256, kTmemCols = 512;
 constexpr float kRaiseLog2 = 8.0f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
+// mbar_wait and mbar_test_wait by a whole warp: the same answer in every lane.
+// (A phase may complete between two lanes' tests; lanes that then took different
+// branches would meet in different votes and shuffles.)
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+}
+
+__device__ __forceinline__ bool warp_test(uint32_t bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_test_wait(bar, parity));
 }
 
 // Keys a query row sees: its own token and those before it, or all.
@@ -384,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         done_bar = 0;
       };
       auto peek = [&](uint32_t bar, uint32_t parity) {
-        if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) {
+        if (warp_test(bar, parity)) {
           done_bar = bar;
           done_parity = parity;
         }
@@ -452,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int item = 0; ok; ++item) {
         // (What is held back does not wait for a record, or an item without keys,
         // to come.)
-        if (!__all_sync(0xffffffffu, mbar_test_wait(ITEM_FULL(item), PARITY(item)))) issue_held(DRAIN, 0);
+        if (!warp_test(ITEM_FULL(item), PARITY(item))) issue_held(DRAIN, 0);
         if (!(ok = ok && warp_wait(ITEM_FULL(item), PARITY(item)))) break;
         const int work = __shfl_sync(0xffffffffu, record(item).work, 0);
         const int nt0 = __shfl_sync(0xffffffffu, record(item).nt0, 0);
@@ -466,8 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // (A new item's q and first keys may not have landed yet: then the
             // P V that is held back does not wait for them.)
             if (j == 0) {
-              if (held && !__all_sync(0xffffffffu, mbar_test_wait(Q_FULL(0), items0 & 1) &&
-                                                       mbar_test_wait(K_FULL(t), PARITY(t))))
+              if (held && !(warp_test(Q_FULL(0), items0 & 1) && warp_test(K_FULL(t), PARITY(t))))
                 issue_held(K_FULL(t), PARITY(t));
               ok = ok && warp_wait(Q_FULL(0), items0 & 1);
               ++items0;
@@ -493,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           commit(K_EMPTY(t));
           if (j < nt0) {
-            if (!mbar_test_wait(V_FULL(t), PARITY(t))) ok = warp_wait(V_FULL(t), PARITY(t));
+            ok = warp_wait(V_FULL(t), PARITY(t));
             want(P_FULL(0), c0 & 1);
             tc_fence_after();
             if (!ok) break;

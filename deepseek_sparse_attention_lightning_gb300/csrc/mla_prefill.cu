@@ -43,6 +43,7 @@
 //
 // Warps 0-3 and 4-7: softmax and epilogue of query tile 0 and 1, a row a
 // thread.  Warp 8: copies.  Warp 9: MMAs, issued from uniform control flow.
+// Warps 10 and 11: the query offsets' order, which no output is stored before.
 // The running maximum is raised lazily (by 2^8 at least), by the row's own
 // thread, which then rescales its row of O.  P is rounded to bf16 for the
 // matrix pipe, its sum kept unrounded in fp32.
@@ -78,10 +79,11 @@ constexpr int kNumBars = 24;
 constexpr int kOffTaken = kOffBar + kNumBars * 8;     // an answer of 16 bytes
 constexpr int kOffItem = kOffTaken + 16;             // two records
 constexpr int kOffSlot = kOffItem + 2 * 48;
+constexpr int kOffFalling = kOffSlot + 4, kOffOrder = kOffSlot + 8;      // the query offsets' order
 constexpr int kSmemBytes = kOffSlot + 16 + 1024;
 static_assert(kOffTaken % 16 == 0, "alignment");
 static_assert(kSmemBytes <= 232448, "shared memory");
-constexpr int kThreads = 384;                  // two softmax warpgroups; copies, MMAs and two idle warps
+constexpr int kThreads = 384;                  // two softmax warpgroups; copies, MMAs, two that check offsets
 // Registers: launched with 168 a thread (384 x 168 = 64512); the softmax holds a
 // row of 128 scores and takes 216, the third warpgroup keeps 72 (256 x 216 +
 // 128 x 72 = 64512).
@@ -123,9 +125,27 @@ static_assert(sizeof(Item) <= 48, "record");
 // Request r begins at slot (cu_q[r] + 255 r) / 256 of the grid's x: that leaves
 // it as many slots as it has blocks of 256 queries, or one more (a single request
 // none), and the slot of a CTA needs no walk over the requests before it to find
-// its own.
+// its own.  (Offsets outside the packed tensor count as its end nearest to them:
+// the requests inside keep their slots.)
 __device__ __forceinline__ int first_slot(const MlaPrefillLaunch& p, int r) {
-  return static_cast<int>((static_cast<uint32_t>(max(0, __ldg(p.cu_q + r))) + (kCtaRows - 1u) * r) / kCtaRows);
+  return static_cast<int>((static_cast<uint32_t>(min(max(0, __ldg(p.cu_q + r)), p.total_q)) + (kCtaRows - 1u) * r) /
+                          kCtaRows);
+}
+
+// Whether the query offsets decrease anywhere, looked for by `threads` threads
+// (the answer is a thread's own).  Requests then share rows, and slots are not
+// theirs: nothing of the call is written.  Offsets outside the packed tensor are
+// reported here too (they need not have a slot); their requests are skipped.
+__device__ __forceinline__ bool falling_offsets(const MlaPrefillLaunch& p, int tid, int threads) {
+  bool falls = false, outside = false;
+#pragma unroll 8
+  for (int r = tid; r < p.batch; r += threads) {
+    const int a = __ldg(p.cu_q + r), b = __ldg(p.cu_q + r + 1);
+    falls |= b < a;
+    outside |= a < 0 || b > p.total_q;
+  }
+  if (falls || outside) raise_error(kErrCheck);
+  return falls;
 }
 
 // Item i of the grid: head groups one after another, in a group the slots, a
@@ -241,6 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                              ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffSlot);
+  volatile int* falling = reinterpret_cast<int*>(smem + kOffFalling);
   const uint32_t bar0 = sbase + kOffBar;
 // K / V of key tile j, counted over the CTA's items (at most two of each are in
 // the ring): landed, and read.
@@ -261,6 +282,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Item k's record written / no longer needed by any role.
 #define ITEM_FULL(k) (bar0 + 160u + 8u * ((k) & 1))
 #define ITEM_EMPTY(k) (bar0 + 176u + 8u * ((k) & 1))
+// The query offsets have been looked through.
+#define ORDER (sbase + kOffOrder)
 
   if (warp == 8 && lane == 0) {
     for (int q = 0; q < 2; ++q) {
@@ -278,6 +301,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(DRAIN, 1);
     mbar_init(TAKEN, 1);
+    mbar_init(ORDER, 2);
+    *falling = 0;
     fence_mbar_init();
     prefetch_tmap(&tmap_q);
     prefetch_tmap(&tmap_kv);
@@ -523,6 +548,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (el) tc_commit(DRAIN);      // every MMA is done before TMEM is freed
       __syncwarp();
       mbar_wait(DRAIN, 0);
+    } else {
+      // ------------------------------------------------ order of the offsets
+      const bool falls = __any_sync(0xffffffffu, falling_offsets(p, (warp - 10) * 32 + lane, 64));
+      if (lane == 0) {
+        if (falls) *falling = 1;
+        mbar_arrive(ORDER);
+      }
     }
     __syncwarp();
     if (p.parts > 1) cluster_sync();      // the softmax warps' parts are written
@@ -533,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tS = tmem + (static_cast<uint32_t>(w4 * 32) << 16) + kColS + kTile * q;
     const uint32_t tO = tmem + (static_cast<uint32_t>(w4 * 32) << 16) + kColO + kHeadDim * q;
     const float sc = p.sm_scale * kLog2e;
-    bool ok = true;
+    bool ok = true, refused = false;
     int phase = 0;             // parities: bit 0 of the scores, bit 1 of the outputs
     int n = 0;                 // key tiles of the item
     float mrun = ninf, lrun = 0.f;
@@ -624,8 +656,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         phase ^= 2;
       }
+      if (item == 0) {
+        const bool known = warp_wait(ORDER, 0);
+        ok = ok && known;
+        refused = !known || *falling;
+      }
       const Item& it = record(item);
-      if (p.parts == 1 && it.row0 + q * kTile < it.qlen) {
+      if (p.parts == 1 && !refused && it.row0 + q * kTile < it.qlen) {
         const bool live = it.row0 + row < it.qlen;
         const bool any = lrun > 0.f || lrun != lrun;
         const float inv = any ? 1.f / lrun : 0.f;
@@ -679,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       cluster_sync();
       const Item it = record(0);
       const int rank = static_cast<int>(cluster_ctarank());
-      if (ok && it.work) {
+      if (ok && it.work && !refused) {
         const uint32_t o = sbase + kOffRing, stat = sbase + kOffQ;
         switch (p.parts) {
           case 2: join_parts<2>(p, it, o, stat, rank, warp, lane); break;
@@ -714,6 +751,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #undef ITEM_FULL
 #undef ITEM_EMPTY
 #undef DRAIN
+#undef ORDER
 }
 
 }  // namespace

@@ -413,9 +413,10 @@ size_t dsa_mla_decode_workspace_bytes(const dsa_decode_desc* desc);
  *           512 with ld_rope = 576), 16-B aligned
  *   out     [dev] bf16 [total_q, heads, 128], 16-B aligned
  *   lse     [dev] float [total_q, heads] or NULL
- * Needs no workspace.  Offsets outside the packed tensors skip their request; a
- * request with more than max_q queries (rounded up to 256) is not written
- * whole; both raise DSA_ERR_DEVICE_CHECK.  Values that any query of the request
+ * Needs no workspace.  Offsets outside the packed tensors, or key offsets that
+ * decrease, skip their request; a request with more than max_q queries (rounded
+ * up to 256) is not written whole; query offsets that decrease anywhere skip the
+ * whole call; all raise DSA_ERR_DEVICE_CHECK.  Values that any query of the request
  * sees have to be finite (a masked one counts as probability 0 times the value).
  * How the work is split follows from the arguments alone: the same call gives
  * the same bits.

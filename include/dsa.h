@@ -404,7 +404,9 @@ size_t dsa_mla_decode_workspace_bytes(const dsa_decode_desc* desc);
  *   batch, heads    1 .. DSA_MAX_PREFILL_BATCH, 1 .. DSA_MAX_PREFILL_HEADS
  *   total_q/total_k rows of the packed tensors (cu_q[batch] and cu_k[batch] at
  *                   most; rows behind the last request are left as they were)
- *   max_q           the largest number of queries of a request (or more)
+ *   max_q           the largest number of queries of a request (or more); 0, as
+ *                   total_q = 0, says that there is none: the call returns without
+ *                   a launch and does not look at the offsets
  *   cu_q, cu_k      [dev] int32 [batch + 1], not decreasing
  *   q       [dev] bf16 [total_q, heads, 192] (nope 128, rope 64), 16-B aligned
  *   kv      [dev] bf16 [total_k, heads, 256] (key nope 128, value 128), 16-B aligned

@@ -4,6 +4,7 @@
 #include <cmath>
 #include <cstdio>
 #include <algorithm>
+#include <climits>
 #include <cstring>
 #include <mutex>
 
@@ -367,6 +368,7 @@ dsa_status dsa_mla_prefill(int32_t batch, int32_t heads, int32_t total_q, int32_
   a.cu_k = cu_k; a.out = out; a.lse = lse; a.ld_rope = ld_rope; a.batch = batch; a.heads = heads;
   a.total_q = total_q; a.total_k = total_k; a.max_q = max_q < total_q ? max_q : total_q;
   a.causal = causal != 0; a.sm_scale = sm_scale;
+  if (dsa::mla_prefill_items(a) > INT_MAX) return DSA_ERR_UNSUPPORTED;
   return cuda_status(dsa::launch_mla_prefill(a, static_cast<cudaStream_t>(stream)));
 }
 

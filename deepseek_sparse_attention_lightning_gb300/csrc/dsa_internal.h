@@ -143,6 +143,9 @@ cudaError_t launch_rmsnorm(const RmsNormLaunch& a, cudaStream_t s);
 // pairs, workspace bytes; no kernel) and its launch.
 void mla_decode_plan(int nq, int heads, int* row_tiles, int* groups, size_t* ws_bytes);
 cudaError_t launch_mla_decode(MlaDecodeLaunch a, void* ws, cudaStream_t s);
+// Prompt attention: blocks of its grid before keys are shared (at most INT_MAX;
+// no kernel), and its launch.
+long long mla_prefill_items(const MlaPrefillLaunch& a);
 cudaError_t launch_mla_prefill(MlaPrefillLaunch a, cudaStream_t s);
 cudaError_t launch_merge(int rows, int splits, const float* mid_o, const float* mid_lse,
                          float* out, float* out_lse, cudaStream_t s, bool pdl = false);

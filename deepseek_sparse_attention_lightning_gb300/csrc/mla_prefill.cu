@@ -834,6 +834,12 @@ int choose_parts(const MlaPrefillLaunch& a) {
 
 }  // namespace
 
+namespace {
+long long slots_of(const MlaPrefillLaunch& a) { return (a.total_q + (kCtaRows - 1LL) * a.batch) / kCtaRows; }
+}  // namespace
+
+long long mla_prefill_items(const MlaPrefillLaunch& a) { return slots_of(a) * a.heads; }
+
 cudaError_t launch_mla_prefill(MlaPrefillLaunch a, cudaStream_t s) {
   // Outputs of a thread's row are stored 32 bytes (a whole sector) at a time
   // where they are aligned so.
@@ -855,10 +861,10 @@ cudaError_t launch_mla_prefill(MlaPrefillLaunch a, cudaStream_t s) {
                                        kSmemBytes);
   if (e != cudaSuccess) return e;
   a.parts = choose_parts(a);
-  a.slots = static_cast<int>((a.total_q + (kCtaRows - 1LL) * a.batch) / kCtaRows);
+  a.slots = static_cast<int>(slots_of(a));
   a.head_group = heads_at_once(a);
-  const long long ctas = static_cast<long long>(a.slots) * a.heads * a.parts;
-  if (ctas > INT_MAX) return cudaErrorInvalidValue;
+  const long long ctas = mla_prefill_items(a) * a.parts;
+  if (ctas > INT_MAX) return cudaErrorInvalidValue;      // (parts are 1 where there are many items)
   const dim3 grid(static_cast<unsigned>(ctas));
   return launch_kernel(mla_prefill_kernel, grid, dim3(kThreads), kSmemBytes, s, false, a.parts, tq, tk, tr, a);
 }

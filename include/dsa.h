@@ -402,6 +402,8 @@ size_t dsa_mla_decode_workspace_bytes(const dsa_decode_desc* desc);
  * every query sees, e.g. another part of a long prompt, joined by their lse).  A
  * query without a key gets out = 0, lse = -inf.  Arithmetic as dsa_mla_decode.
  *   batch, heads    1 .. DSA_MAX_PREFILL_BATCH, 1 .. DSA_MAX_PREFILL_HEADS
+ *                   (DSA_ERR_UNSUPPORTED; so are more than 2^31 - 1 blocks,
+ *                   (total_q + 255 batch) / 256 for each head)
  *   total_q/total_k rows of the packed tensors (cu_q[batch] and cu_k[batch] at
  *                   most; rows behind the last request are left as they were)
  *   max_q           the largest number of queries of a request (or more); 0, as

@@ -160,9 +160,13 @@ __global__ void __launch_bounds__(kWarp ? kNormBlock : 1024, V == 2 ? 6 : 1) rms
       for (int o = 8; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
     }
     if (c >= nvec) continue;
-    // (A row whose rms is zero or not finite keeps its NaN in the scale.)
+    // amax |y|.  A tile of zeros has scale 1 and codes 0, also where y is zero
+    // because the row's sum of squares overflowed (rstd = 0) or amax |t| / rms
+    // rounds to zero.  (A row whose rms is zero or not a number keeps its NaN in
+    // the scale.)
+    const float ymax = a * rstd;
     if (p.group != 0 ? (c & 15) == 0 : c == 0) {
-      const float scale = a > 0.f || !isfinite(rstd) ? a * rstd / 448.f : 1.f;
+      const float scale = ymax == 0.f ? 1.f : ymax / 448.f;
       if (p.group != 0) p.y_scale[row * ((p.dim + 127) >> 7) + (c >> 4)] = scale;
       else p.y_scale[row] = scale;
     }
@@ -177,7 +181,7 @@ __global__ void __launch_bounds__(kWarp ? kNormBlock : 1024, V == 2 ? 6 : 1) rms
 #pragma unroll
       for (int e = 0; e < 4; ++e) h[k][e] = mul2(h[k][e], make_float2(0x1p64f, 0x1p64f));
     }
-    const float inv = top > 0.f ? 448.f / top : 1.f;
+    const float inv = ymax == 0.f ? 0.f : top > 0.f ? 448.f / top : 1.f;
     uint32_t o[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {

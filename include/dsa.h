@@ -440,7 +440,7 @@ dsa_status dsa_mla_prefill(int32_t batch, int32_t heads, int32_t total_q, int32_
  *   y = h / sqrt(sum(h^2) / dim + eps) * weight
  *   scale = amax(|y| over a tile) / 448 (a tile of zeros: 1),
  *   code = E4M3(y / scale), rounded to nearest even and saturated at 448
- * in fp32; h, y and the codes are each rounded once, where they are stored (y
+ * in fp32 (where a sum of squares passes its range, y is 0); h, y and the codes are each rounded once, where they are stored (y
  * is normalised from the unrounded h, the codes come from the unrounded y).
  *   rows, dim     dim a multiple of 8, at most DSA_MAX_NORM_DIM
  *                 (DSA_ERR_UNSUPPORTED); rows may be 0

@@ -1,10 +1,13 @@
-"""Dense latent attention over FP8 rows against the formula over the rows as they are multiplied.
+"""Dense latent attention where scores span many powers of two, and FP8 rows against the formula over the
+rows as they are multiplied.
 
 FP8 rows: a value is its code times its scale in fp32, rounded to bf16.  Rounding the float64 formula's keys
 the same way leaves the kernel only the roundings that it makes for bf16 rows, so that their tolerance holds
 (tests/test_mla_dense.py) without a term for the keys.  That term, 2^-8 of the sum of a score's 576 products'
 sizes, would allow outputs of half their size over many keys.
 """
+import math
+
 import pytest
 import torch
 
@@ -65,3 +68,52 @@ def test_the_tolerance_shows_a_wrong_result(n, H):
         _check(c, fewer, None)
     with pytest.raises(AssertionError):
         _check(c, out, fewer_lse)
+
+
+# Scores (natural logarithms) that a position adds through the last rope dim: rising by ten powers of two a
+# 128-token tile, falling as fast, and rising in waves.
+RAMPS = {
+    "rise": lambda t: t * (10 * math.log(2) / 128),
+    "fall": lambda t: -t * (10 * math.log(2) / 128),
+    "waves": lambda t: t * (3 * math.log(2) / 128) + 25 * torch.sin(t / 90),
+}
+STEP = 16.0     # the queries' value in that dim
+
+
+def _ramped(lens, nq, H, ramp, seed):
+    c = _case(lens, nq, H, seed)
+    c["q"][..., 575] = STEP
+    table = c["keep"][1].cpu()
+    for r, n in enumerate(lens):
+        t = torch.arange(n)
+        c["keys"][r][:, 575] = (RAMPS[ramp](t.float()) / (STEP * SM)).to(torch.bfloat16).cuda()
+        c["kv"][(table[r, t // 64].long() * 64 + t % 64).cuda()] = c["keys"][r]
+    return c
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("ramp", sorted(RAMPS))
+@pytest.mark.parametrize("lens,nq,H", [
+    ([3000] * 40, 1, 128),            # stretches of 13 tiles of bf16 rows, 25 of FP8 rows
+    ([2900, 3100] * 20, 2, 128),      # of 26, 50
+    ([20000] * 2, 1, 16),             # of 4, 8: parts whose weights differ by up to 2^1500
+    ([6000, 300, 9000], 3, 96),
+])
+def test_scores_over_many_powers_of_two(L, lens, nq, H, ramp, fp8):
+    c = _ramped(lens, nq, H, ramp, seed=len(lens) + nq + H)
+    if ramp != "fall":
+        # The running maximum over a request's tiles rises by more than 2^8 again and again.
+        x = SM / math.log(2) * (c["q"][0].double() @ c["keys"][0].double().T)
+        tops = torch.stack([p.amax(1) for p in x.split(128, dim=1)], dim=1)
+        run = torch.cummax(tops, dim=1).values
+        assert ((run[:, 1:] - run[:, :-1]) > 8).sum(1).min() >= (8 if ramp == "rise" else 2)
+    call, cache = api.dsa_mla_decode, None
+    if fp8:
+        c, cache = _rounded_rows(c)
+        call = api.dsa_mla_decode_fp8kv
+    out, lse = _run(c, call=call, kv=cache)
+    assert api.dsa_get_device_error() == 0
+    _check(c, out, lse)
+    again, _ = _run(c, lse=False, call=call, kv=cache)
+    assert torch.equal(out, again)

@@ -239,10 +239,14 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
                : "memory");
 }
 
-// The same for a writer whose shared-memory writes the tensor cores read (made
-// visible by fence_proxy_async_smem before it): without the cluster-scope
-// release, which waits for every outstanding memory operation of the thread
-// (measured at ~1900 cycles an arrival beside a full copy pipeline).
+// The same for a writer whose writes to its own CTA's shared memory the pair's
+// tensor cores read (made visible to them by fence_proxy_async_smem before it):
+// without the cluster-scope release, which waits for every outstanding memory
+// operation of the thread (measured at ~1900 cycles an arrival beside a full copy
+// pipeline).  The arrival's own scope is the default, the CTA: no thread of the
+// other CTA reads the data, its MMA does, through the async proxy that the fence
+// ordered the writes before.  That this suffices between the CTAs of a pair is
+// what the tests show, not what the scope alone says.
 __device__ __forceinline__ void mbar_arrive_remote_async(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }

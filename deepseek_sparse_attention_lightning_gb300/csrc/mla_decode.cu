@@ -53,7 +53,7 @@
 // scales, 64 rope dims in bf16): a tile is one page, which halves K, V and P and
 // makes room for three stages of raw codes and scales (25 KB each) that the copy
 // engine runs ahead with.  Eight warps dequantise them for K, eight for V: a
-// code times its scale, rounded once to bf16, written in the layout that the
+// code times its scale in fp32, rounded to bf16, written in the layout that the
 // MMAs read.  (Read by the warps themselves, the codes of a two-page tile cost
 // more than all else: the load path took 2 of 4.3 us a tile, and 8 ragged
 // requests 351 us.)  K's three groups are dims 0-255, 256-511 and rope, which
@@ -251,7 +251,8 @@ struct PageIds {
   }
 };
 
-// 16 E4M3 codes times their scale, as bf16.
+// 16 E4M3 codes times their scale (in fp32), rounded to bf16 as the cache's other
+// rows are: the MMAs take no wider operands at their rate.
 __device__ __forceinline__ void dequant16(const uint4 raw, float scale, uint4& lo, uint4& hi) {
   const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
   uint32_t o[8];

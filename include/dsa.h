@@ -369,7 +369,8 @@ dsa_status dsa_decode_fused_fp8kv(const dsa_decode_desc* desc,
  * (they may hold anything); values that any query of the request sees have to be
  * finite (a masked one counts as probability 0 times the value).  A page id
  * outside [0, num_pages) masks the page's tokens, a seqlens[r] above
- * max_pages * 64 is cut to it; both raise DSA_ERR_DEVICE_CHECK.
+ * max_pages * 64 is cut to it; both raise DSA_ERR_DEVICE_CHECK.  (A negative one
+ * counts as 0.)
  */
 dsa_status dsa_mla_decode(const dsa_decode_desc* desc, const uint16_t* q, const uint16_t* kv,
                           float sm_scale, uint16_t* out, float* lse, void* ws, size_t ws_bytes,
@@ -377,8 +378,8 @@ dsa_status dsa_mla_decode(const dsa_decode_desc* desc, const uint16_t* q, const 
 
 /*
  * dsa_mla_decode over the FP8 latent cache kv8 [num_pages * 64, 656] (rows of
- * dsa_latent_to_fp8; 16-byte aligned): each value is its code times its scale,
- * rounded once to bf16 for the tensor cores.  Other arguments, outputs,
+ * dsa_latent_to_fp8; 16-byte aligned): each value is its code times its scale in
+ * fp32, rounded to bf16 for the tensor cores.  Other arguments, outputs,
  * workspace and errors as there.
  */
 dsa_status dsa_mla_decode_fp8kv(const dsa_decode_desc* desc, const uint16_t* q, const uint8_t* kv8,

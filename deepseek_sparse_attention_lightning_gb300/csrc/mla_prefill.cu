@@ -15,8 +15,9 @@
 // worth of traffic a key tile.  One CTA = 256 queries of one head, as two query
 // tiles of 128 (M = 128): while one tile's scores are in the softmax, the matrix
 // pipe works on the other's.  Measured: one prompt of 8192 tokens, 128 heads,
-// 1712 us = 1606 TFLOP/s over the visible pairs (84 % of the measured matrix
-// rate, 94 % of the sustained one); 8 ragged prompts of 414 .. 2047, 489 us.
+// 1.70 to 1.77 ms by the machine = 1550 to 1615 TFLOP/s over the visible pairs (81
+// to 84 % of the measured matrix rate); 8 ragged prompts of 414 .. 2047, 479 to 509
+// us; every query over all of 4096 keys, 862 us = 1594 TFLOP/s.
 //
 // Tensor memory (512 columns): S of the two tiles (128 each, fp32), O of the
 // two (128 each).  P (bf16, 64 columns) overwrites the S it came from and is
@@ -46,7 +47,8 @@
 // Warps 10 and 11: the query offsets' order, which no output is stored before.
 // The running maximum is raised lazily (by 2^8 at least), by the row's own
 // thread, which then rescales its row of O.  P is rounded to bf16 for the
-// matrix pipe, its sum kept unrounded in fp32.
+// matrix pipe (it takes operands of one type, and values are bf16), its sum kept
+// unrounded in fp32.
 //
 // Keys behind a request's end (the next request's rows in the packed tensors)
 // get probability zero, and their rows of V are cleared in shared memory: they

@@ -91,6 +91,24 @@ _SIGS = {
     "dsa_mla_prefill": (c_int32, [c_int32, c_int32, c_int32, c_int32, c_int32, c_void_p, c_void_p,
                                   c_void_p, c_void_p, c_void_p, c_int64, c_float, c_int32, c_void_p,
                                   c_void_p, c_void_p]),
+    "dsa_pages_update": (c_int32, [c_int32, c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_void_p,
+                                   c_void_p, c_void_p, c_void_p, c_int32, c_void_p, c_void_p,
+                                   c_void_p]),
+    "dsa_kv_write": (c_int32, [c_int32, c_int32, c_int32, c_void_p, c_int64, c_void_p, c_int64,
+                               c_void_p, c_int32, c_void_p, c_void_p, c_void_p]),
+    "dsa_kv_write_fp8": (c_int32, [c_int32, c_int32, c_int32, c_void_p, c_int64, c_void_p, c_int64,
+                                   c_void_p, c_int32, c_void_p, c_void_p, c_void_p, c_void_p,
+                                   c_void_p]),
+    "dsa_gqa_decode": (c_int32, [ctypes.POINTER(DecodeDesc), c_int32, c_int32, c_void_p, c_void_p,
+                                 c_void_p, c_float, c_void_p, c_void_p, c_void_p, c_size_t,
+                                 c_void_p]),
+    "dsa_gqa_decode_fp8kv": (c_int32, [ctypes.POINTER(DecodeDesc), c_int32, c_int32, c_void_p,
+                                       c_void_p, c_void_p, c_void_p, c_void_p, c_float, c_void_p,
+                                       c_void_p, c_void_p, c_size_t, c_void_p]),
+    "dsa_gqa_decode_workspace_bytes": (c_size_t, [ctypes.POINTER(DecodeDesc), c_int32, c_int32]),
+    "dsa_gqa_prefill": (c_int32, [c_int32, c_int32, c_int32, c_int32, c_int32, c_int32, c_int32,
+                                  c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_int64, c_void_p,
+                                  c_int64, c_float, c_int32, c_void_p, c_void_p, c_void_p]),
     "dsa_rmsnorm": (c_int32, [c_int32, c_int32, c_void_p, c_int64, c_void_p, c_void_p, c_float,
                               c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
     "dsa_decode_mli": (c_int32, [ctypes.POINTER(DecodeDesc), c_void_p, c_void_p, c_void_p,
@@ -344,6 +362,24 @@ def _rows_arg(t, dtype, dev, name):
     return t.data_ptr(), (ld if rows > 1 else cols)
 
 
+def _heads_arg(t, shape, dev, name):
+    """(pointer, row stride) of a bf16 tensor [rows, heads, dim] whose heads lie side by side; its rows may
+    be strided (columns of a wider projection)."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or t.dim() != 3:
+        raise TypeError(f"{name}: expected a 3-D {torch.bfloat16} tensor")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: expected a tensor on the current device cuda:{dev}, got {t.device}")
+    rows, heads, dim = shape
+    ld, hs, step = t.stride()
+    if (dim > 1 and step != 1) or (heads > 1 and hs != dim):
+        raise ValueError(f"{name}: expected contiguous heads")
+    return t.data_ptr(), (ld if rows > 1 else heads * dim)
+
+
 def _stream_on(stream, dev) -> int:
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(dev)
@@ -398,6 +434,122 @@ def dsa_mla_prefill(q, kv, k_rope, cu_q, cu_k, out, max_q, sm_scale, causal=True
               _arg(out, bf16, (Tq, H, 128), dev, "out"),
               _arg(lse, torch.float32, (Tq, H), dev, "lse"), _stream_on(stream, dev)),
            "dsa_mla_prefill")
+
+
+def dsa_pages_update(change, seqlens, page_table, free_pages, free_count, cu_new, slots, seqlens_out=None,
+                     free_count_out=None, stream=None):
+    """Pages and cache rows for the ``change`` [B] new tokens of each request (negative: it has ended and
+    gives its pages back), from the stack ``free_pages`` [num_pages] of ``free_count`` [1] pages: updates
+    ``page_table`` [B, max_pages], ``seqlens`` and ``free_count`` (or writes the new ones to ``seqlens_out``
+    and ``free_count_out``), writes ``cu_new`` [B + 1] and ``slots`` [max_tokens]; all int32; see
+    include/dsa.h."""
+    fn, dev, i32 = lib().dsa_pages_update, torch.cuda.current_device(), torch.int32
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise TypeError("page_table: expected a 2-D tensor")
+    if not isinstance(free_pages, torch.Tensor) or free_pages.dim() != 1:
+        raise TypeError("free_pages: expected a 1-D tensor")
+    if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
+        raise TypeError("slots: expected a 1-D tensor")
+    B, max_pages = page_table.shape
+    num_pages, max_tokens = free_pages.shape[0], slots.shape[0]
+    seq, cnt = _arg(seqlens, i32, (B,), dev, "seqlens"), _arg(free_count, i32, (1,), dev, "free_count")
+    _check(fn(B, max_pages, num_pages, _arg(change, i32, (B,), dev, "change"), seq,
+              seq if seqlens_out is None else _arg(seqlens_out, i32, (B,), dev, "seqlens_out"),
+              _arg(page_table, i32, (B, max_pages), dev, "page_table"),
+              _arg(free_pages, i32, (num_pages,), dev, "free_pages"), cnt,
+              cnt if free_count_out is None else _arg(free_count_out, i32, (1,), dev, "free_count_out"),
+              max_tokens, _arg(cu_new, i32, (B + 1,), dev, "cu_new"),
+              _arg(slots, i32, (max_tokens,), dev, "slots"), _stream_on(stream, dev)), "dsa_pages_update")
+
+
+def _write_args(k, v, slots, k_cache, dev):
+    """What the cache writes share: (tokens, heads, dim), pages, and the arguments up to num_pages."""
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise TypeError("k: expected a 3-D tensor")
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        raise TypeError("k_cache: expected a 4-D tensor")
+    T, K, D = shape = k.shape
+    P = k_cache.shape[0]
+    kp, ldk = _heads_arg(k, shape, dev, "k")
+    vp, ldv = _heads_arg(v, shape, dev, "v")
+    return (T, K, D, kp, ldk, vp, ldv, _arg(slots, torch.int32, (T,), dev, "slots"), P), (P, K, PAGE_SIZE, D)
+
+
+def dsa_kv_write(k, v, slots, k_cache, v_cache, stream=None):
+    """Keys and values ``k``, ``v`` bf16 [tokens, K, D] (rows may be strided, e.g. columns of one
+    projection) to the cache rows ``slots`` (int32; -1: none) of ``k_cache``, ``v_cache`` bf16
+    [num_pages, K, 64, D]; see include/dsa.h."""
+    fn, dev, bf16 = lib().dsa_kv_write, torch.cuda.current_device(), torch.bfloat16
+    args, shape = _write_args(k, v, slots, k_cache, dev)
+    _check(fn(*args, _arg(k_cache, bf16, shape, dev, "k_cache"), _arg(v_cache, bf16, shape, dev, "v_cache"),
+              _stream_on(stream, dev)), "dsa_kv_write")
+
+
+def dsa_kv_write_fp8(k, v, slots, k8, k_scale, v8, v_scale, stream=None):
+    """dsa_kv_write into FP8 caches: ``k8``, ``v8`` E4M3 codes as uint8 [num_pages, K, 64, 128], ``k_scale``,
+    ``v_scale`` float32 [num_pages, K, 64]."""
+    fn, dev, u8, f32 = lib().dsa_kv_write_fp8, torch.cuda.current_device(), torch.uint8, torch.float32
+    args, shape = _write_args(k, v, slots, k8, dev)
+    _check(fn(*args, _arg(k8, u8, shape, dev, "k8"), _arg(k_scale, f32, shape[:3], dev, "k_scale"),
+              _arg(v8, u8, shape, dev, "v8"), _arg(v_scale, f32, shape[:3], dev, "v_scale"),
+              _stream_on(stream, dev)), "dsa_kv_write_fp8")
+
+
+def dsa_gqa_decode_workspace_bytes(desc, kv_heads, dim) -> int:
+    return int(lib().dsa_gqa_decode_workspace_bytes(ctypes.byref(desc), kv_heads, dim))
+
+
+def _grouped_shape(desc, cache, name):
+    """(kv_heads, dim) of a cache [num_pages, kv_heads, 64, dim], and its shape."""
+    if not isinstance(cache, torch.Tensor) or cache.dim() != 4:
+        raise TypeError(f"{name}: expected a 4-D tensor")
+    K, D = cache.shape[1], cache.shape[3]
+    return K, D, (desc.num_pages, K, PAGE_SIZE, D)
+
+
+def dsa_gqa_decode(desc, q, k, v, out, ws, sm_scale, lse=None, stream=None):
+    """Attention of a decode step's queries ``q`` bf16 [T, H, D] over the paged caches ``k``, ``v`` bf16
+    [num_pages, K, 64, D] of a layer with grouped heads: ``out`` bf16 [T, H, D], ``lse`` float32 [T, H] or
+    None; see include/dsa.h."""
+    fn, dev, bf16 = lib().dsa_gqa_decode, torch.cuda.current_device(), torch.bfloat16
+    T, H = desc.batch * desc.q_per_req, desc.num_heads
+    K, D, shape = _grouped_shape(desc, k, "k")
+    _check(fn(ctypes.byref(desc), K, D, _arg(q, bf16, (T, H, D), dev, "q"), _arg(k, bf16, shape, dev, "k"),
+              _arg(v, bf16, shape, dev, "v"), sm_scale, _arg(out, bf16, (T, H, D), dev, "out"),
+              _arg(lse, torch.float32, (T, H), dev, "lse"), _arg(ws, torch.uint8, (ws.numel(),), dev, "ws"),
+              ws.numel(), _stream_on(stream, dev)), "dsa_gqa_decode")
+
+
+def dsa_gqa_decode_fp8kv(desc, q, k8, k_scale, v8, v_scale, out, ws, sm_scale, lse=None, stream=None):
+    """dsa_gqa_decode over the FP8 caches of dsa_kv_write_fp8."""
+    fn, dev, bf16 = lib().dsa_gqa_decode_fp8kv, torch.cuda.current_device(), torch.bfloat16
+    u8, f32 = torch.uint8, torch.float32
+    T, H = desc.batch * desc.q_per_req, desc.num_heads
+    K, D, shape = _grouped_shape(desc, k8, "k8")
+    _check(fn(ctypes.byref(desc), K, D, _arg(q, bf16, (T, H, D), dev, "q"), _arg(k8, u8, shape, dev, "k8"),
+              _arg(k_scale, f32, shape[:3], dev, "k_scale"), _arg(v8, u8, shape, dev, "v8"),
+              _arg(v_scale, f32, shape[:3], dev, "v_scale"), sm_scale, _arg(out, bf16, (T, H, D), dev, "out"),
+              _arg(lse, f32, (T, H), dev, "lse"), _arg(ws, u8, (ws.numel(),), dev, "ws"), ws.numel(),
+              _stream_on(stream, dev)), "dsa_gqa_decode_fp8kv")
+
+
+def dsa_gqa_prefill(q, k, v, cu_q, cu_k, out, max_q, sm_scale, causal=True, lse=None, stream=None):
+    """Attention of packed prompts with grouped heads: ``q`` [total_q, H, D], ``k``, ``v`` [total_k, K, D]
+    (rows may be strided: columns of one projection), ``out`` [total_q, H, D], all bf16; see
+    include/dsa.h."""
+    fn, dev, bf16, i32 = lib().dsa_gqa_prefill, torch.cuda.current_device(), torch.bfloat16, torch.int32
+    if not isinstance(q, torch.Tensor) or q.dim() != 3 or not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise TypeError("q, k: expected 3-D tensors")
+    if not isinstance(cu_q, torch.Tensor) or cu_q.dim() != 1 or cu_q.shape[0] < 2:
+        raise TypeError("cu_q: expected a 1-D tensor of at least two offsets")
+    (Tq, H, D), (Tk, K, _), B1 = q.shape, k.shape, cu_q.shape[0]
+    qp, ldq = _heads_arg(q, (Tq, H, D), dev, "q")
+    kp, ldk = _heads_arg(k, (Tk, K, D), dev, "k")
+    vp, ldv = _heads_arg(v, (Tk, K, D), dev, "v")
+    _check(fn(B1 - 1, H, K, D, Tq, Tk, max_q, _arg(cu_q, i32, (B1,), dev, "cu_q"),
+              _arg(cu_k, i32, (B1,), dev, "cu_k"), qp, ldq, kp, ldk, vp, ldv, sm_scale, 1 if causal else 0,
+              _arg(out, bf16, (Tq, H, D), dev, "out"), _arg(lse, torch.float32, (Tq, H), dev, "lse"),
+              _stream_on(stream, dev)), "dsa_gqa_prefill")
 
 
 def dsa_rmsnorm(x, weight, eps, residual=None, residual_out=None, y=None, y8=None, y_scale=None,

@@ -372,6 +372,144 @@ dsa_status dsa_mla_prefill(int32_t batch, int32_t heads, int32_t total_q, int32_
   return cuda_status(dsa::launch_mla_prefill(a, static_cast<cudaStream_t>(stream)));
 }
 
+namespace {
+
+bool dim_known(int32_t dim) { return dim == 64 || dim == 128; }
+
+// What the cache writes of layers with grouped heads have in common.
+dsa_status kv_write(int32_t tokens, int32_t kv_heads, int32_t dim, const uint16_t* k, int64_t ld_k,
+                    const uint16_t* v, int64_t ld_v, const int32_t* slots, int32_t num_pages,
+                    void* k_cache, float* k_scale, void* v_cache, float* v_scale, void* stream) {
+  if (tokens < 0 || kv_heads < 1 || num_pages < 1) return DSA_ERR_INVALID_ARG;
+  if (kv_heads > DSA_MAX_PREFILL_HEADS || !dim_known(dim) || (k_scale && dim != 128)) return DSA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(num_pages) * DSA_PAGE_SIZE >= (int64_t(1) << 31)) return DSA_ERR_UNSUPPORTED;
+  const int64_t row = static_cast<int64_t>(kv_heads) * dim;
+  if (ld_k < row || ld_v < row || ld_k % 8 != 0 || ld_v % 8 != 0) return DSA_ERR_INVALID_ARG;
+  if (tokens == 0) return DSA_OK;
+  if (!k || !v || !slots || !k_cache || !v_cache || !aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 4) ||
+      !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_scale, 4) || !aligned(v_scale, 4))
+    return DSA_ERR_INVALID_ARG;
+  dsa::KvWriteLaunch a{};
+  a.k = k; a.v = v; a.slots = slots; a.k_cache = k_cache; a.v_cache = v_cache; a.k_scale = k_scale;
+  a.v_scale = v_scale; a.ld_k = ld_k; a.ld_v = ld_v; a.tokens = tokens; a.kv_heads = kv_heads;
+  a.dim = dim; a.num_pages = num_pages;
+  return cuda_status(dsa::launch_kv_write(a, static_cast<cudaStream_t>(stream)));
+}
+
+// The sizes of a decode call over grouped heads.
+dsa_status check_grouped(const dsa_decode_desc* d, int32_t kv_heads, int32_t dim) {
+  const dsa_status st = check_dense_desc(d);
+  if (st != DSA_OK) return st;
+  if (kv_heads < 1 || d->num_heads % kv_heads != 0) return DSA_ERR_INVALID_ARG;
+  return dim_known(dim) ? DSA_OK : DSA_ERR_UNSUPPORTED;
+}
+
+dsa_status gqa_decode(const dsa_decode_desc* d, int32_t kv_heads, int32_t dim, const uint16_t* q,
+                      const void* k, const float* k_scale, const void* v, const float* v_scale,
+                      float sm_scale, uint16_t* out, float* lse, void* ws, size_t ws_bytes,
+                      void* stream) {
+  const dsa_status st = check_grouped(d, kv_heads, dim);
+  if (st != DSA_OK) return st;
+  if (!q || !k || !v || !out || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) ||
+      !aligned(lse, 4) || !aligned(k_scale, 16) || !aligned(v_scale, 16))
+    return DSA_ERR_INVALID_ARG;
+  if (!(sm_scale > 0.f) || !std::isfinite(sm_scale)) return DSA_ERR_INVALID_ARG;
+  if (!ws || !aligned(ws, 256) || ws_bytes < dsa_gqa_decode_workspace_bytes(d, kv_heads, dim))
+    return DSA_ERR_WORKSPACE;
+  dsa::GqaDecodeLaunch a{};
+  a.q = q; a.k = k; a.v = v; a.k_scale = k_scale; a.v_scale = v_scale; a.seqlens = d->seqlens;
+  a.page_table = d->page_table; a.out = out; a.lse = lse; a.batch = d->batch; a.nq = d->q_per_req;
+  a.heads = d->num_heads; a.kv_heads = kv_heads; a.dim = dim; a.max_pages = d->max_pages;
+  a.num_pages = d->num_pages; a.sm_scale = sm_scale;
+  return cuda_status(dsa::launch_gqa_decode(a, ws, static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+dsa_status dsa_pages_update(int32_t batch, int32_t max_pages, int32_t num_pages,
+                            const int32_t* change, const int32_t* seqlens, int32_t* seqlens_out,
+                            int32_t* page_table, int32_t* free_pages, const int32_t* free_count,
+                            int32_t* free_count_out, int32_t max_tokens, int32_t* cu_new,
+                            int32_t* slots, void* stream) {
+  if (batch < 1 || max_pages < 1 || num_pages < 1 || max_tokens < 0) return DSA_ERR_INVALID_ARG;
+  if (batch > DSA_MAX_PREFILL_BATCH || static_cast<int64_t>(num_pages) * DSA_PAGE_SIZE >= (int64_t(1) << 31) ||
+      static_cast<int64_t>(max_pages) * DSA_PAGE_SIZE >= (int64_t(1) << 31))
+    return DSA_ERR_UNSUPPORTED;
+  const void* words[] = {change, seqlens, seqlens_out, page_table, free_pages, free_count, free_count_out, cu_new};
+  for (const void* w : words)
+    if (!w || !aligned(w, 4)) return DSA_ERR_INVALID_ARG;
+  if ((max_tokens > 0 && !slots) || !aligned(slots, 4)) return DSA_ERR_INVALID_ARG;
+  dsa::PagesLaunch a{};
+  a.change = change; a.seqlens = seqlens; a.seqlens_out = seqlens_out; a.page_table = page_table;
+  a.free_pages = free_pages; a.free_count = free_count; a.free_count_out = free_count_out;
+  a.cu_new = cu_new; a.slots = slots; a.batch = batch; a.max_pages = max_pages;
+  a.num_pages = num_pages; a.max_tokens = max_tokens;
+  return cuda_status(dsa::launch_pages(a, static_cast<cudaStream_t>(stream)));
+}
+
+dsa_status dsa_kv_write(int32_t tokens, int32_t kv_heads, int32_t dim, const uint16_t* k,
+                        int64_t ld_k, const uint16_t* v, int64_t ld_v, const int32_t* slots,
+                        int32_t num_pages, uint16_t* k_cache, uint16_t* v_cache, void* stream) {
+  return kv_write(tokens, kv_heads, dim, k, ld_k, v, ld_v, slots, num_pages, k_cache, nullptr, v_cache, nullptr,
+                  stream);
+}
+
+dsa_status dsa_kv_write_fp8(int32_t tokens, int32_t kv_heads, int32_t dim, const uint16_t* k,
+                            int64_t ld_k, const uint16_t* v, int64_t ld_v, const int32_t* slots,
+                            int32_t num_pages, uint8_t* k8, float* k_scale, uint8_t* v8,
+                            float* v_scale, void* stream) {
+  if (!k_scale || !v_scale) return DSA_ERR_INVALID_ARG;
+  return kv_write(tokens, kv_heads, dim, k, ld_k, v, ld_v, slots, num_pages, k8, k_scale, v8, v_scale, stream);
+}
+
+size_t dsa_gqa_decode_workspace_bytes(const dsa_decode_desc* d, int32_t kv_heads, int32_t dim) {
+  if (check_grouped(d, kv_heads, dim) != DSA_OK) return 0;
+  return dsa::gqa_decode_workspace(d->q_per_req, d->num_heads, kv_heads, dim);
+}
+
+dsa_status dsa_gqa_decode(const dsa_decode_desc* d, int32_t kv_heads, int32_t dim,
+                          const uint16_t* q, const uint16_t* k, const uint16_t* v, float sm_scale,
+                          uint16_t* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  return gqa_decode(d, kv_heads, dim, q, k, nullptr, v, nullptr, sm_scale, out, lse, ws, ws_bytes, stream);
+}
+
+dsa_status dsa_gqa_decode_fp8kv(const dsa_decode_desc* d, int32_t kv_heads, int32_t dim,
+                                const uint16_t* q, const uint8_t* k8, const float* k_scale,
+                                const uint8_t* v8, const float* v_scale, float sm_scale,
+                                uint16_t* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  if (!k_scale || !v_scale) return DSA_ERR_INVALID_ARG;
+  if (dim == 64) return DSA_ERR_UNSUPPORTED;
+  return gqa_decode(d, kv_heads, dim, q, k8, k_scale, v8, v_scale, sm_scale, out, lse, ws, ws_bytes, stream);
+}
+
+dsa_status dsa_gqa_prefill(int32_t batch, int32_t heads, int32_t kv_heads, int32_t dim,
+                           int32_t total_q, int32_t total_k, int32_t max_q, const int32_t* cu_q,
+                           const int32_t* cu_k, const uint16_t* q, int64_t ld_q, const uint16_t* k,
+                           int64_t ld_k, const uint16_t* v, int64_t ld_v, float sm_scale,
+                           int32_t causal, uint16_t* out, float* lse, void* stream) {
+  if (batch < 1 || heads < 1 || kv_heads < 1 || total_q < 0 || total_k < 0 || max_q < 0 || heads % kv_heads != 0)
+    return DSA_ERR_INVALID_ARG;
+  if (!(sm_scale > 0.f) || !std::isfinite(sm_scale)) return DSA_ERR_INVALID_ARG;
+  if (batch > DSA_MAX_PREFILL_BATCH || heads > DSA_MAX_PREFILL_HEADS || heads / kv_heads > DSA_MAX_GROUP ||
+      !dim_known(dim))
+    return DSA_ERR_UNSUPPORTED;
+  const int64_t qrow = static_cast<int64_t>(heads) * dim, krow = static_cast<int64_t>(kv_heads) * dim;
+  if (ld_q < qrow || ld_k < krow || ld_v < krow || ld_q % 8 != 0 || ld_k % 8 != 0 || ld_v % 8 != 0)
+    return DSA_ERR_INVALID_ARG;
+  if (!cu_q || !cu_k || !aligned(cu_q, 4) || !aligned(cu_k, 4)) return DSA_ERR_INVALID_ARG;
+  if (total_q == 0 || max_q == 0) return DSA_OK;
+  if (!q || !out || !aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4)) return DSA_ERR_INVALID_ARG;
+  // Without a key the pointers are not read, but the copies' maps need some.
+  if (total_k > 0 && (!k || !v || !aligned(k, 16) || !aligned(v, 16))) return DSA_ERR_INVALID_ARG;
+  dsa::GqaPrefillLaunch a{};
+  a.q = q; a.k = total_k > 0 ? k : q; a.v = total_k > 0 ? v : q; a.cu_q = cu_q; a.cu_k = cu_k;
+  a.out = out; a.lse = lse; a.ld_q = ld_q; a.ld_k = ld_k; a.ld_v = ld_v; a.batch = batch;
+  a.heads = heads; a.kv_heads = kv_heads; a.dim = dim; a.total_q = total_q; a.total_k = total_k;
+  a.max_q = max_q < total_q ? max_q : total_q; a.causal = causal != 0; a.sm_scale = sm_scale;
+  if (dsa::gqa_prefill_items(a) > INT_MAX) return DSA_ERR_UNSUPPORTED;
+  return cuda_status(dsa::launch_gqa_prefill(a, static_cast<cudaStream_t>(stream)));
+}
+
 dsa_status dsa_rmsnorm(int32_t rows, int32_t dim, const uint16_t* x, int64_t ld_x,
                        const uint16_t* residual, const uint16_t* weight, float eps, int32_t group,
                        uint16_t* residual_out, uint16_t* y, uint8_t* y8, float* y_scale,
@@ -807,9 +945,11 @@ dsa_status dsa_decode_step_ring(const dsa_decode_desc* desc, dsa_step_ring* ring
 
 dsa_status dsa_get_device_error(void* stream) {
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return DSA_ERR_CUDA;
-  const int codes[7] = {dsa::fetch_error_indexer(), dsa::fetch_error_topk(), dsa::fetch_error_mla(),
-                        dsa::fetch_error_merge(), dsa::fetch_error_cache(),
-                        dsa::fetch_error_mla_dense(), dsa::fetch_error_mla_prefill()};
+  const int codes[] = {dsa::fetch_error_indexer(), dsa::fetch_error_topk(), dsa::fetch_error_mla(),
+                       dsa::fetch_error_merge(), dsa::fetch_error_cache(),
+                       dsa::fetch_error_mla_dense(), dsa::fetch_error_mla_prefill(),
+                       dsa::fetch_error_pages(), dsa::fetch_error_kv_write(),
+                       dsa::fetch_error_gqa_prefill(), dsa::fetch_error_gqa_decode()};
   for (int c : codes)
     if (c != 0) return static_cast<dsa_status>(c);
   return DSA_OK;

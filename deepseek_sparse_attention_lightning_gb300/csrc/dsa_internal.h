@@ -130,6 +130,66 @@ struct MlaPrefillLaunch {
   float sm_scale;
 };
 
+struct PagesLaunch {
+  const int32_t* change;         // [batch] tokens added; < 0: the request has ended
+  const int32_t* seqlens;        // [batch]
+  int32_t* seqlens_out;          // [batch], may be seqlens
+  int32_t* page_table;           // [batch][max_pages]
+  int32_t* free_pages;           // [num_pages], a stack
+  const int32_t* free_count;     // pages on it
+  int32_t* free_count_out;       // may be free_count
+  int32_t* cu_new;               // [batch + 1]
+  int32_t* slots;                // [max_tokens]
+  int batch, max_pages, num_pages, max_tokens;
+};
+
+struct KvWriteLaunch {
+  const uint16_t* k;             // [tokens] rows of kv_heads * dim bf16, ld_k apart
+  const uint16_t* v;
+  const int32_t* slots;          // [tokens] cache rows, -1: none
+  void* k_cache;                 // [num_pages][kv_heads][64][dim] bf16, or E4M3 with scales
+  void* v_cache;
+  float* k_scale;                // [num_pages][kv_heads][64], or nullptr (bf16)
+  float* v_scale;
+  long long ld_k, ld_v;
+  int tokens, kv_heads, dim, num_pages;
+};
+
+struct GqaPrefillLaunch {
+  const uint16_t* q;             // [total_q] rows of heads * dim bf16, ld_q apart
+  const uint16_t* k;             // [total_k] rows of kv_heads * dim bf16, ld_k apart
+  const uint16_t* v;
+  const int32_t* cu_q;           // [batch + 1]
+  const int32_t* cu_k;
+  uint16_t* out;                 // [total_q][heads][dim] bf16
+  float* lse;                    // [total_q][heads] or nullptr
+  long long ld_q, ld_k, ld_v;
+  int batch, heads, kv_heads, dim, total_q, total_k, max_q, causal;
+  int group, tile_q;             // set by launch_gqa_prefill: query heads a key head, queries of a tile
+  int out_wide;                  //   out is 32-byte aligned
+  int parts;                     //   CTAs (a cluster) that share an item's keys
+  int slots, head_group;         //   query blocks of all requests; key heads that run together
+  float sm_scale;
+};
+
+struct GqaDecodeLaunch {
+  const uint16_t* q;             // [T][heads][dim] bf16
+  const void* k;                 // [num_pages][kv_heads][64][dim] bf16, or E4M3 with scales
+  const void* v;
+  const float* k_scale;          // [num_pages][kv_heads][64], or nullptr (bf16)
+  const float* v_scale;
+  const int32_t* seqlens;
+  const int32_t* page_table;
+  uint16_t* out;                 // [T][heads][dim] bf16
+  float* lse;                    // [T][heads] or nullptr
+  float* part_o;                 // set by launch_gqa_decode: partial outputs and
+  float* part_lse;               //   their log-sum-exps, in the workspace, and for
+  int4* joins;                   //   each CTA what is joined from it on
+  int batch, nq, heads, kv_heads, dim, max_pages, num_pages;
+  int row_tiles, tile_q, tile_rows, ctas, min_tiles;   // set by launch_gqa_decode
+  float sm_scale;
+};
+
 cudaError_t launch_indexer(const IndexerLaunch& a, cudaStream_t s);
 // Bound, in SM cycles, of the indexer's pipeline waits on later launches
 // (<= 0: the default kWaitCycles).
@@ -147,6 +207,15 @@ cudaError_t launch_mla_decode(MlaDecodeLaunch a, void* ws, cudaStream_t s);
 // no kernel), and its launch.
 long long mla_prefill_items(const MlaPrefillLaunch& a);
 cudaError_t launch_mla_prefill(MlaPrefillLaunch a, cudaStream_t s);
+cudaError_t launch_pages(const PagesLaunch& a, cudaStream_t s);
+cudaError_t launch_kv_write(const KvWriteLaunch& a, cudaStream_t s);
+// Prompt attention with grouped heads: blocks of its grid before keys are shared
+// (no kernel), and its launch.
+long long gqa_prefill_items(const GqaPrefillLaunch& a);
+cudaError_t launch_gqa_prefill(GqaPrefillLaunch a, cudaStream_t s);
+// Paged attention with grouped heads: its workspace (no kernel), and its launch.
+size_t gqa_decode_workspace(int nq, int heads, int kv_heads, int dim);
+cudaError_t launch_gqa_decode(GqaDecodeLaunch a, void* ws, cudaStream_t s);
 cudaError_t launch_merge(int rows, int splits, const float* mid_o, const float* mid_lse,
                          float* out, float* out_lse, cudaStream_t s, bool pdl = false);
 
@@ -190,6 +259,10 @@ int fetch_error_merge();
 int fetch_error_cache();
 int fetch_error_mla_dense();
 int fetch_error_mla_prefill();
+int fetch_error_pages();
+int fetch_error_kv_write();
+int fetch_error_gqa_prefill();
+int fetch_error_gqa_decode();
 
 // Host helpers (dsa_api.cu).
 // The checks every entry point applies to a decode descriptor: a dsa_status.

@@ -1,0 +1,827 @@
+// gqa_decode.cu -- attention of a decode step's queries over the paged cache of a
+// layer with grouped heads (the textbook form): G query heads share a key / value
+// head of 64 or 128 dims, a request has n_q queries.
+//
+//   x[row, s] = sm_scale * q[row] . k[s]      (s < vis[row])
+//   out[row]  = sum_s softmax(x)[s] * v[s],   lse = log sum_s exp(x)
+//
+// Bound by HBM: every key and value is read once, for n_q * G rows that share it.
+//
+// The rows of a request and key head are one row tile (M = 128; more queries than
+// fit: several), its keys tiles of two pages (128 tokens).  With few rows the MMAs
+// have room to spare (1024 cycles a tile of 64 KB, which takes ~2800 to read), and
+// the softmax's latency would bound the kernel instead: a thread that walks a row's
+// 128 scores.  So up to 32 rows stand four times in the tile, once in each 32 lanes
+// of tensor memory, up to 64 twice: every copy has the same scores, and its threads
+// take a quarter (half) of the tile's keys, with a maximum, a sum and an output of
+// their own, joined where the stretch ends.  (P of the other keys is zero; it is
+// stored once, a copy's own columns each tile.)
+//
+// Tensor memory: two buffers of S (128 columns), two of P (bf16, 64), O (D).
+// Shared memory: q, and a ring of granules, K and V of the key tiles in turn, that
+// the copies run ahead in (a page of a head is one contiguous block).
+//
+// Work: the key tiles of all requests and heads (and what it costs to begin one)
+// form one line that is cut evenly over the CTAs, one an SM.  An item (request, key
+// head, row tile) that spans CTAs is joined by gqa_merge_kernel from fp32 partials
+// and their log-sum-exps.
+//
+// Roles (256 threads): warp 0 copies, warp 1 MMAs (Q K^T of tile j + 1 runs while
+// tile j is in the softmax), warps 4-7 softmax and epilogue, warp 3 the outputs of
+// requests without tokens.  The running maximum is raised lazily (only when a tile
+// exceeds it by 2^8 does the output get rescaled).  P is rounded to bf16 for the
+// matrix pipe (as values are); its sum is kept unrounded in fp32.
+//
+// Rows of V that no query sees (behind the request's end in its last page, a page
+// that is not there or whose id is out of range) are cleared in shared memory
+// before P V: their probabilities are zero, but what lies there may be NaN.
+#include <algorithm>
+
+#include "dsa_ptx.cuh"
+#include "dsa_internal.h"
+
+DSA_DEFINE_ERROR_WORD(gqa_decode)
+
+namespace dsa {
+namespace {
+
+constexpr int kRows = 128;                     // of a row tile (M)
+constexpr int kKeys = 2 * kPage;               // of a key tile
+constexpr int kAtomBytes = kRows * 128;        // 128 rows x 64 dims
+constexpr int kPageAtom = kPage * 128;         // 64 rows x 64 dims
+constexpr int kThreads = 256, kSoftThreads = 128;
+constexpr int kStretch = 2;                    // what an item's queries and output cost, in key tiles
+constexpr int kColS = 0, kColP = 256, kColO = 384, kTmemCols = 512;
+constexpr int kStage = kSoftThreads * 32 * 4;  // 32 columns of a copy's rows, fp32
+constexpr float kRaiseLog2 = 8.0f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+template <int kDim>
+struct Geo {
+  static constexpr int kAtoms = kDim / 64;
+  static constexpr int kOperand = kAtoms * kAtomBytes;      // q, or K or V of a tile
+  static constexpr int kRing = kDim == 128 ? 5 : 8;         // granules
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffRing = kOperand;
+  static constexpr int kOffStage = kOffRing + kRing * kOperand;      // two buffers
+  static constexpr int kOffXchg = kOffStage + 2 * kStage;            // (maximum, sum) of 128 threads
+  static constexpr int kOffBar = kOffXchg + kSoftThreads * 8;
+  static constexpr int kOffInfo = kOffBar + 40 * 8;
+  static constexpr int kSmemBytes = kOffInfo + 48 + 1024;
+  static_assert(kSmemBytes <= 232448, "shared memory");
+};
+
+// mbar_wait by a whole warp: the same answer in every lane.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+}
+
+// Tokens of request r: seqlens[r], at least 0 and at most what its row of the page
+// table covers (more is an error the kernel reports).
+__device__ __forceinline__ int request_len(const GqaDecodeLaunch& p, int r) {
+  const int s = __ldg(p.seqlens + r);
+  if (s > p.max_pages * kPage) {
+    raise_error(kErrCheck);
+    return p.max_pages * kPage;
+  }
+  return s < 0 ? 0 : s;
+}
+
+__device__ __forceinline__ int tiles_of(int len) { return (len + kKeys - 1) / kKeys; }
+__device__ __forceinline__ int units_of(int len) { return len > 0 ? tiles_of(len) + kStretch : 0; }
+
+// The line: for each item with tokens kStretch units and one a key tile, the items
+// of a request one after another.  It is cut into parts from unit kStretch on, so
+// that the first item's tiles alone count; a cut among an item's kStretch units
+// falls before its first tile.
+struct Line {
+  long long total;
+  int parts;
+};
+
+__device__ __forceinline__ long long cut(const Line& ln, int g) {
+  return kStretch + (ln.total - kStretch) * g / ln.parts;
+}
+
+// (one warp) The line of all requests.
+__device__ __forceinline__ Line scan_total(const GqaDecodeLaunch& p, int lane) {
+  const int items = p.kv_heads * p.row_tiles;      // of a request
+  long long n = 0;
+  for (int r = lane; r < p.batch; r += 32) n += units_of(request_len(p, r));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+  Line ln;
+  ln.total = n * items;
+  const long long most = (ln.total - kStretch + p.min_tiles - 1) / p.min_tiles;
+  ln.parts = most < p.ctas ? static_cast<int>(most < 1 ? 1 : most) : p.ctas;
+  return ln;
+}
+
+// (one warp) The item that holds unit `at` of the line (at < total): its request,
+// which of the request's it is, and the line position of its first unit.
+__device__ __forceinline__ void locate(const GqaDecodeLaunch& p, long long at, int lane, int& req, int& item,
+                                       long long& first) {
+  const int items = p.kv_heads * p.row_tiles;
+  long long base = 0;
+  req = item = 0;
+  first = 0;
+  for (int r0 = 0; r0 < p.batch; r0 += 32) {
+    const int r = r0 + lane;
+    const long long n = r < p.batch ? static_cast<long long>(units_of(request_len(p, r))) * items : 0;
+    long long incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long u = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += u;
+    }
+    const uint32_t hit = __ballot_sync(0xffffffffu, base + incl > at);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      req = r0 + l;
+      const long long begin = base + __shfl_sync(0xffffffffu, incl - n, l);
+      const int each = static_cast<int>(__shfl_sync(0xffffffffu, n, l) / items);
+      item = static_cast<int>((at - begin) / each);
+      first = begin + static_cast<long long>(item) * each;
+      return;
+    }
+    base += __shfl_sync(0xffffffffu, incl, 31);
+  }
+}
+
+// The stretches of items in a CTA's part [pos, hi) of the line, in order.
+struct Walk {
+  long long pos, hi;     // next unit of the line, end of the part
+  int req, item;         // of the stretch
+  int unit;              // unit of the item at pos
+  int len, nt;           // the request's tokens and key tiles
+  int t0, t1;            // the stretch's tiles
+  __device__ __forceinline__ bool next(const GqaDecodeLaunch& p) {
+    while (pos < hi) {
+      if (unit == nt + kStretch || nt == 0) {     // on to the next item
+        ++item;
+        unit = 0;
+        if (nt == 0 || item == p.kv_heads * p.row_tiles) {
+          item = 0;
+          do {      // (the line has units left: a request with tokens comes)
+            ++req;
+            len = request_len(p, req);
+            nt = tiles_of(len);
+          } while (nt == 0);
+        }
+      }
+      const long long left = hi - pos;
+      const int end = static_cast<int>(left < nt + kStretch - unit ? unit + left : nt + kStretch);
+      t0 = max(0, unit - kStretch);
+      t1 = max(0, end - kStretch);
+      pos += end - unit;
+      unit = end;
+      if (t1 > t0) return true;
+    }
+    return false;
+  }
+};
+
+// Page ids of a stretch's tiles, 32 at a time (an id a lane) and one batch ahead:
+// kNone behind the request's last page, kBad for an id outside the cache.
+struct PageBatch {
+  static constexpr int kNone = -1, kBad = -2, kTiles = 16;      // tiles of a batch
+  const int32_t* table;
+  int pages, num_pages, t0, now, ahead;
+  __device__ __forceinline__ int get(int i) const {
+    if (i >= pages) return kNone;
+    const int id = __ldg(table + i);
+    return id >= 0 && id < num_pages ? id : kBad;
+  }
+  __device__ __forceinline__ PageBatch(const GqaDecodeLaunch& p, const Walk& wk, int lane)
+      : table(p.page_table + static_cast<long long>(wk.req) * p.max_pages), pages((wk.len + kPage - 1) / kPage),
+        num_pages(p.num_pages), t0(wk.t0), now(0) {
+    ahead = get(2 * t0 + lane);
+  }
+  // Before tile t's pages are asked for, t going up by one.
+  __device__ __forceinline__ bool advance(int t, int lane) {
+    if (((t - t0) & (kTiles - 1)) != 0) return false;
+    now = ahead;
+    ahead = get(2 * (t + kTiles) + lane);
+    return true;
+  }
+  // Page h of tile t.
+  __device__ __forceinline__ int page(int t, int h) const {
+    return __shfl_sync(0xffffffffu, now, 2 * ((t - t0) & (kTiles - 1)) + h);
+  }
+};
+
+template <int kN>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t addr, uint32_t (&r)[kN]) {
+  if constexpr (kN == 32) tmem_ld32(addr, r);
+  else if constexpr (kN == 64) tmem_ld64(addr, r);
+  else tmem_ld128(addr, r);
+}
+
+template <int kDim, int kCopies>
+__global__ void __launch_bounds__(kThreads, 1)
+    gqa_decode_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
+                      const __grid_constant__ CUtensorMap tmap_v, const GqaDecodeLaunch p) {
+  using T = Geo<kDim>;
+  constexpr int kCols = kKeys / kCopies;         // keys of a softmax thread
+  constexpr int kCopyRows = kRows / kCopies;     // lanes of a copy
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const float ninf = __int_as_float(0xff800000);
+  const uint32_t bar0 = sbase + T::kOffBar;
+// Granule n (K of tile i: 2 i, V: 2 i + 1): landed, and read.
+#define FULL(n) (bar0 + 8u * ((n) % T::kRing))
+#define EMPTY(n) (bar0 + 64u + 8u * ((n) % T::kRing))
+#define RING_PARITY(n) (((n) / T::kRing) & 1)
+// q of a stretch landed / read; O read by the epilogue; of tile i: scores, probabilities, P V done.
+#define Q_FULL (bar0 + 128u)
+#define Q_EMPTY (bar0 + 136u)
+#define O_FREE (bar0 + 144u)
+#define DRAIN (bar0 + 152u)
+#define S_FULL(i) (bar0 + 160u + 8u * ((i) & 1))
+#define P_FULL(i) (bar0 + 176u + 8u * ((i) & 1))
+#define PV_DONE(i) (bar0 + 192u + 8u * ((i) & 1))
+#define PARITY2(i) (((i) >> 1) & 1)
+  long long* info = reinterpret_cast<long long*>(smem + T::kOffInfo);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + T::kOffInfo + 40);
+
+  if (warp == 0 && lane == 0) {
+    for (int n = 0; n < T::kRing; ++n) {
+      mbar_init(FULL(n), 1);
+      mbar_init(EMPTY(n), 1);
+    }
+    mbar_init(Q_FULL, 1);
+    mbar_init(Q_EMPTY, 1);
+    mbar_init(O_FREE, kSoftThreads / 32);
+    mbar_init(DRAIN, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(S_FULL(i), 1);
+      mbar_init(P_FULL(i), kSoftThreads / 32);
+      mbar_init(PV_DONE(i), 1);
+    }
+    fence_mbar_init();
+    prefetch_tmap(&tmap_q);
+    prefetch_tmap(&tmap_k);
+    prefetch_tmap(&tmap_v);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish();
+  }
+  if (warp == 3) {
+    const Line ln = scan_total(p, lane);
+    const int part = blockIdx.x;
+    long long lo = 0, hi = 0, first = 0;
+    int req = 0, item = 0;
+    if (part < ln.parts && ln.total > 0) {
+      lo = cut(ln, part);
+      hi = cut(ln, part + 1);
+      if (hi > lo) locate(p, lo, lane, req, item, first);
+    }
+    // What the merge has to join: the item that this part's first cut falls into, if
+    // it is the first cut inside that item, and its last part.
+    if (lane == 0) {
+      int4 join = make_int4(-1, 0, 0, 0);
+      const long long tile0 = first + kStretch;
+      if (part > 0 && hi > lo && lo > tile0 && cut(ln, part - 1) <= tile0) {
+        const long long end = tile0 + tiles_of(request_len(p, req)) - kStretch;      // the item's, from unit kStretch
+        join = make_int4(req, item, static_cast<int>((end * ln.parts - 1) / (ln.total - kStretch)), 0);
+      }
+      p.joins[part] = join;
+      info[0] = lo;
+      info[1] = hi;
+      info[2] = first;
+      info[3] = static_cast<long long>(item) << 32 | req;
+    }
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+  Walk wk;
+  wk.pos = info[0];
+  wk.hi = info[1];
+  wk.req = static_cast<int>(info[3] & 0xffffffff);
+  wk.item = static_cast<int>(info[3] >> 32);
+  wk.len = request_len(p, wk.req);
+  wk.nt = tiles_of(wk.len);
+  wk.unit = static_cast<int>(wk.pos - info[2]);
+  wk.t0 = wk.t1 = 0;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------- copies
+    bool ok = true;
+    int it = 0, seg = 0;
+    const uint32_t q_bytes = kCopies * T::kAtoms * p.tile_rows * 128;
+    for (; ok && wk.next(p); ++seg) {
+      PageBatch pages(p, wk, lane);
+      const int head = wk.item / p.row_tiles, mtile = wk.item % p.row_tiles;
+      for (int t = wk.t0; ok && t < wk.t1; ++t, ++it) {
+        if (pages.advance(t, lane) && pages.now == PageBatch::kBad) raise_error(kErrCheck);
+        const int page[2] = {pages.page(t, 0), pages.page(t, 1)};
+        const uint32_t bytes = ((page[0] >= 0) + (page[1] >= 0)) * T::kAtoms * kPageAtom;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const int n = 2 * it + g;
+          if (n >= T::kRing && ok && !mbar_wait(EMPTY(n), RING_PARITY(n - T::kRing))) ok = false;
+          if (ok && lane == 0) {
+            mbar_expect_tx(FULL(n), bytes);
+            const uint32_t dst = sbase + T::kOffRing + (n % T::kRing) * T::kOperand;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              if (page[h] >= 0)
+#pragma unroll
+                for (int a = 0; a < T::kAtoms; ++a)
+                  tma_load_5d(dst + a * kAtomBytes + h * kPageAtom, g == 0 ? &tmap_k : &tmap_v, 0, 0, a, head, page[h],
+                              FULL(n));
+          }
+          if (g == 0 && t == wk.t0) {
+            if (seg > 0 && ok && !mbar_wait(Q_EMPTY, (seg - 1) & 1)) ok = false;
+            if (ok && lane == 0) {
+              mbar_expect_tx(Q_FULL, q_bytes);
+              for (int c = 0; c < kCopies; ++c)
+                for (int a = 0; a < T::kAtoms; ++a)
+                  tma_load_5d(sbase + T::kOffQ + a * kAtomBytes + c * kCopyRows * 128, &tmap_q, 0, 0,
+                              wk.req * p.nq + mtile * p.tile_q, a, head, Q_FULL);
+            }
+          }
+          ok = __all_sync(0xffffffffu, ok);
+        }
+      }
+    }
+    if (!ok && lane == 0) raise_error(kErrTimeout);
+  } else if (warp == 1) {
+    // --------------------------------------------------------------- MMAs
+    // The whole warp runs this; one lane issues.
+    const uint32_t el = elect_one() ? 1u : 0u;
+    constexpr uint32_t idesc_qk = make_idesc(1, 1, 0, 0, kKeys, kRows);
+    constexpr uint32_t idesc_pv = make_idesc(1, 1, 0, 1, kDim, kRows);
+    const uint64_t dq = smem_desc_sw128(sbase + T::kOffQ, 16, 1024);
+    const uint64_t dk0 = smem_desc_sw128(sbase + T::kOffRing, 16, 1024);
+    const uint64_t dv0 = smem_desc_sw128(sbase + T::kOffRing, kAtomBytes, 1024);      // MN-major
+    auto slot_of = [&](int n) -> uint64_t {
+      return static_cast<uint32_t>(__shfl_sync(0xffffffffu, ((n % T::kRing) * T::kOperand) >> 4, 0));
+    };
+    bool ok = true;
+    int it = 0, npv = 0;
+    // P V of tile npv (its stretch's first: the output starts at zero, once the
+    // epilogue has read the stretch before).
+    int pv_seg = 0, pv_left = 0;
+    Walk pvw = wk;
+    auto issue_pv = [&]() -> bool {
+      bool fresh = false;
+      if (pv_left == 0) {
+        pvw.next(p);
+        pv_left = pvw.t1 - pvw.t0;
+        fresh = true;
+        if (pv_seg > 0 && !warp_wait(O_FREE, (pv_seg - 1) & 1)) return false;
+        ++pv_seg;
+      }
+      const int n = 2 * npv + 1;
+      if (!warp_wait(FULL(n), RING_PARITY(n)) || !warp_wait(P_FULL(npv), PARITY2(npv))) return false;
+      tc_fence_after();
+      const uint64_t dv = dv0 + slot_of(n);
+      const uint32_t tp = tmem + kColP + 64 * (npv & 1);
+#pragma unroll
+      for (int k = 0; k < kKeys / 16; ++k)
+        mma_f16_ts_uni(tmem + kColO, tp + 8 * k, dv + static_cast<uint64_t>((2048 * k) >> 4), idesc_pv,
+                       (!fresh || k > 0) ? 1u : 0u, el);
+      if (el) {
+        tc_commit(EMPTY(n));
+        tc_commit(PV_DONE(npv));
+      }
+      __syncwarp();
+      --pv_left;
+      ++npv;
+      return true;
+    };
+    for (int seg = 0; ok && wk.next(p); ++seg) {
+      if (!(ok = warp_wait(Q_FULL, seg & 1))) break;
+      for (int t = wk.t0; t < wk.t1; ++t, ++it) {
+        // (Scores of tile it - 2 were read: its P V was issued, after its P_FULL.)
+        const int n = 2 * it;
+        if (!(ok = warp_wait(FULL(n), RING_PARITY(n)))) break;
+        tc_fence_after();
+        const uint64_t dk = dk0 + slot_of(n);
+        const uint32_t ts = tmem + kColS + kKeys * (it & 1);
+#pragma unroll
+        for (int a = 0; a < T::kAtoms; ++a)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_f16_ss_uni(ts, dq + static_cast<uint64_t>((a * kAtomBytes + 32 * k) >> 4),
+                           dk + static_cast<uint64_t>((a * kAtomBytes + 32 * k) >> 4), idesc_qk, (a > 0 || k > 0) ? 1u : 0u, el);
+        if (el) {
+          tc_commit(EMPTY(n));
+          tc_commit(S_FULL(it));
+          if (t == wk.t1 - 1) tc_commit(Q_EMPTY);
+        }
+        __syncwarp();
+        if (it > 0 && !(ok = issue_pv())) break;
+      }
+    }
+    if (ok && it > 0) ok = issue_pv();
+    if (!ok && el) raise_error(kErrTimeout);
+    if (el) tc_commit(DRAIN);      // every MMA is done before TMEM is freed
+    __syncwarp();
+    mbar_wait(DRAIN, 0);
+    __syncwarp();
+  } else if (warp == 3) {
+    // Requests without tokens (no part of the line is theirs).
+    const int rows = p.nq * p.heads;
+    for (int r = blockIdx.x; r < p.batch; r += gridDim.x) {
+      if (request_len(p, r) > 0) continue;
+      const long long row0 = static_cast<long long>(r) * rows;
+      uint4* dst = reinterpret_cast<uint4*>(p.out + row0 * kDim);
+      for (int e = lane; e < rows * (kDim / 8); e += 32) dst[e] = make_uint4(0u, 0u, 0u, 0u);
+      if (p.lse)
+        for (int e = lane; e < rows; e += 32) p.lse[row0 + e] = ninf;
+    }
+  } else if (warp >= 4) {
+    // ---------------------------------------------- softmax and epilogue
+    const int tid = threadIdx.x - 128;             // = TMEM lane
+    const int w4 = warp & 3;
+    const int copy = tid / kCopyRows, row = tid % kCopyRows;      // row of the tile
+    const uint32_t lanebase = static_cast<uint32_t>(w4 * 32) << 16;
+    const int group = p.heads / p.kv_heads;
+    const int my_q = row / group;
+    float2* xchg = reinterpret_cast<float2*>(smem + T::kOffXchg);
+    const float sc = p.sm_scale * kLog2e;
+    if constexpr (kCopies > 1) {
+      // P of the other copies' keys: zero, once.
+      uint32_t z[32];
+#pragma unroll
+      for (int e = 0; e < 32; ++e) z[e] = 0u;
+      for (int c = 0; c < 4; ++c) tmem_st32(tmem + lanebase + kColP + 32 * c, z);
+    }
+    bool ok = true;
+    int it = 0, stage = 0;
+    while (wk.next(p)) {
+      PageBatch pages(p, wk, lane);
+      const int head = wk.item / p.row_tiles, mtile = wk.item % p.row_tiles;
+      const int qi = mtile * p.tile_q + my_q;
+      const bool live = my_q < p.tile_q && qi < p.nq;
+      const int vis = live ? wk.len - (p.nq - 1 - qi) : 0;
+      float mrun = ninf, lrun = 0.f;      // maximum and sum (this thread's keys) in the exp2 domain
+      uint32_t good = 0;                  // validity of the next 32 page ids
+      for (int t = wk.t0; t < wk.t1; ++t, ++it) {
+        if (pages.advance(t, lane)) good = __ballot_sync(0xffffffffu, pages.now >= 0);
+        // Bit h: page h of the tile can be read.
+        const uint32_t ok2 = good >> (2 * ((t - wk.t0) & (PageBatch::kTiles - 1)));
+        if (ok && !mbar_wait(S_FULL(it), PARITY2(it))) ok = false;
+        tc_fence_after();
+        uint32_t s[kCols];
+        tmem_ld_cols<kCols>(tmem + lanebase + kColS + kKeys * (it & 1) + kCols * copy, s);
+        // Visible keys among this thread's: of its page, or of the first and second.
+        const int base = vis - t * kKeys - kCols * copy;
+        const int page0 = kCols * copy / kPage;
+        const int seen0 = ((ok2 >> page0) & 1u) ? base : 0;
+        const int seen1 = kCopies > 1 ? seen0 : ((ok2 >> 1) & 1u) ? base : 0;
+        if (__any_sync(0xffffffffu, min(seen0, seen1) < kCols)) {
+#pragma unroll
+          for (int e = 0; e < kCols; ++e)
+            if (e >= (e < kPage ? seen0 : seen1)) s[e] = __float_as_uint(ninf);
+        }
+        float mx[4] = {ninf, ninf, ninf, ninf};
+#pragma unroll
+        for (int e = 0; e < kCols; e += 2)
+          mx[(e >> 1) & 3] = max3(mx[(e >> 1) & 3], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+        const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+        const bool raise = tmax > mrun + kRaiseLog2;
+        const bool rescale = raise && mrun > ninf;
+        if (__any_sync(0xffffffffu, rescale)) {
+          // P V of the tile before has to be in the output first.
+          if (ok && !mbar_wait(PV_DONE(it - 1), PARITY2(it - 1))) ok = false;
+          tc_fence_after();
+          const float f = rescale ? ex2(mrun - tmax) : 1.f;
+#pragma unroll 1
+          for (int c = 0; c < kDim / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(tmem + lanebase + kColO + 32 * c, o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st32(tmem + lanebase + kColO + 32 * c, o);
+          }
+          lrun *= f;
+        }
+        if (raise) mrun = tmax;
+        const float mref = mrun > ninf ? mrun : 0.f;
+        // P of tile it - 2 has been read.
+        if (it >= 2 && ok && !mbar_wait(PV_DONE(it), PARITY2(it - 2))) ok = false;
+        tc_fence_after();
+        float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        const uint32_t tp = tmem + lanebase + kColP + 64 * (it & 1) + (kCols / 2) * copy;
+#pragma unroll
+        for (int c = 0; c < kCols / 32; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float2 x = fma2(make_float2(__uint_as_float(s[32 * c + 2 * e]), __uint_as_float(s[32 * c + 2 * e + 1])),
+                                  make_float2(sc, sc), make_float2(-mref, -mref));
+            const float2 w = make_float2(ex2(x.x), ex2(x.y));
+            ls[e & 1] = add2(ls[e & 1], w);
+            pk[e] = pack_bf16x2(w.x, w.y);
+          }
+          tmem_st16_async(tp + 16 * c, pk);
+        }
+        lrun += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
+        // Rows of V behind every query's view are cleared.
+        const int vlive = wk.len - t * kKeys;
+        if (vlive < kKeys || (ok2 & 3u) != 3u) {
+          const int n = 2 * it + 1;
+          if (ok && !mbar_wait(FULL(n), RING_PARITY(n))) ok = false;
+          uint4* v = reinterpret_cast<uint4*>(smem + T::kOffRing + (n % T::kRing) * T::kOperand);
+          for (int e = tid; e < T::kOperand / 16; e += kSoftThreads) {
+            const int key = (e >> 3) & (kKeys - 1);
+            if (key >= vlive || !((ok2 >> (key / kPage)) & 1u)) v[e] = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(P_FULL(it));
+      }
+      // ---------------------------------------------------------- epilogue
+      if (ok && !mbar_wait(PV_DONE(it - 1), PARITY2(it - 1))) ok = false;
+      tc_fence_after();
+      const bool whole = wk.t0 == 0 && wk.t1 == wk.nt;
+      // Where row r of the tile goes: its row of out, or of the part's slot.
+      const long long slot0 = (static_cast<long long>(blockIdx.x) * 2 + (wk.t0 > 0 ? 0 : 1)) * kRows;
+      auto place = [&](int r) -> long long {
+        if (!whole) return slot0 + r;
+        const int i = r / group;
+        return (static_cast<long long>(wk.req) * p.nq + mtile * p.tile_q + i) * p.heads + head * group + (r - i * group);
+      };
+      float top = mrun, l = lrun;
+      if constexpr (kCopies > 1) {
+        xchg[tid] = make_float2(mrun, lrun);
+        named_bar_sync(1, kSoftThreads);
+        top = ninf;
+        l = 0.f;
+        float2 other[kCopies];
+#pragma unroll
+        for (int c = 0; c < kCopies; ++c) {
+          other[c] = xchg[c * kCopyRows + row];
+          top = fmaxf(top, other[c].x);
+        }
+        const float mref = top > ninf ? top : 0.f;
+#pragma unroll
+        for (int c = 0; c < kCopies; ++c) l = fmaf(ex2(other[c].x - mref), other[c].y, l);
+      }
+      const bool any = l > 0.f || l != l;
+      const float w = any ? ex2(mrun - (top > ninf ? top : 0.f)) / l : 0.f;
+      if (live && copy == 0) {
+        const float lse = any ? (top + log2f(l)) * kLn2 : ninf;
+        if (!whole) p.part_lse[place(row)] = lse;
+        else if (p.lse) p.lse[place(row)] = lse;
+      }
+      if constexpr (kCopies == 1) {
+        const long long at = live ? place(row) : 0;
+#pragma unroll 1
+        for (int c = 0; c < kDim / 32; ++c) {
+          uint32_t o[32];
+          __syncwarp();
+          tmem_ld32(tmem + lanebase + kColO + 32 * c, o);
+          if (!live) continue;
+          if (whole) {
+            uint4* dst = reinterpret_cast<uint4*>(p.out + at * kDim + 32 * c);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t h[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                h[j] = any ? pack_bf16x2(__uint_as_float(o[8 * e + 2 * j]) * w, __uint_as_float(o[8 * e + 2 * j + 1]) * w) : 0u;
+              dst[e] = make_uint4(h[0], h[1], h[2], h[3]);
+            }
+          } else {
+            float4* dst = reinterpret_cast<float4*>(p.part_o + at * kDim + 32 * c);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              dst[e] = any ? make_float4(__uint_as_float(o[4 * e]) * w, __uint_as_float(o[4 * e + 1]) * w,
+                                         __uint_as_float(o[4 * e + 2]) * w, __uint_as_float(o[4 * e + 3]) * w)
+                           : make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+        }
+      } else {
+        // The copies' outputs, weighted, are added up through shared memory, 32 dims
+        // at a time (16-byte piece i of a row at i ^ (row & 7)): thread = row and
+        // kCopies' share of the 32.
+        constexpr int kPer = 32 / kCopies;                  // dims of a thread
+        const int orow = tid / kCopies, part = tid % kCopies;
+        const int oq = orow / group;
+        const bool olive = oq < p.tile_q && mtile * p.tile_q + oq < p.nq;
+        const long long at = olive ? place(orow) : 0;
+#pragma unroll 1
+        for (int c = 0; c < kDim / 32; ++c, stage ^= 1) {
+          uint32_t o[32];
+          __syncwarp();
+          tmem_ld32(tmem + lanebase + kColO + 32 * c, o);
+          float* buf = reinterpret_cast<float*>(smem + T::kOffStage + stage * kStage);
+          if (live)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              *reinterpret_cast<float4*>(buf + tid * 32 + ((e ^ (tid & 7)) << 2)) =
+                  w > 0.f || w != w ? make_float4(__uint_as_float(o[4 * e]) * w, __uint_as_float(o[4 * e + 1]) * w,
+                                                  __uint_as_float(o[4 * e + 2]) * w, __uint_as_float(o[4 * e + 3]) * w)
+                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+          named_bar_sync(1, kSoftThreads);
+          if (!olive) continue;
+          float sum[kPer];
+#pragma unroll
+          for (int e = 0; e < kPer; ++e) sum[e] = 0.f;
+#pragma unroll
+          for (int cc = 0; cc < kCopies; ++cc) {
+            const int src = cc * kCopyRows + orow;
+#pragma unroll
+            for (int e = 0; e < kPer / 4; ++e) {
+              const float4 v = *reinterpret_cast<const float4*>(buf + src * 32 + (((part * (kPer / 4) + e) ^ (src & 7)) << 2));
+              sum[4 * e] += v.x;
+              sum[4 * e + 1] += v.y;
+              sum[4 * e + 2] += v.z;
+              sum[4 * e + 3] += v.w;
+            }
+          }
+          const long long to = at * kDim + 32 * c + kPer * part;
+          if (whole) {
+#pragma unroll
+            for (int e = 0; e < kPer / 8; ++e)
+              reinterpret_cast<uint4*>(p.out + to)[e] =
+                  make_uint4(pack_bf16x2(sum[8 * e], sum[8 * e + 1]), pack_bf16x2(sum[8 * e + 2], sum[8 * e + 3]),
+                             pack_bf16x2(sum[8 * e + 4], sum[8 * e + 5]), pack_bf16x2(sum[8 * e + 6], sum[8 * e + 7]));
+          } else {
+#pragma unroll
+            for (int e = 0; e < kPer / 4; ++e)
+              reinterpret_cast<float4*>(p.part_o + to)[e] = make_float4(sum[4 * e], sum[4 * e + 1], sum[4 * e + 2], sum[4 * e + 3]);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(O_FREE);
+    }
+    if (!ok && lane == 0) raise_error(kErrTimeout);
+  }
+  __syncthreads();
+  grid_dep_launch();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+#undef FULL
+#undef EMPTY
+#undef RING_PARITY
+#undef Q_FULL
+#undef Q_EMPTY
+#undef O_FREE
+#undef DRAIN
+#undef S_FULL
+#undef P_FULL
+#undef PV_DONE
+#undef PARITY2
+}
+
+// Joins the partials of an item that spans CTAs.  Block (i, c): some rows of the
+// item whose first cut begins part i + 1, if it is one (the attention kernel wrote
+// that down).  Its first part is slot 1 of its CTA (a stretch from the item's
+// start), the others slot 0 of theirs.  D / 4 threads a row, kShare such groups on
+// one row (each takes every kShare-th batch of four parts), joined in shared memory.
+constexpr int kMergeThreads = 256, kBatch = 4;
+
+template <int kDim, int kShare>
+__global__ void __launch_bounds__(kMergeThreads) gqa_merge_kernel(const GqaDecodeLaunch p) {
+  constexpr int kTpr = kDim / 4, kGroups = kMergeThreads / kTpr, kRowsBlock = kGroups / kShare;
+  __shared__ float4 s_acc[kGroups][kTpr];
+  __shared__ float2 s_sum[kGroups];
+  const int g = threadIdx.x / kTpr, c4 = threadIdx.x % kTpr, share = g % kShare;
+  const int row = blockIdx.y * kRowsBlock + g / kShare;
+  const int g0 = blockIdx.x;
+  const float ninf = __int_as_float(0xff800000);
+  grid_dep_wait();
+  const int4 join = p.joins[g0 + 1];
+  if (join.x < 0) return;
+  const int head = join.y / p.row_tiles, mtile = join.y % p.row_tiles, group = p.heads / p.kv_heads;
+  const int qi = mtile * p.tile_q + row / group;
+  const bool live = row < p.tile_rows && qi < p.nq;
+  const int n = live ? join.z - g0 + 1 : 0;      // parts
+  auto slot = [&](int i) { return (static_cast<long long>(g0 + i) * 2 + (i == 0 ? 1 : 0)) * kRows + row; };
+  float mx = ninf, tot = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int b0 = share * kBatch; b0 < n; b0 += kShare * kBatch) {
+    float4 v[kBatch];
+    float e[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const bool in = b0 + u < n;
+      const long long s = slot(in ? b0 + u : 0);
+      e[u] = in ? p.part_lse[s] : ninf;
+      v[u] = reinterpret_cast<const float4*>(p.part_o + s * kDim)[c4];
+    }
+    float top = mx;
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) top = fmaxf(top, e[u]);
+    const float mref = top > ninf ? top : 0.f;
+    const float f = ex2((mx - mref) * kLog2e);      // (0 for the first batch: its sums are 0)
+    mx = top;
+    tot *= f;
+    acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const float w = ex2((e[u] - mref) * kLog2e);
+      // (An empty part holds zeros; its weight is 0.)
+      tot += w;
+      acc = make_float4(fmaf(w, v[u].x, acc.x), fmaf(w, v[u].y, acc.y), fmaf(w, v[u].z, acc.z), fmaf(w, v[u].w, acc.w));
+    }
+  }
+  if constexpr (kShare > 1) {
+    s_acc[g][c4] = acc;
+    if (c4 == 0) s_sum[g] = make_float2(mx, tot);
+    __syncthreads();
+    if (share > 0) return;
+#pragma unroll
+    for (int u = 1; u < kShare; ++u) mx = fmaxf(mx, s_sum[g + u].x);
+    const float mref = mx > ninf ? mx : 0.f;
+    tot = 0.f;
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int u = 0; u < kShare; ++u) {
+      const float2 st = s_sum[g + u];
+      const float w = ex2((st.x - mref) * kLog2e);
+      const float4 v = s_acc[g + u][c4];
+      tot = fmaf(w, st.y, tot);
+      acc = make_float4(fmaf(w, v.x, acc.x), fmaf(w, v.y, acc.y), fmaf(w, v.z, acc.z), fmaf(w, v.w, acc.w));
+    }
+  }
+  if (!live) return;
+  const bool any = tot > 0.f || tot != tot;
+  const float inv = any ? 1.f / tot : 0.f;
+  const long long at = (static_cast<long long>(join.x) * p.nq + qi) * p.heads + head * group + row % group;
+  reinterpret_cast<uint2*>(p.out + at * kDim)[c4] = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv),
+                                                               pack_bf16x2(acc.z * inv, acc.w * inv));
+  if (p.lse && c4 == 0) p.lse[at] = any ? mx + log2f(tot) * kLn2 : ninf;
+}
+
+constexpr int kMinKeys = 256;   // of a CTA's part of the line, at least
+
+// Queries of a row tile: as many as fit, the tiles of a request alike.
+int row_tiles_of(int nq, int group) {
+  const int fit = kRows / group;      // (group <= heads <= 128)
+  return (nq + fit - 1) / fit;
+}
+
+template <int kDim>
+cudaError_t launch(const GqaDecodeLaunch& a, cudaStream_t s) {
+  using T = Geo<kDim>;
+  const uint64_t G = a.heads / a.kv_heads, K = a.kv_heads, tokens = static_cast<uint64_t>(a.batch) * a.nq;
+  // Queries as (64-dim piece, head of the group, query, atom, key head): a box brings
+  // one atom of a tile's rows.  Caches as (piece, row of the page, atom, head, page).
+  const uint64_t qdims[5] = {64, G, tokens, T::kAtoms, K};
+  const uint64_t qstr[4] = {kDim * 2, static_cast<uint64_t>(a.heads) * kDim * 2, 128, G * kDim * 2};
+  const uint32_t qbox[5] = {64, static_cast<uint32_t>(G), static_cast<uint32_t>(a.tile_q), 1, 1};
+  const uint64_t cdims[5] = {64, kPage, T::kAtoms, K, static_cast<uint64_t>(a.num_pages)};
+  const uint64_t cstr[4] = {kDim * 2, 128, kPage * kDim * 2, K * kPage * kDim * 2};
+  const uint32_t cbox[5] = {64, kPage, 1, 1, 1};
+  CUtensorMap tq, tk, tv;
+  if (!encode_tmap_nd(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, 5, qdims, qstr, qbox, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_tmap_nd(&tk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.k, 5, cdims, cstr, cbox, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_tmap_nd(&tv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.v, 5, cdims, cstr, cbox, CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  auto kern = a.tile_rows <= 32 ? gqa_decode_kernel<kDim, 4> : a.tile_rows <= 64 ? gqa_decode_kernel<kDim, 2> : gqa_decode_kernel<kDim, 1>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  e = launch_kernel(kern, dim3(a.ctas), dim3(kThreads), T::kSmemBytes, s, false, 1, tq, tk, tv, a);
+  if (e != cudaSuccess || a.ctas == 1) return e;
+  // (Parts of an item, on average: 1 + CTAs / items.)
+  constexpr int kGroups = kMergeThreads / (kDim / 4);
+  const bool many = 4LL * a.batch * a.kv_heads * a.row_tiles <= a.ctas;
+  const int per = many ? kGroups / 4 : kGroups;
+  return launch_kernel(many ? gqa_merge_kernel<kDim, 4> : gqa_merge_kernel<kDim, 1>,
+                       dim3(a.ctas - 1, (a.tile_rows + per - 1) / per), dim3(kMergeThreads), 0, s, true, 1, a);
+}
+
+}  // namespace
+
+// Two stretches of partials a CTA, one CTA an SM.
+size_t gqa_decode_workspace(int nq, int heads, int kv_heads, int dim) {
+  (void)nq;
+  (void)heads;
+  (void)kv_heads;
+  const size_t ctas = device_sm_count();
+  return ctas * (2 * kRows * (dim + 1) * sizeof(float) + sizeof(int4));
+}
+
+cudaError_t launch_gqa_decode(GqaDecodeLaunch a, void* ws, cudaStream_t s) {
+  if (a.k_scale) return cudaErrorNotSupported;      // FP8 rows: not yet
+  const int group = a.heads / a.kv_heads;
+  a.row_tiles = row_tiles_of(a.nq, group);
+  a.tile_q = (a.nq + a.row_tiles - 1) / a.row_tiles;
+  a.tile_rows = a.tile_q * group;
+  a.ctas = device_sm_count();
+  a.min_tiles = kMinKeys / kKeys;
+  a.part_o = static_cast<float*>(ws);
+  const size_t slots = static_cast<size_t>(a.ctas) * 2 * kRows;
+  a.part_lse = a.part_o + slots * a.dim;
+  a.joins = reinterpret_cast<int4*>(a.part_lse + slots);
+  return a.dim == 128 ? launch<128>(a, s) : launch<64>(a, s);
+}
+
+}  // namespace dsa

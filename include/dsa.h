@@ -71,6 +71,7 @@ typedef enum dsa_status {
 #define DSA_MAX_NORM_DIM 32768
 #define DSA_MAX_PREFILL_BATCH 65535
 #define DSA_MAX_PREFILL_HEADS 1024
+#define DSA_MAX_GROUP 128    /* query heads of a key head (grouped heads)   */
 
 /*
  * One decode batch.  Sizes are host integers; seqlens and page_table are
@@ -464,6 +465,155 @@ dsa_status dsa_rmsnorm(int32_t rows, int32_t dim, const uint16_t* x, int64_t ld_
                        const uint16_t* residual, const uint16_t* weight, float eps, int32_t group,
                        uint16_t* residual_out, uint16_t* y, uint8_t* y8, float* y_scale,
                        void* stream);
+
+/*
+ * Layers with grouped heads: H query heads in groups of H / K share K key / value
+ * heads of D dims (query head h reads key head h / (H / K)).  Such layers stand
+ * beside the latent ones (a draft model's, or some layers of a model), over the
+ * same pages and the same page table.  The textbook formulas; the pages have no
+ * counterpart.  Their caches are [num_pages, K, 64, D], keys and values apart, so
+ * that a page of a head is contiguous: position s of request r and head g is row
+ * s % 64 of (page_table[r][s / 64], g).  In bf16, or in FP8 E4M3 codes with one
+ * fp32 scale for a row, [num_pages, K, 64].
+ */
+
+/*
+ * The page table and slot map of a step, on the GPU: pages for the new tokens of
+ * each request, the cache rows ("slots", page * 64 + row) of these tokens, and the
+ * pages of ended requests given back.  One launch, for decode steps and prompts.
+ * With len = seqlens[r] (a negative one counts as 0) and n = change[r]:
+ *   n >= 0: the request gets n tokens: ceil((len + n) / 64) - ceil(len / 64) pages
+ *           from the top of the stack (free_pages[free_count - 1] first), in the
+ *           order of the requests, into its row of the table behind the pages it
+ *           has; the slots of its tokens len .. len + n - 1 are written to
+ *           slots[cu_new[r]] and on, and its length becomes len + n;
+ *   n < 0:  the request has ended: the pages of its len tokens go on the stack (in
+ *           the order of the requests, above what is left; none of them serves this
+ *           call), its entries become -1 and its length 0.
+ * A request that asks for more pages than are left gets none, and keeps its length
+ * (nor does any behind it that needs pages); so does one whose row or whose slots
+ * do not hold them.  The slots of its tokens are -1, and DSA_ERR_DEVICE_CHECK is
+ * raised.  (So it is for a free_count outside [0, num_pages] or ids outside the
+ * cache, which are not handed out or taken back; the entry is -1 then.)
+ *   batch       1 .. DSA_MAX_PREFILL_BATCH (DSA_ERR_UNSUPPORTED)
+ *   change      [dev] int32 [batch]
+ *   seqlens     [dev] int32 [batch]; seqlens_out: where the new lengths go, seqlens
+ *               itself or another array
+ *   page_table  [dev] int32 [batch, max_pages], updated in place (only entries of
+ *               new pages and of ended requests are written)
+ *   free_pages  [dev] int32 [num_pages], updated in place where requests end
+ *   free_count  [dev] int32; free_count_out: where the new count goes, free_count
+ *               itself or another word
+ *   max_tokens  entries of slots, 0 or more; cu_new is cut to it
+ *   cu_new      [dev] int32 [batch + 1], written: where each request's new tokens
+ *               begin (the offsets of the packed tokens)
+ *   slots       [dev] int32 [max_tokens], written whole (-1 behind the last token);
+ *               may be NULL where max_tokens is 0
+ * No other overlaps.  With seqlens_out and free_count_out apart and no request
+ * ended, a call can be repeated: it writes the same again.
+ */
+dsa_status dsa_pages_update(int32_t batch, int32_t max_pages, int32_t num_pages,
+                            const int32_t* change, const int32_t* seqlens, int32_t* seqlens_out,
+                            int32_t* page_table, int32_t* free_pages, const int32_t* free_count,
+                            int32_t* free_count_out, int32_t max_tokens, int32_t* cu_new,
+                            int32_t* slots, void* stream);
+
+/*
+ * Writes the keys and values of packed tokens to the caches of a layer with
+ * grouped heads, at the rows of a slot map (dsa_pages_update's, or any other).
+ *   tokens    0 or more; slots [dev] int32 [tokens]: cache rows; -1 skips the
+ *             token, a row outside [0, num_pages * 64) as well, and raises
+ *             DSA_ERR_DEVICE_CHECK.  Tokens with the same slot: the row then holds
+ *             parts of any of them.
+ *   kv_heads  K, 1 .. DSA_MAX_PREFILL_HEADS; dim D, 64 or 128 (DSA_ERR_UNSUPPORTED)
+ *   k, v      [dev] bf16 rows of K * D, row t at k + t * ld_k (ld_k >= K * D, a
+ *             multiple of 8: columns of one projection, say), 16-byte aligned
+ *   k_cache, v_cache  [dev] bf16 [num_pages, K, 64, D], 16-byte aligned (written)
+ */
+dsa_status dsa_kv_write(int32_t tokens, int32_t kv_heads, int32_t dim, const uint16_t* k,
+                        int64_t ld_k, const uint16_t* v, int64_t ld_v, const int32_t* slots,
+                        int32_t num_pages, uint16_t* k_cache, uint16_t* v_cache, void* stream);
+
+/*
+ * The same into FP8 caches: for a token and head scale = amax / 448 over its D
+ * values (a row of zeros: 1), codes = E4M3(x / scale), to nearest even, in fp32;
+ * dim 128.  k8, v8 [dev] [num_pages, K, 64, D], 16-byte aligned; k_scale, v_scale
+ * [dev] float [num_pages, K, 64] (all written).
+ */
+dsa_status dsa_kv_write_fp8(int32_t tokens, int32_t kv_heads, int32_t dim, const uint16_t* k,
+                            int64_t ld_k, const uint16_t* v, int64_t ld_v, const int32_t* slots,
+                            int32_t num_pages, uint8_t* k8, float* k_scale, uint8_t* v8,
+                            float* v_scale, void* stream);
+
+/*
+ * Attention of a decode step's queries over the whole paged cache of a layer with
+ * grouped heads, split over its length and joined.  For row (t, h), t = r *
+ * q_per_req + i, g = h / (H / K), over positions s < vis[t]:
+ *   x_s = sm_scale * q[t,h,:] . k[s,g,:],  out[t,h,:] = sum_s softmax(x)_s * v[s,g,:]
+ *   lse[t,h] = log(sum_s exp(x_s))                               (natural log)
+ * A query that sees nothing (seqlens[r] < q_per_req is allowed here, 0 too) gets
+ * out = 0, lse = -inf.  bf16 products accumulated in fp32 on tcgen05 tensor cores,
+ * softmax statistics in fp32, probabilities rounded to bf16 for the second product,
+ * out rounded once from fp32.
+ *   desc      topk is not used; num_heads H may be any of 1 .. 128
+ *   kv_heads  K, a divisor of H; dim D: 64 or 128 (DSA_ERR_UNSUPPORTED)
+ *   q         [dev] bf16 [T, H, D], 16-B aligned
+ *   k, v      [dev] bf16 [num_pages, K, 64, D], 16-B aligned
+ *   out       [dev] bf16 [T, H, D], 16-B aligned;  lse [dev] float [T, H] or NULL
+ *   ws        [dev] dsa_gqa_decode_workspace_bytes(desc, K, D) bytes, 256-B
+ *             aligned: partials of what several CTAs share.  Calls that may run at
+ *             the same time need workspaces of their own; what it holds between
+ *             calls does not matter.
+ * Rows of a request's last page behind its end are not read into the result (they
+ * may hold anything); values that any query of the request sees have to be finite.
+ * Bad page ids and lengths as for dsa_mla_decode.  The same call gives the same
+ * bits.
+ */
+dsa_status dsa_gqa_decode(const dsa_decode_desc* desc, int32_t kv_heads, int32_t dim,
+                          const uint16_t* q, const uint16_t* k, const uint16_t* v, float sm_scale,
+                          uint16_t* out, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * dsa_gqa_decode over FP8 caches (dsa_kv_write_fp8's; dim 128): the attention over
+ * code x scale.  The scales have to be positive and finite.  (Scores as exact as
+ * above: a query is split into two E4M3 parts that hold its bf16 value; codes as
+ * fp16 values and probabilities times the value scale, rounded to fp16, in the
+ * second product.)
+ */
+dsa_status dsa_gqa_decode_fp8kv(const dsa_decode_desc* desc, int32_t kv_heads, int32_t dim,
+                                const uint16_t* q, const uint8_t* k8, const float* k_scale,
+                                const uint8_t* v8, const float* v_scale, float sm_scale,
+                                uint16_t* out, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of dsa_gqa_decode and dsa_gqa_decode_fp8kv (0 for what they reject). */
+size_t dsa_gqa_decode_workspace_bytes(const dsa_decode_desc* desc, int32_t kv_heads, int32_t dim);
+
+/*
+ * Attention over packed prompts for a layer with grouped heads.  Requests are
+ * packed as in dsa_mla_prefill: request b has query rows [cu_q[b], cu_q[b+1]) and
+ * key rows [cu_k[b], cu_k[b+1]); with n queries and m keys, query i is the
+ * request's token m - n + i.  With g = h / (H / K):
+ *   x_j = sm_scale * q[i,h,:] . k[j,g,:],  out[i,h,:] = sum_j softmax(x)_j * v[j,g,:],
+ *   lse = log(sum_j exp(x_j))
+ * over the keys j <= m - n + i (causal != 0) or all m.  A query without a key gets
+ * out = 0, lse = -inf.  Arithmetic as dsa_gqa_decode.
+ *   batch     1 .. DSA_MAX_PREFILL_BATCH; heads H 1 .. DSA_MAX_PREFILL_HEADS;
+ *             kv_heads K a divisor of H with H / K <= DSA_MAX_GROUP; dim D 64 or 128
+ *             (DSA_ERR_UNSUPPORTED; so are more than 2^31 - 1 blocks)
+ *   total_q, total_k, max_q, cu_q, cu_k   as in dsa_mla_prefill
+ *   q         [dev] bf16, row i at q + i * ld_q, H * D values; k, v [dev] bf16, row
+ *             j at k + j * ld_k, K * D values (the columns of one projection, say);
+ *             strides multiples of 8, 16-B aligned
+ *   out       [dev] bf16 [total_q, H, D], 16-B aligned;  lse [dev] float
+ *             [total_q, H] or NULL
+ * Needs no workspace.  Bad offsets, rows behind the last request and finiteness as
+ * for dsa_mla_prefill.  The same call gives the same bits.
+ */
+dsa_status dsa_gqa_prefill(int32_t batch, int32_t heads, int32_t kv_heads, int32_t dim,
+                           int32_t total_q, int32_t total_k, int32_t max_q, const int32_t* cu_q,
+                           const int32_t* cu_k, const uint16_t* q, int64_t ld_q, const uint16_t* k,
+                           int64_t ld_k, const uint16_t* v, int64_t ld_v, float sm_scale,
+                           int32_t causal, uint16_t* out, float* lse, void* stream);
 
 /*
  * One layer of the Multi-layer Indexer schedule ("Multi-layer Indexer:

@@ -35,6 +35,21 @@
 // Rows of V that no query sees (behind the request's end in its last page, a page
 // that is not there or whose id is out of range) are cleared in shared memory
 // before P V: their probabilities are zero, but what lies there may be NaN.
+//
+// FP8 rows (kFp8; 128 dims): a key or value is its E4M3 code times its row's scale,
+// half the bytes, so half the time for the rest.  Nothing is converted for Q K^T: it
+// runs on E4M3, the query in two parts, q / 2^e = hi + lo, each E4M3 (a bf16 value
+// has 8 bits, a code 4: the sum is exact for values down to 2^-9 of the row's largest,
+// and off by 2^-17 of that below), both into the same scores: as many MMA cycles as
+// bf16.
+// The key's scale goes to the score.  For P V the codes become fp16 (exactly; bits
+// moved, one conversion for two), in eight warps of their own, and the value's scale
+// goes into the probability through its exponent: with z = x + log2(scale), P =
+// 2^(z - m) under a running maximum of z, so that scales of any size leave it in
+// fp16's range; the sum takes P / scale.  (P as E4M3 parts would drop keys below
+// 2^-17 of the largest, which a long context can have many of.)
+#include <cuda_fp8.h>
+
 #include <algorithm>
 
 #include "dsa_ptx.cuh"
@@ -49,26 +64,39 @@ constexpr int kRows = 128;                     // of a row tile (M)
 constexpr int kKeys = 2 * kPage;               // of a key tile
 constexpr int kAtomBytes = kRows * 128;        // 128 rows x 64 dims
 constexpr int kPageAtom = kPage * 128;         // 64 rows x 64 dims
-constexpr int kThreads = 256, kSoftThreads = 128;
+constexpr int kThreads = 256, kThreadsFp8 = 512, kSoftThreads = 128;
+constexpr int kDequantWarps = 8, kParamWarps = 4;      // FP8; the latter of the former
+// FP8, registers a thread (launched with 128 each): copies and MMAs, softmax, two
+// warpgroups of dequantisation.
+constexpr int kRegsMma = 88, kRegsSoft = 216, kRegsDequant = 104;
+static_assert(kRegsMma + kRegsSoft + 2 * kRegsDequant <= 4 * 128, "registers");
 constexpr int kStretch = 2;                    // what an item's queries and output cost, in key tiles
 constexpr int kColS = 0, kColP = 256, kColO = 384, kTmemCols = 512;
 constexpr int kStage = kSoftThreads * 32 * 4;  // 32 columns of a copy's rows, fp32
-constexpr float kRaiseLog2 = 8.0f;
+constexpr float kRaiseLog2 = 8.0f, kShift = 7.0f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-template <int kDim>
+template <int kDim, bool kFp8>
 struct Geo {
   static constexpr int kAtoms = kDim / 64;
-  static constexpr int kOperand = kAtoms * kAtomBytes;      // q, or K or V of a tile
-  static constexpr int kRing = kDim == 128 ? 5 : 8;         // granules
+  static constexpr int kOperand = kAtoms * kAtomBytes;      // q (FP8: both parts), or K or V of a tile for the MMAs
+  static constexpr int kGranule = kFp8 ? kKeys * kDim : kOperand;      // K or V of a tile as it is cached
+  static constexpr int kPageBytes = kGranule / 2;
+  static constexpr int kRing = kFp8 ? 6 : kDim == 128 ? 5 : 8;         // granules
+  static constexpr int kStages = kFp8 ? 1 : 2;                         // staging buffers of the epilogue
   static constexpr int kOffQ = 0;
   static constexpr int kOffRing = kOperand;
-  static constexpr int kOffStage = kOffRing + kRing * kOperand;      // two buffers
-  static constexpr int kOffXchg = kOffStage + 2 * kStage;            // (maximum, sum) of 128 threads
-  static constexpr int kOffBar = kOffXchg + kSoftThreads * 8;
+  static constexpr int kOffV16 = kOffRing + kRing * kGranule;          // FP8: two tiles of V in fp16
+  static constexpr int kOffStage = kOffV16 + (kFp8 ? 2 * kOperand : 0);
+  static constexpr int kOffXchg = kOffStage + kStages * kStage;        // (maximum, sum) of 128 threads
+  static constexpr int kOffScale = kOffXchg + kSoftThreads * 8;        // FP8, a tile in the ring: 128 key scales, 128 value scales
+  static constexpr int kOffParam = kOffScale + (kFp8 ? kRing / 2 * 2 * kKeys * 4 : 0);      // two tiles: kk, lg, 1 / scale
+  static constexpr int kOffQScale = kOffParam + (kFp8 ? 2 * 3 * kKeys * 4 : 0);             // four stretches: 2^e of a row
+  static constexpr int kOffBar = kOffQScale + (kFp8 ? 4 * kRows * 4 : 0);
   static constexpr int kOffInfo = kOffBar + 40 * 8;
   static constexpr int kSmemBytes = kOffInfo + 48 + 1024;
   static_assert(kSmemBytes <= 232448, "shared memory");
+  static_assert(!kFp8 || (kDim == 128 && kRing % 2 == 0), "FP8");
 };
 
 // mbar_wait by a whole warp: the same answer in every lane.
@@ -217,11 +245,11 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t addr, uint32_t (&r)[kN]) {
   else tmem_ld128(addr, r);
 }
 
-template <int kDim, int kCopies>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int kDim, int kCopies, bool kFp8>
+__global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kThreads, 1)
     gqa_decode_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                       const __grid_constant__ CUtensorMap tmap_v, const GqaDecodeLaunch p) {
-  using T = Geo<kDim>;
+  using T = Geo<kDim, kFp8>;
   constexpr int kCols = kKeys / kCopies;         // keys of a softmax thread
   constexpr int kCopyRows = kRows / kCopies;     // lanes of a copy
   extern __shared__ uint8_t smem_raw[];
@@ -243,15 +271,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 #define P_FULL(i) (bar0 + 176u + 8u * ((i) & 1))
 #define PV_DONE(i) (bar0 + 192u + 8u * ((i) & 1))
 #define PARITY2(i) (((i) >> 1) & 1)
+// (FP8) Of tile i: scales ready for the softmax, V in fp16.
+#define PARAM_FULL(i) (bar0 + 208u + 8u * ((i) & 1))
+#define V16_FULL(i) (bar0 + 224u + 8u * ((i) & 1))
   long long* info = reinterpret_cast<long long*>(smem + T::kOffInfo);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + T::kOffInfo + 40);
 
   if (warp == 0 && lane == 0) {
     for (int n = 0; n < T::kRing; ++n) {
       mbar_init(FULL(n), 1);
-      mbar_init(EMPTY(n), 1);
+      mbar_init(EMPTY(n), !kFp8 ? 1 : (n & 1) ? kDequantWarps : 1 + kParamWarps);
     }
-    mbar_init(Q_FULL, 1);
+    mbar_init(Q_FULL, kFp8 ? kDequantWarps : 1);
     mbar_init(Q_EMPTY, 1);
     mbar_init(O_FREE, kSoftThreads / 32);
     mbar_init(DRAIN, 1);
@@ -259,9 +290,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(S_FULL(i), 1);
       mbar_init(P_FULL(i), kSoftThreads / 32);
       mbar_init(PV_DONE(i), 1);
+      if (kFp8) {
+        mbar_init(PARAM_FULL(i), kParamWarps);
+        mbar_init(V16_FULL(i), kDequantWarps);
+      }
     }
     fence_mbar_init();
-    prefetch_tmap(&tmap_q);
+    if (!kFp8) prefetch_tmap(&tmap_q);
     prefetch_tmap(&tmap_k);
     prefetch_tmap(&tmap_v);
   }
@@ -308,6 +343,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   wk.unit = static_cast<int>(wk.pos - info[2]);
   wk.t0 = wk.t1 = 0;
 
+  if (warp < 4) {
+  if constexpr (kFp8) setmaxnreg_dec<kRegsMma>();
   if (warp == 0) {
     // ------------------------------------------------------------- copies
     bool ok = true;
@@ -319,23 +356,35 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t = wk.t0; ok && t < wk.t1; ++t, ++it) {
         if (pages.advance(t, lane) && pages.now == PageBatch::kBad) raise_error(kErrCheck);
         const int page[2] = {pages.page(t, 0), pages.page(t, 1)};
-        const uint32_t bytes = ((page[0] >= 0) + (page[1] >= 0)) * T::kAtoms * kPageAtom;
+        const uint32_t present = (page[0] >= 0) + (page[1] >= 0);
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
           const int n = 2 * it + g;
           if (n >= T::kRing && ok && !mbar_wait(EMPTY(n), RING_PARITY(n - T::kRing))) ok = false;
           if (ok && lane == 0) {
-            mbar_expect_tx(FULL(n), bytes);
-            const uint32_t dst = sbase + T::kOffRing + (n % T::kRing) * T::kOperand;
+            // (FP8: the scales of keys and values come with the keys.)
+            mbar_expect_tx(FULL(n), present * (T::kPageBytes + (kFp8 && g == 0 ? 2 * kPage * 4 : 0)));
+            const uint32_t dst = sbase + T::kOffRing + (n % T::kRing) * T::kGranule;
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-              if (page[h] >= 0)
+            for (int h = 0; h < 2; ++h) {
+              if (page[h] < 0) continue;
+              if constexpr (kFp8) {
+                tma_load_4d(dst + h * T::kPageBytes, g == 0 ? &tmap_k : &tmap_v, 0, 0, head, page[h], FULL(n));
+                if (g == 0) {
+                  const long long at = (static_cast<long long>(page[h]) * p.kv_heads + head) * kPage;
+                  const uint32_t to = sbase + T::kOffScale + (it % (T::kRing / 2)) * 2 * kKeys * 4 + h * kPage * 4;
+                  bulk_load(to, p.k_scale + at, kPage * 4, FULL(n));
+                  bulk_load(to + kKeys * 4, p.v_scale + at, kPage * 4, FULL(n));
+                }
+              } else {
 #pragma unroll
                 for (int a = 0; a < T::kAtoms; ++a)
                   tma_load_5d(dst + a * kAtomBytes + h * kPageAtom, g == 0 ? &tmap_k : &tmap_v, 0, 0, a, head, page[h],
                               FULL(n));
+              }
+            }
           }
-          if (g == 0 && t == wk.t0) {
+          if (!kFp8 && g == 0 && t == wk.t0) {
             if (seg > 0 && ok && !mbar_wait(Q_EMPTY, (seg - 1) & 1)) ok = false;
             if (ok && lane == 0) {
               mbar_expect_tx(Q_FULL, q_bytes);
@@ -354,13 +403,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     // --------------------------------------------------------------- MMAs
     // The whole warp runs this; one lane issues.
     const uint32_t el = elect_one() ? 1u : 0u;
-    constexpr uint32_t idesc_qk = make_idesc(1, 1, 0, 0, kKeys, kRows);
-    constexpr uint32_t idesc_pv = make_idesc(1, 1, 0, 1, kDim, kRows);
+    constexpr uint32_t kFmt = kFp8 ? 0 : 1;      // E4M3 and fp16, or bf16
+    constexpr uint32_t idesc_qk = make_idesc(kFmt, kFmt, 0, 0, kKeys, kRows);
+    constexpr uint32_t idesc_pv = make_idesc(kFmt, kFmt, 0, 1, kDim, kRows);
     const uint64_t dq = smem_desc_sw128(sbase + T::kOffQ, 16, 1024);
     const uint64_t dk0 = smem_desc_sw128(sbase + T::kOffRing, 16, 1024);
-    const uint64_t dv0 = smem_desc_sw128(sbase + T::kOffRing, kAtomBytes, 1024);      // MN-major
-    auto slot_of = [&](int n) -> uint64_t {
-      return static_cast<uint32_t>(__shfl_sync(0xffffffffu, ((n % T::kRing) * T::kOperand) >> 4, 0));
+    const uint64_t dv0 = smem_desc_sw128(sbase + (kFp8 ? T::kOffV16 : T::kOffRing), kAtomBytes, 1024);      // MN-major
+    auto slot_of = [&](int slot, int bytes) -> uint64_t {
+      return static_cast<uint32_t>(__shfl_sync(0xffffffffu, (slot * bytes) >> 4, 0));
     };
     bool ok = true;
     int it = 0, npv = 0;
@@ -378,16 +428,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++pv_seg;
       }
       const int n = 2 * npv + 1;
-      if (!warp_wait(FULL(n), RING_PARITY(n)) || !warp_wait(P_FULL(npv), PARITY2(npv))) return false;
+      if (!(kFp8 ? warp_wait(V16_FULL(npv), PARITY2(npv)) : warp_wait(FULL(n), RING_PARITY(n))) ||
+          !warp_wait(P_FULL(npv), PARITY2(npv)))
+        return false;
       tc_fence_after();
-      const uint64_t dv = dv0 + slot_of(n);
+      const uint64_t dv = dv0 + slot_of(kFp8 ? npv & 1 : n % T::kRing, T::kOperand);
       const uint32_t tp = tmem + kColP + 64 * (npv & 1);
 #pragma unroll
       for (int k = 0; k < kKeys / 16; ++k)
         mma_f16_ts_uni(tmem + kColO, tp + 8 * k, dv + static_cast<uint64_t>((2048 * k) >> 4), idesc_pv,
                        (!fresh || k > 0) ? 1u : 0u, el);
       if (el) {
-        tc_commit(EMPTY(n));
+        if (!kFp8) tc_commit(EMPTY(n));
         tc_commit(PV_DONE(npv));
       }
       __syncwarp();
@@ -402,13 +454,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n = 2 * it;
         if (!(ok = warp_wait(FULL(n), RING_PARITY(n)))) break;
         tc_fence_after();
-        const uint64_t dk = dk0 + slot_of(n);
+        const uint64_t dk = dk0 + slot_of(n % T::kRing, T::kGranule);
         const uint32_t ts = tmem + kColS + kKeys * (it & 1);
 #pragma unroll
-        for (int a = 0; a < T::kAtoms; ++a)
+        for (int a = 0; a < T::kAtoms; ++a)      // (FP8: the query's parts, over the same keys)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            mma_f16_ss_uni(ts, dq + static_cast<uint64_t>((a * kAtomBytes + 32 * k) >> 4),
+            if constexpr (kFp8)
+              mma_f8_ss_uni(ts, dq + static_cast<uint64_t>((a * kAtomBytes + 32 * k) >> 4),
+                            dk + static_cast<uint64_t>((32 * k) >> 4), idesc_qk, (a > 0 || k > 0) ? 1u : 0u, el);
+            else
+              mma_f16_ss_uni(ts, dq + static_cast<uint64_t>((a * kAtomBytes + 32 * k) >> 4),
                            dk + static_cast<uint64_t>((a * kAtomBytes + 32 * k) >> 4), idesc_qk, (a > 0 || k > 0) ? 1u : 0u, el);
         if (el) {
           tc_commit(EMPTY(n));
@@ -436,8 +492,140 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (p.lse)
         for (int e = lane; e < rows; e += 32) p.lse[row0 + e] = ninf;
     }
-  } else if (warp >= 4) {
+  }
+  } else if (kFp8 && warp >= 8) {
+    // ------------------------------- queries, scales and values of FP8 rows
+    // A warp converts four rows of V at a time: eight neighbouring lanes hold four
+    // 16-code chunks of each of two rows, of different halves (reads) and with
+    // different swizzles (writes): both fall on distinct banks.
+    if constexpr (kFp8) {
+    setmaxnreg_dec<kRegsDequant>();
+    const int w = warp - 8, tid = threadIdx.x - 256;
+    const int r2 = (lane >> 2) & 1, c = (lane & 3) + 4 * (((lane >> 3) & 1) ^ r2);
+    const int row4 = 2 * (lane >> 4) + r2;
+    const int group = p.heads / p.kv_heads;
+    bool ok = true;
+    int it = 0, seg = 0;
+    for (; ok && wk.next(p); ++seg) {
+      PageBatch pages(p, wk, lane);
+      {
+        // The query's parts, eight lanes a row (16 values each).
+        const int head = wk.item / p.row_tiles, mtile = wk.item % p.row_tiles, piece = tid & 7;
+        if (seg > 0 && !mbar_wait(Q_EMPTY, (seg - 1) & 1)) ok = false;
+        for (int row0 = 0; row0 < p.tile_rows; row0 += 32) {
+          const int row = row0 + (tid >> 3), i = row / group;
+          const int qi = mtile * p.tile_q + i;
+          const bool in = row < p.tile_rows && qi < p.nq;
+          uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
+          if (in) {
+            const uint4* src = reinterpret_cast<const uint4*>(
+                p.q + ((static_cast<long long>(wk.req) * p.nq + qi) * p.heads + head * group + (row - i * group)) * kDim) + 2 * piece;
+            a = __ldg(src);
+            b = __ldg(src + 1);
+          }
+          const uint32_t word[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+          float2 x[8];
+          float amax = 0.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            x[e] = make_float2(bf16lo_to_f32(word[e]), bf16hi_to_f32(word[e]));
+            amax = max3(amax, fabsf(x[e].x), fabsf(x[e].y));
+          }
+#pragma unroll
+          for (int o = 4; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          // 2^e, so that the largest value lies in [128, 256).
+          const int ex = max(static_cast<int>(__float_as_uint(amax) >> 23) - 134, -100);
+          const float down = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float2 v = mul2(x[e], make_float2(down, down));
+            const uint32_t h = __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+            const float2 back = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(h), __NV_E4M3)));
+            const uint32_t l = __nv_cvt_float2_to_fp8x2(make_float2(v.x - back.x, v.y - back.y), __NV_SATFINITE, __NV_E4M3);
+            hi[e >> 1] = (e & 1) ? hi[e >> 1] | h << 16 : h;
+            lo[e >> 1] = (e & 1) ? lo[e >> 1] | l << 16 : l;
+          }
+          if (row < p.tile_rows) {
+#pragma unroll
+            for (int cp = 0; cp < kCopies; ++cp) {
+              const int at = cp * kCopyRows + row;
+              uint8_t* dst = smem + T::kOffQ + at * 128 + ((piece ^ (at & 7)) << 4);
+              *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+              *reinterpret_cast<uint4*>(dst + kAtomBytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
+            if (piece == 0)
+              reinterpret_cast<float*>(smem + T::kOffQScale)[(seg & 3) * kRows + row] =
+                  __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(Q_FULL);
+      }
+      uint32_t good = 0;
+      for (int t = wk.t0; ok && t < wk.t1; ++t, ++it) {
+        if (pages.advance(t, lane)) good = __ballot_sync(0xffffffffu, pages.now >= 0);
+        const uint32_t ok2 = good >> (2 * ((t - wk.t0) & (PageBatch::kTiles - 1)));
+        const int vlive = wk.len - t * kKeys;
+        // Scales and V of tile it - 2 have been read.
+        if (it >= 2 && !mbar_wait(PV_DONE(it), PARITY2(it - 2))) ok = false;
+        if (w < kParamWarps) {
+          const int n = 2 * it;
+          if (ok && !mbar_wait(FULL(n), RING_PARITY(n))) ok = false;
+          const float* scales = reinterpret_cast<const float*>(smem + T::kOffScale) + (it % (T::kRing / 2)) * 2 * kKeys;
+          float* par = reinterpret_cast<float*>(smem + T::kOffParam) + (it & 1) * 3 * kKeys;
+          const bool seen = tid < vlive && ((ok2 >> (tid / kPage)) & 1u);
+          const float vs = seen ? scales[kKeys + tid] : 1.f;
+          par[tid] = seen ? scales[tid] : 0.f;
+          par[kKeys + tid] = log2f(vs);
+          par[2 * kKeys + tid] = 1.f / vs;
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(PARAM_FULL(it));
+            mbar_arrive(EMPTY(n));
+          }
+        }
+        const int n = 2 * it + 1;
+        if (ok && !mbar_wait(FULL(n), RING_PARITY(n))) ok = false;
+        const uint8_t* src = smem + T::kOffRing + (n % T::kRing) * T::kGranule + c * 16;
+        uint4 raw[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int row = 32 * u + 4 * w + row4;
+          raw[u] = *reinterpret_cast<const uint4*>(src + row * 128);
+          // Rows that no query sees are zero, whatever the cache holds.
+          if (row >= vlive || !((ok2 >> (u >> 1)) & 1u)) raw[u] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(EMPTY(n));
+        uint8_t* dst = smem + T::kOffV16 + (it & 1) * T::kOperand + (c >> 2) * kAtomBytes;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int row = 32 * u + 4 * w + row4, piece = (2 * (c & 3)) ^ (row & 7);
+          const uint32_t code[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+          uint32_t h[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const __half2_raw f = __nv_cvt_fp8x2_to_halfraw2(
+                static_cast<__nv_fp8x2_storage_t>((code[e >> 1] >> (16 * (e & 1))) & 0xFFFFu), __NV_E4M3);
+            h[e] = static_cast<uint32_t>(f.x) | static_cast<uint32_t>(f.y) << 16;
+          }
+          *reinterpret_cast<uint4*>(dst + row * 128 + (piece << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(dst + row * 128 + ((piece ^ 1) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(V16_FULL(it));
+        ok = __all_sync(0xffffffffu, ok);
+      }
+      ok = __all_sync(0xffffffffu, ok);
+    }
+    if (!ok && lane == 0) raise_error(kErrTimeout);
+    }
+  } else {
     // ---------------------------------------------- softmax and epilogue
+    if constexpr (kFp8) setmaxnreg_inc<kRegsSoft>();
     const int tid = threadIdx.x - 128;             // = TMEM lane
     const int w4 = warp & 3;
     const int copy = tid / kCopyRows, row = tid % kCopyRows;      // row of the tile
@@ -454,8 +642,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < 4; ++c) tmem_st32(tmem + lanebase + kColP + 32 * c, z);
     }
     bool ok = true;
-    int it = 0, stage = 0;
-    while (wk.next(p)) {
+    int it = 0, stage = 0, seg = 0;
+    for (; wk.next(p); ++seg) {
       PageBatch pages(p, wk, lane);
       const int head = wk.item / p.row_tiles, mtile = wk.item % p.row_tiles;
       const int qi = mtile * p.tile_q + my_q;
@@ -471,6 +659,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         uint32_t s[kCols];
         tmem_ld_cols<kCols>(tmem + lanebase + kColS + kKeys * (it & 1) + kCols * copy, s);
+        const float4* par = reinterpret_cast<const float4*>(smem + T::kOffParam) + (it & 1) * 3 * kKeys / 4 + kCols / 4 * copy;
+        if constexpr (kFp8) {
+          // z = x + log2(value scale), x the score in the exp2 domain.
+          if (ok && !mbar_wait(PARAM_FULL(it), PARITY2(it))) ok = false;
+          const float f = sc * reinterpret_cast<const float*>(smem + T::kOffQScale)[(seg & 3) * kRows + min(row, p.tile_rows - 1)];
+#pragma unroll
+          for (int e = 0; e < kCols; e += 4) {
+            const float4 kk = par[e / 4], lg = par[kKeys / 4 + e / 4];
+            const float2 f2 = make_float2(f, f);
+            const float2 a = fma2(mul2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), make_float2(kk.x, kk.y)), f2, make_float2(lg.x, lg.y));
+            const float2 b = fma2(mul2(make_float2(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), make_float2(kk.z, kk.w)), f2, make_float2(lg.z, lg.w));
+            s[e] = __float_as_uint(a.x);
+            s[e + 1] = __float_as_uint(a.y);
+            s[e + 2] = __float_as_uint(b.x);
+            s[e + 3] = __float_as_uint(b.y);
+          }
+        }
         // Visible keys among this thread's: of its page, or of the first and second.
         const int base = vis - t * kKeys - kCols * copy;
         const int page0 = kCols * copy / kPage;
@@ -485,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int e = 0; e < kCols; e += 2)
           mx[(e >> 1) & 3] = max3(mx[(e >> 1) & 3], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
-        const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+        const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * (kFp8 ? 1.f : sc);
         const bool raise = tmax > mrun + kRaiseLog2;
         const bool rescale = raise && mrun > ninf;
         if (__any_sync(0xffffffffu, rescale)) {
@@ -504,7 +709,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           lrun *= f;
         }
         if (raise) mrun = tmax;
-        const float mref = mrun > ninf ? mrun : 0.f;
+        // (FP8: P up to 2^15, which leaves fp16 40 powers of two below.)
+        const float mref = mrun > ninf ? mrun - (kFp8 ? kShift : 0.f) : 0.f;
         // P of tile it - 2 has been read.
         if (it >= 2 && ok && !mbar_wait(PV_DONE(it), PARITY2(it - 2))) ok = false;
         tc_fence_after();
@@ -515,21 +721,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t pk[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const float2 x = fma2(make_float2(__uint_as_float(s[32 * c + 2 * e]), __uint_as_float(s[32 * c + 2 * e + 1])),
-                                  make_float2(sc, sc), make_float2(-mref, -mref));
+            const float2 y = make_float2(__uint_as_float(s[32 * c + 2 * e]), __uint_as_float(s[32 * c + 2 * e + 1]));
+            const float2 x = kFp8 ? add2(y, make_float2(-mref, -mref)) : fma2(y, make_float2(sc, sc), make_float2(-mref, -mref));
             const float2 w = make_float2(ex2(x.x), ex2(x.y));
-            ls[e & 1] = add2(ls[e & 1], w);
-            pk[e] = pack_bf16x2(w.x, w.y);
+            if constexpr (kFp8) {
+              const float4 inv = par[2 * kKeys / 4 + 8 * c + e / 2];
+              ls[e & 1] = fma2(w, (e & 1) ? make_float2(inv.z, inv.w) : make_float2(inv.x, inv.y), ls[e & 1]);
+              pk[e] = pack_f16x2(w.x, w.y);
+            } else {
+              ls[e & 1] = add2(ls[e & 1], w);
+              pk[e] = pack_bf16x2(w.x, w.y);
+            }
           }
           tmem_st16_async(tp + 16 * c, pk);
         }
         lrun += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
         // Rows of V behind every query's view are cleared.
         const int vlive = wk.len - t * kKeys;
-        if (vlive < kKeys || (ok2 & 3u) != 3u) {
+        if (!kFp8 && (vlive < kKeys || (ok2 & 3u) != 3u)) {
           const int n = 2 * it + 1;
           if (ok && !mbar_wait(FULL(n), RING_PARITY(n))) ok = false;
-          uint4* v = reinterpret_cast<uint4*>(smem + T::kOffRing + (n % T::kRing) * T::kOperand);
+          uint4* v = reinterpret_cast<uint4*>(smem + T::kOffRing + (n % T::kRing) * T::kGranule);
           for (int e = tid; e < T::kOperand / 16; e += kSoftThreads) {
             const int key = (e >> 3) & (kKeys - 1);
             if (key >= vlive || !((ok2 >> (key / kPage)) & 1u)) v[e] = make_uint4(0u, 0u, 0u, 0u);
@@ -571,7 +783,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool any = l > 0.f || l != l;
       const float w = any ? ex2(mrun - (top > ninf ? top : 0.f)) / l : 0.f;
       if (live && copy == 0) {
-        const float lse = any ? (top + log2f(l)) * kLn2 : ninf;
+        const float lse = any ? (top - (kFp8 ? kShift : 0.f) + log2f(l)) * kLn2 : ninf;
         if (!whole) p.part_lse[place(row)] = lse;
         else if (p.lse) p.lse[place(row)] = lse;
       }
@@ -612,10 +824,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool olive = oq < p.tile_q && mtile * p.tile_q + oq < p.nq;
         const long long at = olive ? place(orow) : 0;
 #pragma unroll 1
-        for (int c = 0; c < kDim / 32; ++c, stage ^= 1) {
+        for (int c = 0; c < kDim / 32; ++c, stage = (stage + 1) % T::kStages) {
           uint32_t o[32];
           __syncwarp();
           tmem_ld32(tmem + lanebase + kColO + 32 * c, o);
+          if (T::kStages == 1 && c > 0) named_bar_sync(1, kSoftThreads);      // the others have read it
           float* buf = reinterpret_cast<float*>(smem + T::kOffStage + stage * kStage);
           if (live)
 #pragma unroll
@@ -678,6 +891,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #undef P_FULL
 #undef PV_DONE
 #undef PARITY2
+#undef PARAM_FULL
+#undef V16_FULL
 }
 
 // Joins the partials of an item that spans CTAs.  Block (i, c): some rows of the
@@ -768,27 +983,40 @@ int row_tiles_of(int nq, int group) {
   return (nq + fit - 1) / fit;
 }
 
-template <int kDim>
+template <int kDim, bool kFp8>
 cudaError_t launch(const GqaDecodeLaunch& a, cudaStream_t s) {
-  using T = Geo<kDim>;
+  using T = Geo<kDim, kFp8>;
   const uint64_t G = a.heads / a.kv_heads, K = a.kv_heads, tokens = static_cast<uint64_t>(a.batch) * a.nq;
-  // Queries as (64-dim piece, head of the group, query, atom, key head): a box brings
-  // one atom of a tile's rows.  Caches as (piece, row of the page, atom, head, page).
-  const uint64_t qdims[5] = {64, G, tokens, T::kAtoms, K};
-  const uint64_t qstr[4] = {kDim * 2, static_cast<uint64_t>(a.heads) * kDim * 2, 128, G * kDim * 2};
-  const uint32_t qbox[5] = {64, static_cast<uint32_t>(G), static_cast<uint32_t>(a.tile_q), 1, 1};
-  const uint64_t cdims[5] = {64, kPage, T::kAtoms, K, static_cast<uint64_t>(a.num_pages)};
-  const uint64_t cstr[4] = {kDim * 2, 128, kPage * kDim * 2, K * kPage * kDim * 2};
-  const uint32_t cbox[5] = {64, kPage, 1, 1, 1};
+  const uint64_t pages = static_cast<uint64_t>(a.num_pages);
   CUtensorMap tq, tk, tv;
-  if (!encode_tmap_nd(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, 5, qdims, qstr, qbox, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode_tmap_nd(&tk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.k, 5, cdims, cstr, cbox, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !encode_tmap_nd(&tv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.v, 5, cdims, cstr, cbox, CU_TENSOR_MAP_SWIZZLE_128B))
-    return cudaErrorInvalidValue;
-  auto kern = a.tile_rows <= 32 ? gqa_decode_kernel<kDim, 4> : a.tile_rows <= 64 ? gqa_decode_kernel<kDim, 2> : gqa_decode_kernel<kDim, 1>;
+  if (kFp8) {
+    // Codes as (byte, row of the page, head, page).
+    const uint64_t dims[4] = {kDim, kPage, K, pages}, str[3] = {kDim, kPage * kDim, K * kPage * kDim};
+    const uint32_t box[4] = {kDim, kPage, 1, 1};
+    if (!encode_tmap_nd(&tk, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.k, 4, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_tmap_nd(&tv, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.v, 4, dims, str, box, CU_TENSOR_MAP_SWIZZLE_NONE))
+      return cudaErrorInvalidValue;
+    tq = tk;      // not used
+  } else {
+    // Queries as (64-dim piece, head of the group, query, atom, key head): a box brings
+    // one atom of a tile's rows.  Caches as (piece, row of the page, atom, head, page).
+    const uint64_t qdims[5] = {64, G, tokens, T::kAtoms, K};
+    const uint64_t qstr[4] = {kDim * 2, static_cast<uint64_t>(a.heads) * kDim * 2, 128, G * kDim * 2};
+    const uint32_t qbox[5] = {64, static_cast<uint32_t>(G), static_cast<uint32_t>(a.tile_q), 1, 1};
+    const uint64_t cdims[5] = {64, kPage, T::kAtoms, K, pages};
+    const uint64_t cstr[4] = {kDim * 2, 128, kPage * kDim * 2, K * kPage * kDim * 2};
+    const uint32_t cbox[5] = {64, kPage, 1, 1, 1};
+    if (!encode_tmap_nd(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, 5, qdims, qstr, qbox, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_tmap_nd(&tk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.k, 5, cdims, cstr, cbox, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_tmap_nd(&tv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.v, 5, cdims, cstr, cbox, CU_TENSOR_MAP_SWIZZLE_128B))
+      return cudaErrorInvalidValue;
+  }
+  auto kern = a.tile_rows <= 32   ? gqa_decode_kernel<kDim, 4, kFp8>
+              : a.tile_rows <= 64 ? gqa_decode_kernel<kDim, 2, kFp8>
+                                  : gqa_decode_kernel<kDim, 1, kFp8>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmemBytes);
   if (e != cudaSuccess) return e;
-  e = launch_kernel(kern, dim3(a.ctas), dim3(kThreads), T::kSmemBytes, s, false, 1, tq, tk, tv, a);
+  e = launch_kernel(kern, dim3(a.ctas), dim3(kFp8 ? kThreadsFp8 : kThreads), T::kSmemBytes, s, false, 1, tq, tk, tv, a);
   if (e != cudaSuccess || a.ctas == 1) return e;
   // (Parts of an item, on average: 1 + CTAs / items.)
   constexpr int kGroups = kMergeThreads / (kDim / 4);
@@ -810,7 +1038,6 @@ size_t gqa_decode_workspace(int nq, int heads, int kv_heads, int dim) {
 }
 
 cudaError_t launch_gqa_decode(GqaDecodeLaunch a, void* ws, cudaStream_t s) {
-  if (a.k_scale) return cudaErrorNotSupported;      // FP8 rows: not yet
   const int group = a.heads / a.kv_heads;
   a.row_tiles = row_tiles_of(a.nq, group);
   a.tile_q = (a.nq + a.row_tiles - 1) / a.row_tiles;
@@ -821,7 +1048,8 @@ cudaError_t launch_gqa_decode(GqaDecodeLaunch a, void* ws, cudaStream_t s) {
   const size_t slots = static_cast<size_t>(a.ctas) * 2 * kRows;
   a.part_lse = a.part_o + slots * a.dim;
   a.joins = reinterpret_cast<int4*>(a.part_lse + slots);
-  return a.dim == 128 ? launch<128>(a, s) : launch<64>(a, s);
+  if (a.k_scale) return launch<128, true>(a, s);
+  return a.dim == 128 ? launch<128, false>(a, s) : launch<64, false>(a, s);
 }
 
 }  // namespace dsa

@@ -575,10 +575,11 @@ dsa_status dsa_gqa_decode(const dsa_decode_desc* desc, int32_t kv_heads, int32_t
 
 /*
  * dsa_gqa_decode over FP8 caches (dsa_kv_write_fp8's; dim 128): the attention over
- * code x scale.  The scales have to be positive and finite.  (Scores as exact as
- * above: a query is split into two E4M3 parts that hold its bf16 value; codes as
- * fp16 values and probabilities times the value scale, rounded to fp16, in the
- * second product.)
+ * code x scale.  Scales of tokens that a query sees have to be positive, finite and
+ * at least 2^-100; k_scale, v_scale 16-B aligned.  (The query enters as the sum of
+ * two E4M3 parts, exact but for values below 2^-9 of the largest of its row, which
+ * are off by 2^-17 of that; codes are multiplied as they are, probabilities times
+ * the value's scale rounded to fp16.)
  */
 dsa_status dsa_gqa_decode_fp8kv(const dsa_decode_desc* desc, int32_t kv_heads, int32_t dim,
                                 const uint16_t* q, const uint8_t* k8, const float* k_scale,

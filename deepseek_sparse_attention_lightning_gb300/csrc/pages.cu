@@ -10,7 +10,7 @@
 // launch with two sums over all requests in it.  So one cluster does it all: its
 // CTAs take a stretch of the requests each, exchange their sums through shared
 // memory, hand out pages (a thread a page), and then share the tokens evenly (a
-// thread four slots; whose they are is looked up in the offsets, in shared
+// thread eight slots; whose they are is looked up in the offsets, in shared
 // memory).  Barriers of the cluster stand between the phases, so that lengths,
 // table and count may be updated in place: everything that another CTA reads
 // before a barrier is written behind it.
@@ -24,48 +24,51 @@ DSA_DEFINE_ERROR_WORD(pages)
 namespace dsa {
 namespace {
 
-constexpr int kThreads = 1024;
-constexpr int kOffsetsInSmem = 8192;      // offsets of up to so many requests (32 KB)
+constexpr int kCluster = 16;
+constexpr int kNear = 4096;      // offsets and lengths of up to so many requests in shared memory (32 KB)
 
 __device__ __forceinline__ int pages_of(int len) { return static_cast<int>((len + (kPage - 1LL)) / kPage); }
 
+// Sums of tokens and of pages asked for end at 2^32 - 1 (more than any slot map or
+// stack holds): what lies behind is refused whatever its size.
+__device__ __forceinline__ uint32_t add_sat(uint32_t a, uint32_t b) {
+  const uint32_t s = a + b;
+  return s < a ? 0xffffffffu : s;
+}
+
 struct Sums {
-  long long tokens, need, freed;
+  uint32_t tokens, need, freed;
 };
 
-// Inclusive sums over the block's threads; every thread also gets the block's.
+// Inclusive sums over the block's threads (tokens and pages asked for); every
+// thread also gets the block's.
+template <int kThreads>
 __device__ __forceinline__ Sums block_scan(Sums v, Sums* warp_sums, Sums& total) {
+  constexpr int kWarps = (kThreads / 32);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  auto scan = [&](uint32_t& x) {
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long a = __shfl_up_sync(0xffffffffu, v.tokens, o), b = __shfl_up_sync(0xffffffffu, v.need, o),
-                    c = __shfl_up_sync(0xffffffffu, v.freed, o);
-    if (lane >= o) {
-      v.tokens += a;
-      v.need += b;
-      v.freed += c;
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x = add_sat(x, y);
     }
-  }
+  };
+  scan(v.tokens);
+  scan(v.need);
   __syncthreads();      // the call before has read warp_sums
   if (lane == 31) warp_sums[warp] = v;
   __syncthreads();
-  Sums before = {0, 0, 0};
-  total = before;
-#pragma unroll 4
-  for (int w = 0; w < kThreads / 32; ++w) {
-    const Sums s = warp_sums[w];
-    if (w < warp) {
-      before.tokens += s.tokens;
-      before.need += s.need;
-      before.freed += s.freed;
-    }
-    total.tokens += s.tokens;
-    total.need += s.need;
-    total.freed += s.freed;
+  // Each warp scans the warps' sums for itself.
+  Sums w = lane < kWarps ? warp_sums[lane] : Sums{0u, 0u, 0u};
+  scan(w.tokens);
+  scan(w.need);
+  total.tokens = __shfl_sync(0xffffffffu, w.tokens, 31);
+  total.need = __shfl_sync(0xffffffffu, w.need, 31);
+  const uint32_t bt = __shfl_sync(0xffffffffu, w.tokens, max(warp - 1, 0)), bn = __shfl_sync(0xffffffffu, w.need, max(warp - 1, 0));
+  if (warp > 0) {
+    v.tokens = add_sat(v.tokens, bt);
+    v.need = add_sat(v.need, bn);
   }
-  v.tokens += before.tokens;
-  v.need += before.need;
-  v.freed += before.freed;
   return v;
 }
 
@@ -117,102 +120,117 @@ __device__ __forceinline__ int give_back(const PagesLaunch& p, int r, int len, l
   return found;
 }
 
-__global__ void __launch_bounds__(kThreads) pages_kernel(const PagesLaunch p) {
-  __shared__ Sums warp_sums[kThreads / 32];
-  __shared__ Sums cta_sums;             // of this CTA's requests
-  __shared__ unsigned long long cta_taken;      // pages handed out, up to its last request that got some
-  __shared__ int cta_refused, cta_ended;
+// kCtas: of the cluster (the only one of the grid); kRun: slots of a thread in a row.
+template <int kThreads, int kCtas, int kRun>
+__global__ void __launch_bounds__(kThreads, 1) pages_kernel(const PagesLaunch p) {
+  __shared__ Sums warp_sums[32];
+  __shared__ Sums sums[kCtas];          // of each CTA's requests (every CTA writes its own to all)
+  __shared__ int given[kCtas];          // pages handed out, up to a CTA's last request that got some (~: it refused one)
+  __shared__ int cta_taken, cta_freed, cta_refused, cta_ended;
   __shared__ int need_end[kThreads];    // of a tile of requests: pages asked for up to its end ...
   __shared__ int first_page[kThreads];  // ... and the table entry its new pages begin at (-1: refused)
-  __shared__ int offsets[kOffsetsInSmem + 1];
+  __shared__ int offsets[kNear + 1], lengths[kNear];
 
+  if (kCtas > 1) cluster_arrive();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rank = static_cast<int>(cluster_ctarank()), ctas = gridDim.x;
-  const int per = (p.batch + ctas - 1) / ctas;
+  const int rank = kCtas > 1 ? static_cast<int>(cluster_ctarank()) : 0, per = (p.batch + kCtas - 1) / kCtas;
   const int r_lo = min(p.batch, rank * per), r_hi = min(p.batch, r_lo + per);
   int count = *p.free_count;
   if (count < 0 || count > p.num_pages) {
     raise_error(kErrCheck);
     count = min(max(count, 0), p.num_pages);
   }
-
-  // Pages given back by the ended requests of a warp's lanes, each to its lane.
-  auto freed_pages = [&](const Request& q, int r) {
-    int mine = 0;
-    uint32_t ended = __ballot_sync(0xffffffffu, q.ended && q.len > 0);
-    while (ended) {
-      const int l = __ffs(ended) - 1;
-      ended &= ended - 1;
-      const int n = give_back<false>(p, __shfl_sync(0xffffffffu, r, l), __shfl_sync(0xffffffffu, q.len, l), 0);
-      if (lane == l) mine = n;
-    }
-    return mine;
-  };
-
-  // -------------------------------------------------- sums of the stretches
-  Sums mine = {0, 0, 0};
-  for (int r0 = r_lo; r0 < r_hi; r0 += kThreads) {
-    const int r = r0 + tid < r_hi ? r0 + tid : p.batch;
-    const Request q = load(p, r);
-    Sums total;
-    block_scan({q.add, q.need, freed_pages(q, r)}, warp_sums, total);
-    mine.tokens += total.tokens;
-    mine.need += total.need;
-    mine.freed += total.freed;
-  }
   if (tid == 0) {
-    cta_sums = mine;
-    cta_taken = 0;
+    cta_taken = cta_freed = 0;
     cta_refused = cta_ended = 0;
   }
-  cluster_sync();
-  auto remote64 = [&](const void* v, int c) {
-    const uint32_t a = mapa_shared(smem_u32(v), c);
-    return static_cast<long long>(static_cast<uint64_t>(ld_shared_cluster_u32(a)) |
-                                  static_cast<uint64_t>(ld_shared_cluster_u32(a + 4)) << 32);
+  __syncthreads();
+  // This CTA's value into element `rank` of an array of every CTA (one warp).
+  auto publish = [&](const void* at, uint32_t v) {
+    if (lane < kCtas) st_shared_cluster_u32(mapa_shared(smem_u32(at), lane), v);
   };
-  Sums before = {0, 0, 0};
-  long long all_tokens = 0;
-  for (int c = 0; c < ctas; ++c) {
-    const long long t = remote64(&cta_sums.tokens, c);
-    all_tokens += t;
-    if (c < rank) {
-      before.tokens += t;
-      before.need += remote64(&cta_sums.need, c);
-      before.freed += remote64(&cta_sums.freed, c);
+
+  Sums before = {0, 0, 0};      // of the CTAs before this one
+  uint32_t all_tokens = 0;
+  if constexpr (kCtas > 1) {
+    // ------------------------------------------------ sums of the stretches
+    Sums mine = {0, 0, 0};
+    for (int r0 = r_lo; r0 < r_hi; r0 += kThreads) {
+      const int r = r0 + tid < r_hi ? r0 + tid : p.batch;
+      const Request q = load(p, r);
+      Sums total;
+      block_scan<kThreads>({static_cast<uint32_t>(q.add), static_cast<uint32_t>(q.need), 0u}, warp_sums, total);
+      mine.tokens = add_sat(mine.tokens, total.tokens);
+      mine.need = add_sat(mine.need, total.need);
+      // Pages given back by the ended requests of a warp's lanes.
+      uint32_t ended = __ballot_sync(0xffffffffu, q.ended);
+      int freed = 0;
+      while (ended) {
+        const int l = __ffs(ended) - 1;
+        ended &= ended - 1;
+        freed += give_back<false>(p, __shfl_sync(0xffffffffu, r, l), __shfl_sync(0xffffffffu, q.len, l), 0);
+      }
+      if (lane == 0 && freed) atomicAdd(&cta_freed, freed);
+    }
+    cluster_wait();       // every CTA of the cluster has started
+    __syncthreads();
+    if (warp == 0) {
+      publish(&sums[rank].tokens, mine.tokens);
+      publish(&sums[rank].need, mine.need);
+      publish(&sums[rank].freed, cta_freed);
+    }
+    cluster_sync();
+    // (A lane a CTA.)
+    const Sums of = lane < kCtas ? sums[lane] : Sums{0u, 0u, 0u};
+    all_tokens = of.tokens;
+    before = lane < rank ? of : Sums{0u, 0u, 0u};
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      all_tokens = add_sat(all_tokens, __shfl_xor_sync(0xffffffffu, all_tokens, o));
+      before.tokens = add_sat(before.tokens, __shfl_xor_sync(0xffffffffu, before.tokens, o));
+      before.need = add_sat(before.need, __shfl_xor_sync(0xffffffffu, before.need, o));
+      before.freed += __shfl_xor_sync(0xffffffffu, before.freed, o);
     }
   }
 
   // ------------------------------------- offsets, lengths and the new pages
+  const bool near = p.batch <= kNear;
   const long long freed_before = before.freed;
   for (int r0 = r_lo; r0 < r_hi; r0 += kThreads) {
     const int r = r0 + tid < r_hi ? r0 + tid : p.batch;
     const Request q = load(p, r);
-    Sums total, end = block_scan({q.add, q.need, 0}, warp_sums, total);
-    const long long tok_end = before.tokens + end.tokens, need_all = before.need + end.need;
+    Sums total, end = block_scan<kThreads>({static_cast<uint32_t>(q.add), static_cast<uint32_t>(q.need), 0u}, warp_sums, total);
+    const uint32_t tok_end = add_sat(before.tokens, end.tokens), need_all = add_sat(before.need, end.need);
+    const uint32_t slots = p.max_tokens;
     // Pages in request order: a request that asks for more than are left gets
     // none, nor does any after it.  Nor one whose slots the map does not hold.
-    const bool granted = q.fits && (q.need == 0 || need_all <= count) && (q.add == 0 || tok_end <= p.max_tokens);
+    const bool granted = q.fits && (q.need == 0 || need_all <= static_cast<uint32_t>(count)) && (q.add == 0 || tok_end <= slots);
     if (r < p.batch) {
-      p.cu_new[r + 1] = static_cast<int>(min(tok_end, static_cast<long long>(p.max_tokens)));
+      const int cut = static_cast<int>(min(tok_end, slots));
+      p.cu_new[r + 1] = cut;
       // (A refused request's length is written as ~length, until the slots are; an
       // ended one's is still needed.)
+      const int len = granted ? q.len + q.add : ~q.len;
       if (q.ended) cta_ended = 1;
-      else p.seqlens_out[r] = granted ? q.len + q.add : ~q.len;
+      else p.seqlens_out[r] = len;
+      if (kCtas == 1 && near) {
+        offsets[r + 1] = cut;
+        lengths[r] = len;
+      }
       if (!granted) {
         raise_error(kErrCheck);
         cta_refused = 1;
       } else if (q.need > 0) {
-        atomicMax(&cta_taken, static_cast<unsigned long long>(need_all));
+        atomicMax(&cta_taken, static_cast<int>(need_all));
       }
     }
     __syncthreads();
-    need_end[tid] = static_cast<int>(min(end.need, static_cast<long long>(INT_MAX)));
+    need_end[tid] = static_cast<int>(min(end.need, static_cast<uint32_t>(INT_MAX)));
     first_page[tid] = granted ? pages_of(q.len) : -1;
     __syncthreads();
     // A thread a page.
-    const long long left = count - before.need;
-    const int pages = static_cast<int>(max(0LL, min(total.need, left)));
+    const uint32_t left = before.need < static_cast<uint32_t>(count) ? count - before.need : 0u;
+    const int pages = static_cast<int>(min(total.need, left));
     for (int e = tid; e < pages; e += kThreads) {
       int lo = 0, hi = kThreads - 1;      // the first thread whose request's pages end behind e
       while (lo < hi) {
@@ -221,7 +239,7 @@ __global__ void __launch_bounds__(kThreads) pages_kernel(const PagesLaunch p) {
         else lo = mid + 1;
       }
       if (first_page[lo] < 0) continue;
-      int id = p.free_pages[count - 1 - (before.need + e)];
+      int id = p.free_pages[count - 1 - (static_cast<int>(before.need) + e)];
       if (id < 0 || id >= p.num_pages) {
         raise_error(kErrCheck);
         id = -1;
@@ -229,23 +247,28 @@ __global__ void __launch_bounds__(kThreads) pages_kernel(const PagesLaunch p) {
       const int j = e - (lo > 0 ? need_end[lo - 1] : 0);
       p.page_table[static_cast<long long>(r0 + lo) * p.max_pages + first_page[lo] + j] = id;
     }
-    before.tokens += total.tokens;
-    before.need += total.need;
+    before.tokens = add_sat(before.tokens, total.tokens);
+    before.need = add_sat(before.need, total.need);
   }
   if (rank == 0 && tid == 0) p.cu_new[0] = 0;
-  cluster_sync();      // table, offsets and lengths are written, free pages read
-  long long taken = 0;
-  bool refused = false;
-  for (int c = 0; c < ctas; ++c) {
-    taken = max(taken, remote64(&cta_taken, c));
-    refused |= ld_shared_cluster_u32(mapa_shared(smem_u32(&cta_refused), c)) != 0;
+  __syncthreads();
+  int taken = cta_taken;
+  bool refused = cta_refused != 0;
+  if constexpr (kCtas > 1) {
+    if (warp == 0) publish(&given[rank], refused ? ~taken : taken);
+    cluster_sync();      // table, offsets and lengths are written, free pages read
+    const int v = lane < kCtas ? given[lane] : 0;
+    refused = __any_sync(0xffffffffu, v < 0);
+    taken = __reduce_max_sync(0xffffffffu, v < 0 ? ~v : v);
+  } else {
+    all_tokens = before.tokens;
   }
 
   // ------------------------------------------------------- pages given back
+  long long at = static_cast<long long>(count) - taken + freed_before;      // where this CTA's go
   if (cta_ended) {
     // A warp a request, their ids in the order of the requests.
-    long long at = count - taken + freed_before;
-    for (int r0 = r_lo; r0 < r_hi; r0 += kThreads / 32) {
+    for (int r0 = r_lo; r0 < r_hi; r0 += (kThreads / 32)) {
       const int r = r0 + warp;
       const bool ended = r < r_hi && p.change[r] < 0;
       const int len = ended ? max(0, p.seqlens[r]) : 0;
@@ -253,7 +276,7 @@ __global__ void __launch_bounds__(kThreads) pages_kernel(const PagesLaunch p) {
       if (lane == 0) need_end[warp] = n;
       __syncthreads();
       long long to = at;
-      for (int w = 0; w < kThreads / 32; ++w) {
+      for (int w = 0; w < (kThreads / 32); ++w) {
         if (w < warp) to += need_end[w];
         at += need_end[w];
       }
@@ -265,21 +288,32 @@ __global__ void __launch_bounds__(kThreads) pages_kernel(const PagesLaunch p) {
     }
   }
   if (rank == 0 && tid == 0) {
-    long long freed = 0;
-    for (int c = 0; c < ctas; ++c) freed += remote64(&cta_sums.freed, c);
-    p.free_count_out[0] = static_cast<int>(min(count - taken + freed, static_cast<long long>(p.num_pages)));
+    if constexpr (kCtas > 1) {
+      at = count - taken;
+      for (int c = 0; c < kCtas; ++c) at += sums[c].freed;
+    }
+    p.free_count_out[0] = static_cast<int>(min(at, static_cast<long long>(p.num_pages)));
   }
 
   // ------------------------------------------------------------------ slots
-  const bool near = p.batch <= kOffsetsInSmem;
-  if (near)
-    for (int i = tid; i <= p.batch; i += kThreads) offsets[i] = p.cu_new[i];
+  if (near && kCtas > 1) {
+    for (int i = tid; i <= p.batch; i += kThreads) {
+      offsets[i] = p.cu_new[i];
+      if (i < p.batch) lengths[i] = p.seqlens_out[i];
+    }
+  } else if (near && tid == 0) {
+    offsets[0] = 0;
+  }
   __syncthreads();
   auto offset = [&](int i) { return near ? offsets[i] : p.cu_new[i]; };
-  const int tokens = static_cast<int>(min(all_tokens, static_cast<long long>(p.max_tokens)));
-  const bool wide = (reinterpret_cast<uintptr_t>(p.slots) & 15) == 0;
-  for (long long t0 = 4LL * (rank * kThreads + tid); t0 < p.max_tokens; t0 += 4LL * kThreads * ctas) {
-    int v[4] = {-1, -1, -1, -1};
+  auto length = [&](int r) { return near ? lengths[r] : p.seqlens_out[r]; };
+  const int tokens = static_cast<int>(min(all_tokens, static_cast<uint32_t>(p.max_tokens)));
+  const bool wide = (reinterpret_cast<uintptr_t>(p.slots) & 31) == 0;
+  for (long long t0 = static_cast<long long>(kRun) * (rank * kThreads + tid); t0 < p.max_tokens;
+       t0 += static_cast<long long>(kRun) * kThreads * kCtas) {
+    int v[kRun];
+#pragma unroll
+    for (int e = 0; e < kRun; ++e) v[e] = -1;
     if (t0 < tokens) {
       int r = 0, hi = p.batch - 1;      // the first request that ends behind t0
       while (r < hi) {
@@ -287,31 +321,67 @@ __global__ void __launch_bounds__(kThreads) pages_kernel(const PagesLaunch p) {
         if (offset(mid + 1) > t0) hi = mid;
         else r = mid + 1;
       }
-      int end = offset(r + 1), len = p.seqlens_out[r];
+      int end = offset(r + 1), len = length(r);
+      // Entry of the table for position `pos` of request r; the first row of its
+      // page, or -1.
+      auto entry = [&](int pos) { return p.page_table + static_cast<long long>(r) * p.max_pages + pos / kPage; };
+      auto first_row = [&](int id) {
+        if (id >= 0 && id < p.num_pages) return id * kPage;
+        raise_error(kErrCheck);
+        return -1;
+      };
+      if (kRun > 1 && t0 + kRun <= end) {
+        // One request's tokens, on one page or two.
+        if (len >= 0) {
+          const int pos = len - static_cast<int>(end - t0), row = pos % kPage;
+          const int id_a = *entry(pos), id_b = *entry(pos + kRun - 1);
+          const int a = first_row(id_a), b = first_row(id_b);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int t = static_cast<int>(t0) + e;
-        if (t >= tokens) break;
-        while (t >= end) {      // (requests without new tokens lie between)
-          end = offset(++r + 1);
-          len = p.seqlens_out[r];
+          for (int e = 0; e < kRun; ++e) {
+            const int first = row + e < kPage ? a : b;
+            v[e] = first < 0 ? -1 : first + ((row + e) & (kPage - 1));
+          }
         }
-        if (len < 0) continue;
-        const int pos = len - (end - t);
-        const int id = p.page_table[static_cast<long long>(r) * p.max_pages + pos / kPage];
-        if (id >= 0 && id < p.num_pages) v[e] = id * kPage + pos % kPage;
-        else raise_error(kErrCheck);
+      } else {
+        // Where each token's entry is (all of them first, so that the loads overlap).
+        const int32_t* at[kRun];
+        int row[kRun];
+#pragma unroll
+        for (int e = 0; e < kRun; ++e) {
+          const int t = static_cast<int>(t0) + e;
+          at[e] = nullptr;
+          if (t >= tokens) continue;
+          while (t >= end) {      // (requests without new tokens lie between)
+            end = offset(++r + 1);
+            len = length(r);
+          }
+          const int pos = len - (end - t);
+          if (len >= 0) at[e] = entry(pos);
+          row[e] = pos % kPage;
+        }
+#pragma unroll
+        for (int e = 0; e < kRun; ++e) v[e] = at[e] ? *at[e] : -1;
+#pragma unroll
+        for (int e = 0; e < kRun; ++e) {
+          if (!at[e]) continue;
+          const int first = first_row(v[e]);
+          v[e] = first < 0 ? -1 : first + row[e];
+        }
       }
     }
-    if (wide && t0 + 3 < p.max_tokens) {
-      *reinterpret_cast<int4*>(p.slots + t0) = make_int4(v[0], v[1], v[2], v[3]);
+    if (kRun == 8 && wide && t0 + kRun <= p.max_tokens) {
+      uint32_t w[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] = static_cast<uint32_t>(v[e % kRun]);
+      st_global_32(p.slots + t0, w);
     } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
+      for (int e = 0; e < kRun; ++e)
         if (t0 + e < p.max_tokens) p.slots[t0 + e] = v[e];
     }
   }
-  cluster_sync();      // the others have read this CTA's sums, and the lengths
+  if (refused && kCtas > 1) cluster_sync();      // the others have read the lengths
+  if (kCtas == 1) __syncthreads();
   if (refused)
     for (int r = r_lo + tid; r < r_hi; r += kThreads)
       if (p.seqlens_out[r] < 0) p.seqlens_out[r] = ~p.seqlens_out[r];
@@ -319,15 +389,20 @@ __global__ void __launch_bounds__(kThreads) pages_kernel(const PagesLaunch p) {
 
 }  // namespace
 
-// CTAs of the cluster: one where a block's threads have a request and a few
-// slots each at most.
+// One CTA of 256 threads, or of 1024, where they have a request and a few slots each
+// at most; else a cluster of 16, a thread eight slots in a row where there are many
+// (a prompt's are on one page or two; a step's are on a page each, whose entries
+// would be waited for one after another).  us on the device: 128 requests of a token
+// 5; 256 prompts of 1 .. 4096 tokens, for 4 / 8 / 16 CTAs, 42 / 30 / 21.
 cudaError_t launch_pages(const PagesLaunch& a, cudaStream_t s) {
-  const int ctas = a.batch <= kThreads && a.max_tokens <= 8 * kThreads ? 1 : 16;
-  if (ctas > 8) {
-    cudaError_t e = cudaFuncSetAttribute(pages_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-  }
-  return launch_kernel(pages_kernel, dim3(ctas), dim3(kThreads), 0, s, false, ctas, a);
+  if (a.batch <= 256 && a.max_tokens <= 4 * 256)
+    return launch_kernel(pages_kernel<256, 1, 1>, dim3(1), dim3(256), 0, s, false, 1, a);
+  if (a.batch <= 1024 && a.max_tokens <= 4 * 1024)
+    return launch_kernel(pages_kernel<1024, 1, 1>, dim3(1), dim3(1024), 0, s, false, 1, a);
+  auto kern = a.max_tokens <= 4 * 1024 * kCluster ? pages_kernel<1024, kCluster, 1> : pages_kernel<1024, kCluster, 8>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(kern, dim3(kCluster), dim3(1024), 0, s, false, kCluster, a);
 }
 
 }  // namespace dsa

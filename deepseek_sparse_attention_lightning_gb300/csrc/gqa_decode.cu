@@ -245,13 +245,14 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t addr, uint32_t (&r)[kN]) {
   else tmem_ld128(addr, r);
 }
 
-template <int kDim, int kCopies, bool kFp8>
+template <int kDim, int kCopies, bool kNarrow, bool kFp8>
 __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kThreads, 1)
     gqa_decode_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                       const __grid_constant__ CUtensorMap tmap_v, const GqaDecodeLaunch p) {
   using T = Geo<kDim, kFp8>;
   constexpr int kCols = kKeys / kCopies;         // keys of a softmax thread
   constexpr int kCopyRows = kRows / kCopies;     // lanes of a copy
+  static_assert(!kNarrow || kCopies == 4, "a warp a copy");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -650,13 +651,115 @@ __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kThreads, 1)
       const bool live = my_q < p.tile_q && qi < p.nq;
       const int vis = live ? wk.len - (p.nq - 1 - qi) : 0;
       float mrun = ninf, lrun = 0.f;      // maximum and sum (this thread's keys) in the exp2 domain
+      // (kNarrow) The same of this thread's two rows, lane / 4 and that + 8; their
+      // visible tokens, and FP8 their factors.
+      float mrun2[2] = {ninf, ninf}, lrun2[2] = {0.f, 0.f}, f2[2] = {0.f, 0.f};
+      int vis2[2] = {0, 0};
+      if constexpr (kNarrow) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int r = (lane >> 2) + 8 * u, i = mtile * p.tile_q + r / group;
+          if (r < p.tile_rows && i < p.nq) vis2[u] = wk.len - (p.nq - 1 - i);
+        }
+      }
       uint32_t good = 0;                  // validity of the next 32 page ids
+      auto narrow_tile = [&](int t, uint32_t ok2) {
+        uint32_t s[16];
+        tmem_ld16x32(tmem + lanebase + kColS + kKeys * (it & 1) + kCols * copy, s);
+        const int col = 2 * (lane & 3);      // of each eight
+        const float* par = reinterpret_cast<const float*>(smem + T::kOffParam) + (it & 1) * 3 * kKeys + kCols * copy + col;
+        if constexpr (kFp8) {
+          // z = x + log2(value scale), x the score in the exp2 domain.
+          if (ok && !mbar_wait(PARAM_FULL(it), PARITY2(it))) ok = false;
+          if (t == wk.t0) {
+            const float* qs = reinterpret_cast<const float*>(smem + T::kOffQScale) + (seg & 3) * kRows;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) f2[u] = sc * qs[min((lane >> 2) + 8 * u, p.tile_rows - 1)];
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 kk = *reinterpret_cast<const float2*>(par + 8 * j);
+            const float2 lg = *reinterpret_cast<const float2*>(par + kKeys + 8 * j);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const float2 z = fma2(mul2(make_float2(__uint_as_float(s[4 * j + 2 * u]), __uint_as_float(s[4 * j + 2 * u + 1])), kk),
+                                    make_float2(f2[u], f2[u]), lg);
+              s[4 * j + 2 * u] = __float_as_uint(z.x);
+              s[4 * j + 2 * u + 1] = __float_as_uint(z.y);
+            }
+          }
+        }
+        float tmax[2], fac[2];
+        bool rescale = false;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int seen = ((ok2 >> (kCols * copy / kPage)) & 1u) ? vis2[u] - t * kKeys - kCols * copy - col : 0;
+          if (seen < 26) {      // (columns 8 j and 8 j + 1 from `col` on)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (8 * (e >> 1) + (e & 1) >= seen) s[4 * (e >> 1) + 2 * u + (e & 1)] = __float_as_uint(ninf);
+          }
+          float m = ninf;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) m = max3(m, __uint_as_float(s[4 * j + 2 * u]), __uint_as_float(s[4 * j + 2 * u + 1]));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+          tmax[u] = m * (kFp8 ? 1.f : sc);
+          const bool raise = tmax[u] > mrun2[u] + kRaiseLog2;
+          fac[u] = raise && mrun2[u] > ninf ? ex2(mrun2[u] - tmax[u]) : 1.f;
+          rescale |= raise && mrun2[u] > ninf;
+          if (raise) mrun2[u] = tmax[u];
+          lrun2[u] *= fac[u];
+        }
+        if (__any_sync(0xffffffffu, rescale)) {
+          // P V of the tile before has to be in the output first.
+          if (ok && !mbar_wait(PV_DONE(it - 1), PARITY2(it - 1))) ok = false;
+          tc_fence_after();
+          const float fa = __shfl_sync(0xffffffffu, fac[0], 4 * (lane & 7)), fb = __shfl_sync(0xffffffffu, fac[1], 4 * (lane & 7));
+          const float f = lane < 8 ? fa : lane < 16 ? fb : 1.f;
+#pragma unroll 1
+          for (int c = 0; c < kDim / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(tmem + lanebase + kColO + 32 * c, o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st32(tmem + lanebase + kColO + 32 * c, o);
+          }
+        }
+        // P of tile it - 2 has been read.
+        if (it >= 2 && ok && !mbar_wait(PV_DONE(it), PARITY2(it - 2))) ok = false;
+        tc_fence_after();
+        uint32_t pk[8];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const float mref = mrun2[u] > ninf ? mrun2[u] - (kFp8 ? kShift : 0.f) : 0.f;
+          float2 ls = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 y = make_float2(__uint_as_float(s[4 * j + 2 * u]), __uint_as_float(s[4 * j + 2 * u + 1]));
+            const float2 x = kFp8 ? add2(y, make_float2(-mref, -mref)) : fma2(y, make_float2(sc, sc), make_float2(-mref, -mref));
+            const float2 w = make_float2(ex2(x.x), ex2(x.y));
+            if constexpr (kFp8) {
+              ls = fma2(w, *reinterpret_cast<const float2*>(par + 2 * kKeys + 8 * j), ls);
+              pk[2 * j + u] = pack_f16x2(w.x, w.y);
+            } else {
+              ls = add2(ls, w);
+              pk[2 * j + u] = pack_bf16x2(w.x, w.y);
+            }
+          }
+          lrun2[u] += ls.x + ls.y;
+        }
+        tmem_st16x16_async(tmem + lanebase + kColP + 64 * (it & 1) + (kCols / 2) * copy, pk);
+      };
       for (int t = wk.t0; t < wk.t1; ++t, ++it) {
         if (pages.advance(t, lane)) good = __ballot_sync(0xffffffffu, pages.now >= 0);
         // Bit h: page h of the tile can be read.
         const uint32_t ok2 = good >> (2 * ((t - wk.t0) & (PageBatch::kTiles - 1)));
         if (ok && !mbar_wait(S_FULL(it), PARITY2(it))) ok = false;
         tc_fence_after();
+        if constexpr (kNarrow) {
+          narrow_tile(t, ok2);
+        } else {
         uint32_t s[kCols];
         tmem_ld_cols<kCols>(tmem + lanebase + kColS + kKeys * (it & 1) + kCols * copy, s);
         const float4* par = reinterpret_cast<const float4*>(smem + T::kOffParam) + (it & 1) * 3 * kKeys / 4 + kCols / 4 * copy;
@@ -736,6 +839,7 @@ __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kThreads, 1)
           tmem_st16_async(tp + 16 * c, pk);
         }
         lrun += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
+        }
         // Rows of V behind every query's view are cleared.
         const int vlive = wk.len - t * kKeys;
         if (!kFp8 && (vlive < kKeys || (ok2 & 3u) != 3u)) {
@@ -752,6 +856,19 @@ __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(P_FULL(it));
+      }
+      if constexpr (kNarrow) {
+        // From two rows a thread to a row a lane.
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          lrun2[u] += __shfl_xor_sync(0xffffffffu, lrun2[u], 1);
+          lrun2[u] += __shfl_xor_sync(0xffffffffu, lrun2[u], 2);
+          const float m = __shfl_sync(0xffffffffu, mrun2[u], 4 * (lane & 7)), l = __shfl_sync(0xffffffffu, lrun2[u], 4 * (lane & 7));
+          if ((lane >> 3) == u) {
+            mrun = m;
+            lrun = l;
+          }
+        }
       }
       // ---------------------------------------------------------- epilogue
       if (ok && !mbar_wait(PV_DONE(it - 1), PARITY2(it - 1))) ok = false;
@@ -1011,9 +1128,10 @@ cudaError_t launch(const GqaDecodeLaunch& a, cudaStream_t s) {
         !encode_tmap_nd(&tv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.v, 5, cdims, cstr, cbox, CU_TENSOR_MAP_SWIZZLE_128B))
       return cudaErrorInvalidValue;
   }
-  auto kern = a.tile_rows <= 32   ? gqa_decode_kernel<kDim, 4, kFp8>
-              : a.tile_rows <= 64 ? gqa_decode_kernel<kDim, 2, kFp8>
-                                  : gqa_decode_kernel<kDim, 1, kFp8>;
+  auto kern = a.tile_rows <= 16   ? gqa_decode_kernel<kDim, 4, true, kFp8>
+              : a.tile_rows <= 32 ? gqa_decode_kernel<kDim, 4, false, kFp8>
+              : a.tile_rows <= 64 ? gqa_decode_kernel<kDim, 2, false, kFp8>
+                                  : gqa_decode_kernel<kDim, 1, false, kFp8>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmemBytes);
   if (e != cudaSuccess) return e;
   e = launch_kernel(kern, dim3(a.ctas), dim3(kFp8 ? kThreadsFp8 : kThreads), T::kSmemBytes, s, false, 1, tq, tk, tv, a);

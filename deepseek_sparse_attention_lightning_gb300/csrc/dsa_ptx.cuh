@@ -499,8 +499,18 @@ __device__ __forceinline__ void mma_f8_ss_uni(uint32_t d, uint64_t a, uint64_t b
       : "memory");
 }
 
+// A read from TMEM.
+__device__ __forceinline__ void mma_f8_ts_uni(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc,
+                                              uint32_t accumulate, uint32_t issue) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate), "r"(issue)
+      : "memory");
+}
+
 // Instruction descriptor for kind::f16 / kind::f8f6f4 with an fp32 accumulator.
-//   fmt: 0 = E4M3 (f8f6f4) or F16 (f16), 1 = BF16 (f16)
+//   fmt: 0 = E4M3 (f8f6f4) or F16 (f16), 1 = E5M2 (f8f6f4) or BF16 (f16)
 //   a_mn / b_mn: 1 if that operand is MN-major (transposed), 0 if K-major
 __host__ __device__ constexpr uint32_t make_idesc(uint32_t a_fmt, uint32_t b_fmt, uint32_t a_mn,
                                                   uint32_t b_mn, uint32_t n, uint32_t m) {
@@ -614,6 +624,13 @@ __device__ __forceinline__ void tmem_ld16x32(uint32_t taddr, uint32_t (&r)[16]) 
 __device__ __forceinline__ void tmem_st16x16_async(uint32_t taddr, const uint32_t (&r)[8]) {
   asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(taddr), "r"(r[0]),
                "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+// The same for 8 columns.
+__device__ __forceinline__ void tmem_st16x8_async(uint32_t taddr, const uint32_t (&r)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3])
                : "memory");
 }
 

@@ -36,18 +36,34 @@
 // that is not there or whose id is out of range) are cleared in shared memory
 // before P V: their probabilities are zero, but what lies there may be NaN.
 //
+// Up to 16 rows (kNarrow; most decode steps) lie in the first 16 lanes of a copy and
+// are read as 16 lanes x 8 columns, two rows a thread, so that all lanes of the warp
+// work on them (FP8, 32 ragged requests of 16384 .. 65536: 629 us by a row a thread,
+// 534 so).
+//
 // FP8 rows (kFp8; 128 dims): a key or value is its E4M3 code times its row's scale,
 // half the bytes, so half the time for the rest.  Nothing is converted for Q K^T: it
 // runs on E4M3, the query in two parts, q / 2^e = hi + lo, each E4M3 (a bf16 value
 // has 8 bits, a code 4: the sum is exact for values down to 2^-9 of the row's largest,
-// and off by 2^-17 of that below), both into the same scores: as many MMA cycles as
-// bf16.
-// The key's scale goes to the score.  For P V the codes become fp16 (exactly; bits
-// moved, one conversion for two), in eight warps of their own, and the value's scale
-// goes into the probability through its exponent: with z = x + log2(scale), P =
-// 2^(z - m) under a running maximum of z, so that scales of any size leave it in
-// fp16's range; the sum takes P / scale.  (P as E4M3 parts would drop keys below
-// 2^-17 of the largest, which a long context can have many of.)
+// and off by 2^-17 of that below).  The key's scale goes to the score.  The value's
+// scale goes into the probability through its exponent: with z = x + log2(scale), P =
+// 2^(z - m) under a running maximum of z, so that scales of any size leave P in fp16's
+// range; the sum takes P / scale.
+//
+//   Up to 16 rows (kParts): P V on codes too.  P, rounded to fp16, is four E5M2 parts
+//   (its upper byte, the upper byte of what is left, ...), which lose what lies below
+//   2^-29 of the largest; the running maximum is raised from 2^2 on, to keep it there.
+//   The query's two parts, and P's, stand sixteen lanes apart in a copy: half the MMAs
+//   of two products, and the scores are added where they are read, the outputs with
+//   those of the copies.  A thread holds pairs of keys 8 apart, so the copies bring V's
+//   rows in the order 0 1 8 9 2 3 10 11 ... and the pairs make bytes of one column.
+//   768 cycles of MMAs a tile, 32 KB.  (445 us for the requests above.)
+//
+//   More rows: the query's parts side by side, into the same scores; V's codes become
+//   fp16 (exactly) in eight warps of their own, which the conversions bound.
+//
+//   (P in E4M3 parts would drop keys below 2^-17 of the largest, which a long context
+//   can have many of.)
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -64,7 +80,7 @@ constexpr int kRows = 128;                     // of a row tile (M)
 constexpr int kKeys = 2 * kPage;               // of a key tile
 constexpr int kAtomBytes = kRows * 128;        // 128 rows x 64 dims
 constexpr int kPageAtom = kPage * 128;         // 64 rows x 64 dims
-constexpr int kThreads = 256, kThreadsFp8 = 512, kSoftThreads = 128;
+constexpr int kThreads = 256, kThreadsFp8 = 512, kThreadsParts = 384, kSoftThreads = 128;
 constexpr int kDequantWarps = 8, kParamWarps = 4;      // FP8; the latter of the former
 // FP8, registers a thread (launched with 128 each): copies and MMAs, softmax, two
 // warpgroups of dequantisation.
@@ -73,27 +89,31 @@ static_assert(kRegsMma + kRegsSoft + 2 * kRegsDequant <= 4 * 128, "registers");
 constexpr int kStretch = 2;                    // what an item's queries and output cost, in key tiles
 constexpr int kColS = 0, kColP = 256, kColO = 384, kTmemCols = 512;
 constexpr int kStage = kSoftThreads * 32 * 4;  // 32 columns of a copy's rows, fp32
-constexpr float kRaiseLog2 = 8.0f, kShift = 7.0f;
+constexpr float kRaiseLog2 = 8.0f, kRaiseParts = 2.0f, kShiftFp8 = 7.0f, kShiftParts = 13.0f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-template <int kDim, bool kFp8>
+// kParts: FP8 rows whose P V runs on codes, P in parts; kDequant: whose codes become
+// fp16 first.
+template <int kDim, bool kNarrow, bool kFp8>
 struct Geo {
+  static constexpr bool kParts = kFp8 && kNarrow, kDequant = kFp8 && !kNarrow;
   static constexpr int kAtoms = kDim / 64;
-  static constexpr int kOperand = kAtoms * kAtomBytes;      // q (FP8: both parts), or K or V of a tile for the MMAs
+  static constexpr int kOperand = kAtoms * kAtomBytes;      // q, or K or V of a tile for the MMAs (16-bit)
+  static constexpr int kQBytes = kParts ? kAtomBytes : kOperand;       // (FP8: both parts, one below the other or side by side)
   static constexpr int kGranule = kFp8 ? kKeys * kDim : kOperand;      // K or V of a tile as it is cached
   static constexpr int kPageBytes = kGranule / 2;
-  static constexpr int kRing = kFp8 ? 6 : kDim == 128 ? 5 : 8;         // granules
-  static constexpr int kStages = kFp8 ? 1 : 2;                         // staging buffers of the epilogue
+  static constexpr int kRing = kParts ? 10 : kFp8 ? 6 : kDim == 128 ? 5 : 8;      // granules
+  static constexpr int kStages = kDequant ? 1 : 2;                     // staging buffers of the epilogue
   static constexpr int kOffQ = 0;
-  static constexpr int kOffRing = kOperand;
-  static constexpr int kOffV16 = kOffRing + kRing * kGranule;          // FP8: two tiles of V in fp16
-  static constexpr int kOffStage = kOffV16 + (kFp8 ? 2 * kOperand : 0);
+  static constexpr int kOffRing = kQBytes;
+  static constexpr int kOffV16 = kOffRing + kRing * kGranule;          // kDequant: two tiles of V in fp16
+  static constexpr int kOffStage = kOffV16 + (kDequant ? 2 * kOperand : 0);
   static constexpr int kOffXchg = kOffStage + kStages * kStage;        // (maximum, sum) of 128 threads
   static constexpr int kOffScale = kOffXchg + kSoftThreads * 8;        // FP8, a tile in the ring: 128 key scales, 128 value scales
   static constexpr int kOffParam = kOffScale + (kFp8 ? kRing / 2 * 2 * kKeys * 4 : 0);      // two tiles: kk, lg, 1 / scale
   static constexpr int kOffQScale = kOffParam + (kFp8 ? 2 * 3 * kKeys * 4 : 0);             // four stretches: 2^e of a row
   static constexpr int kOffBar = kOffQScale + (kFp8 ? 4 * kRows * 4 : 0);
-  static constexpr int kOffInfo = kOffBar + 40 * 8;
+  static constexpr int kOffInfo = kOffBar + 40 * 8;      // (34 barriers)
   static constexpr int kSmemBytes = kOffInfo + 48 + 1024;
   static_assert(kSmemBytes <= 232448, "shared memory");
   static_assert(!kFp8 || (kDim == 128 && kRing % 2 == 0), "FP8");
@@ -246,12 +266,14 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t addr, uint32_t (&r)[kN]) {
 }
 
 template <int kDim, int kCopies, bool kNarrow, bool kFp8>
-__global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kThreads, 1)
+__global__ void __launch_bounds__(!kFp8 ? kThreads : kNarrow ? kThreadsParts : kThreadsFp8, 1)
     gqa_decode_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                       const __grid_constant__ CUtensorMap tmap_v, const GqaDecodeLaunch p) {
-  using T = Geo<kDim, kFp8>;
+  using T = Geo<kDim, kNarrow, kFp8>;
+  constexpr bool kParts = T::kParts, kDequant = T::kDequant;
   constexpr int kCols = kKeys / kCopies;         // keys of a softmax thread
   constexpr int kCopyRows = kRows / kCopies;     // lanes of a copy
+  constexpr int kSets = kParts ? 2 * kCopies : kCopies, kSetRows = kRows / kSets;      // outputs to be added up
   static_assert(!kNarrow || kCopies == 4, "a warp a copy");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -261,29 +283,29 @@ __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kThreads, 1)
   const uint32_t bar0 = sbase + T::kOffBar;
 // Granule n (K of tile i: 2 i, V: 2 i + 1): landed, and read.
 #define FULL(n) (bar0 + 8u * ((n) % T::kRing))
-#define EMPTY(n) (bar0 + 64u + 8u * ((n) % T::kRing))
+#define EMPTY(n) (bar0 + 80u + 8u * ((n) % T::kRing))
 #define RING_PARITY(n) (((n) / T::kRing) & 1)
 // q of a stretch landed / read; O read by the epilogue; of tile i: scores, probabilities, P V done.
-#define Q_FULL (bar0 + 128u)
-#define Q_EMPTY (bar0 + 136u)
-#define O_FREE (bar0 + 144u)
-#define DRAIN (bar0 + 152u)
-#define S_FULL(i) (bar0 + 160u + 8u * ((i) & 1))
-#define P_FULL(i) (bar0 + 176u + 8u * ((i) & 1))
-#define PV_DONE(i) (bar0 + 192u + 8u * ((i) & 1))
+#define Q_FULL (bar0 + 160u)
+#define Q_EMPTY (bar0 + 168u)
+#define O_FREE (bar0 + 176u)
+#define DRAIN (bar0 + 184u)
+#define S_FULL(i) (bar0 + 192u + 8u * ((i) & 1))
+#define P_FULL(i) (bar0 + 208u + 8u * ((i) & 1))
+#define PV_DONE(i) (bar0 + 224u + 8u * ((i) & 1))
 #define PARITY2(i) (((i) >> 1) & 1)
 // (FP8) Of tile i: scales ready for the softmax, V in fp16.
-#define PARAM_FULL(i) (bar0 + 208u + 8u * ((i) & 1))
-#define V16_FULL(i) (bar0 + 224u + 8u * ((i) & 1))
+#define PARAM_FULL(i) (bar0 + 240u + 8u * ((i) & 1))
+#define V16_FULL(i) (bar0 + 256u + 8u * ((i) & 1))
   long long* info = reinterpret_cast<long long*>(smem + T::kOffInfo);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + T::kOffInfo + 40);
 
   if (warp == 0 && lane == 0) {
     for (int n = 0; n < T::kRing; ++n) {
       mbar_init(FULL(n), 1);
-      mbar_init(EMPTY(n), !kFp8 ? 1 : (n & 1) ? kDequantWarps : 1 + kParamWarps);
+      mbar_init(EMPTY(n), (n & 1) ? (kDequant ? kDequantWarps : 1) : (kFp8 ? 1 + kParamWarps : 1));
     }
-    mbar_init(Q_FULL, kFp8 ? kDequantWarps : 1);
+    mbar_init(Q_FULL, kParts ? kParamWarps : kFp8 ? kDequantWarps : 1);
     mbar_init(Q_EMPTY, 1);
     mbar_init(O_FREE, kSoftThreads / 32);
     mbar_init(DRAIN, 1);
@@ -345,7 +367,7 @@ __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kThreads, 1)
   wk.t0 = wk.t1 = 0;
 
   if (warp < 4) {
-  if constexpr (kFp8) setmaxnreg_dec<kRegsMma>();
+  if constexpr (kDequant) setmaxnreg_dec<kRegsMma>();
   if (warp == 0) {
     // ------------------------------------------------------------- copies
     bool ok = true;
@@ -370,9 +392,12 @@ __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kThreads, 1)
             for (int h = 0; h < 2; ++h) {
               if (page[h] < 0) continue;
               if constexpr (kFp8) {
-                tma_load_4d(dst + h * T::kPageBytes, g == 0 ? &tmap_k : &tmap_v, 0, 0, head, page[h], FULL(n));
+                const long long at = (static_cast<long long>(page[h]) * p.kv_heads + head) * kPage;      // its first row
+                if (kParts && g == 1)
+                  tma_load_5d(dst + h * T::kPageBytes, &tmap_v, 0, 0, 0, 0, static_cast<int>(at / 16), FULL(n));
+                else
+                  tma_load_4d(dst + h * T::kPageBytes, g == 0 ? &tmap_k : &tmap_v, 0, 0, head, page[h], FULL(n));
                 if (g == 0) {
-                  const long long at = (static_cast<long long>(page[h]) * p.kv_heads + head) * kPage;
                   const uint32_t to = sbase + T::kOffScale + (it % (T::kRing / 2)) * 2 * kKeys * 4 + h * kPage * 4;
                   bulk_load(to, p.k_scale + at, kPage * 4, FULL(n));
                   bulk_load(to + kKeys * 4, p.v_scale + at, kPage * 4, FULL(n));
@@ -406,10 +431,10 @@ __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kThreads, 1)
     const uint32_t el = elect_one() ? 1u : 0u;
     constexpr uint32_t kFmt = kFp8 ? 0 : 1;      // E4M3 and fp16, or bf16
     constexpr uint32_t idesc_qk = make_idesc(kFmt, kFmt, 0, 0, kKeys, kRows);
-    constexpr uint32_t idesc_pv = make_idesc(kFmt, kFmt, 0, 1, kDim, kRows);
+    constexpr uint32_t idesc_pv = make_idesc(kParts ? 1 : kFmt, kFmt, 0, 1, kDim, kRows);      // (kParts: E5M2 and E4M3)
     const uint64_t dq = smem_desc_sw128(sbase + T::kOffQ, 16, 1024);
     const uint64_t dk0 = smem_desc_sw128(sbase + T::kOffRing, 16, 1024);
-    const uint64_t dv0 = smem_desc_sw128(sbase + (kFp8 ? T::kOffV16 : T::kOffRing), kAtomBytes, 1024);      // MN-major
+    const uint64_t dv0 = smem_desc_sw128(sbase + (kDequant ? T::kOffV16 : T::kOffRing), kAtomBytes, 1024);      // MN-major
     auto slot_of = [&](int slot, int bytes) -> uint64_t {
       return static_cast<uint32_t>(__shfl_sync(0xffffffffu, (slot * bytes) >> 4, 0));
     };
@@ -429,18 +454,22 @@ __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kThreads, 1)
         ++pv_seg;
       }
       const int n = 2 * npv + 1;
-      if (!(kFp8 ? warp_wait(V16_FULL(npv), PARITY2(npv)) : warp_wait(FULL(n), RING_PARITY(n))) ||
+      if (!(kDequant ? warp_wait(V16_FULL(npv), PARITY2(npv)) : warp_wait(FULL(n), RING_PARITY(n))) ||
           !warp_wait(P_FULL(npv), PARITY2(npv)))
         return false;
       tc_fence_after();
-      const uint64_t dv = dv0 + slot_of(kFp8 ? npv & 1 : n % T::kRing, T::kOperand);
+      const uint64_t dv = dv0 + slot_of(kDequant ? npv & 1 : n % T::kRing, kDequant ? T::kOperand : T::kGranule);
       const uint32_t tp = tmem + kColP + 64 * (npv & 1);
 #pragma unroll
       for (int k = 0; k < kKeys / 16; ++k)
-        mma_f16_ts_uni(tmem + kColO, tp + 8 * k, dv + static_cast<uint64_t>((2048 * k) >> 4), idesc_pv,
-                       (!fresh || k > 0) ? 1u : 0u, el);
+        if constexpr (kParts)      // (the first and second parts' 32 keys at a time, then the others')
+          mma_f8_ts_uni(tmem + kColO, tp + 8 * k, dv + static_cast<uint64_t>((4096 * (k & 3)) >> 4), idesc_pv,
+                        (!fresh || k > 0) ? 1u : 0u, el);
+        else
+          mma_f16_ts_uni(tmem + kColO, tp + 8 * k, dv + static_cast<uint64_t>((2048 * k) >> 4), idesc_pv,
+                         (!fresh || k > 0) ? 1u : 0u, el);
       if (el) {
-        if (!kFp8) tc_commit(EMPTY(n));
+        if (!kDequant) tc_commit(EMPTY(n));
         tc_commit(PV_DONE(npv));
       }
       __syncwarp();
@@ -458,7 +487,7 @@ __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kThreads, 1)
         const uint64_t dk = dk0 + slot_of(n % T::kRing, T::kGranule);
         const uint32_t ts = tmem + kColS + kKeys * (it & 1);
 #pragma unroll
-        for (int a = 0; a < T::kAtoms; ++a)      // (FP8: the query's parts, over the same keys)
+        for (int a = 0; a < (kParts ? 1 : T::kAtoms); ++a)      // (FP8: the query's parts, over the same keys)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             if constexpr (kFp8)
@@ -500,7 +529,8 @@ __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kThreads, 1)
     // 16-code chunks of each of two rows, of different halves (reads) and with
     // different swizzles (writes): both fall on distinct banks.
     if constexpr (kFp8) {
-    setmaxnreg_dec<kRegsDequant>();
+    if constexpr (kDequant) setmaxnreg_dec<kRegsDequant>();
+    constexpr int kRowsAtOnce = kParts ? 16 : 32;
     const int w = warp - 8, tid = threadIdx.x - 256;
     const int r2 = (lane >> 2) & 1, c = (lane & 3) + 4 * (((lane >> 3) & 1) ^ r2);
     const int row4 = 2 * (lane >> 4) + r2;
@@ -513,7 +543,7 @@ __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kThreads, 1)
         // The query's parts, eight lanes a row (16 values each).
         const int head = wk.item / p.row_tiles, mtile = wk.item % p.row_tiles, piece = tid & 7;
         if (seg > 0 && !mbar_wait(Q_EMPTY, (seg - 1) & 1)) ok = false;
-        for (int row0 = 0; row0 < p.tile_rows; row0 += 32) {
+        for (int row0 = 0; row0 < p.tile_rows; row0 += kRowsAtOnce) {
           const int row = row0 + (tid >> 3), i = row / group;
           const int qi = mtile * p.tile_q + i;
           const bool in = row < p.tile_rows && qi < p.nq;
@@ -553,7 +583,8 @@ __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kThreads, 1)
               const int at = cp * kCopyRows + row;
               uint8_t* dst = smem + T::kOffQ + at * 128 + ((piece ^ (at & 7)) << 4);
               *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-              *reinterpret_cast<uint4*>(dst + kAtomBytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+              // (kParts: sixteen rows below; a multiple of 8, so swizzled alike.)
+              *reinterpret_cast<uint4*>(dst + (kParts ? 16 * 128 : kAtomBytes)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             }
             if (piece == 0)
               reinterpret_cast<float*>(smem + T::kOffQScale)[(seg & 3) * kRows + row] =
@@ -587,6 +618,7 @@ __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kThreads, 1)
             mbar_arrive(EMPTY(n));
           }
         }
+        if constexpr (kDequant) {
         const int n = 2 * it + 1;
         if (ok && !mbar_wait(FULL(n), RING_PARITY(n))) ok = false;
         const uint8_t* src = smem + T::kOffRing + (n % T::kRing) * T::kGranule + c * 16;
@@ -618,6 +650,7 @@ __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kThreads, 1)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(V16_FULL(it));
+        }
         ok = __all_sync(0xffffffffu, ok);
       }
       ok = __all_sync(0xffffffffu, ok);
@@ -626,10 +659,11 @@ __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kThreads, 1)
     }
   } else {
     // ---------------------------------------------- softmax and epilogue
-    if constexpr (kFp8) setmaxnreg_inc<kRegsSoft>();
+    if constexpr (kDequant) setmaxnreg_inc<kRegsSoft>();
+    constexpr float kRaise = kParts ? kRaiseParts : kRaiseLog2, kShift = kParts ? kShiftParts : kFp8 ? kShiftFp8 : 0.f;
     const int tid = threadIdx.x - 128;             // = TMEM lane
     const int w4 = warp & 3;
-    const int copy = tid / kCopyRows, row = tid % kCopyRows;      // row of the tile
+    const int copy = tid / kCopyRows, set = tid / kSetRows, row = tid % kSetRows;      // row of the tile
     const uint32_t lanebase = static_cast<uint32_t>(w4 * 32) << 16;
     const int group = p.heads / p.kv_heads;
     const int my_q = row / group;
@@ -666,6 +700,13 @@ __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kThreads, 1)
       auto narrow_tile = [&](int t, uint32_t ok2) {
         uint32_t s[16];
         tmem_ld16x32(tmem + lanebase + kColS + kKeys * (it & 1) + kCols * copy, s);
+        if constexpr (kParts) {
+          // The scores of the query's lower part, sixteen lanes on.
+          uint32_t lo[16];
+          tmem_ld16x32(tmem + lanebase + (16u << 16) + kColS + kKeys * (it & 1) + kCols * copy, lo);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) s[e] = __float_as_uint(__uint_as_float(s[e]) + __uint_as_float(lo[e]));
+        }
         const int col = 2 * (lane & 3);      // of each eight
         const float* par = reinterpret_cast<const float*>(smem + T::kOffParam) + (it & 1) * 3 * kKeys + kCols * copy + col;
         if constexpr (kFp8) {
@@ -705,7 +746,7 @@ __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kThreads, 1)
           m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
           m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
           tmax[u] = m * (kFp8 ? 1.f : sc);
-          const bool raise = tmax[u] > mrun2[u] + kRaiseLog2;
+          const bool raise = tmax[u] > mrun2[u] + kRaise;
           fac[u] = raise && mrun2[u] > ninf ? ex2(mrun2[u] - tmax[u]) : 1.f;
           rescale |= raise && mrun2[u] > ninf;
           if (raise) mrun2[u] = tmax[u];
@@ -716,7 +757,7 @@ __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kThreads, 1)
           if (ok && !mbar_wait(PV_DONE(it - 1), PARITY2(it - 1))) ok = false;
           tc_fence_after();
           const float fa = __shfl_sync(0xffffffffu, fac[0], 4 * (lane & 7)), fb = __shfl_sync(0xffffffffu, fac[1], 4 * (lane & 7));
-          const float f = lane < 8 ? fa : lane < 16 ? fb : 1.f;
+          const float f = !kParts && lane >= 16 ? 1.f : (lane & 15) < 8 ? fa : fb;
 #pragma unroll 1
           for (int c = 0; c < kDim / 32; ++c) {
             uint32_t o[32];
@@ -732,7 +773,7 @@ __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kThreads, 1)
         uint32_t pk[8];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const float mref = mrun2[u] > ninf ? mrun2[u] - (kFp8 ? kShift : 0.f) : 0.f;
+          const float mref = mrun2[u] > ninf ? mrun2[u] - kShift : 0.f;
           float2 ls = make_float2(0.f, 0.f);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -749,7 +790,34 @@ __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kThreads, 1)
           }
           lrun2[u] += ls.x + ls.y;
         }
-        tmem_st16x16_async(tmem + lanebase + kColP + 64 * (it & 1) + (kCols / 2) * copy, pk);
+        const uint32_t tp = tmem + lanebase + kColP + 64 * (it & 1);
+        if constexpr (kParts) {
+          // E5M2 is the upper byte of fp16: a part is what that holds of what is left
+          // (exact, 11 bits in four parts of 3).  Parts 0 and 1 in the lanes of the
+          // query's parts, 2 and 3 in those of 32 columns on; a column holds the 4 keys
+          // of two of this thread's pairs (V's rows are ordered so).
+          uint32_t left[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) left[e] = pk[e];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t part[4];
+#pragma unroll
+            for (int g = 0; g < 2; ++g)
+#pragma unroll
+              for (int u = 0; u < 2; ++u) part[2 * g + u] = __byte_perm(left[4 * g + u], left[4 * g + 2 + u], 0x7531);
+            tmem_st16x8_async(tp + ((q & 1) ? 16u << 16 : 0u) + 32 * (q >> 1) + 8 * copy, part);
+            if (q < 3)
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const uint32_t top = left[e] & 0xff00ff00u;
+                const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&left[e]), *reinterpret_cast<const __half2*>(&top));
+                left[e] = *reinterpret_cast<const uint32_t*>(&d);
+              }
+          }
+        } else {
+          tmem_st16x16_async(tp + (kCols / 2) * copy, pk);
+        }
       };
       for (int t = wk.t0; t < wk.t1; ++t, ++it) {
         if (pages.advance(t, lane)) good = __ballot_sync(0xffffffffu, pages.now >= 0);
@@ -794,7 +862,7 @@ __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kThreads, 1)
         for (int e = 0; e < kCols; e += 2)
           mx[(e >> 1) & 3] = max3(mx[(e >> 1) & 3], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
         const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * (kFp8 ? 1.f : sc);
-        const bool raise = tmax > mrun + kRaiseLog2;
+        const bool raise = tmax > mrun + kRaise;
         const bool rescale = raise && mrun > ninf;
         if (__any_sync(0xffffffffu, rescale)) {
           // P V of the tile before has to be in the output first.
@@ -813,7 +881,7 @@ __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kThreads, 1)
         }
         if (raise) mrun = tmax;
         // (FP8: P up to 2^15, which leaves fp16 40 powers of two below.)
-        const float mref = mrun > ninf ? mrun - (kFp8 ? kShift : 0.f) : 0.f;
+        const float mref = mrun > ninf ? mrun - kShift : 0.f;
         // P of tile it - 2 has been read.
         if (it >= 2 && ok && !mbar_wait(PV_DONE(it), PARITY2(it - 2))) ok = false;
         tc_fence_after();
@@ -842,12 +910,14 @@ __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kThreads, 1)
         }
         // Rows of V behind every query's view are cleared.
         const int vlive = wk.len - t * kKeys;
-        if (!kFp8 && (vlive < kKeys || (ok2 & 3u) != 3u)) {
+        if (!kDequant && (vlive < kKeys || (ok2 & 3u) != 3u)) {
           const int n = 2 * it + 1;
           if (ok && !mbar_wait(FULL(n), RING_PARITY(n))) ok = false;
           uint4* v = reinterpret_cast<uint4*>(smem + T::kOffRing + (n % T::kRing) * T::kGranule);
-          for (int e = tid; e < T::kOperand / 16; e += kSoftThreads) {
-            const int key = (e >> 3) & (kKeys - 1);
+          for (int e = tid; e < T::kGranule / 16; e += kSoftThreads) {
+            const int at = (e >> 3) & (kKeys - 1);
+            // (kParts: of each sixteen rows 0 1 8 9 2 3 10 11 ...)
+            const int key = kParts ? (at & ~15) | ((at & 2) << 2) | ((at >> 1) & 6) | (at & 1) : at;
             if (key >= vlive || !((ok2 >> (key / kPage)) & 1u)) v[e] = make_uint4(0u, 0u, 0u, 0u);
           }
           fence_proxy_async_smem();
@@ -864,9 +934,9 @@ __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kThreads, 1)
           lrun2[u] += __shfl_xor_sync(0xffffffffu, lrun2[u], 1);
           lrun2[u] += __shfl_xor_sync(0xffffffffu, lrun2[u], 2);
           const float m = __shfl_sync(0xffffffffu, mrun2[u], 4 * (lane & 7)), l = __shfl_sync(0xffffffffu, lrun2[u], 4 * (lane & 7));
-          if ((lane >> 3) == u) {
+          if (((lane >> 3) & (kParts ? 1 : 3)) == u) {
             mrun = m;
-            lrun = l;
+            lrun = kParts && lane >= 16 ? 0.f : l;      // (counted once)
           }
         }
       }
@@ -882,29 +952,29 @@ __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kThreads, 1)
         return (static_cast<long long>(wk.req) * p.nq + mtile * p.tile_q + i) * p.heads + head * group + (r - i * group);
       };
       float top = mrun, l = lrun;
-      if constexpr (kCopies > 1) {
+      if constexpr (kSets > 1) {
         xchg[tid] = make_float2(mrun, lrun);
         named_bar_sync(1, kSoftThreads);
         top = ninf;
         l = 0.f;
-        float2 other[kCopies];
+        float2 other[kSets];
 #pragma unroll
-        for (int c = 0; c < kCopies; ++c) {
-          other[c] = xchg[c * kCopyRows + row];
+        for (int c = 0; c < kSets; ++c) {
+          other[c] = xchg[c * kSetRows + row];
           top = fmaxf(top, other[c].x);
         }
         const float mref = top > ninf ? top : 0.f;
 #pragma unroll
-        for (int c = 0; c < kCopies; ++c) l = fmaf(ex2(other[c].x - mref), other[c].y, l);
+        for (int c = 0; c < kSets; ++c) l = fmaf(ex2(other[c].x - mref), other[c].y, l);
       }
       const bool any = l > 0.f || l != l;
       const float w = any ? ex2(mrun - (top > ninf ? top : 0.f)) / l : 0.f;
-      if (live && copy == 0) {
-        const float lse = any ? (top - (kFp8 ? kShift : 0.f) + log2f(l)) * kLn2 : ninf;
+      if (live && set == 0) {
+        const float lse = any ? (top - kShift + log2f(l)) * kLn2 : ninf;
         if (!whole) p.part_lse[place(row)] = lse;
         else if (p.lse) p.lse[place(row)] = lse;
       }
-      if constexpr (kCopies == 1) {
+      if constexpr (kSets == 1) {
         const long long at = live ? place(row) : 0;
 #pragma unroll 1
         for (int c = 0; c < kDim / 32; ++c) {
@@ -934,9 +1004,9 @@ __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kThreads, 1)
       } else {
         // The copies' outputs, weighted, are added up through shared memory, 32 dims
         // at a time (16-byte piece i of a row at i ^ (row & 7)): thread = row and
-        // kCopies' share of the 32.
-        constexpr int kPer = 32 / kCopies;                  // dims of a thread
-        const int orow = tid / kCopies, part = tid % kCopies;
+        // kSets' share of the 32.
+        constexpr int kPer = 32 / kSets;                  // dims of a thread
+        const int orow = tid / kSets, part = tid % kSets;
         const int oq = orow / group;
         const bool olive = oq < p.tile_q && mtile * p.tile_q + oq < p.nq;
         const long long at = olive ? place(orow) : 0;
@@ -960,8 +1030,8 @@ __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kThreads, 1)
 #pragma unroll
           for (int e = 0; e < kPer; ++e) sum[e] = 0.f;
 #pragma unroll
-          for (int cc = 0; cc < kCopies; ++cc) {
-            const int src = cc * kCopyRows + orow;
+          for (int cc = 0; cc < kSets; ++cc) {
+            const int src = cc * kSetRows + orow;
 #pragma unroll
             for (int e = 0; e < kPer / 4; ++e) {
               const float4 v = *reinterpret_cast<const float4*>(buf + src * 32 + (((part * (kPer / 4) + e) ^ (src & 7)) << 2));
@@ -972,7 +1042,9 @@ __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kThreads, 1)
             }
           }
           const long long to = at * kDim + 32 * c + kPer * part;
-          if (whole) {
+          if (whole && kPer == 4) {
+            *reinterpret_cast<uint2*>(p.out + to) = make_uint2(pack_bf16x2(sum[0], sum[1]), pack_bf16x2(sum[2], sum[3]));
+          } else if (whole) {
 #pragma unroll
             for (int e = 0; e < kPer / 8; ++e)
               reinterpret_cast<uint4*>(p.out + to)[e] =
@@ -1100,18 +1172,22 @@ int row_tiles_of(int nq, int group) {
   return (nq + fit - 1) / fit;
 }
 
-template <int kDim, bool kFp8>
+template <int kDim, int kCopies, bool kNarrow, bool kFp8>
 cudaError_t launch(const GqaDecodeLaunch& a, cudaStream_t s) {
-  using T = Geo<kDim, kFp8>;
+  using T = Geo<kDim, kNarrow, kFp8>;
   const uint64_t G = a.heads / a.kv_heads, K = a.kv_heads, tokens = static_cast<uint64_t>(a.batch) * a.nq;
   const uint64_t pages = static_cast<uint64_t>(a.num_pages);
   CUtensorMap tq, tk, tv;
   if (kFp8) {
-    // Codes as (byte, row of the page, head, page).
+    // Codes as (byte, row of the page, head, page); kParts: values as (byte, r % 2, r / 8
+    // % 2, r / 2 % 4, r / 16) of their rows r, in that order.
     const uint64_t dims[4] = {kDim, kPage, K, pages}, str[3] = {kDim, kPage * kDim, K * kPage * kDim};
     const uint32_t box[4] = {kDim, kPage, 1, 1};
+    const uint64_t vdims[5] = {kDim, 2, 2, 4, 4 * K * pages}, vstr[4] = {kDim, 8 * kDim, 2 * kDim, 16 * kDim};
+    const uint32_t vbox[5] = {kDim, 2, 2, 4, 4};
     if (!encode_tmap_nd(&tk, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.k, 4, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_tmap_nd(&tv, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.v, 4, dims, str, box, CU_TENSOR_MAP_SWIZZLE_NONE))
+        !(T::kParts ? encode_tmap_nd(&tv, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.v, 5, vdims, vstr, vbox, CU_TENSOR_MAP_SWIZZLE_128B)
+                    : encode_tmap_nd(&tv, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.v, 4, dims, str, box, CU_TENSOR_MAP_SWIZZLE_NONE)))
       return cudaErrorInvalidValue;
     tq = tk;      // not used
   } else {
@@ -1128,13 +1204,11 @@ cudaError_t launch(const GqaDecodeLaunch& a, cudaStream_t s) {
         !encode_tmap_nd(&tv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.v, 5, cdims, cstr, cbox, CU_TENSOR_MAP_SWIZZLE_128B))
       return cudaErrorInvalidValue;
   }
-  auto kern = a.tile_rows <= 16   ? gqa_decode_kernel<kDim, 4, true, kFp8>
-              : a.tile_rows <= 32 ? gqa_decode_kernel<kDim, 4, false, kFp8>
-              : a.tile_rows <= 64 ? gqa_decode_kernel<kDim, 2, false, kFp8>
-                                  : gqa_decode_kernel<kDim, 1, false, kFp8>;
+  auto kern = gqa_decode_kernel<kDim, kCopies, kNarrow, kFp8>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmemBytes);
   if (e != cudaSuccess) return e;
-  e = launch_kernel(kern, dim3(a.ctas), dim3(kFp8 ? kThreadsFp8 : kThreads), T::kSmemBytes, s, false, 1, tq, tk, tv, a);
+  e = launch_kernel(kern, dim3(a.ctas), dim3(!kFp8 ? kThreads : kNarrow ? kThreadsParts : kThreadsFp8), T::kSmemBytes, s, false, 1,
+                    tq, tk, tv, a);
   if (e != cudaSuccess || a.ctas == 1) return e;
   // (Parts of an item, on average: 1 + CTAs / items.)
   constexpr int kGroups = kMergeThreads / (kDim / 4);
@@ -1142,6 +1216,15 @@ cudaError_t launch(const GqaDecodeLaunch& a, cudaStream_t s) {
   const int per = many ? kGroups / 4 : kGroups;
   return launch_kernel(many ? gqa_merge_kernel<kDim, 4> : gqa_merge_kernel<kDim, 1>,
                        dim3(a.ctas - 1, (a.tile_rows + per - 1) / per), dim3(kMergeThreads), 0, s, true, 1, a);
+}
+
+// As many copies of the rows as fit into a tile.
+template <int kDim, bool kFp8>
+cudaError_t launch_rows(const GqaDecodeLaunch& a, cudaStream_t s) {
+  if (a.tile_rows <= 16) return launch<kDim, 4, true, kFp8>(a, s);
+  if (a.tile_rows <= 32) return launch<kDim, 4, false, kFp8>(a, s);
+  if (a.tile_rows <= 64) return launch<kDim, 2, false, kFp8>(a, s);
+  return launch<kDim, 1, false, kFp8>(a, s);
 }
 
 }  // namespace
@@ -1166,8 +1249,8 @@ cudaError_t launch_gqa_decode(GqaDecodeLaunch a, void* ws, cudaStream_t s) {
   const size_t slots = static_cast<size_t>(a.ctas) * 2 * kRows;
   a.part_lse = a.part_o + slots * a.dim;
   a.joins = reinterpret_cast<int4*>(a.part_lse + slots);
-  if (a.k_scale) return launch<128, true>(a, s);
-  return a.dim == 128 ? launch<128, false>(a, s) : launch<64, false>(a, s);
+  if (a.k_scale) return launch_rows<128, true>(a, s);
+  return a.dim == 128 ? launch_rows<128, false>(a, s) : launch_rows<64, false>(a, s);
 }
 
 }  // namespace dsa

@@ -5,8 +5,10 @@ Q the largest sm_scale * max|q| * sum_d |k_d|: scores are sums of 2 * 128 produc
 scales (258 * 2^-24 E), of a query that is off by 2^-17 of its largest value where a value is below 2^-9 of it
 (2^-17 Q): dx.  A weight is 2^(x + log2(scale) - m): its exponent is off by dx / ln 2, by the logarithm (2^-22 of it)
 and by the roundings of the sum (2^-23 of its terms, at most z = |x| / ln 2 + |log2 scale|): 2^-21 z; it is rounded to
-fp16 (2^-11), and is lost below 2^-31 of the largest.  So out is off by 2^-8 |out| + (2^-11 + 2.1 (dx + 2^-21 z) + n 2^-24
-+ 2^-18) A + n 2^-31 max|v|, and the log-sum-exp by dx + 2^-21 z + n 2^-24 + 2^-20 + 2^-23 |lse|.
+fp16 (2^-11).  Up to 16 rows it is then four E5M2 parts, whole multiples of 2^-16 where the largest weight is 2^13 at
+least: cut by up to 2^-29 of the largest.  (More rows: fp16's smallest step, 2^-24, where the largest is 2^7: 2^-32, half
+a step.)  So out is off by 2^-8 |out| + (2^-11 + 2.1 (dx + 2^-21 z) + n 2^-24 + 2^-18) A + n 2^-29 max|v|, and the
+log-sum-exp by dx + 2^-21 z + n 2^-24 + 2^-20 + 2^-23 |lse|.
 """
 import math
 
@@ -119,7 +121,7 @@ def _check(c, out, lse, heads=None, keys=None):
             dx = 258 * 2.0 ** -24 * E + 2.0 ** -17 * Q + 2.0 ** -21 * z
             ref, A = p @ v, p @ v.abs()
             tol = 2.0 ** -8 * ref.abs() + (2.0 ** -11 + 2.1 * dx[:, None] + n * 2.0 ** -24 + 2.0 ** -18) * A \
-                + n * 2.0 ** -31 * v.abs().amax()
+                + n * 2.0 ** -29 * v.abs().amax()
             assert ((got - ref).abs() <= tol).all(), (r, n, h, ((got - ref).abs() / tol).max())
             if lse is not None:
                 bound = dx + n * 2.0 ** -24 + 2.0 ** -20 + 2.0 ** -23 * e.abs()

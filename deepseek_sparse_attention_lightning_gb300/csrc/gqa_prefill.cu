@@ -66,7 +66,7 @@ namespace {
 
 constexpr int kTile = 128;                     // rows of a query tile, keys of a key tile
 constexpr int kAtomBytes = kTile * 128;        // 128 rows x 64 dims: 16 KB
-constexpr int kNumBars = 32;
+constexpr int kNumBars = 34;
 
 // Shared memory for heads of kDim dims.
 template <int kDim>
@@ -93,7 +93,7 @@ constexpr int kThreads = 384;                  // two softmax warpgroups; copies
 constexpr int kSoftRegs = 216, kOtherRegs = 72;
 static_assert(256 * kSoftRegs + 128 * kOtherRegs <= 384 * 168, "registers");
 constexpr int kSoftWarps = 8;
-constexpr int kItemReaders = kSoftWarps + 1;   // and the MMA warp
+constexpr int kItemReaders = kSoftWarps + 2;   // and the MMA warps
 constexpr int kMaxParts = 8;                   // CTAs of a cluster that share an item's keys
 constexpr int kColS = 0, kColO = 256, kTmemCols = 512;
 constexpr float kRaiseLog2 = 8.0f;
@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #define S_FULL(q) (bar0 + 160u + 8u * (q))
 #define O_FULL(q) (bar0 + 176u + 8u * (q))
 #define P_FULL(q) (bar0 + 192u + 8u * (q))
-#define DRAIN (bar0 + 208u)
+#define DRAIN(q) (bar0 + 256u + 8u * (q))
 #define TAKEN (bar0 + 216u)
 // Item k's record written / no longer needed by any role.
 #define ITEM_FULL(k) (bar0 + 224u + 8u * ((k) & 1))
@@ -316,8 +316,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int st = 0; st < kStages; ++st) {
       mbar_init(K_FULL(st), 1);
       mbar_init(V_FULL(st), 1);
-      mbar_init(K_EMPTY(st), 1);
-      mbar_init(V_EMPTY(st), 1);
+      mbar_init(K_EMPTY(st), 2);      // an MMA warp of each query tile
+      mbar_init(V_EMPTY(st), 2);
     }
     for (int q = 0; q < 2; ++q) {
       mbar_init(Q_FULL(q), 1);
@@ -328,9 +328,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(P_FULL(q), kTile);
       mbar_init(O_FULL(q), 1);
     }
-    mbar_init(DRAIN, 1);
+    mbar_init(DRAIN(0), 1);
+    mbar_init(DRAIN(1), 1);
     mbar_init(TAKEN, 1);
-    mbar_init(ORDER, 2);
+    mbar_init(ORDER, 1);
     *falling = 0;
     fence_mbar_init();
     prefetch_tmap(&tmap_q);
@@ -424,156 +425,87 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok && uses1 > 0) mbar_wait(Q_FULL(1), (uses1 - 1) & 1);
       }
       __syncwarp();
-    } else if (warp == 9) {
+    } else if (warp < 11) {
       // --------------------------------------------------------------- MMAs
+      // A warp a query tile, each on its own: it answers its tile's probabilities at
+      // once, whatever the other is at.
+      const int q = warp - 9;
       const uint32_t el = elect_one() ? 1u : 0u;
       constexpr uint32_t idesc_qk = make_idesc(1, 1, 0, 0, kTile, kTile);
       constexpr uint32_t idesc_pv = make_idesc(1, 1, 0, 1, kDim, kTile);
-      const uint64_t dq0 = smem_desc_sw128(sbase + T::kOffQ, 16, 1024);
+      const uint64_t dq = smem_desc_sw128(sbase + T::kOffQ + q * T::kOperand, 16, 1024);
       const uint64_t dk0 = smem_desc_sw128(sbase + T::kOffRing, 16, 1024);
       const uint64_t dv0 = smem_desc_sw128(sbase + T::kOffRing + T::kOperand, kAtomBytes, 1024);      // MN-major
+      const uint32_t ts = tmem + kColS + kTile * q, to = tmem + kColO + kDim * q;
       bool ok = true;
       // A phase is tested before the last MMAs of the step before go out, so that
       // the test's latency hides behind them; `want` waits only if it was not
       // complete then.
-      uint32_t done_bar = 0, done_parity = 0;
+      bool done = false;
       auto want = [&](uint32_t bar, uint32_t parity) {
-        if (ok && !(done_bar == bar && done_parity == parity)) ok = warp_wait(bar, parity);
-        done_bar = 0;
+        if (ok && !done) ok = warp_wait(bar, parity);
+        done = false;
       };
-      auto peek = [&](uint32_t bar, uint32_t parity) {
-        if (warp_test(bar, parity)) {
-          done_bar = bar;
-          done_parity = parity;
-        }
-      };
-      // (A phase that completed stays the barrier's latest until its data has
-      // been used, so a remembered answer does not go stale before that; it is
-      // dropped after a use.)
       // Descriptor offset of tile t's stage, broadcast: the compiler then knows it to
       // be the same in every lane and keeps it in uniform registers.
       auto stage_of = [&](int t) -> uint64_t {
         return static_cast<uint32_t>(__shfl_sync(0xffffffffu, ((t % kStages) * 2 * T::kOperand) >> 4, 0));
       };
-      // Q K^T and P V of query tile q over key tile t (counted over the items);
-      // next_bar: what the step after it waits for.
-      auto qk = [&](int q, int t, uint32_t next_bar, uint32_t next_parity) {
-        const uint64_t dk = dk0 + stage_of(t);
-        const uint64_t dq = dq0 + static_cast<uint64_t>((q * T::kOperand) >> 4);
-#pragma unroll
-        for (int a = 0; a < T::kAtoms; ++a) {
-          if (a == T::kAtoms - 1) peek(next_bar, next_parity);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_f16_ss_uni(tmem + kColS + kTile * q, dq + static_cast<uint64_t>((a * kAtomBytes + 32 * k) >> 4),
-                           dk + static_cast<uint64_t>((a * kAtomBytes + 32 * k) >> 4), idesc_qk, (a > 0 || k > 0) ? 1u : 0u,
-                           el);
-        }
-        if (el) tc_commit(S_FULL(q));
-        __syncwarp();
-      };
-      auto pv = [&](int q, int t, bool first, uint32_t next_bar, uint32_t next_parity) {
-        const uint64_t dv = dv0 + stage_of(t);
-#pragma unroll
-        for (int k = 0; k < kTile / 16; ++k) {
-          if (k == kTile / 32) peek(next_bar, next_parity);
-          mma_f16_ts_uni(tmem + kColO + kDim * q, tmem + kColS + kTile * q + 8 * k,
-                         dv + static_cast<uint64_t>((2048 * k) >> 4), idesc_pv, (!first || k > 0) ? 1u : 0u, el);
-        }
-      };
       auto commit = [&](uint32_t bar) {
         if (el) tc_commit(bar);
         __syncwarp();
       };
-      int base = 0, c0 = 0, c1 = 0;          // key tiles so far: all, and of each query tile
-      int items0 = 0, items1 = 0;            // items that had each query tile
-      // P V of query tile 1 goes out one step late, after Q K^T of query tile 0
-      // over the next key tile (the next item's first, at the end of one).
-      bool held = false, held_pv = false, held_v = false, held_first = false, held_last = false;
-      int held_t = 0, held_c = 0;
-      auto issue_held = [&](uint32_t next_bar, uint32_t next_parity) {
-        if (!held || !ok) return;
-        held = false;
-        if (held_pv) {
-          if (!held_v) ok = warp_wait(V_FULL(held_t), STAGE_PARITY(held_t));
-          want(P_FULL(1), held_c & 1);
-          tc_fence_after();
-          if (!ok) return;
-          pv(1, held_t, held_first, next_bar, next_parity);
-          if (held_last) commit(O_FULL(1));
-        }
-        commit(V_EMPTY(held_t));
-      };
+      int t = 0, c = 0, uses = 0;      // key tiles so far: all, and of this query tile; items that had it
       for (int item = 0; ok; ++item) {
-        // (What is held back does not wait for a record, or an item without keys,
-        // to come.)
-        if (!warp_test(ITEM_FULL(item), PARITY(item))) issue_held(DRAIN, 0);
-        if (!(ok = ok && warp_wait(ITEM_FULL(item), PARITY(item)))) break;
+        if (!(ok = warp_wait(ITEM_FULL(item), PARITY(item)))) break;
         const int work = __shfl_sync(0xffffffffu, record(item).work, 0);
         const int nt0 = __shfl_sync(0xffffffffu, record(item).nt0, 0);
-        const int nt1 = __shfl_sync(0xffffffffu, record(item).nt1, 0), ntmax = max(nt0, nt1);
+        const int nt1 = __shfl_sync(0xffffffffu, record(item).nt1, 0), ntmax = max(nt0, nt1), nt = q == 0 ? nt0 : nt1;
         if (lane == 0) mbar_arrive(ITEM_EMPTY(item));
         if (!work) break;
-        if (ntmax == 0) issue_held(DRAIN, 0);
-        for (int j = 0; ok && j < ntmax; ++j) {
-          const int t = base + j;
-          if (j < nt0) {
-            // (A new item's q and first keys may not have landed yet: then the
-            // P V that is held back does not wait for them.)
-            if (j == 0) {
-              if (held && !(warp_test(Q_FULL(0), items0 & 1) && warp_test(K_FULL(t), STAGE_PARITY(t))))
-                issue_held(K_FULL(t), STAGE_PARITY(t));
-              ok = ok && warp_wait(Q_FULL(0), items0 & 1);
-              ++items0;
-            }
-            want(K_FULL(t), STAGE_PARITY(t));
-            tc_fence_after();
-            if (!ok) break;
-            qk(0, t, P_FULL(1), held_c & 1);
-            if (j == nt0 - 1) commit(Q_EMPTY(0));
-          }
-          issue_held(K_FULL(t), STAGE_PARITY(t));
+        if (nt > 0) ok = warp_wait(Q_FULL(q), uses++ & 1);
+        for (int j = 0; ok && j < nt; ++j, ++t, ++c) {
+          const uint64_t stage = stage_of(t), dk = dk0 + stage, dv = dv0 + stage;
+          want(K_FULL(t), STAGE_PARITY(t));
+          tc_fence_after();
           if (!ok) break;
-          if (j < nt1) {
-            if (j == 0) {
-              ok = warp_wait(Q_FULL(1), items1 & 1);
-              ++items1;
-            }
-            if (j >= nt0) want(K_FULL(t), STAGE_PARITY(t));
-            tc_fence_after();
-            if (!ok) break;
-            qk(1, t, P_FULL(0), c0 & 1);
-            if (j == nt1 - 1) commit(Q_EMPTY(1));
-          }
+#pragma unroll
+          for (int a = 0; a < T::kAtoms; ++a)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_f16_ss_uni(ts, dq + static_cast<uint64_t>((a * kAtomBytes + 32 * k) >> 4),
+                             dk + static_cast<uint64_t>((a * kAtomBytes + 32 * k) >> 4), idesc_qk, (a > 0 || k > 0) ? 1u : 0u,
+                             el);
+          commit(S_FULL(q));
           commit(K_EMPTY(t));
-          if (j < nt0) {
-            ok = warp_wait(V_FULL(t), STAGE_PARITY(t));
-            want(P_FULL(0), c0 & 1);
-            tc_fence_after();
-            if (!ok) break;
-            pv(0, t, j == 0, K_FULL(t + 1), STAGE_PARITY(t + 1));
-            if (j == nt0 - 1) commit(O_FULL(0));
-            ++c0;
+          if (j == nt - 1) commit(Q_EMPTY(q));
+          ok = warp_wait(V_FULL(t), STAGE_PARITY(t)) && warp_wait(P_FULL(q), c & 1);
+          tc_fence_after();
+          if (!ok) break;
+#pragma unroll
+          for (int k = 0; k < kTile / 16; ++k) {
+            if (k == kTile / 32) done = warp_test(K_FULL(t + 1), STAGE_PARITY(t + 1));
+            mma_f16_ts_uni(to, ts + 8 * k, dv + static_cast<uint64_t>((2048 * k) >> 4), idesc_pv, (j > 0 || k > 0) ? 1u : 0u, el);
           }
-          held = true;
-          held_pv = j < nt1;
-          held_v = j < nt0;
-          held_first = j == 0;
-          held_last = j == nt1 - 1;
-          held_t = t;
-          held_c = c1;
-          if (j < nt1) ++c1;
+          commit(V_EMPTY(t));
+          if (j == nt - 1) commit(O_FULL(q));
         }
-        base += ntmax;
+        // Tiles that the other query tile alone reads.  (Each in its time: a phase of
+        // their barriers takes both warps' arrivals.)
+        for (int j = nt; ok && j < ntmax; ++j, ++t) {
+          want(K_FULL(t), STAGE_PARITY(t));
+          if (lane == 0) mbar_arrive(K_EMPTY(t));
+          ok = ok && warp_wait(V_FULL(t), STAGE_PARITY(t));
+          if (lane == 0) mbar_arrive(V_EMPTY(t));
+        }
       }
-      issue_held(DRAIN, 0);
       if (!ok && el) raise_error(kErrTimeout);
-      if (el) tc_commit(DRAIN);      // every MMA is done before TMEM is freed
+      if (el) tc_commit(DRAIN(q));      // every MMA is done before TMEM is freed
       __syncwarp();
-      mbar_wait(DRAIN, 0);
+      mbar_wait(DRAIN(q), 0);
     } else {
       // ------------------------------------------------ order of the offsets
-      const bool falls = __any_sync(0xffffffffu, falling_offsets(p, (warp - 10) * 32 + lane, 64));
+      const bool falls = __any_sync(0xffffffffu, falling_offsets(p, lane, 32));
       if (lane == 0) {
         if (falls) *falling = 1;
         mbar_arrive(ORDER);
@@ -648,9 +580,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (raise) mrun = tmax;
         const float mref = mrun > ninf ? mrun : 0.f;
-        // Rows of V behind the request's end are cleared, by the first query
-        // tile that reads them.
-        if (vlive < kTile && (q == 0 || j >= record(item).nt0)) {
+        // Rows of V behind the request's end are cleared, by both query tiles (either's
+        // P V may come first).
+        if (vlive < kTile) {
           const int t = record(item).base + j;
           if (ok && !mbar_wait(V_FULL(t), STAGE_PARITY(t))) ok = false;
   #pragma unroll 1

@@ -86,7 +86,9 @@ constexpr int kDequantWarps = 8, kParamWarps = 4;      // FP8; the latter of the
 // warpgroups of dequantisation.
 constexpr int kRegsMma = 88, kRegsSoft = 216, kRegsDequant = 104;
 static_assert(kRegsMma + kRegsSoft + 2 * kRegsDequant <= 4 * 128, "registers");
-constexpr int kStretch = 2;                    // what an item's queries and output cost, in key tiles
+// What an item's queries and output cost, in key tiles: bf16, FP8 (whose tiles take half
+// the time).  64 requests of 1000 .. 6000 FP8 tokens: 107 us for 1, 103 for 2, 97 for 4.
+constexpr int kStretchBf16 = 2, kStretchFp8 = 4;
 constexpr int kColS = 0, kColP = 256, kColO = 384, kTmemCols = 512;
 constexpr int kStage = kSoftThreads * 32 * 4;  // 32 columns of a copy's rows, fp32
 constexpr float kRaiseLog2 = 8.0f, kRaiseParts = 2.0f, kShiftFp8 = 7.0f, kShiftParts = 13.0f;
@@ -136,7 +138,10 @@ __device__ __forceinline__ int request_len(const GqaDecodeLaunch& p, int r) {
 }
 
 __device__ __forceinline__ int tiles_of(int len) { return (len + kKeys - 1) / kKeys; }
-__device__ __forceinline__ int units_of(int len) { return len > 0 ? tiles_of(len) + kStretch : 0; }
+template <int kStretch>
+__device__ __forceinline__ int units_of(int len) {
+  return len > 0 ? tiles_of(len) + kStretch : 0;
+}
 
 // The line: for each item with tokens kStretch units and one a key tile, the items
 // of a request one after another.  It is cut into parts from unit kStretch on, so
@@ -147,15 +152,17 @@ struct Line {
   int parts;
 };
 
+template <int kStretch>
 __device__ __forceinline__ long long cut(const Line& ln, int g) {
   return kStretch + (ln.total - kStretch) * g / ln.parts;
 }
 
 // (one warp) The line of all requests.
+template <int kStretch>
 __device__ __forceinline__ Line scan_total(const GqaDecodeLaunch& p, int lane) {
   const int items = p.kv_heads * p.row_tiles;      // of a request
   long long n = 0;
-  for (int r = lane; r < p.batch; r += 32) n += units_of(request_len(p, r));
+  for (int r = lane; r < p.batch; r += 32) n += units_of<kStretch>(request_len(p, r));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
   Line ln;
@@ -167,6 +174,7 @@ __device__ __forceinline__ Line scan_total(const GqaDecodeLaunch& p, int lane) {
 
 // (one warp) The item that holds unit `at` of the line (at < total): its request,
 // which of the request's it is, and the line position of its first unit.
+template <int kStretch>
 __device__ __forceinline__ void locate(const GqaDecodeLaunch& p, long long at, int lane, int& req, int& item,
                                        long long& first) {
   const int items = p.kv_heads * p.row_tiles;
@@ -175,7 +183,7 @@ __device__ __forceinline__ void locate(const GqaDecodeLaunch& p, long long at, i
   first = 0;
   for (int r0 = 0; r0 < p.batch; r0 += 32) {
     const int r = r0 + lane;
-    const long long n = r < p.batch ? static_cast<long long>(units_of(request_len(p, r))) * items : 0;
+    const long long n = r < p.batch ? static_cast<long long>(units_of<kStretch>(request_len(p, r))) * items : 0;
     long long incl = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -197,6 +205,7 @@ __device__ __forceinline__ void locate(const GqaDecodeLaunch& p, long long at, i
 }
 
 // The stretches of items in a CTA's part [pos, hi) of the line, in order.
+template <int kStretch>
 struct Walk {
   long long pos, hi;     // next unit of the line, end of the part
   int req, item;         // of the stretch
@@ -240,7 +249,8 @@ struct PageBatch {
     const int id = __ldg(table + i);
     return id >= 0 && id < num_pages ? id : kBad;
   }
-  __device__ __forceinline__ PageBatch(const GqaDecodeLaunch& p, const Walk& wk, int lane)
+  template <int kStretch>
+  __device__ __forceinline__ PageBatch(const GqaDecodeLaunch& p, const Walk<kStretch>& wk, int lane)
       : table(p.page_table + static_cast<long long>(wk.req) * p.max_pages), pages((wk.len + kPage - 1) / kPage),
         num_pages(p.num_pages), t0(wk.t0), now(0) {
     ahead = get(2 * t0 + lane);
@@ -272,6 +282,7 @@ __global__ void __launch_bounds__(!kFp8 ? kThreads : kNarrow ? kThreadsParts : k
   using T = Geo<kDim, kNarrow, kFp8>;
   constexpr bool kParts = T::kParts, kDequant = T::kDequant;
   constexpr int kCols = kKeys / kCopies;         // keys of a softmax thread
+  constexpr int kStretch = kFp8 ? kStretchFp8 : kStretchBf16;
   constexpr int kCopyRows = kRows / kCopies;     // lanes of a copy
   constexpr int kSets = kParts ? 2 * kCopies : kCopies, kSetRows = kRows / kSets;      // outputs to be added up
   static_assert(!kNarrow || kCopies == 4, "a warp a copy");
@@ -328,21 +339,21 @@ __global__ void __launch_bounds__(!kFp8 ? kThreads : kNarrow ? kThreadsParts : k
     tmem_relinquish();
   }
   if (warp == 3) {
-    const Line ln = scan_total(p, lane);
+    const Line ln = scan_total<kStretch>(p, lane);
     const int part = blockIdx.x;
     long long lo = 0, hi = 0, first = 0;
     int req = 0, item = 0;
     if (part < ln.parts && ln.total > 0) {
-      lo = cut(ln, part);
-      hi = cut(ln, part + 1);
-      if (hi > lo) locate(p, lo, lane, req, item, first);
+      lo = cut<kStretch>(ln, part);
+      hi = cut<kStretch>(ln, part + 1);
+      if (hi > lo) locate<kStretch>(p, lo, lane, req, item, first);
     }
     // What the merge has to join: the item that this part's first cut falls into, if
     // it is the first cut inside that item, and its last part.
     if (lane == 0) {
       int4 join = make_int4(-1, 0, 0, 0);
       const long long tile0 = first + kStretch;
-      if (part > 0 && hi > lo && lo > tile0 && cut(ln, part - 1) <= tile0) {
+      if (part > 0 && hi > lo && lo > tile0 && cut<kStretch>(ln, part - 1) <= tile0) {
         const long long end = tile0 + tiles_of(request_len(p, req)) - kStretch;      // the item's, from unit kStretch
         join = make_int4(req, item, static_cast<int>((end * ln.parts - 1) / (ln.total - kStretch)), 0);
       }
@@ -356,7 +367,7 @@ __global__ void __launch_bounds__(!kFp8 ? kThreads : kNarrow ? kThreadsParts : k
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-  Walk wk;
+  Walk<kStretch> wk;
   wk.pos = info[0];
   wk.hi = info[1];
   wk.req = static_cast<int>(info[3] & 0xffffffff);
@@ -443,7 +454,7 @@ __global__ void __launch_bounds__(!kFp8 ? kThreads : kNarrow ? kThreadsParts : k
     // P V of tile npv (its stretch's first: the output starts at zero, once the
     // epilogue has read the stretch before).
     int pv_seg = 0, pv_left = 0;
-    Walk pvw = wk;
+    Walk<kStretch> pvw = wk;
     auto issue_pv = [&]() -> bool {
       bool fresh = false;
       if (pv_left == 0) {

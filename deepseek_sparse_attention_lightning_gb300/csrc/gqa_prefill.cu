@@ -64,19 +64,26 @@ DSA_DEFINE_ERROR_WORD(gqa_prefill)
 namespace dsa {
 namespace {
 
-constexpr int kTile = 128;                     // rows of a query tile, keys of a key tile
+constexpr int kTile = 128;                     // rows of a query tile
 constexpr int kAtomBytes = kTile * 128;        // 128 rows x 64 dims: 16 KB
-constexpr int kNumBars = 34;
+constexpr int kNumBars = 40;
 
 // Shared memory for heads of kDim dims.
 template <int kDim>
 struct Geo {
   static constexpr int kAtoms = kDim / 64;
-  static constexpr int kOperand = kAtoms * kAtomBytes;      // q of a tile, K or V of a key tile
+  // Keys of a key tile, and buffers of scores: with two, Q K^T of a query tile's next key
+  // tile is done while this one's is in the softmax (D = 64: 4 x 96 columns of tensor
+  // memory, and 2 x 64 of outputs; D = 128 leaves room for one of 128).
+  static constexpr int kBufs = kDim == 128 ? 1 : 2, kKeys = kDim == 128 ? 128 : 96;
+  static constexpr int kColO = 2 * kBufs * kKeys;
+  static_assert(kColO + 2 * kDim <= 512, "tensor memory");
+  static constexpr int kOperand = kAtoms * kAtomBytes;      // q of a tile
+  static constexpr int kKeyAtom = kKeys * 128, kKeyOperand = kAtoms * kKeyAtom;      // K or V of a key tile
   static constexpr int kStages = kDim == 128 ? 2 : 4;       // key tiles in the ring
   static constexpr int kOffQ = 0;
   static constexpr int kOffRing = 2 * kOperand;             // a stage: K, V
-  static constexpr int kOffBar = kOffRing + kStages * 2 * kOperand;
+  static constexpr int kOffBar = kOffRing + kStages * 2 * kKeyOperand;
   static constexpr int kOffTaken = kOffBar + kNumBars * 8;  // an answer of 16 bytes
   static constexpr int kOffItem = kOffTaken + 16;           // two records
   static constexpr int kOffSlot = kOffItem + 2 * 48;
@@ -84,7 +91,7 @@ struct Geo {
   static constexpr int kSmemBytes = kOffSlot + 16 + 1024;
   static_assert(kOffTaken % 16 == 0, "alignment");
   static_assert(kSmemBytes <= 232448, "shared memory");
-  static_assert(2 * kTile * kDim * 4 <= kStages * 2 * kOperand, "a part's outputs lie in the ring");
+  static_assert(2 * kTile * kDim * 4 <= kStages * 2 * kKeyOperand, "a part's outputs lie in the ring");
 };
 constexpr int kThreads = 384;                  // two softmax warpgroups; copies, MMAs, two that check offsets
 // Registers: launched with 168 a thread (384 x 168 = 64512); the softmax holds a
@@ -95,7 +102,7 @@ static_assert(256 * kSoftRegs + 128 * kOtherRegs <= 384 * 168, "registers");
 constexpr int kSoftWarps = 8;
 constexpr int kItemReaders = kSoftWarps + 2;   // and the MMA warps
 constexpr int kMaxParts = 8;                   // CTAs of a cluster that share an item's keys
-constexpr int kColS = 0, kColO = 256, kTmemCols = 512;
+constexpr int kColS = 0, kTmemCols = 512;
 constexpr float kRaiseLog2 = 8.0f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -153,6 +160,7 @@ __device__ __forceinline__ bool falling_offsets(const GqaPrefillLaunch& p, int t
 
 // Item i of the grid: head groups one after another, in a group the slots, a
 // slot's heads next to each other.
+template <int kKeys>
 __device__ __forceinline__ Item item_of(const GqaPrefillLaunch& p, int i) {
   const int block = 2 * p.tile_q;
   const int group = i / (p.slots * p.head_group), first = group * p.head_group;
@@ -183,7 +191,7 @@ __device__ __forceinline__ Item item_of(const GqaPrefillLaunch& p, int i) {
   auto tiles_from = [&](int first) {
     if (!it.work || first >= it.qlen) return 0;
     const int lim = key_limit(min(first + p.tile_q, it.qlen) - 1, it.qlen, it.klen, p.causal);
-    return (min(lim, it.klen) + kTile - 1) / kTile;
+    return (min(lim, it.klen) + kKeys - 1) / kKeys;
   };
   it.nt0 = tiles_from(it.row0);
   it.nt1 = tiles_from(it.row0 + p.tile_q);
@@ -192,12 +200,13 @@ __device__ __forceinline__ Item item_of(const GqaPrefillLaunch& p, int i) {
 
 // Part `rank` of `parts` of an item's key tiles, as an item of its own (keys and
 // limits count from the part's first).
+template <int kKeys>
 __device__ __forceinline__ void keep_part(Item& it, int rank, int parts) {
   const int nt = max(it.nt0, it.nt1), lo = nt * rank / parts, hi = nt * (rank + 1) / parts;
   it.nt0 = min(max(it.nt0 - lo, 0), hi - lo);
   it.nt1 = min(max(it.nt1 - lo, 0), hi - lo);
-  it.k0 += lo * kTile;
-  it.klen -= lo * kTile;
+  it.k0 += lo * kKeys;
+  it.klen -= lo * kKeys;
 }
 
 // Joins the parts of an item whose keys the kParts CTAs of a cluster shared.
@@ -279,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                        const __grid_constant__ CUtensorMap tmap_k,
                        const __grid_constant__ CUtensorMap tmap_v, const GqaPrefillLaunch p) {
   using T = Geo<kDim>;
-  constexpr int kStages = T::kStages;
+  constexpr int kStages = T::kStages, kKeys = T::kKeys;
   extern __shared__ uint8_t smem_raw[];
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const float ninf = __int_as_float(0xff800000);
@@ -297,15 +306,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #define V_EMPTY(j) (bar0 + 96u + 8u * ((j) % kStages))
 #define STAGE_PARITY(j) (((j) / kStages) & 1)
 #define PARITY(j) (((j) >> 1) & 1)
-// Of query tile q: q landed / read by its last Q K^T, scores, probabilities,
-// output of the item complete.
+// Of query tile q: q landed / read by its last Q K^T; of its c-th key tile: scores,
+// probabilities, P V done (kBufs 2: one may come before the last has been waited for).
 #define Q_FULL(q) (bar0 + 128u + 8u * (q))
 #define Q_EMPTY(q) (bar0 + 144u + 8u * (q))
-#define S_FULL(q) (bar0 + 160u + 8u * (q))
-#define O_FULL(q) (bar0 + 176u + 8u * (q))
-#define P_FULL(q) (bar0 + 192u + 8u * (q))
-#define DRAIN(q) (bar0 + 256u + 8u * (q))
-#define TAKEN (bar0 + 216u)
+#define S_FULL(q, c) (bar0 + 160u + 16u * (q) + 8u * ((c) % T::kBufs))
+#define PV_DONE(q, c) (bar0 + 256u + 16u * (q) + 8u * ((c) % T::kBufs))
+#define P_FULL(q, c) (bar0 + 192u + 16u * (q) + 8u * ((c) % T::kBufs))
+#define UNIT_PARITY(c) (((c) / T::kBufs) & 1)
+#define DRAIN(q) (bar0 + 288u + 8u * (q))
+#define TAKEN (bar0 + 304u)
 // Item k's record written / no longer needed by any role.
 #define ITEM_FULL(k) (bar0 + 224u + 8u * ((k) & 1))
 #define ITEM_EMPTY(k) (bar0 + 240u + 8u * ((k) & 1))
@@ -324,9 +334,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(Q_EMPTY(q), 1);
       mbar_init(ITEM_FULL(q), 1);
       mbar_init(ITEM_EMPTY(q), kItemReaders);
-      mbar_init(S_FULL(q), 1);
-      mbar_init(P_FULL(q), kTile);
-      mbar_init(O_FULL(q), 1);
+      for (int c = 0; c < T::kBufs; ++c) {
+        mbar_init(S_FULL(q, c), 1);
+        mbar_init(P_FULL(q, c), kTile);
+        mbar_init(PV_DONE(q, c), 1);
+      }
     }
     mbar_init(DRAIN(0), 1);
     mbar_init(DRAIN(1), 1);
@@ -359,8 +371,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         int uses0 = 0, uses1 = 0;                           // items that had each query tile
         const uint32_t q_bytes = T::kAtoms * p.tile_q * p.group * 128;
-        Item it = item_of(p, static_cast<int>(blockIdx.x) / p.parts);
-        if (p.parts > 1) keep_part(it, static_cast<int>(blockIdx.x) % p.parts, p.parts);
+        Item it = item_of<kKeys>(p, static_cast<int>(blockIdx.x) / p.parts);
+        if (p.parts > 1) keep_part<kKeys>(it, static_cast<int>(blockIdx.x) % p.parts, p.parts);
         int base = 0, k = 0, asked = 0;
         bool more = true;
         while (ok) {
@@ -376,10 +388,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const int ntmax = max(it.nt0, it.nt1);
           for (int j = 0; ok && j < ntmax; ++j) {
-            const int t = base + j, row = it.k0 + j * kTile;
-            const uint32_t dst = sbase + T::kOffRing + (t % kStages) * 2 * T::kOperand;
+            const int t = base + j, row = it.k0 + j * kKeys;
+            const uint32_t dst = sbase + T::kOffRing + (t % kStages) * 2 * T::kKeyOperand;
             if (t >= kStages && !(ok = mbar_wait(K_EMPTY(t), STAGE_PARITY(t - kStages)))) break;
-            mbar_expect_tx(K_FULL(t), T::kOperand);
+            mbar_expect_tx(K_FULL(t), T::kKeyOperand);
             tma_load_4d(dst, &tmap_k, 0, row, 0, it.head, K_FULL(t));
             if (j == 0) {
               for (int g = 0; ok && g < 2; ++g) {
@@ -394,8 +406,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!ok) break;
             }
             if (t >= kStages && !(ok = mbar_wait(V_EMPTY(t), STAGE_PARITY(t - kStages)))) break;
-            mbar_expect_tx(V_FULL(t), T::kOperand);
-            tma_load_4d(dst + T::kOperand, &tmap_v, 0, row, 0, it.head, V_FULL(t));
+            mbar_expect_tx(V_FULL(t), T::kKeyOperand);
+            tma_load_4d(dst + T::kKeyOperand, &tmap_v, 0, row, 0, it.head, V_FULL(t));
           }
           base += ntmax;
           // The next item, once this one's copies are under way (not earlier:
@@ -411,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t x, y, z;
           more = taken_cta(sbase + T::kOffTaken, x, y, z);
           fence_proxy_async_smem();      // read before the next answer is written there
-          if (more) it = item_of(p, x);
+          if (more) it = item_of<kKeys>(p, x);
         }
         if (!ok) raise_error(kErrTimeout);
         // No copy is in flight when the CTA ends.  (After a wait that ran out, the
@@ -431,12 +443,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       // once, whatever the other is at.
       const int q = warp - 9;
       const uint32_t el = elect_one() ? 1u : 0u;
-      constexpr uint32_t idesc_qk = make_idesc(1, 1, 0, 0, kTile, kTile);
+      constexpr uint32_t idesc_qk = make_idesc(1, 1, 0, 0, kKeys, kTile);
       constexpr uint32_t idesc_pv = make_idesc(1, 1, 0, 1, kDim, kTile);
       const uint64_t dq = smem_desc_sw128(sbase + T::kOffQ + q * T::kOperand, 16, 1024);
       const uint64_t dk0 = smem_desc_sw128(sbase + T::kOffRing, 16, 1024);
-      const uint64_t dv0 = smem_desc_sw128(sbase + T::kOffRing + T::kOperand, kAtomBytes, 1024);      // MN-major
-      const uint32_t ts = tmem + kColS + kTile * q, to = tmem + kColO + kDim * q;
+      const uint64_t dv0 = smem_desc_sw128(sbase + T::kOffRing + T::kKeyOperand, T::kKeyAtom, 1024);      // MN-major
+      const uint32_t ts0 = tmem + kColS + T::kBufs * kKeys * q, to = tmem + T::kColO + kDim * q;
       bool ok = true;
       // A phase is tested before the last MMAs of the step before go out, so that
       // the test's latency hides behind them; `want` waits only if it was not
@@ -449,11 +461,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Descriptor offset of tile t's stage, broadcast: the compiler then knows it to
       // be the same in every lane and keeps it in uniform registers.
       auto stage_of = [&](int t) -> uint64_t {
-        return static_cast<uint32_t>(__shfl_sync(0xffffffffu, ((t % kStages) * 2 * T::kOperand) >> 4, 0));
+        return static_cast<uint32_t>(__shfl_sync(0xffffffffu, ((t % kStages) * 2 * T::kKeyOperand) >> 4, 0));
       };
       auto commit = [&](uint32_t bar) {
         if (el) tc_commit(bar);
         __syncwarp();
+      };
+      // Column of the scores of this query tile's c-th key tile.
+      auto col_s = [&](int c) -> uint32_t {
+        if (T::kBufs == 1) return ts0;
+        return ts0 + static_cast<uint32_t>(__shfl_sync(0xffffffffu, (c % T::kBufs) * kKeys, 0));
+      };
+      // Q K^T over tile t, this query tile's c-th (the item's last: q is free then).
+      auto qk = [&](int t, int c, bool last) {
+        const uint64_t dk = dk0 + stage_of(t);
+        const uint32_t ts = col_s(c);
+        want(K_FULL(t), STAGE_PARITY(t));
+        tc_fence_after();
+        if (!ok) return;
+#pragma unroll
+        for (int a = 0; a < T::kAtoms; ++a)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_f16_ss_uni(ts, dq + static_cast<uint64_t>((a * kAtomBytes + 32 * k) >> 4),
+                           dk + static_cast<uint64_t>((a * T::kKeyAtom + 32 * k) >> 4), idesc_qk, (a > 0 || k > 0) ? 1u : 0u, el);
+        commit(S_FULL(q, c));
+        commit(K_EMPTY(t));
+        if (last) commit(Q_EMPTY(q));
       };
       int t = 0, c = 0, uses = 0;      // key tiles so far: all, and of this query tile; items that had it
       for (int item = 0; ok; ++item) {
@@ -463,35 +497,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int nt1 = __shfl_sync(0xffffffffu, record(item).nt1, 0), ntmax = max(nt0, nt1), nt = q == 0 ? nt0 : nt1;
         if (lane == 0) mbar_arrive(ITEM_EMPTY(item));
         if (!work) break;
-        if (nt > 0) ok = warp_wait(Q_FULL(q), uses++ & 1);
+        if (nt > 0) {
+          ok = warp_wait(Q_FULL(q), uses++ & 1);
+          if (T::kBufs == 2) qk(t, c, nt == 1);
+        }
         for (int j = 0; ok && j < nt; ++j, ++t, ++c) {
-          const uint64_t stage = stage_of(t), dk = dk0 + stage, dv = dv0 + stage;
-          want(K_FULL(t), STAGE_PARITY(t));
+          // (kBufs 2: P V of the tile before has gone out, so the buffer that its scores
+          // were in can be written.)
+          if (T::kBufs == 1) qk(t, c, j == nt - 1);
+          else if (j + 1 < nt) qk(t + 1, c + 1, j + 1 == nt - 1);
+          const uint64_t dv = dv0 + stage_of(t);
+          const uint32_t ts = col_s(c);
+          ok = ok && warp_wait(V_FULL(t), STAGE_PARITY(t)) && warp_wait(P_FULL(q, c), UNIT_PARITY(c));
           tc_fence_after();
           if (!ok) break;
 #pragma unroll
-          for (int a = 0; a < T::kAtoms; ++a)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_f16_ss_uni(ts, dq + static_cast<uint64_t>((a * kAtomBytes + 32 * k) >> 4),
-                             dk + static_cast<uint64_t>((a * kAtomBytes + 32 * k) >> 4), idesc_qk, (a > 0 || k > 0) ? 1u : 0u,
-                             el);
-          commit(S_FULL(q));
-          commit(K_EMPTY(t));
-          if (j == nt - 1) commit(Q_EMPTY(q));
-          ok = warp_wait(V_FULL(t), STAGE_PARITY(t)) && warp_wait(P_FULL(q), c & 1);
-          tc_fence_after();
-          if (!ok) break;
-#pragma unroll
-          for (int k = 0; k < kTile / 16; ++k) {
-            if (k == kTile / 32) done = warp_test(K_FULL(t + 1), STAGE_PARITY(t + 1));
+          for (int k = 0; k < kKeys / 16; ++k) {
+            if (k == kKeys / 32) done = warp_test(K_FULL(t + T::kBufs), STAGE_PARITY(t + T::kBufs));
             mma_f16_ts_uni(to, ts + 8 * k, dv + static_cast<uint64_t>((2048 * k) >> 4), idesc_pv, (j > 0 || k > 0) ? 1u : 0u, el);
           }
+          if (T::kBufs == 2 || j == nt - 1) commit(PV_DONE(q, T::kBufs == 2 ? c : 0));
           commit(V_EMPTY(t));
-          if (j == nt - 1) commit(O_FULL(q));
         }
         // Tiles that the other query tile alone reads.  (Each in its time: a phase of
         // their barriers takes both warps' arrivals.)
+        if (T::kBufs == 2) done = false;
         for (int j = nt; ok && j < ntmax; ++j, ++t) {
           want(K_FULL(t), STAGE_PARITY(t));
           if (lane == 0) mbar_arrive(K_EMPTY(t));
@@ -517,14 +547,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------------------------------------- softmax and epilogue
     setmaxnreg_inc<kSoftRegs>();
     const int q = warp >> 2, w4 = warp & 3;
-    const uint32_t tS = tmem + (static_cast<uint32_t>(w4 * 32) << 16) + kColS + kTile * q;
-    const uint32_t tO = tmem + (static_cast<uint32_t>(w4 * 32) << 16) + kColO + kDim * q;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(w4 * 32) << 16);
+    const uint32_t tO = lanes + T::kColO + kDim * q;
     const float sc = p.sm_scale * kLog2e;
     // This thread's row: head my_head of the group, of the tile's query my_query.
     const int row_t = w4 * 32 + lane, my_query = row_t / p.group, my_head = row_t - my_query * p.group;
     const bool used = my_query < p.tile_q;
     bool ok = true;
-    int phase = 0;             // parities: bit 0 of the scores, bit 1 of the outputs
+    int c = 0, outs = 0;       // key tiles so far, items that had some
     int n = 0;                 // key tiles of the item
     float mrun = ninf, lrun = 0.f;
     // (Ahead of the items: the offsets have been looked through before the first
@@ -547,34 +577,40 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       mrun = ninf;
       lrun = 0.f;
-      for (int j = 0; j < n; ++j, phase ^= 1, lim -= kTile, vlive -= kTile) {
-        if (ok && !mbar_wait(S_FULL(q), phase & 1)) ok = false;
+      for (int j = 0; j < n; ++j, ++c, lim -= kKeys, vlive -= kKeys) {
+        const uint32_t tS = lanes + kColS + kKeys * (T::kBufs * q + c % T::kBufs);
+        if (ok && !mbar_wait(S_FULL(q, c), UNIT_PARITY(c))) ok = false;
         tc_fence_after();
-        uint32_t s[128];
-        tmem_ld128(tS, s);
+        uint32_t s[kKeys];
+        if constexpr (kKeys == 128) tmem_ld128(tS, s);
+        else tmem_ld96(tS, s);
         const int seen = lim;
         float mx[4] = {ninf, ninf, ninf, ninf};
-        if (__any_sync(0xffffffffu, seen < kTile)) {
+        if (__any_sync(0xffffffffu, seen < kKeys)) {
   #pragma unroll
-          for (int e = 0; e < kTile; ++e)
+          for (int e = 0; e < kKeys; ++e)
             if (e >= seen) s[e] = __float_as_uint(ninf);
         }
   #pragma unroll
-        for (int e = 0; e < kTile; e += 2)
+        for (int e = 0; e < kKeys; e += 2)
           mx[(e >> 1) & 3] = max3(mx[(e >> 1) & 3], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
         const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
         const bool raise = tmax > mrun + kRaiseLog2;
         const bool rescale = raise && mrun > ninf;
         if (__any_sync(0xffffffffu, rescale)) {
-          // (P V of the tile before is done: it was issued before this Q K^T.)
+          // (kBufs 1: P V of the tile before is done: it was issued before this Q K^T.)
+          if (T::kBufs == 2) {
+            if (ok && !mbar_wait(PV_DONE(q, c - 1), UNIT_PARITY(c - 1))) ok = false;
+            tc_fence_after();
+          }
           const float f = rescale ? ex2(mrun - tmax) : 1.f;
   #pragma unroll 1
-          for (int c = 0; c < kDim / 32; ++c) {
+          for (int d = 0; d < kDim; d += 32) {
             uint32_t o[32];
-            tmem_ld32(tO + 32 * c, o);
+            tmem_ld32(tO + d, o);
   #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tmem_st32(tO + 32 * c, o);
+            tmem_st32(tO + d, o);
           }
           lrun *= f;
         }
@@ -582,13 +618,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float mref = mrun > ninf ? mrun : 0.f;
         // Rows of V behind the request's end are cleared, by both query tiles (either's
         // P V may come first).
-        if (vlive < kTile) {
+        if (vlive < kKeys) {
           const int t = record(item).base + j;
           if (ok && !mbar_wait(V_FULL(t), STAGE_PARITY(t))) ok = false;
   #pragma unroll 1
           for (int a = 0; a < T::kAtoms; ++a) {
-            uint4* v = reinterpret_cast<uint4*>(smem + T::kOffRing + ((t % kStages) * 2 + 1) * T::kOperand + a * kAtomBytes);
-            for (int e = (threadIdx.x & 127) + vlive * 8; e < kAtomBytes / 16; e += 128)
+            uint4* v = reinterpret_cast<uint4*>(smem + T::kOffRing + ((t % kStages) * 2 + 1) * T::kKeyOperand + a * T::kKeyAtom);
+            for (int e = (threadIdx.x & 127) + vlive * 8; e < T::kKeyAtom / 16; e += 128)
               v[e] = make_uint4(0u, 0u, 0u, 0u);
           }
           fence_proxy_async_smem();
@@ -596,28 +632,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         // P V over the first 64 keys starts while the others' exponentials run.
         float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
   #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int g = 0; g < kKeys / 32; ++g) {
           uint32_t pk[16];
   #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const float2 x = fma2(make_float2(__uint_as_float(s[32 * c + 2 * e]),
-                                              __uint_as_float(s[32 * c + 2 * e + 1])),
+            const float2 x = fma2(make_float2(__uint_as_float(s[32 * g + 2 * e]),
+                                              __uint_as_float(s[32 * g + 2 * e + 1])),
                                   make_float2(sc, sc), make_float2(-mref, -mref));
             const float2 w = make_float2(ex2(x.x), ex2(x.y));
             ls[e & 1] = add2(ls[e & 1], w);
             pk[e] = pack_bf16x2(w.x, w.y);
           }
-          tmem_st16_async(tS + 16 * c, pk);
+          tmem_st16_async(tS + 16 * g, pk);
         }
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(P_FULL(q));
+        mbar_arrive(P_FULL(q, c));
         lrun += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
       }
       if (n > 0) {
-        if (ok && !mbar_wait(O_FULL(q), (phase >> 1) & 1)) ok = false;
+        if (ok && !(T::kBufs == 2 ? mbar_wait(PV_DONE(q, c - 1), UNIT_PARITY(c - 1)) : mbar_wait(PV_DONE(q, 0), outs & 1))) ok = false;
         tc_fence_after();
-        phase ^= 2;
+        ++outs;
       }
       const Item& it = record(item);
       if (p.parts == 1 && !refused && it.row0 + q * p.tile_q < it.qlen) {
@@ -704,7 +740,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #undef Q_FULL
 #undef S_FULL
 #undef P_FULL
-#undef O_FULL
+#undef PV_DONE
+#undef UNIT_PARITY
 #undef Q_EMPTY
 #undef TAKEN
 #undef ITEM_FULL
@@ -754,10 +791,10 @@ struct Host {
     const double queries = static_cast<double>(a.total_q) / a.batch;
     const double blocks = std::max(1.0, std::ceil(queries / (2 * a.tile_q)));      // of a request
     const double items = blocks * a.batch * a.kv_heads;
-    const double keys = static_cast<double>(a.total_k) / a.batch / kTile;    // key tiles of a late item ...
+    const double keys = static_cast<double>(a.total_k) / a.batch / Geo<kDim>::kKeys;    // key tiles of a late item ...
     if (keys <= 4) return 1;                                                 // two parts cost 8 at least
     const double spread =                                                    // ... and how many fewer an early one has
-        a.causal ? std::min(keys, queries * (blocks - 1) / blocks / kTile) : 0;
+        a.causal ? std::min(keys, queries * (blocks - 1) / blocks / Geo<kDim>::kKeys) : 0;
     int best = 1;
     double best_cost = 0;
     for (int c = 1; c <= kMaxParts; ++c) {
@@ -784,7 +821,7 @@ struct Host {
     // (Without a key q stands in for k and v, whose strides say nothing then.)
     const uint64_t ld_k = a.total_k > 0 ? a.ld_k : H * kDim, ld_v = a.total_k > 0 ? a.ld_v : H * kDim;
     const uint64_t kdims[4] = {64, Tk, T::kAtoms, K}, kstr[3] = {ld_k * 2, 128, kDim * 2}, vstr[3] = {ld_v * 2, 128, kDim * 2};
-    const uint32_t kbox[4] = {64, kTile, T::kAtoms, 1};
+    const uint32_t kbox[4] = {64, T::kKeys, T::kAtoms, 1};
     CUtensorMap tq, tk, tv;
     if (!encode_tmap_nd(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, 5, qdims, qstr, qbox, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !encode_tmap_nd(&tk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.k, 4, kdims, kstr, kbox, CU_TENSOR_MAP_SWIZZLE_128B) ||

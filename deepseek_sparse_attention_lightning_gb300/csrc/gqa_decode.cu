@@ -93,6 +93,9 @@ constexpr int kColS = 0, kColP = 256, kColO = 384, kTmemCols = 512;
 constexpr int kStage = kSoftThreads * 32 * 4;  // 32 columns of a copy's rows, fp32
 constexpr float kRaiseLog2 = 8.0f, kRaiseParts = 2.0f, kShiftFp8 = 7.0f, kShiftParts = 13.0f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+// Smaller value scales count as this one (a row of values below 2^-71, to which dsa_kv_write_fp8
+// may give a subnormal scale): P / scale is 2^95 at most, and 2^31 of them stay in fp32's range.
+constexpr float kLeastScale = 0x1p-80f;
 
 // kParts: FP8 rows whose P V runs on codes, P in parts; kDequant: whose codes become
 // fp16 first.
@@ -619,7 +622,7 @@ __global__ void __launch_bounds__(!kFp8 ? kThreads : kNarrow ? kThreadsParts : k
           const float* scales = reinterpret_cast<const float*>(smem + T::kOffScale) + (it % (T::kRing / 2)) * 2 * kKeys;
           float* par = reinterpret_cast<float*>(smem + T::kOffParam) + (it & 1) * 3 * kKeys;
           const bool seen = tid < vlive && ((ok2 >> (tid / kPage)) & 1u);
-          const float vs = seen ? scales[kKeys + tid] : 1.f;
+          const float vs = seen ? fmaxf(scales[kKeys + tid], kLeastScale) : 1.f;
           par[tid] = seen ? scales[tid] : 0.f;
           par[kKeys + tid] = log2f(vs);
           par[2 * kKeys + tid] = 1.f / vs;

@@ -536,8 +536,8 @@ dsa_status dsa_kv_write(int32_t tokens, int32_t kv_heads, int32_t dim, const uin
 
 /*
  * The same into FP8 caches: for a token and head scale = amax / 448 over its D
- * values (a row of zeros: 1), codes = E4M3(x / scale), to nearest even, in fp32;
- * dim 128.  k8, v8 [dev] [num_pages, K, 64, D], 16-byte aligned; k_scale, v_scale
+ * values (finite ones; a row of zeros: 1), codes = E4M3(x / scale), to nearest even,
+ * in fp32; dim 128.  k8, v8 [dev] [num_pages, K, 64, D], 16-byte aligned; k_scale, v_scale
  * [dev] float [num_pages, K, 64] (all written).
  */
 dsa_status dsa_kv_write_fp8(int32_t tokens, int32_t kv_heads, int32_t dim, const uint16_t* k,
@@ -575,8 +575,10 @@ dsa_status dsa_gqa_decode(const dsa_decode_desc* desc, int32_t kv_heads, int32_t
 
 /*
  * dsa_gqa_decode over FP8 caches (dsa_kv_write_fp8's; dim 128): the attention over
- * code x scale.  Scales of tokens that a query sees have to be positive, finite and
- * at least 2^-100; k_scale, v_scale 16-B aligned.  (The query enters as the sum of
+ * code x scale.  Scales of tokens that a query sees have to be 0 or more and finite;
+ * values' scales below 2^-80 count as 2^-80 (their values are below 2^-71 then), and
+ * a request's others lie within 2^100 of its smallest.  k_scale, v_scale 16-B
+ * aligned.  (The query enters as the sum of
  * two E4M3 parts, exact but for values below 2^-9 of the largest of its row, which
  * are off by 2^-17 of that; codes are multiplied as they are, probabilities times
  * the value's scale rounded to fp16.)

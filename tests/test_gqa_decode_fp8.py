@@ -196,6 +196,38 @@ def test_a_peak_and_a_long_tail(L):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("H,K", [(8, 2), (48, 2)])
+def test_tiny_value_scales(L, H, K):
+    """Value scales below 2^-80, down to 0, count as 2^-80, among others and alone, over many tokens: sums of weights
+    over them stay finite."""
+    c = _case([500, 300, 70000], 1, H, K, seed=4, spread=2)
+    for r, scales in enumerate(([0.0, 2.0 ** -130, 2.0 ** -90, 2.0 ** -8], [2.0 ** -140, 2.0 ** -79], [2.0 ** -100])):
+        at = c["table"][r, :-(-c["lens"][r] // 64)].long()
+        rows = c["vs"][at].transpose(1, 2).reshape(-1, K)
+        rows[:c["lens"][r]] = torch.tensor(scales, device="cuda")[torch.arange(c["lens"][r], device="cuda") % len(scales)][:, None]
+        c["vs"][at] = rows.view(len(at), 64, K).transpose(1, 2)
+    out, lse = _run(c)
+    assert api.dsa_get_device_error() == 0
+    _check(dict(c, vs=c["vs"].clamp(min=2.0 ** -80)), out, lse, heads=(0, H - 1))
+
+
+@pytest.mark.gpu
+def test_rows_of_tiny_values_as_written(L):
+    """What dsa_kv_write_fp8 makes of rows down to the smallest bf16 values can be read."""
+    n, K, H = 130, 2, 8
+    x = [torch.randn(n, K, D, device="cuda", generator=torch.Generator(device="cuda").manual_seed(i)) for i in (5, 6)]
+    x[1] *= torch.tensor([2.0 ** -120, 2.0 ** -70, 1.0, 0.0, 2.0 ** -131], device="cuda")[torch.arange(n, device="cuda") % 5][:, None, None]
+    k, v = (t.to(torch.bfloat16) for t in x)
+    c = _case([n], 1, H, K, seed=7)
+    table = c["table"][0].long()
+    slots = (table[torch.arange(n, device="cuda") // 64] * 64 + torch.arange(n, device="cuda") % 64).to(torch.int32)
+    api.dsa_kv_write_fp8(k, v, slots, c["k"], c["ks"], c["v"], c["vs"])
+    out, lse = _run(c)
+    assert api.dsa_get_device_error() == 0
+    _check(dict(c, vs=c["vs"].clamp(min=2.0 ** -80)), out, lse)
+
+
+@pytest.mark.gpu
 def test_bad_pages_streams_and_graph(L):
     c = _case([700, 300, 64, 500], 1, 8, 2, seed=3, max_pages=11)
     good, e_good = _run(c)

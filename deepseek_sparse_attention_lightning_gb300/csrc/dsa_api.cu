@@ -464,7 +464,7 @@ dsa_status dsa_kv_write_fp8(int32_t tokens, int32_t kv_heads, int32_t dim, const
 
 size_t dsa_gqa_decode_workspace_bytes(const dsa_decode_desc* d, int32_t kv_heads, int32_t dim) {
   if (check_grouped(d, kv_heads, dim) != DSA_OK) return 0;
-  return dsa::gqa_decode_workspace(d->q_per_req, d->num_heads, kv_heads, dim);
+  return dsa::gqa_decode_workspace(dim);
 }
 
 dsa_status dsa_gqa_decode(const dsa_decode_desc* d, int32_t kv_heads, int32_t dim,

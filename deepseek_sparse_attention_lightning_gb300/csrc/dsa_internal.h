@@ -214,7 +214,7 @@ cudaError_t launch_kv_write(const KvWriteLaunch& a, cudaStream_t s);
 long long gqa_prefill_items(const GqaPrefillLaunch& a);
 cudaError_t launch_gqa_prefill(GqaPrefillLaunch a, cudaStream_t s);
 // Paged attention with grouped heads: its workspace (no kernel), and its launch.
-size_t gqa_decode_workspace(int nq, int heads, int kv_heads, int dim);
+size_t gqa_decode_workspace(int dim);
 cudaError_t launch_gqa_decode(GqaDecodeLaunch a, void* ws, cudaStream_t s);
 cudaError_t launch_merge(int rows, int splits, const float* mid_o, const float* mid_lse,
                          float* out, float* out_lse, cudaStream_t s, bool pdl = false);

@@ -15,19 +15,29 @@
 // masked.  (Rows 128 / G * G and up, where G is no divisor, are computed and not
 // used.)
 //
-// Bound by the matrix pipe where D = 128 (512 flop a visible pair), and by the
-// softmax's instructions where D = 64.  One CTA = two query tiles over the same
-// keys: while one tile's scores are in the softmax, the matrix pipe works on the
-// other's.
+// D = 128 is bound by the matrix pipe (512 flop a visible pair): 4096 queries over
+// 4096 keys, 64 heads on 8, take 317 us, 1.73 PFLOP/s, 91 % of the measured matrix
+// rate; a prompt of 8192 with a causal mask 640 us (1.72).  D = 64 is bound by the
+// softmax, which has as many exponentials for half the products: 263 us for the
+// first (1.05 PFLOP/s), the matrix pipe and the special function units 44 % busy
+// each.  (Without the exponentials and the maximum, whose results it could not do
+// without, it would take 195.)
 //
-// Tensor memory (512 columns): S of the two tiles (128 each, fp32), O of the two
-// (D each).  P (bf16, 64 columns) overwrites the S it came from and is the A
-// operand of P V, so it never passes through shared memory.
-// Shared memory: q of both tiles, and a ring of key tiles (128 keys), K and V of
-// each in atoms of 64 dims (128B swizzle).
+// One CTA = two query tiles over the same keys: while one tile's scores are in the
+// softmax, the matrix pipe works on the other's.
 //
-// MMA order: QK0(j), PV1(j-1), QK1(j), PV0(j), QK0(j+1), ...: a tile's softmax
-// has the other tile's P V and Q K^T to hide in.
+// Tensor memory (512 columns): S (fp32) of the two tiles, one buffer of 128 keys each
+// (D = 128), two of 96 (D = 64: Q K^T of the next key tile is done while this one's
+// is in the softmax; 16 ragged prompts, 32 heads: one buffer of 128 158 us, two of 96
+// 137; three query tiles with one buffer of 96 each, 141), and O of the two.  P (bf16)
+// overwrites the S it came from and is the A operand of P V, so it never passes
+// through shared memory.
+// Shared memory: q of both tiles, and a ring of key tiles, K and V of each in atoms of
+// 64 dims (128B swizzle).
+//
+// Each query tile has an MMA warp of its own, which answers that tile's probabilities
+// at once, whatever the other is at.  (One for both in a fixed order: 321 us for the
+// 4096 by 4096 above, instead of 317.)
 //
 // A grid of one CTA for each block of two query tiles of a key head (and at most
 // one more a request), late queries (most keys) first, heads that fit into L2
@@ -42,8 +52,9 @@
 // have one item each.  choose_parts has the rule and figures.
 //
 // Warps 0-3 and 4-7: softmax and epilogue of query tile 0 and 1, a row a thread.
-// Warp 8: copies.  Warp 9: MMAs, issued from uniform control flow.  Warps 10 and
-// 11: the query offsets' order, which no output is stored before.  The running
+// Warp 8: copies.  Warps 9 and 10: MMAs of query tile 0 and 1, issued from uniform
+// control flow.  Warp 11: the query offsets' order, which no output is stored before.
+// (16 softmax warps, half a row a thread, D = 64: 317 us instead of 270.)  The running
 // maximum is raised lazily (by 2^8 at least), by the row's own thread, which then
 // rescales its row of O.  P is rounded to bf16 for the matrix pipe (it takes
 // operands of one type, and values are bf16), its sum kept unrounded in fp32.
@@ -93,7 +104,7 @@ struct Geo {
   static_assert(kSmemBytes <= 232448, "shared memory");
   static_assert(2 * kTile * kDim * 4 <= kStages * 2 * kKeyOperand, "a part's outputs lie in the ring");
 };
-constexpr int kThreads = 384;                  // two softmax warpgroups; copies, MMAs, two that check offsets
+constexpr int kThreads = 384;                  // two softmax warpgroups; copies, MMAs, the offsets
 // Registers: launched with 168 a thread (384 x 168 = 64512); the softmax holds a
 // row of 128 scores and takes 216, the third warpgroup keeps 72 (256 x 216 +
 // 128 x 72 = 64512).
@@ -587,11 +598,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int seen = lim;
         float mx[4] = {ninf, ninf, ninf, ninf};
         if (__any_sync(0xffffffffu, seen < kKeys)) {
-  #pragma unroll
+#pragma unroll
           for (int e = 0; e < kKeys; ++e)
             if (e >= seen) s[e] = __float_as_uint(ninf);
         }
-  #pragma unroll
+#pragma unroll
         for (int e = 0; e < kKeys; e += 2)
           mx[(e >> 1) & 3] = max3(mx[(e >> 1) & 3], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
         const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
@@ -604,11 +615,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
           }
           const float f = rescale ? ex2(mrun - tmax) : 1.f;
-  #pragma unroll 1
+#pragma unroll 1
           for (int d = 0; d < kDim; d += 32) {
             uint32_t o[32];
             tmem_ld32(tO + d, o);
-  #pragma unroll
+#pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
             tmem_st32(tO + d, o);
           }
@@ -621,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (vlive < kKeys) {
           const int t = record(item).base + j;
           if (ok && !mbar_wait(V_FULL(t), STAGE_PARITY(t))) ok = false;
-  #pragma unroll 1
+#pragma unroll 1
           for (int a = 0; a < T::kAtoms; ++a) {
             uint4* v = reinterpret_cast<uint4*>(smem + T::kOffRing + ((t % kStages) * 2 + 1) * T::kKeyOperand + a * T::kKeyAtom);
             for (int e = (threadIdx.x & 127) + vlive * 8; e < T::kKeyAtom / 16; e += 128)
@@ -629,12 +640,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           fence_proxy_async_smem();
         }
-        // P V over the first 64 keys starts while the others' exponentials run.
         float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-  #pragma unroll
+#pragma unroll
         for (int g = 0; g < kKeys / 32; ++g) {
           uint32_t pk[16];
-  #pragma unroll
+#pragma unroll
           for (int e = 0; e < 16; ++e) {
             const float2 x = fma2(make_float2(__uint_as_float(s[32 * g + 2 * e]),
                                               __uint_as_float(s[32 * g + 2 * e + 1])),
@@ -662,17 +672,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float inv = any ? 1.f / lrun : 0.f;
         const long long at = static_cast<long long>(it.q0 + it.row0 + query) * p.heads + it.head * p.group + my_head;
         uint4* dst = reinterpret_cast<uint4*>(p.out + at * kDim);
-  #pragma unroll 1
+#pragma unroll 1
         for (int c = 0; c < kDim / 32; ++c) {
           uint32_t o[32];
           if (n > 0) tmem_ld32(tO + 32 * c, o);
           if (!live) continue;
           uint32_t w[2][8];
-  #pragma unroll
+#pragma unroll
           for (int e = 0; e < 16; ++e)
             w[e >> 3][e & 7] =
                 any ? pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv) : 0u;
-  #pragma unroll
+#pragma unroll
           for (int e = 0; e < 2; ++e) {
             if (p.out_wide) {
               st_global_32(dst + 4 * c + 2 * e, w[e]);
@@ -786,7 +796,10 @@ struct Host {
   // CTAs that share an item's keys.  Costs in key tiles, from the mean lengths (the
   // lengths themselves are on the device): the late items' tiles, 4 for the start
   // and end of an item of one CTA, 5.5 + 0.3 c with the join of c parts; items that
-  // come in rounds leave SMs idle in the last one.
+  // come in rounds leave SMs idle in the last one.  us for 1 .. 8 parts (chosen *):
+  // a query over 16002 keys, 64 heads on 8, 161 91 65 51 44 38 34 32*; 64 queries, 24
+  // heads, 208 114 83 66 58 50 47 43*; 4 chunks of 512 over 16001 more, 40 heads, 630
+  // 579* 658 655 728 778; 1000 queries over 5000, 32 heads, 62* 77 92.
   static int choose_parts(const GqaPrefillLaunch& a) {
     const double queries = static_cast<double>(a.total_q) / a.batch;
     const double blocks = std::max(1.0, std::ceil(queries / (2 * a.tile_q)));      // of a request
@@ -841,7 +854,8 @@ struct Host {
 // the order late to early over all heads ends with short ones and the SMs end close
 // together; but heads that run together share L2, and each item reads a head's keys
 // from its first.  So as many as have 48 MB of keys and values, in groups of equal
-// size.
+// size.  (16384 queries, 64 heads on 32, causal: 2.61 ms; all heads together 2.84, one
+// at a time 2.63.  32768, 64 heads on 8: 9.94, 10.35, 10.20.)
 int heads_at_once(const GqaPrefillLaunch& a) {
   const double bytes = 48 << 20, head = static_cast<double>(a.total_k) / a.batch * 2 * a.dim * 2;
   const int groups = static_cast<int>(std::ceil(a.kv_heads / std::max(1.0, std::min<double>(a.kv_heads, bytes / (head + 1)))));

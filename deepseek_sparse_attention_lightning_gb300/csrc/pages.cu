@@ -393,7 +393,8 @@ __global__ void __launch_bounds__(kThreads, 1) pages_kernel(const PagesLaunch p)
 // at most; else a cluster of 16, a thread eight slots in a row where there are many
 // (a prompt's are on one page or two; a step's are on a page each, whose entries
 // would be waited for one after another).  us on the device: 128 requests of a token
-// 5; 256 prompts of 1 .. 4096 tokens, for 4 / 8 / 16 CTAs, 42 / 30 / 21.
+// 3.4 (in a cluster of 16: 10.9); 256 prompts of 1 .. 4096 tokens, half a million
+// slots, 16.2 (before the runs of eight, for 4 / 8 / 16 CTAs, 42 / 30 / 21).
 cudaError_t launch_pages(const PagesLaunch& a, cudaStream_t s) {
   if (a.batch <= 256 && a.max_tokens <= 4 * 256)
     return launch_kernel(pages_kernel<256, 1, 1>, dim3(1), dim3(256), 0, s, false, 1, a);

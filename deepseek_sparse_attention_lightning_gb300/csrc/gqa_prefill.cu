@@ -581,7 +581,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Item& it = record(item);
         if (!it.work) break;
         n = q == 0 ? it.nt0 : it.nt1;
-        lim = used ? min(it.klen, key_limit(it.row0 + query, it.qlen, it.klen, p.causal)) : 0;
+        // (A row behind the tile's last query sees what that one does: were it to see
+        // nothing, its warp would mask every tile, 571 us instead of 495 for four chunks of
+        // 500 over 16001 keys in groups of five heads.)
+        const int seer = it.row0 + q * p.tile_q + min(my_query, p.tile_q - 1);
+        lim = min(it.klen, key_limit(seer, it.qlen, it.klen, p.causal));
         // Keys of the request behind the tile's start, where this query tile is
         // the first to read the tile's V.
         vlive = it.klen;

@@ -168,6 +168,7 @@ struct GqaPrefillLaunch {
   int group, tile_q;             // set by launch_gqa_prefill: query heads a key head, queries of a tile
   int out_wide;                  //   out is 32-byte aligned
   int parts;                     //   CTAs (a cluster) that share an item's keys
+  int first_item;                //   of the launch
   int slots, head_group;         //   query blocks of all requests; key heads that run together
   float sm_scale;
 };

@@ -46,10 +46,11 @@
 // the next item while this one's last tiles and output are under way, and the SMs
 // end close together.
 //
-// Few items with many keys (a short chunk over a long prefix, few heads): the CTAs
+// Few items with many keys (a short chunk over a long prefix, few heads; or the last
+// ones of a call, which would leave most SMs idle): the CTAs
 // of a cluster share an item's key tiles, leave their outputs and (maximum, sum)
 // in shared memory, and each joins some of the rows from all of them.  Such CTAs
-// have one item each.  choose_parts has the rule and figures.
+// have one item each.  choose_plan has the rule and figures.
 //
 // Warps 0-3 and 4-7: softmax and epilogue of query tile 0 and 1, a row a thread.
 // Warp 8: copies.  Warps 9 and 10: MMAs of query tile 0 and 1, issued from uniform
@@ -169,10 +170,11 @@ __device__ __forceinline__ bool falling_offsets(const GqaPrefillLaunch& p, int t
   return falls;
 }
 
-// Item i of the grid: head groups one after another, in a group the slots, a
-// slot's heads next to each other.
+// Item i of the call, the launch's first and so many more: head groups one after
+// another, in a group the slots, a slot's heads next to each other.
 template <int kKeys>
-__device__ __forceinline__ Item item_of(const GqaPrefillLaunch& p, int i) {
+__device__ __forceinline__ Item item_of(const GqaPrefillLaunch& p, int from_first) {
+  const int i = p.first_item + from_first;
   const int block = 2 * p.tile_q;
   const int group = i / (p.slots * p.head_group), first = group * p.head_group;
   const int heads = min(p.head_group, p.kv_heads - first), at = i - first * p.slots;
@@ -797,22 +799,39 @@ struct Host {
     return n;
   }
 
-  // CTAs that share an item's keys.  Costs in key tiles, from the mean lengths (the
-  // lengths themselves are on the device): the late items' tiles, 4 for the start
-  // and end of an item of one CTA, 5.5 + 0.3 c with the join of c parts; items that
-  // come in rounds leave SMs idle in the last one.  us for 1 .. 8 parts (chosen *):
-  // a query over 16002 keys, 64 heads on 8, 161 91 65 51 44 38 34 32*; 64 queries, 24
-  // heads, 208 114 83 66 58 50 47 43*; 4 chunks of 512 over 16001 more, 40 heads, 630
-  // 579* 658 655 728 778; 1000 queries over 5000, 32 heads, 62* 77 92.
-  static int choose_parts(const GqaPrefillLaunch& a) {
+  // How the call is launched: its first `whole` items a CTA each, then the rest, `parts`
+  // CTAs (a cluster) an item.
+  struct Plan {
+    long long whole;
+    int parts;
+  };
+
+  // Costs in key tiles, from the mean lengths (the lengths themselves are on the device):
+  // the late items' tiles, 4 for the start and end of an item of one CTA, 5.5 + 0.3 c with
+  // the join of c parts; items that come in rounds leave SMs idle in the last one.  So
+  // that a last round which leaves many idle may share its keys alone, after whole
+  // rounds, for the cost of a second launch: where the call is one request, whose
+  // lengths are known.  (Several leave empty blocks in places that the host does not
+  // know: four chunks of 504, 48 heads, 530 us with all items a CTA each, 582 shared so.)
+  // us:
+  //   parts 1 .. 8 of all items (chosen *): a query over 16002 keys, 64 heads on 8, 161
+  //   91 65 51 44 38 34 32*; 64 queries, 24 heads, 208 114 83 66 58 50 47 43*; 1000
+  //   queries over 5000, 32 heads, 62* 77 92; 4 chunks of 512 over 16001 more, 40 heads,
+  //   547 487*;
+  //   all items alike, or the last round's keys shared: 1300 queries over 16001 more, 64
+  //   heads on 8, 507 and 470; 4572 over 7211 more, 20 heads on 4, 325 and 296; 2642 over
+  //   24501 more, 16 heads of 64 dims on one, 322 and 280.
+  static Plan choose_plan(const GqaPrefillLaunch& a) {
     const double queries = static_cast<double>(a.total_q) / a.batch;
     const double blocks = std::max(1.0, std::ceil(queries / (2 * a.tile_q)));      // of a request
     const double items = blocks * a.batch * a.kv_heads;
     const double keys = static_cast<double>(a.total_k) / a.batch / Geo<kDim>::kKeys;    // key tiles of a late item ...
-    if (keys <= 4) return 1;                                                 // two parts cost 8 at least
+    Plan best = {0, 1};
+    if (keys <= 4) return best;                                              // two parts cost 8 at least
     const double spread =                                                    // ... and how many fewer an early one has
         a.causal ? std::min(keys, queries * (blocks - 1) / blocks / Geo<kDim>::kKeys) : 0;
-    int best = 1;
+    const double sms = clusters_at_once(1), mean1 = keys - spread / 2 + 4;
+    const double whole = std::floor(items / sms) * sms, rest = items - whole;
     double best_cost = 0;
     for (int c = 1; c <= kMaxParts; ++c) {
       const double extra = c == 1 ? 4 : 5.5 + 0.3 * c, n = clusters_at_once(c);
@@ -820,8 +839,14 @@ struct Host {
       const double mean = (keys - spread / 2) / c + extra, least = (keys - spread) / c + extra;
       const double cost = std::max(most, (items * mean + (std::ceil(items / n) * n - items) * least) / n);
       if (c == 1 || cost < 0.97 * best_cost) {
-        best = c;
+        best = {0, c};
         best_cost = cost;
+      }
+      if (c == 1 || a.batch > 1 || whole == 0 || rest == 0) continue;
+      const double after = whole * mean1 / sms + std::ceil(rest / n) * mean + 8;
+      if (after < 0.97 * best_cost) {
+        best = {static_cast<long long>(whole), c};
+        best_cost = after;
       }
     }
     return best;
@@ -846,11 +871,16 @@ struct Host {
       return cudaErrorInvalidValue;
     cudaError_t e = cudaFuncSetAttribute(gqa_prefill_kernel<kDim>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmemBytes);
     if (e != cudaSuccess) return e;
-    a.parts = choose_parts(a);
-    const long long ctas = items * a.parts;
-    if (ctas > INT_MAX) return cudaErrorInvalidValue;      // (parts are 1 where there are many items)
-    return launch_kernel(gqa_prefill_kernel<kDim>, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), T::kSmemBytes, s, false,
-                         a.parts, tq, tk, tv, a);
+    const Plan plan = choose_plan(a);
+    if ((items - plan.whole) * plan.parts > INT_MAX) return cudaErrorInvalidValue;      // (parts are 1 where there are many items)
+    auto run = [&](long long first, long long count, int parts) {
+      a.first_item = static_cast<int>(first);
+      a.parts = parts;
+      return launch_kernel(gqa_prefill_kernel<kDim>, dim3(static_cast<unsigned>(count * parts)), dim3(kThreads), T::kSmemBytes, s,
+                           false, parts, tq, tk, tv, a);
+    };
+    if (plan.whole > 0 && (e = run(0, plan.whole, 1)) != cudaSuccess) return e;
+    return run(plan.whole, items - plan.whole, plan.parts);
   }
 };
 

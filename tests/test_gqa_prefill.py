@@ -154,6 +154,20 @@ RAMPS = {
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("n,m,H,K", [(1300, 5400, 64, 8), (2700, 6000, 16, 1), (1235, 3001, 40, 8), (2600, 1900, 64, 8)])
+def test_a_last_round_that_shares_keys(L, n, m, H, K, causal, D):
+    """One request of a few more blocks than there are SMs (or twice as many): all of them are done, once."""
+    c = _case([n], [m], H, K, D, seed=n + m)
+    out, lse = _run(c, causal)
+    assert api.dsa_get_device_error() == 0
+    _check(c, causal, out, lse, heads=range(0, H, max(1, H // 5)))
+    again, _ = _run(c, causal, lse=False)
+    assert torch.equal(out, again)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("ramp", sorted(RAMPS))
 @pytest.mark.parametrize("qlens,klens,H,K", [([1500, 700], [1500, 2500], 6, 2), ([130], [4100], 8, 8), ([300] * 8, [900] * 8, 40, 8)])
 def test_scores_over_many_powers_of_two(L, qlens, klens, H, K, ramp, D):

@@ -283,16 +283,18 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t addr, uint32_t (&r)[kN]) {
   else tmem_ld128(addr, r);
 }
 
-template <int kDim, int kCopies, bool kNarrow, bool kFp8>
+// kNarrow: 8 or 16, where the tile has so many rows at most (a thread has one or two), else 0.
+template <int kDim, int kCopies, int kNarrow, bool kFp8>
 __global__ void __launch_bounds__(!kFp8 ? kThreads : kNarrow ? kThreadsParts : kThreadsFp8, 1)
     gqa_decode_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                       const __grid_constant__ CUtensorMap tmap_v, const GqaDecodeLaunch p) {
-  using T = Geo<kDim, kNarrow, kFp8>;
+  using T = Geo<kDim, (kNarrow > 0), kFp8>;
   constexpr bool kParts = T::kParts, kDequant = T::kDequant;
   constexpr int kCols = kKeys / kCopies;         // keys of a softmax thread
   constexpr int kStretch = kFp8 ? kStretchFp8 : kStretchBf16;
   constexpr int kCopyRows = kRows / kCopies;     // lanes of a copy
   constexpr int kSets = kParts ? 2 * kCopies : kCopies, kSetRows = kRows / kSets;      // outputs to be added up
+  constexpr int kMine = kNarrow / 8;             // rows of a softmax thread (kNarrow)
   static_assert(!kNarrow || kCopies == 4, "a warp a copy");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -702,17 +704,19 @@ __global__ void __launch_bounds__(!kFp8 ? kThreads : kNarrow ? kThreadsParts : k
       const int head = wk.item / p.row_tiles, mtile = wk.item % p.row_tiles;
       const int qi = mtile * p.tile_q + my_q;
       const bool live = my_q < p.tile_q && qi < p.nq;
-      const int vis = live ? wk.len - (p.nq - 1 - qi) : 0;
+      // (A row behind the last query's sees what that one does, so that its warp does not
+      // mask every tile.  Its scores are of what lies in shared memory: they go nowhere.)
+      const int vis = wk.len - (p.nq - 1 - min(mtile * p.tile_q + min(my_q, p.tile_q - 1), p.nq - 1));
       float mrun = ninf, lrun = 0.f;      // maximum and sum (this thread's keys) in the exp2 domain
-      // (kNarrow) The same of this thread's two rows, lane / 4 and that + 8; their
-      // visible tokens, and FP8 their factors.
+      // (kNarrow) The same of this thread's rows, lane / 4 and that + 8; their visible
+      // tokens, and FP8 their factors.
       float mrun2[2] = {ninf, ninf}, lrun2[2] = {0.f, 0.f}, f2[2] = {0.f, 0.f};
       int vis2[2] = {0, 0};
-      if constexpr (kNarrow) {
+      if constexpr (kNarrow > 0) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int r = (lane >> 2) + 8 * u, i = mtile * p.tile_q + r / group;
-          if (r < p.tile_rows && i < p.nq) vis2[u] = wk.len - (p.nq - 1 - i);
+        for (int u = 0; u < kMine; ++u) {
+          const int r = min((lane >> 2) + 8 * u, p.tile_rows - 1);
+          vis2[u] = wk.len - (p.nq - 1 - min(mtile * p.tile_q + r / group, p.nq - 1));
         }
       }
       uint32_t good = 0;                  // validity of the next 32 page ids
@@ -724,7 +728,8 @@ __global__ void __launch_bounds__(!kFp8 ? kThreads : kNarrow ? kThreadsParts : k
           uint32_t lo[16];
           tmem_ld16x32(tmem + lanebase + (16u << 16) + kColS + kKeys * (it & 1) + kCols * copy, lo);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) s[e] = __float_as_uint(__uint_as_float(s[e]) + __uint_as_float(lo[e]));
+          for (int e = 0; e < 16; ++e)
+            if (((e >> 1) & 1) < kMine) s[e] = __float_as_uint(__uint_as_float(s[e]) + __uint_as_float(lo[e]));
         }
         const int col = 2 * (lane & 3);      // of each eight
         const float* par = reinterpret_cast<const float*>(smem + T::kOffParam) + (it & 1) * 3 * kKeys + kCols * copy + col;
@@ -734,14 +739,14 @@ __global__ void __launch_bounds__(!kFp8 ? kThreads : kNarrow ? kThreadsParts : k
           if (t == wk.t0) {
             const float* qs = reinterpret_cast<const float*>(smem + T::kOffQScale) + (seg & 3) * kRows;
 #pragma unroll
-            for (int u = 0; u < 2; ++u) f2[u] = sc * qs[min((lane >> 2) + 8 * u, p.tile_rows - 1)];
+            for (int u = 0; u < kMine; ++u) f2[u] = sc * qs[min((lane >> 2) + 8 * u, p.tile_rows - 1)];
           }
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const float2 kk = *reinterpret_cast<const float2*>(par + 8 * j);
             const float2 lg = *reinterpret_cast<const float2*>(par + kKeys + 8 * j);
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
+            for (int u = 0; u < kMine; ++u) {
               const float2 z = fma2(mul2(make_float2(__uint_as_float(s[4 * j + 2 * u]), __uint_as_float(s[4 * j + 2 * u + 1])), kk),
                                     make_float2(f2[u], f2[u]), lg);
               s[4 * j + 2 * u] = __float_as_uint(z.x);
@@ -749,10 +754,10 @@ __global__ void __launch_bounds__(!kFp8 ? kThreads : kNarrow ? kThreadsParts : k
             }
           }
         }
-        float tmax[2], fac[2];
+        float tmax[2], fac[2] = {1.f, 1.f};
         bool rescale = false;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+        for (int u = 0; u < kMine; ++u) {
           const int seen = ((ok2 >> (kCols * copy / kPage)) & 1u) ? vis2[u] - t * kKeys - kCols * copy - col : 0;
           if (seen < 26) {      // (columns 8 j and 8 j + 1 from `col` on)
 #pragma unroll
@@ -767,7 +772,7 @@ __global__ void __launch_bounds__(!kFp8 ? kThreads : kNarrow ? kThreadsParts : k
           tmax[u] = m * (kFp8 ? 1.f : sc);
           const bool raise = tmax[u] > mrun2[u] + kRaise;
           fac[u] = raise && mrun2[u] > ninf ? ex2(mrun2[u] - tmax[u]) : 1.f;
-          rescale |= raise && mrun2[u] > ninf;
+          rescale |= raise && mrun2[u] > ninf && (lane >> 2) + 8 * u < p.tile_rows;
           if (raise) mrun2[u] = tmax[u];
           lrun2[u] *= fac[u];
         }
@@ -789,9 +794,9 @@ __global__ void __launch_bounds__(!kFp8 ? kThreads : kNarrow ? kThreadsParts : k
         // P of tile it - 2 has been read.
         if (it >= 2 && ok && !mbar_wait(PV_DONE(it), PARITY2(it - 2))) ok = false;
         tc_fence_after();
-        uint32_t pk[8];
+        uint32_t pk[8] = {};
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+        for (int u = 0; u < kMine; ++u) {
           const float mref = mrun2[u] > ninf ? mrun2[u] - kShift : 0.f;
           float2 ls = make_float2(0.f, 0.f);
 #pragma unroll
@@ -844,7 +849,7 @@ __global__ void __launch_bounds__(!kFp8 ? kThreads : kNarrow ? kThreadsParts : k
         const uint32_t ok2 = good >> (2 * ((t - wk.t0) & (PageBatch::kTiles - 1)));
         if (ok && !mbar_wait(S_FULL(it), PARITY2(it))) ok = false;
         tc_fence_after();
-        if constexpr (kNarrow) {
+        if constexpr (kNarrow > 0) {
           narrow_tile(t, ok2);
         } else {
         uint32_t s[kCols];
@@ -882,7 +887,7 @@ __global__ void __launch_bounds__(!kFp8 ? kThreads : kNarrow ? kThreadsParts : k
           mx[(e >> 1) & 3] = max3(mx[(e >> 1) & 3], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
         const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * (kFp8 ? 1.f : sc);
         const bool raise = tmax > mrun + kRaise;
-        const bool rescale = raise && mrun > ninf;
+        const bool rescale = raise && mrun > ninf && live;
         if (__any_sync(0xffffffffu, rescale)) {
           // P V of the tile before has to be in the output first.
           if (ok && !mbar_wait(PV_DONE(it - 1), PARITY2(it - 1))) ok = false;
@@ -946,8 +951,8 @@ __global__ void __launch_bounds__(!kFp8 ? kThreads : kNarrow ? kThreadsParts : k
         __syncwarp();
         if (lane == 0) mbar_arrive(P_FULL(it));
       }
-      if constexpr (kNarrow) {
-        // From two rows a thread to a row a lane.
+      if constexpr (kNarrow > 0) {
+        // From a thread's rows to a row a lane.
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           lrun2[u] += __shfl_xor_sync(0xffffffffu, lrun2[u], 1);
@@ -1192,9 +1197,9 @@ int row_tiles_of(int nq, int group) {
   return (nq + fit - 1) / fit;
 }
 
-template <int kDim, int kCopies, bool kNarrow, bool kFp8>
+template <int kDim, int kCopies, int kNarrow, bool kFp8>
 cudaError_t launch(const GqaDecodeLaunch& a, cudaStream_t s) {
-  using T = Geo<kDim, kNarrow, kFp8>;
+  using T = Geo<kDim, (kNarrow > 0), kFp8>;
   const uint64_t G = a.heads / a.kv_heads, K = a.kv_heads, tokens = static_cast<uint64_t>(a.batch) * a.nq;
   const uint64_t pages = static_cast<uint64_t>(a.num_pages);
   CUtensorMap tq, tk, tv;
@@ -1238,10 +1243,11 @@ cudaError_t launch(const GqaDecodeLaunch& a, cudaStream_t s) {
 // As many copies of the rows as fit into a tile.
 template <int kDim, bool kFp8>
 cudaError_t launch_rows(const GqaDecodeLaunch& a, cudaStream_t s) {
-  if (a.tile_rows <= 16) return launch<kDim, 4, true, kFp8>(a, s);
-  if (a.tile_rows <= 32) return launch<kDim, 4, false, kFp8>(a, s);
-  if (a.tile_rows <= 64) return launch<kDim, 2, false, kFp8>(a, s);
-  return launch<kDim, 1, false, kFp8>(a, s);
+  if (a.tile_rows <= 8) return launch<kDim, 4, 8, kFp8>(a, s);
+  if (a.tile_rows <= 16) return launch<kDim, 4, 16, kFp8>(a, s);
+  if (a.tile_rows <= 32) return launch<kDim, 4, 0, kFp8>(a, s);
+  if (a.tile_rows <= 64) return launch<kDim, 2, 0, kFp8>(a, s);
+  return launch<kDim, 1, 0, kFp8>(a, s);
 }
 
 }  // namespace

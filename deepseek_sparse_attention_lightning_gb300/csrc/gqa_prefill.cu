@@ -613,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mx[(e >> 1) & 3] = max3(mx[(e >> 1) & 3], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
         const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
         const bool raise = tmax > mrun + kRaiseLog2;
-        const bool rescale = raise && mrun > ninf;
+        const bool rescale = raise && mrun > ninf && used;
         if (__any_sync(0xffffffffu, rescale)) {
           // (kBufs 1: P V of the tile before is done: it was issued before this Q K^T.)
           if (T::kBufs == 2) {

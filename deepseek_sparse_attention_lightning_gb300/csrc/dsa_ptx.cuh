@@ -645,6 +645,20 @@ __device__ __forceinline__ void tmem_ld16x32(uint32_t taddr, uint32_t (&r)[16]) 
       : "memory");
 }
 
+// Two of these and one wait.
+__device__ __forceinline__ void tmem_ld16x32_two(uint32_t taddr_r, uint32_t taddr_q, uint32_t (&r)[16], uint32_t (&q)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n"
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%33];\n"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : "=&r"(r[0]), "=&r"(r[1]), "=&r"(r[2]), "=&r"(r[3]), "=&r"(r[4]), "=&r"(r[5]), "=&r"(r[6]), "=&r"(r[7]),
+        "=&r"(r[8]), "=&r"(r[9]), "=&r"(r[10]), "=&r"(r[11]), "=&r"(r[12]), "=&r"(r[13]), "=&r"(r[14]), "=&r"(r[15]),
+        "=&r"(q[0]), "=&r"(q[1]), "=&r"(q[2]), "=&r"(q[3]), "=&r"(q[4]), "=&r"(q[5]), "=&r"(q[6]), "=&r"(q[7]),
+        "=&r"(q[8]), "=&r"(q[9]), "=&r"(q[10]), "=&r"(q[11]), "=&r"(q[12]), "=&r"(q[13]), "=&r"(q[14]), "=&r"(q[15])
+      : "r"(taddr_r), "r"(taddr_q)
+      : "memory");
+}
+
 // Registers -> 16 lanes x 16 columns of TMEM: registers 2 j and 2 j + 1 of lane l are
 // column 4 j + l % 4 of rows l / 4 and l / 4 + 8.
 __device__ __forceinline__ void tmem_st16x16_async(uint32_t taddr, const uint32_t (&r)[8]) {

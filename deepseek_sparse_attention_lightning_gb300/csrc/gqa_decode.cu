@@ -722,11 +722,13 @@ __global__ void __launch_bounds__(!kFp8 ? kThreads : kNarrow ? kThreadsParts : k
       uint32_t good = 0;                  // validity of the next 32 page ids
       auto narrow_tile = [&](int t, uint32_t ok2) {
         uint32_t s[16];
-        tmem_ld16x32(tmem + lanebase + kColS + kKeys * (it & 1) + kCols * copy, s);
-        if constexpr (kParts) {
+        const uint32_t ts = tmem + lanebase + kColS + kKeys * (it & 1) + kCols * copy;
+        if constexpr (!kParts) {
+          tmem_ld16x32(ts, s);
+        } else {
           // The scores of the query's lower part, sixteen lanes on.
           uint32_t lo[16];
-          tmem_ld16x32(tmem + lanebase + (16u << 16) + kColS + kKeys * (it & 1) + kCols * copy, lo);
+          tmem_ld16x32_two(ts, ts + (16u << 16), s, lo);
 #pragma unroll
           for (int e = 0; e < 16; ++e)
             if (((e >> 1) & 1) < kMine) s[e] = __float_as_uint(__uint_as_float(s[e]) + __uint_as_float(lo[e]));
@@ -754,8 +756,8 @@ __global__ void __launch_bounds__(!kFp8 ? kThreads : kNarrow ? kThreadsParts : k
             }
           }
         }
-        float tmax[2], fac[2] = {1.f, 1.f};
-        bool rescale = false;
+        float top[2];
+        bool above = false;
 #pragma unroll
         for (int u = 0; u < kMine; ++u) {
           const int seen = ((ok2 >> (kCols * copy / kPage)) & 1u) ? vis2[u] - t * kKeys - kCols * copy - col : 0;
@@ -767,33 +769,41 @@ __global__ void __launch_bounds__(!kFp8 ? kThreads : kNarrow ? kThreadsParts : k
           float m = ninf;
 #pragma unroll
           for (int j = 0; j < 4; ++j) m = max3(m, __uint_as_float(s[4 * j + 2 * u]), __uint_as_float(s[4 * j + 2 * u + 1]));
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-          tmax[u] = m * (kFp8 ? 1.f : sc);
-          const bool raise = tmax[u] > mrun2[u] + kRaise;
-          fac[u] = raise && mrun2[u] > ninf ? ex2(mrun2[u] - tmax[u]) : 1.f;
-          rescale |= raise && mrun2[u] > ninf && (lane >> 2) + 8 * u < p.tile_rows;
-          if (raise) mrun2[u] = tmax[u];
-          lrun2[u] *= fac[u];
+          top[u] = m * (kFp8 ? 1.f : sc);
+          above |= top[u] > mrun2[u] + kRaise;
         }
-        if (__any_sync(0xffffffffu, rescale)) {
-          // P V of the tile before has to be in the output first.
-          if (ok && !mbar_wait(PV_DONE(it - 1), PARITY2(it - 1))) ok = false;
-          tc_fence_after();
-          const float fa = __shfl_sync(0xffffffffu, fac[0], 4 * (lane & 7)), fb = __shfl_sync(0xffffffffu, fac[1], 4 * (lane & 7));
-          const float f = !kParts && lane >= 16 ? 1.f : (lane & 15) < 8 ? fa : fb;
-#pragma unroll 1
-          for (int c = 0; c < kDim / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld32(tmem + lanebase + kColO + 32 * c, o);
+        // (The row's maximum, over four lanes, is asked for only where one of them is
+        // above.)
+        if (__any_sync(0xffffffffu, above)) {
+          float fac[2] = {1.f, 1.f};
+          bool rescale = false;
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tmem_st32(tmem + lanebase + kColO + 32 * c, o);
+          for (int u = 0; u < kMine; ++u) {
+            top[u] = fmaxf(top[u], __shfl_xor_sync(0xffffffffu, top[u], 1));
+            top[u] = fmaxf(top[u], __shfl_xor_sync(0xffffffffu, top[u], 2));
+            const bool raise = top[u] > mrun2[u] + kRaise;
+            fac[u] = raise && mrun2[u] > ninf ? ex2(mrun2[u] - top[u]) : 1.f;
+            rescale |= raise && mrun2[u] > ninf && (lane >> 2) + 8 * u < p.tile_rows;
+            if (raise) mrun2[u] = top[u];
+            lrun2[u] *= fac[u];
+          }
+          if (__any_sync(0xffffffffu, rescale)) {
+            // P V of the tile before has to be in the output first.
+            if (ok && !mbar_wait(PV_DONE(it - 1), PARITY2(it - 1))) ok = false;
+            tc_fence_after();
+            const float fa = __shfl_sync(0xffffffffu, fac[0], 4 * (lane & 7)), fb = __shfl_sync(0xffffffffu, fac[1], 4 * (lane & 7));
+            const float f = !kParts && lane >= 16 ? 1.f : (lane & 15) < 8 ? fa : fb;
+#pragma unroll 1
+            for (int c = 0; c < kDim / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(tmem + lanebase + kColO + 32 * c, o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st32(tmem + lanebase + kColO + 32 * c, o);
+            }
           }
         }
-        // P of tile it - 2 has been read.
-        if (it >= 2 && ok && !mbar_wait(PV_DONE(it), PARITY2(it - 2))) ok = false;
-        tc_fence_after();
+        // (P of tile it - 2 has been read: that P V was issued before this Q K^T.)
         uint32_t pk[8] = {};
 #pragma unroll
         for (int u = 0; u < kMine; ++u) {
@@ -906,9 +916,7 @@ __global__ void __launch_bounds__(!kFp8 ? kThreads : kNarrow ? kThreadsParts : k
         if (raise) mrun = tmax;
         // (FP8: P up to 2^15, which leaves fp16 40 powers of two below.)
         const float mref = mrun > ninf ? mrun - kShift : 0.f;
-        // P of tile it - 2 has been read.
-        if (it >= 2 && ok && !mbar_wait(PV_DONE(it), PARITY2(it - 2))) ok = false;
-        tc_fence_after();
+        // (P of tile it - 2 has been read: that P V was issued before this Q K^T.)
         float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         const uint32_t tp = tmem + lanebase + kColP + 64 * (it & 1) + (kCols / 2) * copy;
 #pragma unroll
@@ -1243,7 +1251,8 @@ cudaError_t launch(const GqaDecodeLaunch& a, cudaStream_t s) {
 // As many copies of the rows as fit into a tile.
 template <int kDim, bool kFp8>
 cudaError_t launch_rows(const GqaDecodeLaunch& a, cudaStream_t s) {
-  if (a.tile_rows <= 8) return launch<kDim, 4, 8, kFp8>(a, s);
+  if constexpr (kFp8)      // (bf16: the same time)
+    if (a.tile_rows <= 8) return launch<kDim, 4, 8, kFp8>(a, s);
   if (a.tile_rows <= 16) return launch<kDim, 4, 16, kFp8>(a, s);
   if (a.tile_rows <= 32) return launch<kDim, 4, 0, kFp8>(a, s);
   if (a.tile_rows <= 64) return launch<kDim, 2, 0, kFp8>(a, s);

@@ -6,10 +6,10 @@
 //   out[row]  = sum_s softmax(x)[s] * v[s],   lse = log sum_s exp(x)
 //
 // Bound by HBM: every key and value is read once, for n_q * G rows that share it.  64
-// heads on 8, bf16: 8 requests of 131072 tokens 601 us (7.1 TB/s; the measured copy
-// rate is 6.8), 8 of 32768 162 us (6.6 TB/s).  FP8: 8 of 32768 104 us (5.3 TB/s: the
-// softmax warps' instructions, of which codes need more, for half the bytes).  A short
-// context is bound by latency: 1 request of 4096, 32 heads, 10.8 us, of which the bytes
+// heads on 8, bf16: 8 requests of 131072 tokens 602 us (7.1 TB/s; the measured copy
+// rate is 6.8), 8 of 32768 160 us (6.7 TB/s).  FP8, 8 of 32768: 97.5 us (5.7 TB/s: a
+// tile's way through the softmax, some 1500 cycles, is as long as its copy).  A short
+// context is bound by latency: 1 request of 4096, 32 heads, 10.9 us, of which the bytes
 // take 2.4.
 //
 // The rows of a request and key head are one row tile (M = 128; more queries than
@@ -42,9 +42,9 @@
 // before P V: their probabilities are zero, but what lies there may be NaN.
 //
 // Up to 16 rows (kNarrow; most decode steps) lie in the first 16 lanes of a copy and
-// are read as 16 lanes x 8 columns, two rows a thread, so that all lanes of the warp
-// work on them (FP8, 32 ragged requests of 16384 .. 65536: 629 us by a row a thread,
-// 534 so).
+// are read as 16 lanes x 8 columns, two rows a thread (up to 8 FP8 rows: one), so that
+// all lanes of the warp work on them (FP8, 32 ragged requests of 16384 .. 65536, with
+// codes made fp16: 629 us by a row a thread, 534 so).
 //
 // FP8 rows (kFp8; 128 dims): a key or value is its E4M3 code times its row's scale,
 // half the bytes, so half the time for the rest.  Nothing is converted for Q K^T: it
@@ -62,7 +62,8 @@
 //   of two products, and the scores are added where they are read, the outputs with
 //   those of the copies.  A thread holds pairs of keys 8 apart, so the copies bring V's
 //   rows in the order 0 1 8 9 2 3 10 11 ... and the pairs make bytes of one column.
-//   768 cycles of MMAs a tile, 32 KB.  (445 us for the requests above.)
+//   768 cycles of MMAs a tile, 32 KB.  (421 us for the requests above, 2.75 GB: 6.6
+//   TB/s.)
 //
 //   More rows: the query's parts side by side, into the same scores; V's codes become
 //   fp16 (exactly) in eight warps of their own, which the conversions bound.
@@ -92,7 +93,8 @@ constexpr int kDequantWarps = 8, kParamWarps = 4;      // FP8; the latter of the
 constexpr int kRegsMma = 88, kRegsSoft = 216, kRegsDequant = 104;
 static_assert(kRegsMma + kRegsSoft + 2 * kRegsDequant <= 4 * 128, "registers");
 // What an item's queries and output cost, in key tiles: bf16, FP8 (whose tiles take half
-// the time).  64 requests of 1000 .. 6000 FP8 tokens: 107 us for 1, 103 for 2, 97 for 4.
+// the time).  128 requests of 100 .. 900 bf16 tokens: 60.0 us for 1, 58.7 for 2, 59.7 for
+// 3; 64 of 1000 .. 6000 FP8 tokens: 100.8 for 1, 97.3 for 2, 90.6 for 4, 91.7 for 6.
 constexpr int kStretchBf16 = 2, kStretchFp8 = 4;
 constexpr int kColS = 0, kColP = 256, kColO = 384, kTmemCols = 512;
 constexpr int kStage = kSoftThreads * 32 * 4;  // 32 columns of a copy's rows, fp32
@@ -1196,7 +1198,7 @@ __global__ void __launch_bounds__(kMergeThreads) gqa_merge_kernel(const GqaDecod
 }
 
 // Keys of a CTA's part of the line, at least: less is not worth a CTA (1 request of 4000
-// tokens, 32 heads on 8: 128 11.4 us, 256 10.8, 512 12.9, 1024 15.6).
+// tokens, 32 heads on 8: 128 11.4 us, 256 10.9, 512 13.1).
 constexpr int kMinKeys = 256;
 
 // Queries of a row tile: as many as fit, the tiles of a request alike.

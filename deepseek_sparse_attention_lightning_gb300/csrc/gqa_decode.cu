@@ -62,7 +62,7 @@
 //   of two products, and the scores are added where they are read, the outputs with
 //   those of the copies.  A thread holds pairs of keys 8 apart, so the copies bring V's
 //   rows in the order 0 1 8 9 2 3 10 11 ... and the pairs make bytes of one column.
-//   768 cycles of MMAs a tile, 32 KB.  (421 us for the requests above, 2.75 GB: 6.6
+//   768 cycles of MMAs a tile, 32 KB.  (421 us for the requests above, 2.77 GB: 6.6
 //   TB/s.)
 //
 //   More rows: the query's parts side by side, into the same scores; V's codes become

@@ -1,6 +1,6 @@
-"""Times the cases of perf/operators.py on the current GPU.
+"""Times the cases of perf/operators.py, or with --grouped those of perf/more_operators.py, on the current GPU.
 
-    python -m perf.time_operators [--plain] [CASE ...]
+    python -m perf.time_operators [--grouped] [--plain] [CASE ...]
 
 For each case, the kernels' calls (--plain: the plain forms) over three states of different inputs in turn, timed
 with CUDA events around a run of passes after warm-up: the median of five runs in microseconds a pass, and the
@@ -11,17 +11,17 @@ import argparse
 
 import torch
 
-from perf import operators
+from perf import more_operators, operators
 
 
-def pass_us(states, budget_ms=60.0):
+def pass_us(states, run=operators.run, budget_ms=60.0):
     """Microseconds a pass over `states` in turn."""
     start, stop = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
 
     def once(n):
         start.record()
         for i in range(n):
-            operators.run(states[i % len(states)])
+            run(states[i % len(states)])
         stop.record()
         stop.synchronize()
         return start.elapsed_time(stop) / n
@@ -33,17 +33,19 @@ def pass_us(states, budget_ms=60.0):
 
 def main():
     parser = argparse.ArgumentParser()
+    parser.add_argument("--grouped", action="store_true")
     parser.add_argument("--plain", action="store_true")
     parser.add_argument("case", nargs="*")
     args = parser.parse_args()
-    operators.own = not args.plain
-    known = {c["name"]: c for c in operators.listed()}
+    cases = more_operators if args.grouped else operators
+    cases.own = not args.plain
+    known = {c["name"]: c for c in cases.listed()}
     for name in args.case or known:
         if name not in known:
             parser.error(f"no case {name}; there are {', '.join(known)}")
     for name in args.case or known:
-        work = operators.work(known[name])
-        us = pass_us([operators.prepare(known[name], seed) for seed in range(3)])
+        work = cases.work(known[name])
+        us = pass_us([cases.prepare(known[name], seed) for seed in range(3)], cases.run)
         print(f"{name:20s} {us:10.2f} us  {work['bytes'] / us * 1e-3:8.0f} GB/s  {work['flops'] / us * 1e-6:8.1f} TFLOP/s",
               flush=True)
         torch.cuda.empty_cache()

@@ -309,75 +309,94 @@ __global__ void __launch_bounds__(kThreads, 1) pages_kernel(const PagesLaunch p)
   auto length = [&](int r) { return near ? lengths[r] : p.seqlens_out[r]; };
   const int tokens = static_cast<int>(min(all_tokens, static_cast<uint32_t>(p.max_tokens)));
   const bool wide = (reinterpret_cast<uintptr_t>(p.slots) & 31) == 0;
-  for (long long t0 = static_cast<long long>(kRun) * (rank * kThreads + tid); t0 < p.max_tokens;
-       t0 += static_cast<long long>(kRun) * kThreads * kCtas) {
-    int v[kRun];
-#pragma unroll
-    for (int e = 0; e < kRun; ++e) v[e] = -1;
-    if (t0 < tokens) {
-      int r = 0, hi = p.batch - 1;      // the first request that ends behind t0
+  // A thread has runs of kRun slots: one every grid's width, or (kRun 8) as many as there
+  // are for it one behind the other, so that it looks for a request once (256 prompts of
+  // 1 .. 4096 tokens: 16.4 us a run every grid's width, 13.4 so).
+  constexpr long long kWidth = static_cast<long long>(kRun) * kThreads * kCtas;
+  const int runs = kRun > 1 ? static_cast<int>((p.max_tokens + kWidth - 1) / kWidth) : 1;
+  const int first_run = kRun > 1 ? (warp * kCtas + rank) * 32 + lane : rank * kThreads + tid;
+  for (long long c0 = static_cast<long long>(kRun) * runs * first_run; c0 < p.max_tokens; c0 += kWidth * runs) {
+    int r = 0, end = 0, len = 0;
+    if (c0 < tokens) {
+      int hi = p.batch - 1;      // the first request that ends behind c0
       while (r < hi) {
         const int mid = (r + hi) >> 1;
-        if (offset(mid + 1) > t0) hi = mid;
+        if (offset(mid + 1) > c0) hi = mid;
         else r = mid + 1;
       }
-      int end = offset(r + 1), len = length(r);
-      // Entry of the table for position `pos` of request r; the first row of its
-      // page, or -1.
-      auto entry = [&](int pos) { return p.page_table + static_cast<long long>(r) * p.max_pages + pos / kPage; };
-      auto first_row = [&](int id) {
-        if (id >= 0 && id < p.num_pages) return id * kPage;
-        raise_error(kErrCheck);
-        return -1;
-      };
-      if (kRun > 1 && t0 + kRun <= end) {
-        // One request's tokens, on one page or two.
-        if (len >= 0) {
-          const int pos = len - static_cast<int>(end - t0), row = pos % kPage;
-          const int id_a = *entry(pos), id_b = *entry(pos + kRun - 1);
-          const int a = first_row(id_a), b = first_row(id_b);
+      end = offset(r + 1);
+      len = length(r);
+    }
+    // Entry of the table for position `pos` of request r; the first row of its
+    // page, or -1.
+    auto entry = [&](int pos) { return p.page_table + static_cast<long long>(r) * p.max_pages + pos / kPage; };
+    auto first_row = [&](int id) {
+      if (id >= 0 && id < p.num_pages) return id * kPage;
+      raise_error(kErrCheck);
+      return -1;
+    };
+    auto to_request_of = [&](int t) {      // (requests without new tokens lie between)
+      while (t >= end) {
+        end = offset(++r + 1);
+        len = length(r);
+      }
+    };
+    for (int k = 0; k < runs; ++k) {
+      const long long t0 = c0 + static_cast<long long>(kRun) * k;
+      if (t0 >= p.max_tokens) break;
+      int v[kRun];
+#pragma unroll
+      for (int e = 0; e < kRun; ++e) v[e] = -1;
+      if (t0 < tokens) {
+        to_request_of(static_cast<int>(t0));
+        if (kRun > 1 && t0 + kRun <= end) {
+          // One request's tokens, on one page or two.
+          if (len >= 0) {
+            const int pos = len - static_cast<int>(end - t0), row = pos % kPage;
+            const int id_a = *entry(pos), id_b = *entry(pos + kRun - 1);
+            const int a = first_row(id_a), b = first_row(id_b);
+#pragma unroll
+            for (int e = 0; e < kRun; ++e) v[e] = row + e < kPage ? a + row + e : b + row + e - kPage;
+            if ((a | b) < 0) {
+#pragma unroll
+              for (int e = 0; e < kRun; ++e)
+                if ((row + e < kPage ? a : b) < 0) v[e] = -1;
+            }
+          }
+        } else {
+          // Where each token's entry is (all of them first, so that the loads overlap).
+          const int32_t* at[kRun];
+          int row[kRun];
 #pragma unroll
           for (int e = 0; e < kRun; ++e) {
-            const int first = row + e < kPage ? a : b;
-            v[e] = first < 0 ? -1 : first + ((row + e) & (kPage - 1));
+            const int t = static_cast<int>(t0) + e;
+            at[e] = nullptr;
+            if (t >= tokens) continue;
+            to_request_of(t);
+            const int pos = len - (end - t);
+            if (len >= 0) at[e] = entry(pos);
+            row[e] = pos % kPage;
           }
-        }
-      } else {
-        // Where each token's entry is (all of them first, so that the loads overlap).
-        const int32_t* at[kRun];
-        int row[kRun];
 #pragma unroll
-        for (int e = 0; e < kRun; ++e) {
-          const int t = static_cast<int>(t0) + e;
-          at[e] = nullptr;
-          if (t >= tokens) continue;
-          while (t >= end) {      // (requests without new tokens lie between)
-            end = offset(++r + 1);
-            len = length(r);
+          for (int e = 0; e < kRun; ++e) v[e] = at[e] ? *at[e] : -1;
+#pragma unroll
+          for (int e = 0; e < kRun; ++e) {
+            if (!at[e]) continue;
+            const int first = first_row(v[e]);
+            v[e] = first < 0 ? -1 : first + row[e];
           }
-          const int pos = len - (end - t);
-          if (len >= 0) at[e] = entry(pos);
-          row[e] = pos % kPage;
-        }
-#pragma unroll
-        for (int e = 0; e < kRun; ++e) v[e] = at[e] ? *at[e] : -1;
-#pragma unroll
-        for (int e = 0; e < kRun; ++e) {
-          if (!at[e]) continue;
-          const int first = first_row(v[e]);
-          v[e] = first < 0 ? -1 : first + row[e];
         }
       }
-    }
-    if (kRun == 8 && wide && t0 + kRun <= p.max_tokens) {
-      uint32_t w[8];
+      if (kRun == 8 && wide && t0 + kRun <= p.max_tokens) {
+        uint32_t w[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) w[e] = static_cast<uint32_t>(v[e % kRun]);
-      st_global_32(p.slots + t0, w);
-    } else {
+        for (int e = 0; e < 8; ++e) w[e] = static_cast<uint32_t>(v[e % kRun]);
+        st_global_32(p.slots + t0, w);
+      } else {
 #pragma unroll
-      for (int e = 0; e < kRun; ++e)
-        if (t0 + e < p.max_tokens) p.slots[t0 + e] = v[e];
+        for (int e = 0; e < kRun; ++e)
+          if (t0 + e < p.max_tokens) p.slots[t0 + e] = v[e];
+      }
     }
   }
   if (refused && kCtas > 1) cluster_sync();      // the others have read the lengths
@@ -394,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1) pages_kernel(const PagesLaunch p)
 // (a prompt's are on one page or two; a step's are on a page each, whose entries
 // would be waited for one after another).  us on the device: 128 requests of a token
 // 3.4 (in a cluster of 16: 10.9); 256 prompts of 1 .. 4096 tokens, half a million
-// slots, 16.2 (before the runs of eight, for 4 / 8 / 16 CTAs, 42 / 30 / 21).
+// slots, 13.4 (with a slot at a time, for 4 / 8 / 16 CTAs, 42 / 30 / 21).
 cudaError_t launch_pages(const PagesLaunch& a, cudaStream_t s) {
   if (a.batch <= 256 && a.max_tokens <= 4 * 256)
     return launch_kernel(pages_kernel<256, 1, 1>, dim3(1), dim3(256), 0, s, false, 1, a);

@@ -610,7 +610,8 @@ size_t dsa_gqa_decode_workspace_bytes(const dsa_decode_desc* desc, int32_t kv_he
  *   out       [dev] bf16 [total_q, H, D], 16-B aligned;  lse [dev] float
  *             [total_q, H] or NULL
  * Needs no workspace.  Bad offsets, rows behind the last request and finiteness as
- * for dsa_mla_prefill.  The same call gives the same bits.
+ * for dsa_mla_prefill (max_q rounded up to 2 * (128 / (H / K)) there).  The same call
+ * gives the same bits.
  */
 dsa_status dsa_gqa_prefill(int32_t batch, int32_t heads, int32_t kv_heads, int32_t dim,
                            int32_t total_q, int32_t total_k, int32_t max_q, const int32_t* cu_q,

@@ -52,8 +52,8 @@
 // has 8 bits, a code 4: the sum is exact for values down to 2^-9 of the row's largest,
 // and off by 2^-17 of that below).  The key's scale goes to the score.  The value's
 // scale goes into the probability through its exponent: with z = x + log2(scale), P =
-// 2^(z - m) under a running maximum of z, so that scales of any size leave P in fp16's
-// range; the sum takes P / scale.
+// 2^(z - m) under a running maximum of z, so that no scale takes P above fp16's range; the
+// sum takes P / scale.
 //
 //   Up to 16 rows (kParts): P V on codes too.  P, rounded to fp16, is four E5M2 parts
 //   (its upper byte, the upper byte of what is left, ...), which lose what lies below
@@ -70,6 +70,16 @@
 //
 //   (P in E4M3 parts would drop keys below 2^-17 of the largest, which a long context
 //   can have many of.)
+//
+//   So what P loses is relative to the largest weight times scale, whatever the codes of
+//   that row: a weight times scale 2^-24 of it still has 5 bits, and what lies below 2^-29
+//   (more rows: 2^-31) adds to the sum alone.  Rows of a request may differ so much where
+//   they bring little; but a row of zeros brings nothing, and dsa_kv_write_fp8 gives it
+//   scale 1, far above a row's of small values.  So such rows (scale 1, all codes zero) are
+//   looked for and count with kLeastScale: their P is as small as it gets, and their weight
+//   is in the sum all the same.  (The search for scales of 1 costs 0 to 1 %: 32 ragged
+//   requests 434 -> 436 us in calls of three states; where every row's scale is 1, each
+//   tile's codes are looked at, 446.)
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -631,7 +641,21 @@ __global__ void __launch_bounds__(!kFp8 ? kThreads : kNarrow ? kThreadsParts : k
           const float* scales = reinterpret_cast<const float*>(smem + T::kOffScale) + (it % (T::kRing / 2)) * 2 * kKeys;
           float* par = reinterpret_cast<float*>(smem + T::kOffParam) + (it & 1) * 3 * kKeys;
           const bool seen = tid < vlive && ((ok2 >> (tid / kPage)) & 1u);
-          const float vs = seen ? fmaxf(scales[kKeys + tid], kLeastScale) : 1.f;
+          float vs = seen ? fmaxf(scales[kKeys + tid], kLeastScale) : 1.f;
+          // A row of zeros, whose scale is 1, counts with the least scale.  (Only where there
+          // is such a scale are V's codes waited for.)
+          if (__any_sync(0xffffffffu, seen && vs == 1.f)) {
+            if (ok && !mbar_wait(FULL(n + 1), RING_PARITY(n + 1))) ok = false;
+            const int at = kParts ? (tid & ~15) | ((tid & 8) >> 2) | ((tid & 6) << 1) | (tid & 1) : tid;      // where its codes lie
+            const uint4* codes = reinterpret_cast<const uint4*>(smem + T::kOffRing + ((n + 1) % T::kRing) * T::kGranule + at * kDim);
+            uint32_t any = 0u;
+#pragma unroll
+            for (int e = 0; e < kDim / 16; ++e) {      // (neighbouring lanes on different banks)
+              const uint4 w4 = codes[(e + lane) % (kDim / 16)];
+              any |= w4.x | w4.y | w4.z | w4.w;
+            }
+            if (seen && vs == 1.f && (any & 0x7f7f7f7fu) == 0u) vs = kLeastScale;
+          }
           par[tid] = seen ? scales[tid] : 0.f;
           par[kKeys + tid] = log2f(vs);
           par[2 * kKeys + tid] = 1.f / vs;

@@ -577,11 +577,14 @@ dsa_status dsa_gqa_decode(const dsa_decode_desc* desc, int32_t kv_heads, int32_t
  * dsa_gqa_decode over FP8 caches (dsa_kv_write_fp8's; dim 128): the attention over
  * code x scale.  Scales of tokens that a query sees have to be 0 or more and finite;
  * values' scales below 2^-80 count as 2^-80 (their values are below 2^-71 then), and
- * a request's others lie within 2^100 of its smallest.  k_scale, v_scale 16-B
- * aligned.  (The query enters as the sum of
- * two E4M3 parts, exact but for values below 2^-9 of the largest of its row, which
- * are off by 2^-17 of that; codes are multiplied as they are, probabilities times
- * the value's scale rounded to fp16.)
+ * so do rows of zeros as dsa_kv_write_fp8 writes them (scale 1, every code 0); a
+ * request's others lie within 2^100 of its smallest (of what lies further below the
+ * largest, weights may be missing in the sum, lse included).  k_scale, v_scale 16-B
+ * aligned.  (The query enters as the sum of two E4M3 parts, exact but for values below
+ * 2^-9 of the largest of its row, which are off by 2^-17 of that; codes are multiplied
+ * as they are, probabilities times the value's scale rounded to fp16 and, where up to
+ * 16 query rows share a key head, cut below 2^-29 of the largest such product; with
+ * more, fp16's smallest step is 2^-31 of it.  The sum has the weights unrounded.)
  */
 dsa_status dsa_gqa_decode_fp8kv(const dsa_decode_desc* desc, int32_t kv_heads, int32_t dim,
                                 const uint16_t* q, const uint8_t* k8, const float* k_scale,

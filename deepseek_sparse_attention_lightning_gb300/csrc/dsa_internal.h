@@ -251,19 +251,19 @@ cudaError_t launch_kernel(void (*kern)(Exp...), dim3 grid, dim3 block, size_t sm
   return cudaLaunchKernelEx(&cfg, kern, static_cast<Act&&>(args)...);
 }
 
-// Each translation unit keeps its own device error word; these read and clear
-// them (synchronous).  Return 0 or a dsa_status code.
-int fetch_error_indexer();
-int fetch_error_topk();
-int fetch_error_mla();
-int fetch_error_merge();
-int fetch_error_cache();
-int fetch_error_mla_dense();
-int fetch_error_mla_prefill();
-int fetch_error_pages();
-int fetch_error_kv_write();
-int fetch_error_gqa_prefill();
-int fetch_error_gqa_decode();
+// Each translation unit keeps its own device error word (0 or a dsa_status code);
+// these give its address on the current device, or nullptr.
+int* error_word_indexer();
+int* error_word_topk();
+int* error_word_mla();
+int* error_word_merge();
+int* error_word_cache();
+int* error_word_mla_dense();
+int* error_word_mla_prefill();
+int* error_word_pages();
+int* error_word_kv_write();
+int* error_word_gqa_prefill();
+int* error_word_gqa_decode();
 
 // Host helpers (dsa_api.cu).
 // The checks every entry point applies to a decode descriptor: a dsa_status.
@@ -280,17 +280,15 @@ int device_sm_count();
 
 }  // namespace dsa
 
-// Defines the per-TU device error word and its host accessor.
+// Defines the per-TU device error word and what gives its address.
 #define DSA_DEFINE_ERROR_WORD(NAME)                                                    \
   namespace dsa {                                                                      \
   static __device__ int g_error_word = 0;                                              \
   __device__ __forceinline__ void raise_error(int code) {                              \
     atomicCAS(&g_error_word, 0, code);                                                 \
   }                                                                                    \
-  int fetch_error_##NAME() {                                                           \
-    int v = 0, zero = 0;                                                               \
-    if (cudaMemcpyFromSymbol(&v, g_error_word, sizeof(int)) != cudaSuccess) return 4;  \
-    if (v != 0) cudaMemcpyToSymbol(g_error_word, &zero, sizeof(int));                  \
-    return v;                                                                          \
+  int* error_word_##NAME() {                                                           \
+    void* at = nullptr;                                                                \
+    return cudaGetSymbolAddress(&at, g_error_word) == cudaSuccess ? static_cast<int*>(at) : nullptr; \
   }                                                                                    \
   }

@@ -7,7 +7,7 @@
 //
 // Bound by HBM: every key and value is read once, for n_q * G rows that share it.  64
 // heads on 8, bf16: 8 requests of 131072 tokens 602 us (7.1 TB/s; the measured copy
-// rate is 6.8), 8 of 32768 160 us (6.7 TB/s).  FP8, 8 of 32768: 97.5 us (5.7 TB/s: a
+// rate is 6.8), 8 of 32768 160 us (6.7 TB/s).  FP8, 8 of 32768: 98 us (5.7 TB/s: a
 // tile's way through the softmax, some 1500 cycles, is as long as its copy).  A short
 // context is bound by latency: 1 request of 4096, 32 heads, 10.9 us, of which the bytes
 // take 2.4.
